@@ -1,0 +1,103 @@
+/*
+ * forge_ops.h - C ABI of the operators around the fused weight-gradient step
+ * (forge.h) for AMD Instinct MI355X (gfx950): the global gradient norm with
+ * the clipped optimizer steps.
+ *
+ * The conventions of forge.h hold here too: device pointers owned by the
+ * caller, dense row-major arrays, 16-byte aligned pointers, nothing allocated,
+ * no state between calls, validation before anything is launched,
+ * asynchronous and ordered on `stream`, current device gfx950. Outputs must
+ * not overlap each other or an input, unless said otherwise. Sums are float32 or wider and no call uses atomics, so
+ * every result is bitwise the same from run to run.
+ *
+ * Workspaces. Where a call takes `workspace`, it is caller-owned device memory
+ * of at least the stated size, 16-byte aligned, overlapping nothing else; its
+ * contents are scratch, need no initialisation and mean nothing after the call.
+ * Two calls that may run at the same time (two streams, two captured graphs
+ * replayed side by side) need two workspaces.
+ */
+#ifndef FORGE_OPS_H
+#define FORGE_OPS_H
+
+#include "forge.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ------------------------------------------------------------------------
+ * The global gradient norm over many tensors, and clipping.
+ *
+ * Exact global-norm clipping needs the norm of the whole gradient before any
+ * weight moves, so it is refused by the fused steps
+ * (FORGE_ERR_CLIP_NOT_FUSABLE). This is the path for it: gradients stored by
+ * forge_wgrad, forge_wgrad_bf16 or forge_wgrad_fp8, one pass for their norm, one for the step. */
+
+/*
+ * One tensor of a list. n elements, any n >= 0; a tensor of n == 0 is skipped
+ * and its pointers are not looked at. Each call names the fields that it uses
+ * and does not look at the others.
+ */
+typedef struct {
+  const void* grad;       /* gradient, FORGE_F32 or FORGE_BF16          */
+  void* out;              /* clipped gradient, of the gradient's type   */
+  float* W;               /* weight                                     */
+  float* m;               /* first moment (AdamW) or momentum buffer    */
+  float* v;               /* second moment (AdamW)                      */
+  int64_t n;              /* elements                                   */
+  forge_dtype grad_dtype; /* FORGE_F32 or FORGE_BF16                    */
+} forge_tensor;
+
+/* Most tensors of one list. */
+#define FORGE_MAX_TENSORS 65536
+
+/* Bytes of forge_grad_norm's workspace for `count` tensors, at least 16; 0 if
+ * count is out of range. */
+FORGE_API int64_t forge_grad_norm_workspace(int32_t count);
+
+/*
+ * norm_coef[0] = sqrt(sum over all tensors of g^2), norm_coef[1] =
+ * min(1, max_norm / (norm + 1e-6)), both float32 on the device.
+ *   tensors HOST array of count entries; uses grad, n, grad_dtype. Gradients
+ *   may overlap or recur (each entry counts). Squares are formed and summed
+ *   in 64 bits, so no finite gradient overflows or vanishes; a norm beyond
+ *   float32 is stored as +inf, with the coefficient of its 64-bit value. A
+ *   NaN or infinity among the gradients gives a NaN or +inf norm and a
+ *   coefficient of NaN or 0. With no elements at all the norm is 0.
+ *   max_norm >= 0; +inf asks for the norm alone (the coefficient is then 1,
+ *   or NaN where the norm is not finite). NaN or negative: FORGE_ERR_HPARAM.
+ *   workspace: forge_grad_norm_workspace(count) bytes.
+ */
+FORGE_API forge_status forge_grad_norm(const forge_tensor* tensors, int32_t count, double max_norm,
+                             float* norm_coef, void* workspace, int64_t workspace_bytes,
+                             void* stream);
+
+/*
+ * out = coef * grad for every tensor: the float32 product, rounded to the
+ * gradient's type.
+ *   coef: ONE float32 on the device (norm_coef + 1 of forge_grad_norm; any
+ *   alignment that a float has). Uses grad, out, n, grad_dtype. out may equal
+ *   grad (in place); partial overlap of any two arrays is FORGE_ERR_ALIAS.
+ */
+FORGE_API forge_status forge_clip_grads(const forge_tensor* tensors, int32_t count, const float* coef,
+                              void* stream);
+
+/*
+ * The optimizer step of forge_adamw / forge_sgdm on coef * grad for every
+ * tensor, the product formed in float32 in registers: no clipped gradient is
+ * stored. Uses grad, W, m (and v for AdamW), n, grad_dtype; W, m, v are
+ * float32 and updated in place. coef as in forge_clip_grads. With a
+ * coefficient of exactly 1 the result is bitwise forge_adamw's (forge_sgdm's).
+ * The clip is in coef: p->max_grad_norm must be 0, as in forge.h. Gradients
+ * may overlap each other; W, m and v overlap nothing.
+ */
+FORGE_API forge_status forge_adamw_clipped(const forge_tensor* tensors, int32_t count,
+                                 const float* coef, const forge_adamw_params* p, void* stream);
+FORGE_API forge_status forge_sgdm_clipped(const forge_tensor* tensors, int32_t count,
+                                const float* coef, const forge_sgdm_params* p, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FORGE_OPS_H */

@@ -1,0 +1,201 @@
+"""The entry points of include/forge_ops.h without a GPU: the header is C, the
+library exports what it declares, the binding's struct equals the header's,
+and bad arguments are rejected with the documented status before any buffer is
+touched. Fake, never-dereferenced pointers throughout.
+"""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+from weight_gradient_gemm_amd import _lib, _ops
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+NULL = None
+A, B, C, D, E, F = (k << 33 for k in range(1, 7))     # far apart, 16-byte aligned
+NAN, INF = float("nan"), float("inf")
+(OK, E_NULL, E_SHAPE, E_ALIGN, E_ALIAS, E_HPARAM, E_CLIP, E_TILE, E_DEVICE, _,
+ E_DTYPE) = range(11)
+F32, BF16 = _lib.FORGE_F32, _lib.FORGE_BF16
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _ops.library()
+
+
+def declared():
+    with open(os.path.join(ROOT, "include", "forge_ops.h")) as f:
+        text = f.read()
+    return sorted(set(re.findall(r"FORGE_API\s+[\w\s\*]*?\b(forge_\w+)\s*\(", text)))
+
+
+def adam(**kw):
+    base = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, step=1,
+                max_grad_norm=0.0)
+    base.update(kw)
+    return _lib.AdamWParams(*base.values())
+
+
+def sgd(**kw):
+    base = dict(lr=1e-3, momentum=0.9, weight_decay=0.0, max_grad_norm=0.0)
+    base.update(kw)
+    return _lib.SgdmParams(*base.values())
+
+
+def no_gpu():
+    import torch
+    if torch.cuda.device_count() > 0:
+        pytest.skip("a GPU is visible: valid fake pointers would launch a kernel")
+
+
+def test_every_declared_symbol_is_exported_and_bound(lib):
+    names = declared()
+    assert names == sorted(_ops._SIGNATURES)
+    out = subprocess.run(["nm", "-D", "--defined-only", _lib.library_path], check=True,
+                         capture_output=True, text=True).stdout
+    assert set(names) <= set(re.findall(r"\bT (forge_\w+)", out))
+    import weight_gradient_gemm_amd as wg
+    for n in names:
+        assert n.endswith("_workspace") or callable(getattr(wg, n))
+
+
+@pytest.mark.parametrize("std", ["c99", "c11"])
+def test_header_is_c(tmp_path, std):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src, exe, lib_dir = tmp_path / "use.c", tmp_path / "use", os.path.dirname(_lib.library_path)
+    src.write_text(
+        "#include \"forge_ops.h\"\n#include <stddef.h>\n#include <stdio.h>\n"
+        "typedef void (*fn_t)(void);\n"
+        "int main(void) {\n  const fn_t fns[] = {"
+        + ", ".join(f"(fn_t)&{n}" for n in declared()) + "};\n"
+        "  printf(\"%d %d %d %d %d\\n\", (int)(sizeof fns / sizeof fns[0]), "
+        "(int)sizeof(forge_tensor), (int)offsetof(forge_tensor, W), "
+        "(int)offsetof(forge_tensor, n), (int)offsetof(forge_tensor, grad_dtype));\n"
+        "  return 0;\n}\n")
+    r = subprocess.run([cc, f"-std={std}", "-Wall", "-Wextra", "-Werror", "-pedantic", "-I",
+                        os.path.join(ROOT, "include"), str(src), "-o", str(exe), "-L", lib_dir,
+                        "-lforge", f"-Wl,-rpath,{lib_dir}"], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60, check=True)
+    T = _ops.ForgeTensor
+    assert [int(x) for x in out.stdout.split()] == [
+        len(declared()), ctypes.sizeof(T), T.W.offset, T.n.offset, T.grad_dtype.offset]
+
+
+# --------------------------------------------------------------------------
+# global gradient norm and clipping
+# --------------------------------------------------------------------------
+def tensor(**kw):
+    base = dict(grad=A, out=B, W=C, m=D, v=E, n=100, grad_dtype=F32)
+    base.update(kw)
+    return _ops.ForgeTensor(**base)
+
+
+def rows(*ts):
+    return (_ops.ForgeTensor * max(1, len(ts)))(*ts), len(ts)
+
+
+def norm(lib, *ts, max_norm=1.0, out=F, ws=F + 4096, ws_bytes=1 << 20):
+    return lib.forge_grad_norm(*rows(*ts), max_norm, out, ws, ws_bytes, None)
+
+
+def test_norm_workspace_sizes(lib):
+    f = lib.forge_grad_norm_workspace
+    assert f(-1) == 0 and f(65537) == 0
+    assert f(0) >= 16 and f(1) == f(128) == 2048 * 8 and f(129) == 2 * f(128)
+    assert f(65536) == 512 * f(1)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n=-1), E_SHAPE), (dict(n=(1 << 40) + 1), E_SHAPE), (dict(grad_dtype=2), E_DTYPE),
+    (dict(grad=NULL), E_NULL), (dict(grad=A + 4), E_ALIGN), (dict(grad_dtype=-1), E_DTYPE),
+    (dict(grad=F), E_ALIAS), (dict(grad=F + 4096 - 16), E_ALIAS),
+])
+def test_norm_rejects_tensors(lib, kw, status):
+    assert norm(lib, tensor(), tensor(**kw)) == status
+
+
+def test_norm_rejects(lib):
+    assert norm(lib, tensor(), out=NULL) == E_NULL
+    assert norm(lib, tensor(), ws=NULL) == E_NULL
+    assert lib.forge_grad_norm(None, 1, 1.0, F, F + 4096, 1 << 20, None) == E_NULL
+    assert lib.forge_grad_norm(None, -1, 1.0, F, F + 4096, 1 << 20, None) == E_SHAPE
+    assert lib.forge_grad_norm(None, 65537, 1.0, F, F + 4096, 1 << 40, None) == E_SHAPE
+    assert norm(lib, tensor(), ws_bytes=2048 * 8 - 1) == E_SHAPE
+    assert norm(lib, *[tensor(n=1 << 40)] * 5) == E_SHAPE           # 5 * 2^40 > 2^42 in all
+    assert norm(lib, tensor(), out=F + 2) == E_ALIGN
+    assert norm(lib, tensor(), ws=F + 4096 + 8) == E_ALIGN
+    assert norm(lib, tensor(), out=F + 4096) == E_ALIAS
+    for bad in (-1.0, NAN, -INF):
+        assert norm(lib, tensor(), max_norm=bad) == E_HPARAM
+
+
+def test_steps_reject(lib):
+    def clip(*ts, coef=F):
+        return lib.forge_clip_grads(*rows(*ts), coef, None)
+
+    def step(*ts, coef=F, p=None):
+        return lib.forge_adamw_clipped(*rows(*ts), coef, ctypes.byref(p or adam()), None)
+
+    def mom(*ts, coef=F, p=None):
+        return lib.forge_sgdm_clipped(*rows(*ts), coef, ctypes.byref(p or sgd()), None)
+
+    for f in (clip, step, mom):
+        assert f(tensor(), coef=NULL) == E_NULL
+        assert f(tensor(), coef=F + 1) == E_ALIGN
+        assert f(tensor(grad=NULL)) == E_NULL
+        assert f(tensor(n=-3)) == E_SHAPE
+        assert f(tensor(grad_dtype=9)) == E_DTYPE
+        assert f() == OK and f(tensor(n=0, grad=NULL, W=NULL, grad_dtype=77)) == OK
+    assert clip(tensor(out=NULL)) == E_NULL
+    assert clip(tensor(out=A + 16)) == E_ALIAS                      # shifted, not in place
+    assert clip(tensor(out=A), tensor(grad=B, out=A + 384)) == E_ALIAS
+    assert clip(tensor(), tensor()) == E_ALIAS                      # one output twice
+    assert clip(tensor(out=F)) == E_ALIAS                           # the coefficient itself
+    assert clip(tensor(grad_dtype=BF16, out=A + 192)) == E_ALIAS    # 100 * 2 bytes reach it
+    for name in ("W", "m"):
+        for f in (step, mom):
+            assert f(tensor(**{name: NULL})) == E_NULL
+            assert f(tensor(**{name: B + 8})) == E_ALIGN
+            assert f(tensor(**{name: A + 384})) == E_ALIAS
+            assert f(tensor(), tensor(grad=B, **{"W": B + 4096, "m": B + 8192, "v": B + 12288,
+                                                 name: C})) == E_ALIAS
+    assert step(tensor(v=NULL)) == E_NULL and step(tensor(v=D)) == E_ALIAS
+    assert step(tensor(), p=adam(max_grad_norm=1.0)) == E_CLIP
+    assert step(tensor(), p=adam(beta2=1.0)) == E_HPARAM
+    assert mom(tensor(), p=sgd(max_grad_norm=1.0)) == E_CLIP
+    assert mom(tensor(), p=sgd(momentum=1.0)) == E_HPARAM
+    assert lib.forge_adamw_clipped(*rows(tensor()), F, None, None) == E_NULL
+    assert lib.forge_sgdm_clipped(*rows(tensor()), F, None, None) == E_NULL
+
+
+def test_clip_calls_reach_the_device_check(lib):
+    no_gpu()
+    assert norm(lib, tensor(), tensor()) == E_DEVICE                # gradients may recur
+    assert norm(lib) == E_DEVICE                                    # no tensors: the norm is 0
+    assert norm(lib, tensor(), max_norm=INF) == E_DEVICE
+    assert lib.forge_clip_grads(*rows(tensor(out=A)), F, None) == E_DEVICE          # in place
+    assert lib.forge_clip_grads(*rows(tensor(grad_dtype=BF16, out=A + 208)), F, None) == E_DEVICE
+    two = rows(tensor(), tensor(W=C + 400, m=D + 400, v=E + 400))   # neighbours, one gradient
+    assert lib.forge_adamw_clipped(*two, F, ctypes.byref(adam()), None) == E_DEVICE
+    assert lib.forge_sgdm_clipped(*rows(tensor(v=NULL)), F, ctypes.byref(sgd()), None) == E_DEVICE
+
+
+def test_tensor_list_checks():
+    import torch
+    import weight_gradient_gemm_amd as wg
+    g = torch.zeros(4)
+    with pytest.raises(ValueError, match="on the GPU"):
+        wg.ForgeTensorList([g])
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        wg.ForgeTensorList([g.double()])
+    with pytest.raises(ValueError, match="same field"):
+        wg.ForgeTensorList([], m=[], mom=[])
+    with pytest.raises(ValueError, match="0 tensors|has 1 tensors"):
+        wg.ForgeTensorList([], W=[g])

@@ -42,3 +42,10 @@ from ._lib import (  # noqa: F401
     library,
     library_path,
 )
+from ._ops import (  # noqa: F401
+    ForgeTensorList,
+    forge_adamw_clipped,
+    forge_clip_grads,
+    forge_grad_norm,
+    forge_sgdm_clipped,
+)

@@ -1,0 +1,163 @@
+"""ctypes binding of the entry points of include/forge_ops.h; argument
+marshalling only, in the manner of _lib: torch tensors on the current HIP
+device, sizes read off them, everything else validated by the library.
+
+A call that needs a workspace takes one from torch's allocator, on the stream
+it runs on, unless the caller passes its own (``workspace``, a uint8 tensor):
+then two calls that may run at the same time need two.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _lib
+from ._lib import (SgdmParams, _adamw, _check, _dtype_code, _ptr, _stream,
+                   _torch, _want)
+
+_i32, _i64, _vp, _d = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_double
+_adam_p = ctypes.POINTER(_lib.AdamWParams)
+_sgdm_p = ctypes.POINTER(_lib.SgdmParams)
+
+
+class ForgeTensor(ctypes.Structure):
+    """forge_tensor of the C header."""
+    _fields_ = [("grad", _vp), ("out", _vp), ("W", _vp), ("m", _vp), ("v", _vp), ("n", _i64),
+                ("grad_dtype", _i32)]
+
+
+_list_p = ctypes.POINTER(ForgeTensor)
+
+# Result type (None: a status) and arguments of each entry point.
+_SIGNATURES = {
+    "forge_grad_norm_workspace": (_i64, [_i32]),
+    "forge_grad_norm": (None, [_list_p, _i32, _d, _vp, _vp, _i64, _vp]),
+    "forge_clip_grads": (None, [_list_p, _i32, _vp, _vp]),
+    "forge_adamw_clipped": (None, [_list_p, _i32, _vp, _adam_p, _vp]),
+    "forge_sgdm_clipped": (None, [_list_p, _i32, _vp, _sgdm_p, _vp]),
+}
+
+_DONE = None
+
+
+def library() -> ctypes.CDLL:
+    """The loaded libforge.so with the signatures of forge_ops.h."""
+    global _DONE
+    lib = _lib.library()
+    if _DONE is not lib:
+        for name, (res, args) in _SIGNATURES.items():
+            f = getattr(lib, name)
+            f.restype, f.argtypes = res or _i32, args
+        _DONE = lib
+    return lib
+
+
+def _workspace(nbytes, workspace, stream):
+    """`workspace`, or one of nbytes that belongs to the stream the call runs on."""
+    torch = _torch()
+    if workspace is not None:
+        _want(workspace, torch.uint8, "workspace")
+        return workspace
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+# --------------------------------------------------------------------------
+# global gradient norm and clipping
+# --------------------------------------------------------------------------
+class ForgeTensorList:
+    """Gradients, and what goes with each, of one training step: built once and
+    passed to forge_grad_norm, forge_clip_grads, forge_adamw_clipped and
+    forge_sgdm_clipped as often as the tensors stay where they are.
+
+    ``grads``: float32 or bfloat16 tensors of any shape, contiguous. ``out``:
+    the clipped gradients' places (the gradients themselves: in place), of the
+    gradients' types. ``W`` and ``m``, ``v`` (AdamW) or ``mom`` (SGD-momentum):
+    float32. The list keeps the tensors alive.
+    """
+
+    def __init__(self, grads, *, out=None, W=None, m=None, v=None, mom=None):
+        torch = _torch()
+        if m is not None and mom is not None:
+            raise ValueError("m (AdamW) and mom (SGD-momentum) are the same field: give one")
+        grads = list(grads)
+        fields = {"out": out, "W": W, "m": m if mom is None else mom, "v": v}
+        self.tensors = {"grad": grads}
+        rows = (ForgeTensor * max(1, len(grads)))()
+        for row, g in zip(rows, grads):
+            if not isinstance(g, torch.Tensor):
+                raise TypeError("grads must be torch.Tensors")
+            row.grad_dtype = _dtype_code(g, "grads")
+            _want(g, g.dtype, "grads")
+            row.grad, row.n = g.data_ptr() or None, g.numel()
+        for name, ts in fields.items():
+            if ts is None:
+                continue
+            ts = list(ts)
+            if len(ts) != len(grads):
+                raise ValueError(f"{name} has {len(ts)} tensors, grads has {len(grads)}")
+            for row, g, t in zip(rows, grads, ts):
+                _want(t, g.dtype if name == "out" else torch.float32, name)
+                if t.numel() != g.numel():
+                    raise ValueError(f"{name} has a tensor of {t.numel()} elements where the "
+                                     f"gradient has {g.numel()}")
+                setattr(row, name, t.data_ptr() or None)
+            self.tensors[name] = ts
+        self.rows, self.count = rows, len(grads)
+        self.device = grads[0].device.index if grads else None
+
+    def _args(self, *need):
+        for name in need:
+            if name not in self.tensors:
+                raise ValueError(f"the list was built without {name}")
+        cur = _torch().cuda.current_device()
+        if self.device not in (None, cur):
+            raise ValueError(f"the list is on cuda:{self.device} but the current device is "
+                             f"cuda:{cur} (select it with torch.cuda.device)")
+        return self.rows, self.count
+
+
+def _norm2(norm):
+    _want(norm, _torch().float32, "norm")
+    if norm.numel() != 2:
+        raise ValueError(f"norm must hold 2 elements (norm, coefficient), got {norm.numel()}")
+    return norm.data_ptr()
+
+
+def forge_grad_norm(tensors, norm, *, max_norm, workspace=None, stream=None) -> None:
+    """norm[0] <- the 2-norm of all gradients of the list together, norm[1] <-
+    min(1, max_norm / (norm[0] + 1e-6)), the coefficient that clips to max_norm.
+
+    ``norm`` is a float32 tensor of 2 elements; nothing is copied to the host."""
+    rows, count = tensors._args()
+    out = _norm2(norm)
+    lib = library()
+    ws = _workspace(lib.forge_grad_norm_workspace(count), workspace, stream)
+    _check(lib.forge_grad_norm(rows, count, float(max_norm), out, _ptr(ws), ws.numel(),
+                               _stream(stream)), "forge_grad_norm")
+
+
+def forge_clip_grads(tensors, norm, *, stream=None) -> None:
+    """out <- norm[1] * grad for every tensor of the list."""
+    rows, count = tensors._args("out")
+    _check(library().forge_clip_grads(rows, count, _norm2(norm) + 4, _stream(stream)),
+           "forge_clip_grads")
+
+
+def forge_adamw_clipped(tensors, norm, *, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
+                        weight_decay=0.01, max_grad_norm=0.0, stream=None) -> None:
+    """AdamW on W, m, v of every tensor of the list from norm[1] * grad."""
+    rows, count = tensors._args("W", "m", "v")
+    p = _adamw(step, lr, beta1, beta2, eps, weight_decay, max_grad_norm)
+    _check(library().forge_adamw_clipped(rows, count, _norm2(norm) + 4, ctypes.byref(p),
+                                         _stream(stream)), "forge_adamw_clipped")
+
+
+def forge_sgdm_clipped(tensors, norm, *, lr=1e-3, momentum=0.9, weight_decay=0.0,
+                       max_grad_norm=0.0, stream=None) -> None:
+    """SGD-momentum on W, mom of every tensor of the list from norm[1] * grad."""
+    rows, count = tensors._args("W", "m")
+    p = SgdmParams(float(lr), float(momentum), float(weight_decay), float(max_grad_norm))
+    _check(library().forge_sgdm_clipped(rows, count, _norm2(norm) + 4, ctypes.byref(p),
+                                        _stream(stream)), "forge_sgdm_clipped")

@@ -45,16 +45,19 @@ def _run(cmd, verbose):
 
 
 # HIP translation units (compiled in parallel) and the host-only validation.
-HIP_UNITS = ("host.hip", "forge.hip", "forge_dgrad.hip", "forge_fp8.hip")
+HIP_UNITS = ("host.hip", "forge.hip", "forge_dgrad.hip", "forge_fp8.hip", "forge_clip.hip")
+CXX_UNITS = ("validate.cpp", "validate_ops.cpp")
 
 
 def build(verbose: bool = True) -> str:
     """Compile every source and link libforge.so; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
     inc = ["-I", INCLUDE, "-I", CSRC]
-    v_obj = os.path.join(BUILD, "validate.o")
-    jobs = [["g++", *CXX_FLAGS, *inc, "-c", os.path.join(CSRC, "validate.cpp"), "-o", v_obj]]
-    objs = [v_obj]
+    jobs, objs = [], []
+    for unit in CXX_UNITS:
+        obj = os.path.join(BUILD, unit.replace(".cpp", ".o"))
+        jobs.append(["g++", *CXX_FLAGS, *inc, "-c", os.path.join(CSRC, unit), "-o", obj])
+        objs.append(obj)
     for unit in HIP_UNITS:
         obj = os.path.join(BUILD, unit.replace(".hip", ".o"))
         jobs.append([_hipcc(), *HIP_FLAGS, *inc, "-c", os.path.join(CSRC, unit), "-o", obj])

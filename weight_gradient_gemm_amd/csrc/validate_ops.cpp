@@ -1,0 +1,146 @@
+// Host-side argument validation of the entry points of forge_ops.h (pure C++,
+// no HIP).
+#include "validate_ops.hpp"
+
+#include <algorithm>
+#include <cmath>
+#include <memory>
+#include <new>
+
+namespace forge {
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Byte ranges of one call, read only or written.
+struct Range {
+  uintptr_t begin, end;
+  bool written;
+};
+
+// Collects a call's ranges and looks for a written one that overlaps another.
+// Sorting instead of comparing pairs keeps a list of thousands of tensors
+// cheap; the caller's order is usually ascending already.
+class Ranges {
+ public:
+  explicit Ranges(int64_t room) : r_(new (std::nothrow) Range[size_t(room)]) {}
+  bool ok() const { return r_ != nullptr; }
+  void add(const void* p, uint64_t bytes, bool written) {
+    if (bytes == 0) return;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    r_[n_++] = Range{b, b + bytes, written};
+  }
+  bool clash() {
+    std::sort(r_.get(), r_.get() + n_, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+    uintptr_t any = 0, written = 0;      // ends of what came before
+    for (int64_t k = 0; k < n_; ++k) {
+      if (r_[k].begin < written || (r_[k].written && r_[k].begin < any)) return true;
+      any = std::max(any, r_[k].end);
+      if (r_[k].written) written = std::max(written, r_[k].end);
+    }
+    return false;
+  }
+
+ private:
+  std::unique_ptr<Range[]> r_;
+  int64_t n_ = 0;
+};
+
+// Which of a tensor's fields a call uses, beside grad, n and grad_dtype.
+enum : int { USE_OUT = 1, USE_W_M = 2, USE_V = 4 };
+
+forge_status check_list(const forge_tensor* tensors, int32_t count, int use) {
+  if (count < 0 || count > FORGE_MAX_TENSORS) return FORGE_ERR_SHAPE;
+  if (count > 0 && !tensors) return FORGE_ERR_NULL;
+  int64_t total = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const forge_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    if (t.n < 0 || t.n > kMaxElems) return FORGE_ERR_SHAPE;
+    if (dtype_bytes(t.grad_dtype) == 0) return FORGE_ERR_DTYPE;
+    if (!t.grad || ((use & USE_OUT) && !t.out) || ((use & USE_W_M) && (!t.W || !t.m)) ||
+        ((use & USE_V) && !t.v))
+      return FORGE_ERR_NULL;
+    if (!aligned16(t.grad) || ((use & USE_OUT) && !aligned16(t.out)) ||
+        ((use & USE_W_M) && (!aligned16(t.W) || !aligned16(t.m))) ||
+        ((use & USE_V) && !aligned16(t.v)))
+      return FORGE_ERR_ALIGN;
+    total += t.n;
+    if (total > kMaxListElems) return FORGE_ERR_SHAPE;
+  }
+  return FORGE_OK;
+}
+
+forge_status check_list_overlap(const forge_tensor* tensors, int32_t count, const float* coef,
+                                int use) {
+  Ranges r(4 * int64_t(count) + 1);
+  if (!r.ok()) return FORGE_ERR_SHAPE;
+  r.add(coef, 4, false);
+  for (int32_t i = 0; i < count; ++i) {
+    const forge_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    const uint64_t gb = uint64_t(t.n) * uint64_t(dtype_bytes(t.grad_dtype));
+    const uint64_t sb = uint64_t(t.n) * 4u;
+    if (!((use & USE_OUT) && t.out == t.grad)) r.add(t.grad, gb, false);
+    if (use & USE_OUT) r.add(t.out, gb, true);
+    if (use & USE_W_M) {
+      r.add(t.W, sb, true);
+      r.add(t.m, sb, true);
+    }
+    if (use & USE_V) r.add(t.v, sb, true);
+  }
+  return r.clash() ? FORGE_ERR_ALIAS : FORGE_OK;
+}
+
+forge_status check_clipped(const forge_tensor* tensors, int32_t count, const float* coef, int use) {
+  if (!coef) return FORGE_ERR_NULL;
+  if (forge_status s = check_list(tensors, count, use)) return s;
+  if (!aligned4(coef)) return FORGE_ERR_ALIGN;
+  return check_list_overlap(tensors, count, coef, use);
+}
+
+}  // namespace
+
+// One launch takes 128 tensors and leaves at most 2048 float64 partial sums.
+int64_t grad_norm_workspace(int32_t count) {
+  if (count < 0 || count > FORGE_MAX_TENSORS) return 0;
+  return std::max<int64_t>(16, (int64_t(count) + 127) / 128 * 2048 * 8);
+}
+
+forge_status validate_grad_norm(const forge_tensor* tensors, int32_t count, double max_norm,
+                                const float* norm_coef, const void* workspace,
+                                int64_t workspace_bytes) {
+  if (!norm_coef || !workspace) return FORGE_ERR_NULL;
+  if (forge_status s = check_list(tensors, count, 0)) return s;
+  if (workspace_bytes < grad_norm_workspace(count)) return FORGE_ERR_SHAPE;
+  if (!aligned4(norm_coef) || !aligned16(workspace)) return FORGE_ERR_ALIGN;
+  const Span out{norm_coef, 8}, ws{workspace, uint64_t(workspace_bytes)};
+  if (spans_overlap(out, ws)) return FORGE_ERR_ALIAS;
+  for (int32_t i = 0; i < count; ++i) {
+    const Span g{tensors[i].grad, uint64_t(tensors[i].n) * uint64_t(dtype_bytes(tensors[i].grad_dtype))};
+    if (spans_overlap(out, g) || spans_overlap(ws, g)) return FORGE_ERR_ALIAS;
+  }
+  return std::isnan(max_norm) || max_norm < 0.0 ? FORGE_ERR_HPARAM : FORGE_OK;
+}
+
+forge_status validate_clip_grads(const forge_tensor* tensors, int32_t count, const float* coef) {
+  return check_clipped(tensors, count, coef, USE_OUT);
+}
+
+forge_status validate_adamw_clipped(const forge_tensor* tensors, int32_t count, const float* coef,
+                                    const forge_adamw_params* p) {
+  if (!p) return FORGE_ERR_NULL;
+  if (forge_status s = check_clipped(tensors, count, coef, USE_W_M | USE_V)) return s;
+  return check_adamw_params(p);
+}
+
+forge_status validate_sgdm_clipped(const forge_tensor* tensors, int32_t count, const float* coef,
+                                   const forge_sgdm_params* p) {
+  if (!p) return FORGE_ERR_NULL;
+  if (forge_status s = check_clipped(tensors, count, coef, USE_W_M)) return s;
+  return check_sgdm_params(p);
+}
+
+}  // namespace forge
