@@ -1,7 +1,7 @@
 /*
  * forge_ops.h - C ABI of the operators around the fused weight-gradient step
- * (forge.h) for AMD Instinct MI355X (gfx950): the global gradient norm with
- * the clipped optimizer steps.
+ * (forge.h) for AMD Instinct MI355X (gfx950): the embedding's lookup and
+ * gradient, and the global gradient norm with the clipped optimizer steps.
  *
  * The conventions of forge.h hold here too: device pointers owned by the
  * caller, dense row-major arrays, 16-byte aligned pointers, nothing allocated,
@@ -31,7 +31,8 @@ extern "C" {
  * Exact global-norm clipping needs the norm of the whole gradient before any
  * weight moves, so it is refused by the fused steps
  * (FORGE_ERR_CLIP_NOT_FUSABLE). This is the path for it: gradients stored by
- * forge_wgrad, forge_wgrad_bf16 or forge_wgrad_fp8, one pass for their norm, one for the step. */
+ * forge_wgrad, forge_wgrad_bf16, forge_wgrad_fp8 or
+ * forge_embedding_grad, one pass for their norm, one for the step. */
 
 /*
  * One tensor of a list. n elements, any n >= 0; a tensor of n == 0 is skipped
@@ -95,6 +96,64 @@ FORGE_API forge_status forge_adamw_clipped(const forge_tensor* tensors, int32_t 
                                  const float* coef, const forge_adamw_params* p, void* stream);
 FORGE_API forge_status forge_sgdm_clipped(const forge_tensor* tensors, int32_t count,
                                 const float* coef, const forge_sgdm_params* p, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The embedding: lookup with scaling, and its gradient by sorted tokens.
+ *
+ * The embedding is the weight whose gradient is a sum over tokens without a
+ * matrix product: g[r] = scale * sum over t with ids[t] == r of dY[t].
+ *   ids [T] int32 or int64 (id_bytes 4 or 8, else FORGE_ERR_DTYPE), on the
+ *   device. An id outside [0, V) is nobody's row: its lookup is a row of
+ *   zeros and it adds to no gradient (padding, or the tokens of another
+ *   shard of the vocabulary).
+ *   scale: finite (else FORGE_ERR_HPARAM), rounded to float32.
+ *   0 <= T < 2^30, 0 <= V <= 2^22, d a multiple of 8 up to 2^22. T == 0, V == 0
+ *   and d == 0 are allowed.
+ */
+
+/*
+ * out[t] = scale * table[ids[t]]: the float32 product, rounded to out's type.
+ *   table [V, d] of table_dtype, out [T, d] of out_dtype, each FORGE_F32 or
+ *   FORGE_BF16.
+ */
+FORGE_API forge_status forge_embedding(const void* table, forge_dtype table_dtype, const void* ids,
+                             int32_t id_bytes, void* out, forge_dtype out_dtype, int64_t T,
+                             int64_t V, int64_t d, double scale, void* stream);
+
+/* Bytes of the workspace of the gradient calls below, at least 16; 0 if a size
+ * is out of range. */
+FORGE_API int64_t forge_embedding_workspace(int64_t T, int64_t V, int64_t d);
+
+/*
+ * grad [V, d] float32: the gradient of every row, zero for rows without a
+ * token; accumulate != 0 adds it to what grad holds instead (a tied weight,
+ * after the output layer's forge_wgrad), and rows without a token are then
+ * neither read nor written.
+ *   dY [T, d] of dY_dtype (FORGE_F32 or FORGE_BF16). A row's tokens are summed
+ *   in float32 in an order that ids alone decide, and the sum is scaled once.
+ */
+FORGE_API forge_status forge_embedding_grad(const void* ids, int32_t id_bytes, const void* dY,
+                                  forge_dtype dY_dtype, float* grad, int64_t T, int64_t V,
+                                  int64_t d, double scale, int32_t accumulate, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
+/*
+ * The same gradient consumed by the optimizer as it is formed, never stored:
+ * the step of forge_wgrad_adamw (forge_wgrad_sgdm) on W, m, v (W, mom)
+ * [V, d] float32, in place. Rows without a token take the step with a zero
+ * gradient: their moments and weights still decay. For an untied embedding
+ * (see the preconditions in forge.h). The result is bitwise
+ * forge_embedding_grad followed by forge_adamw (forge_sgdm).
+ */
+FORGE_API forge_status forge_embedding_adamw(const void* ids, int32_t id_bytes, const void* dY,
+                                   forge_dtype dY_dtype, float* W, float* m, float* v, int64_t T,
+                                   int64_t V, int64_t d, double scale,
+                                   const forge_adamw_params* p, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+FORGE_API forge_status forge_embedding_sgdm(const void* ids, int32_t id_bytes, const void* dY,
+                                  forge_dtype dY_dtype, float* W, float* mom, int64_t T,
+                                  int64_t V, int64_t d, double scale, const forge_sgdm_params* p,
+                                  void* workspace, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -199,3 +199,99 @@ def test_tensor_list_checks():
         wg.ForgeTensorList([], m=[], mom=[])
     with pytest.raises(ValueError, match="0 tensors|has 1 tensors"):
         wg.ForgeTensorList([], W=[g])
+
+
+# --------------------------------------------------------------------------
+# embedding
+# --------------------------------------------------------------------------
+def lookup(lib, table=A, tt=F32, ids=B, ib=8, out=C, ot=BF16, T=10, V=100, d=64, scale=1.0):
+    return lib.forge_embedding(table, tt, ids, ib, out, ot, T, V, d, scale, None)
+
+
+def embgrad(lib, ids=A, ib=8, dY=B, yt=BF16, grad=C, T=10, V=100, d=64, scale=1.0, acc=0, ws=D,
+            ws_bytes=1 << 20):
+    return lib.forge_embedding_grad(ids, ib, dY, yt, grad, T, V, d, scale, acc, ws, ws_bytes, None)
+
+
+def embadamw(lib, W=C, m=E, v=F, ws=D, p=None, T=10, V=100, d=64, ids=A, dY=B, ib=8, yt=BF16,
+             scale=1.0, ws_bytes=1 << 20):
+    return lib.forge_embedding_adamw(ids, ib, dY, yt, W, m, v, T, V, d, scale,
+                                     ctypes.byref(p or adam()), ws, ws_bytes, None)
+
+
+def embsgdm(lib, W=C, m=E, ws=D, p=None, T=10, V=100, d=64, ids=A, dY=B, ib=8, yt=BF16, scale=1.0,
+            ws_bytes=1 << 20):
+    return lib.forge_embedding_sgdm(ids, ib, dY, yt, W, m, T, V, d, scale,
+                                    ctypes.byref(p or sgd()), ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(tt=2), E_DTYPE), (dict(ot=3), E_DTYPE), (dict(ib=2), E_DTYPE), (dict(ib=0), E_DTYPE),
+    (dict(table=NULL), E_NULL), (dict(ids=NULL), E_NULL), (dict(out=NULL), E_NULL),
+    (dict(T=-1), E_SHAPE), (dict(V=-1), E_SHAPE), (dict(d=-8), E_SHAPE),
+    (dict(T=(1 << 30) + 1), E_SHAPE), (dict(V=(1 << 22) + 1), E_SHAPE),
+    (dict(d=(1 << 22) + 8), E_SHAPE),
+    (dict(d=60), E_ALIGN), (dict(table=A + 8), E_ALIGN), (dict(out=C + 4), E_ALIGN),
+    (dict(ids=B + 4), E_ALIGN), (dict(ids=B + 2, ib=4), E_ALIGN),
+    (dict(out=A), E_ALIAS), (dict(out=A + 100 * 64 * 4 - 16), E_ALIAS), (dict(out=B), E_ALIAS),
+    (dict(scale=NAN), E_HPARAM), (dict(scale=INF), E_HPARAM), (dict(scale=1e39), E_HPARAM),
+    (dict(T=0, ids=NULL, out=NULL), OK), (dict(d=0, table=NULL, ids=NULL, out=NULL), OK),
+])
+def test_embedding_rejects(lib, kw, status):
+    assert lookup(lib, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(yt=7), E_DTYPE), (dict(ib=1), E_DTYPE),
+    (dict(ids=NULL), E_NULL), (dict(dY=NULL), E_NULL), (dict(ws=NULL), E_NULL),
+    (dict(T=-1), E_SHAPE), (dict(V=(1 << 22) + 1), E_SHAPE), (dict(ws_bytes=100), E_SHAPE),
+    (dict(d=12), E_ALIGN), (dict(dY=B + 2), E_ALIGN), (dict(ws=D + 8), E_ALIGN),
+    (dict(ids=A + 4), E_ALIGN), (dict(ws=C), E_ALIAS), (dict(ws=B), E_ALIAS),
+    (dict(ws=A - 64), E_ALIAS), (dict(scale=NAN), E_HPARAM),
+    (dict(V=0, ws=NULL, ids=NULL, dY=NULL), OK), (dict(d=0, ws=NULL), OK),
+])
+def test_embedding_gradient_rejects(lib, kw, status):
+    for f in (embgrad, embadamw, embsgdm):
+        assert f(lib, **kw) == status, f.__name__
+
+
+def test_embedding_steps_reject(lib):
+    assert embgrad(lib, grad=NULL) == E_NULL and embgrad(lib, grad=C + 4) == E_ALIGN
+    assert embgrad(lib, grad=B + 16) == E_ALIAS and embgrad(lib, grad=A) == E_ALIAS
+    for f in (embadamw, embsgdm):
+        for name in ("W", "m"):
+            assert f(lib, **{name: NULL}) == E_NULL
+            assert f(lib, **{name: B}) == E_ALIAS
+        assert f(lib, m=C + 100 * 64 * 4 - 16) == E_ALIAS
+    assert embadamw(lib, v=NULL) == E_NULL and embadamw(lib, v=E) == E_ALIAS
+    assert embadamw(lib, p=adam(max_grad_norm=1.0)) == E_CLIP
+    assert embadamw(lib, p=adam(step=0)) == E_HPARAM
+    assert embsgdm(lib, p=sgd(max_grad_norm=INF)) == E_CLIP
+    assert embsgdm(lib, p=sgd(lr=-1.0)) == E_HPARAM
+    assert lib.forge_embedding_adamw(A, 8, B, BF16, C, E, F, 10, 100, 64, 1.0, None, D, 1 << 20,
+                                     None) == E_NULL
+    assert lib.forge_embedding_sgdm(A, 8, B, BF16, C, E, 10, 100, 64, 1.0, None, D, 1 << 20,
+                                    None) == E_NULL
+
+
+def test_embedding_workspace_sizes(lib):
+    f = lib.forge_embedding_workspace
+    for bad in ((-1, 1, 8), (1, -1, 8), (1, 1, -8), ((1 << 30) + 1, 1, 8), (1, 1 << 23, 8)):
+        assert f(*bad) == 0
+    assert f(0, 0, 0) >= 16
+    need = f(4097, 1000, 64)
+    # keys and positions twice, two tiles' digit counts, bounds, 128 chunk sums
+    assert need >= 4 * 4 * 4097 + 2 * 512 * 4 + 4 * 1001 + 128 * 64 * 4
+    assert f(1 << 30, 1 << 22, 1 << 22) > 0
+
+
+def test_embedding_calls_reach_the_device_check(lib):
+    no_gpu()
+    assert lookup(lib) == E_DEVICE and lookup(lib, V=0, table=NULL) == E_DEVICE
+    assert lookup(lib, out=A + 100 * 64 * 4) == E_DEVICE
+    assert lookup(lib, ids=B + 4, ib=4) == E_DEVICE
+    need = lib.forge_embedding_workspace(10, 100, 64)
+    for f in (embgrad, embadamw, embsgdm):
+        assert f(lib, ws_bytes=need) == E_DEVICE and f(lib, ws_bytes=need - 1) == E_SHAPE
+        assert f(lib, T=0, ids=NULL, dY=NULL) == E_DEVICE
+    assert embgrad(lib, acc=1) == E_DEVICE

@@ -46,6 +46,10 @@ from ._ops import (  # noqa: F401
     ForgeTensorList,
     forge_adamw_clipped,
     forge_clip_grads,
+    forge_embedding,
+    forge_embedding_adamw,
+    forge_embedding_grad,
+    forge_embedding_sgdm,
     forge_grad_norm,
     forge_sgdm_clipped,
 )

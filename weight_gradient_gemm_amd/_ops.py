@@ -34,6 +34,14 @@ _SIGNATURES = {
     "forge_clip_grads": (None, [_list_p, _i32, _vp, _vp]),
     "forge_adamw_clipped": (None, [_list_p, _i32, _vp, _adam_p, _vp]),
     "forge_sgdm_clipped": (None, [_list_p, _i32, _vp, _sgdm_p, _vp]),
+    "forge_embedding": (None, [_vp, _i32, _vp, _i32, _vp, _i32, _i64, _i64, _i64, _d, _vp]),
+    "forge_embedding_workspace": (_i64, [_i64, _i64, _i64]),
+    "forge_embedding_grad": (None, [_vp, _i32, _vp, _i32, _vp, _i64, _i64, _i64, _d, _i32, _vp,
+                                    _i64, _vp]),
+    "forge_embedding_adamw": (None, [_vp, _i32, _vp, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _d,
+                                     _adam_p, _vp, _i64, _vp]),
+    "forge_embedding_sgdm": (None, [_vp, _i32, _vp, _i32, _vp, _vp, _i64, _i64, _i64, _d, _sgdm_p,
+                                    _vp, _i64, _vp]),
 }
 
 _DONE = None
@@ -161,3 +169,79 @@ def forge_sgdm_clipped(tensors, norm, *, lr=1e-3, momentum=0.9, weight_decay=0.0
     p = SgdmParams(float(lr), float(momentum), float(weight_decay), float(max_grad_norm))
     _check(library().forge_sgdm_clipped(rows, count, _norm2(norm) + 4, ctypes.byref(p),
                                         _stream(stream)), "forge_sgdm_clipped")
+
+
+# --------------------------------------------------------------------------
+# embedding
+# --------------------------------------------------------------------------
+def _ids(ids):
+    torch = _torch()
+    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be a torch.Tensor of int32 or int64")
+    _want(ids, ids.dtype, "ids")
+    return ids.numel(), ids.element_size()
+
+
+def _rows_like(t, shape, name, dtype=None):
+    code = _dtype_code(t, name) if dtype is None else None
+    _want(t, dtype or t.dtype, name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return code
+
+
+def forge_embedding(table, ids, out, *, scale=1.0, stream=None) -> None:
+    """out[t] <- scale * table[ids[t]]; ids outside the table give rows of zeros.
+
+    table [V, d] and out [*ids.shape, d] float32 or bfloat16, ids int32 or
+    int64 of any shape."""
+    T, id_bytes = _ids(ids)
+    V, d = _lib._shape2(table, "table")
+    tc = _rows_like(table, (V, d), "table")
+    oc = _rows_like(out, (*ids.shape, d), "out")
+    _check(library().forge_embedding(_ptr(table), tc, _ptr(ids), id_bytes, _ptr(out), oc, T, V, d,
+                                     float(scale), _stream(stream)), "forge_embedding")
+
+
+def _embedding_args(ids, dY, outs, workspace, stream):
+    """ids of any shape, dY [*ids.shape, d]; outs: (name, [V, d] float32) pairs."""
+    T, id_bytes = _ids(ids)
+    V, d = _lib._shape2(outs[0][1], outs[0][0])
+    yc = _rows_like(dY, (*ids.shape, d), "dY")
+    for name, t in outs:
+        _rows_like(t, (V, d), name, _torch().float32)
+    ws = _workspace(library().forge_embedding_workspace(T, V, d), workspace, stream)
+    return (_ptr(ids), id_bytes, _ptr(dY), yc), (T, V, d), ws
+
+
+def forge_embedding_grad(ids, dY, grad, *, scale=1.0, accumulate=False, workspace=None,
+                         stream=None) -> None:
+    """grad[r] <- scale * the sum of dY[t] over the tokens with ids[t] == r (or
+    += with ``accumulate``, which leaves rows without a token alone)."""
+    head, (T, V, d), ws = _embedding_args(ids, dY, (("grad", grad),), workspace, stream)
+    _check(library().forge_embedding_grad(*head, _ptr(grad), T, V, d, float(scale),
+                                          int(bool(accumulate)), _ptr(ws), ws.numel(),
+                                          _stream(stream)), "forge_embedding_grad")
+
+
+def forge_embedding_adamw(ids, dY, W, m, v, *, step, scale=1.0, lr=1e-3, beta1=0.9, beta2=0.999,
+                          eps=1e-8, weight_decay=0.01, max_grad_norm=0.0, workspace=None,
+                          stream=None) -> None:
+    """W, m, v <- AdamW on the embedding's gradient, in place, the gradient
+    never stored; rows without a token take the step with a zero gradient."""
+    head, (T, V, d), ws = _embedding_args(ids, dY, (("W", W), ("m", m), ("v", v)), workspace,
+                                          stream)
+    p = _adamw(step, lr, beta1, beta2, eps, weight_decay, max_grad_norm)
+    _check(library().forge_embedding_adamw(*head, _ptr(W), _ptr(m), _ptr(v), T, V, d,
+                                           float(scale), ctypes.byref(p), _ptr(ws), ws.numel(),
+                                           _stream(stream)), "forge_embedding_adamw")
+
+
+def forge_embedding_sgdm(ids, dY, W, mom, *, scale=1.0, lr=1e-3, momentum=0.9, weight_decay=0.0,
+                         max_grad_norm=0.0, workspace=None, stream=None) -> None:
+    """W, mom <- SGD-momentum on the embedding's gradient, in place."""
+    head, (T, V, d), ws = _embedding_args(ids, dY, (("W", W), ("mom", mom)), workspace, stream)
+    p = SgdmParams(float(lr), float(momentum), float(weight_decay), float(max_grad_norm))
+    _check(library().forge_embedding_sgdm(*head, _ptr(W), _ptr(mom), T, V, d, float(scale),
+                                          ctypes.byref(p), _ptr(ws), ws.numel(),
+                                          _stream(stream)), "forge_embedding_sgdm")

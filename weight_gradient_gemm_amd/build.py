@@ -45,7 +45,8 @@ def _run(cmd, verbose):
 
 
 # HIP translation units (compiled in parallel) and the host-only validation.
-HIP_UNITS = ("host.hip", "forge.hip", "forge_dgrad.hip", "forge_fp8.hip", "forge_clip.hip")
+HIP_UNITS = ("host.hip", "forge.hip", "forge_dgrad.hip", "forge_fp8.hip", "forge_clip.hip",
+             "forge_embedding.hip")
 CXX_UNITS = ("validate.cpp", "validate_ops.cpp")
 
 

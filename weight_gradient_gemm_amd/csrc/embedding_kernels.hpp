@@ -1,0 +1,438 @@
+// The embedding: lookup with scaling, and its gradient by sorted tokens.
+//
+//   out[t] = scale table[ids[t]]
+//   g[r]   = scale sum_{t: ids[t] = r} dY[t]
+//
+// The gradient needs, for every row, its tokens in a fixed order. The token
+// positions are sorted by id, stably (a radix sort, so that no distribution of
+// ids is slow), the rows' bounds in the sorted order are found by bisection,
+// and one pass over the rows sums each row's tokens in registers and stores
+// the gradient or steps the optimizer at once. Ids outside [0, V) get the key
+// V and end up behind the last row.
+//
+// Frequent ids: the sorted order is cut into chunks of kSumChunk tokens. A
+// chunk that lies within one row is summed beforehand by workgroups of its
+// own; the row's pass then adds such sums, and the tokens before and after
+// them, in ascending order. A row of n tokens costs its pass at most
+// 2 (kSumChunk - 1) + n / kSumChunk additions in a row, and the order of
+// additions depends on the ids alone.
+//
+// No atomics: a wave ranks its 64 keys with ballots (lanes of equal digit),
+// and the lowest lane of each group advances the wave's own counter.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "wgrad_kernels.hpp"
+
+namespace forge {
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kDigitBits = 9;                        // largest digit of a pass
+constexpr int kDigits = 1 << kDigitBits;
+constexpr int kSortOneRounds = 16;                   // keys per thread of the one-workgroup sort
+constexpr int kSortOne = kSortThreads * kSortOneRounds;
+constexpr int kSortTileRounds = 4;                   // keys per thread of a tile of the larger sort
+constexpr int kSortTile = kSortThreads * kSortTileRounds;
+constexpr int kSumChunk = 32;
+
+struct IdSource {
+  const void* ids;
+  int32_t bytes;       // 4 or 8
+  uint32_t V;
+};
+
+__device__ __forceinline__ int64_t load_id(const IdSource& src, int64_t t) {
+  return src.bytes == 8 ? static_cast<const int64_t*>(src.ids)[t]
+                        : int64_t(static_cast<const int32_t*>(src.ids)[t]);
+}
+
+// Sort key of token t: its row, or V for nobody's.
+__device__ __forceinline__ uint32_t load_key(const IdSource& src, int64_t t) {
+  const int64_t id = load_id(src, t);
+  return id >= 0 && id < int64_t(src.V) ? uint32_t(id) : src.V;
+}
+
+// Lanes of this wave whose digit equals this lane's.
+__device__ __forceinline__ uint64_t match_digit(uint32_t digit, int bits) {
+  uint64_t m = ~uint64_t(0);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (digit >> b) & 1;
+    const uint64_t v = __ballot(one);
+    m &= one ? v : ~v;
+  }
+  return m;
+}
+
+// Memory accesses of the wave's lanes before this point come before those
+// after it, in the compiled code as in the source.
+__device__ __forceinline__ void wave_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
+
+struct SortLds {
+  uint32_t count[kSortWaves][kDigits];
+  uint32_t wave_total[kSortWaves];
+};
+
+// Ranks this wave's keys, `rounds` of 64 in ascending position: rank[j] is the
+// number of earlier keys of the wave with the same digit; count[wave] ends as
+// the wave's digit counts. The workgroup synchronises before and after.
+template <int R>
+__device__ __forceinline__ void rank_keys(SortLds& s, const uint32_t (&key)[R], uint32_t (&rank)[R],
+                                          int rounds, int shift, int bits) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int d = lane; d < (1 << bits); d += 64) s.count[wave][d] = 0;
+  const uint64_t lower = (uint64_t(1) << lane) - 1;
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    if (j < rounds) {
+      const uint32_t digit = (key[j] >> shift) & ((1u << bits) - 1u);
+      const uint64_t same = match_digit(digit, bits);
+      // One wave's LDS operations complete in order; wave_order() keeps the
+      // compiler's order the same.
+      wave_order();
+      const uint32_t before = s.count[wave][digit];
+      wave_order();
+      if ((same & lower) == 0) s.count[wave][digit] = before + __popcll(same);
+      rank[j] = before + __popcll(same & lower);
+    }
+  }
+}
+
+// Exclusive sum of one value per thread over the workgroup's first `n` threads
+// (a multiple of 64; the others pass 0).
+__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* wave_total) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  uint32_t inc = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t up = __shfl_up(inc, d);
+    if (lane >= d) inc += up;
+  }
+  if (lane == 63) wave_total[wave] = inc;
+  __syncthreads();
+  uint32_t base = 0;
+  for (int w = 0; w < wave; ++w) base += wave_total[w];
+  __syncthreads();
+  return base + inc - v;
+}
+
+// Turns the waves' digit counts into each wave's first place per digit, from
+// `base(digit, total)`.
+template <class Base>
+__device__ __forceinline__ void place_waves(SortLds& s, int bits, const Base& base) {
+  const int d = threadIdx.x;
+  if (d < (1 << bits)) {
+    uint32_t at = base(d);
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = s.count[w][d];
+      s.count[w][d] = at;
+      at += c;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t digit_total(const SortLds& s, int bits) {
+  uint32_t sum = 0;
+  if (int(threadIdx.x) < (1 << bits))
+    for (int w = 0; w < kSortWaves; ++w) sum += s.count[w][threadIdx.x];
+  return sum;
+}
+
+// Up to kSortOne tokens by one workgroup, in LDS.
+__global__ __launch_bounds__(kSortThreads) void sort_one_kernel(IdSource src, int T, int key_bits,
+                                                                uint32_t* keys, uint32_t* pos) {
+  __shared__ SortLds s;
+  __shared__ uint32_t lk[kSortOne];
+  __shared__ uint16_t lp[kSortOne];
+  static_assert(kSortOne <= 65536, "positions are kept in 16 bits");
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int rounds = (T + kSortThreads - 1) / kSortThreads;
+  const int first = wave * rounds * 64 + lane;
+  uint32_t key[kSortOneRounds], p[kSortOneRounds], rank[kSortOneRounds];
+#pragma unroll
+  for (int j = 0; j < kSortOneRounds; ++j) {
+    const int t = first + j * 64;
+    // Past the last token: behind every key, in every pass.
+    key[j] = j < rounds && t < T ? load_key(src, t) : 0xffffffffu;
+    p[j] = t;
+  }
+  const int passes = (key_bits + kDigitBits - 1) / kDigitBits;
+  for (int k = 0; k < passes; ++k) {
+    const int shift = key_bits * k / passes, bits = key_bits * (k + 1) / passes - shift;
+    rank_keys(s, key, rank, rounds, shift, bits);
+    __syncthreads();
+    const uint32_t at = block_exclusive(digit_total(s, bits), s.wave_total);
+    place_waves(s, bits, [&](int) { return at; });
+    __syncthreads();
+    const bool last = k + 1 == passes;
+#pragma unroll
+    for (int j = 0; j < kSortOneRounds; ++j) {
+      if (j < rounds) {
+        const uint32_t to = s.count[wave][(key[j] >> shift) & ((1u << bits) - 1u)] + rank[j];
+        if (!last) {
+          lk[to] = key[j];
+          lp[to] = uint16_t(p[j]);
+        } else if (to < uint32_t(T)) {
+          keys[to] = key[j];
+          pos[to] = p[j];
+        }
+      }
+    }
+    if (!last) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kSortOneRounds; ++j)
+        if (j < rounds) {
+          key[j] = lk[first + j * 64];
+          p[j] = lp[first + j * 64];
+        }
+      __syncthreads();
+    }
+  }
+}
+
+// The larger sort: per pass, the tiles' digit counts, their sums, the scatter.
+// keys_in == nullptr: the first pass, from the ids.
+struct SortPass {
+  IdSource src;
+  const uint32_t *keys_in, *pos_in;
+  uint32_t *keys_out, *pos_out;
+  uint32_t* count;     // [digits][tiles]
+  int64_t T;
+  int32_t tiles, shift, bits;
+};
+
+__device__ __forceinline__ void load_tile(const SortPass& a, uint32_t (&key)[kSortTileRounds],
+                                          uint32_t (&p)[kSortTileRounds]) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t first = int64_t(blockIdx.x) * kSortTile + wave * kSortTileRounds * 64 + lane;
+#pragma unroll
+  for (int j = 0; j < kSortTileRounds; ++j) {
+    const int64_t t = first + j * 64;
+    const bool in = t < a.T;
+    key[j] = !in ? 0xffffffffu : a.keys_in ? a.keys_in[t] : load_key(a.src, t);
+    p[j] = !in ? 0u : a.keys_in ? a.pos_in[t] : uint32_t(t);
+  }
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortPass a) {
+  __shared__ SortLds s;
+  uint32_t key[kSortTileRounds], p[kSortTileRounds], rank[kSortTileRounds];
+  load_tile(a, key, p);
+  rank_keys(s, key, rank, kSortTileRounds, a.shift, a.bits);
+  __syncthreads();
+  const uint32_t total = digit_total(s, a.bits);
+  if (int(threadIdx.x) < (1 << a.bits)) a.count[int64_t(threadIdx.x) * a.tiles + blockIdx.x] = total;
+}
+
+// Exclusive sum of n counts, in place, by one workgroup.
+__global__ __launch_bounds__(kSortThreads) void sort_sum_kernel(uint32_t* count, int64_t n) {
+  __shared__ uint32_t wave_total[kSortWaves];
+  constexpr int E = 8;
+  uint32_t carry = 0;
+  for (int64_t k = 0; k < n; k += kSortThreads * E) {
+    uint32_t v[E], sum = 0;
+    const int64_t at = k + int64_t(threadIdx.x) * E;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      v[j] = at + j < n ? count[at + j] : 0;
+      sum += v[j];
+    }
+    uint32_t before = carry + block_exclusive(sum, wave_total);
+    for (int w = 0; w < kSortWaves; ++w) carry += wave_total[w];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      if (at + j < n) count[at + j] = before;
+      before += v[j];
+    }
+  }
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortPass a) {
+  __shared__ SortLds s;
+  uint32_t key[kSortTileRounds], p[kSortTileRounds], rank[kSortTileRounds];
+  load_tile(a, key, p);
+  rank_keys(s, key, rank, kSortTileRounds, a.shift, a.bits);
+  __syncthreads();
+  place_waves(s, a.bits, [&](int d) { return a.count[int64_t(d) * a.tiles + blockIdx.x]; });
+  __syncthreads();
+  const int wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int j = 0; j < kSortTileRounds; ++j) {
+    const uint32_t to = s.count[wave][(key[j] >> a.shift) & ((1u << a.bits) - 1u)] + rank[j];
+    if (int64_t(to) < a.T) {       // keys past the last token come last
+      a.keys_out[to] = key[j];
+      a.pos_out[to] = p[j];
+    }
+  }
+}
+
+struct EmbeddingArgs {
+  const uint32_t *keys, *pos;      // sorted
+  uint32_t* bound;                 // [V + 1]: first sorted place of each row
+  float* chunk;                    // [T / kSumChunk, d]: sums of chunks within one row
+  const void* dY;
+  float *W, *m, *v;                // W: the gradient, where it is stored
+  int64_t T;
+  int32_t V, d;
+  int32_t lanes;                   // threads across a row in a workgroup: a power of two
+  int32_t slices;                  // workgroups across a row
+  int32_t bound_blocks;            // workgroups of the bounds kernel that search
+  int64_t blocks;                  // workgroups of a pass (a launch may have fewer, and loop)
+  float scale;
+  AdamWConsts adam;
+  SgdmConsts sgd;
+};
+
+template <bool BF16>
+__device__ __forceinline__ f32x4_t load_dy4(const void* dY, int64_t i) {
+  if constexpr (BF16)
+    return __builtin_convertvector(
+        *reinterpret_cast<const bf16x4_t*>(static_cast<const __bf16*>(dY) + i), f32x4_t);
+  else
+    return *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(dY) + i);
+}
+
+// acc += the tokens at sorted places [s, e), in order, four loads in flight.
+template <bool BF16>
+__device__ __forceinline__ void add_tokens(const EmbeddingArgs& a, f32x4_t& acc, uint32_t s,
+                                           uint32_t e, int col) {
+  for (; s + 4 <= e; s += 4) {
+    f32x4_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = load_dy4<BF16>(a.dY, int64_t(a.pos[s + j]) * a.d + col);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc = acc + r[j];
+  }
+  for (; s < e; ++s) acc = acc + load_dy4<BF16>(a.dY, int64_t(a.pos[s]) * a.d + col);
+}
+
+// The rows' bounds (the first workgroups, one row per thread), and the sums of
+// the chunks that lie within one row (the others, one slice of a chunk each).
+template <bool BF16>
+__global__ __launch_bounds__(256) void embedding_bounds_kernel(EmbeddingArgs a) {
+  for (int64_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
+    if (b < a.bound_blocks) {
+      const int64_t r = b * 256 + threadIdx.x;
+      if (r <= a.V) {
+        uint32_t lo = 0, hi = uint32_t(a.T);       // first place whose key is >= r
+        while (lo < hi) {
+          const uint32_t mid = lo + (hi - lo) / 2;
+          if (a.keys[mid] < uint32_t(r))
+            lo = mid + 1;
+          else
+            hi = mid;
+        }
+        a.bound[r] = lo;
+      }
+      continue;
+    }
+    const int64_t c = (b - a.bound_blocks) / a.slices;
+    const int slice = int((b - a.bound_blocks) - c * a.slices);
+    const uint32_t s = uint32_t(c) * kSumChunk, key = a.keys[s];
+    if (key >= uint32_t(a.V) || a.keys[s + kSumChunk - 1] != key) continue;
+    const int col = (slice * 256 + int(threadIdx.x)) * 4;
+    if (col < a.d) {
+      f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+      add_tokens<BF16>(a, acc, s, s + kSumChunk, col);
+      *reinterpret_cast<f32x4_t*>(a.chunk + c * a.d + col) = acc;
+    }
+  }
+}
+
+enum EmbOp : int { EMB_GRAD = 0, EMB_GRAD_ADD = 1, EMB_ADAMW = 2, EMB_ADAMW_EXACT = 3, EMB_SGDM = 4 };
+
+// One row (or several short ones) per workgroup, 4 columns per thread.
+template <int OP, bool BF16>
+__global__ __launch_bounds__(256) void embedding_rows_kernel(EmbeddingArgs a) {
+  constexpr bool ADAM = OP == EMB_ADAMW || OP == EMB_ADAMW_EXACT;
+  const int rows = 256 / a.lanes;
+  for (int64_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
+    const int64_t rb = b / a.slices;
+    const int slice = int(b - rb * a.slices);
+    const int64_t row = rb * rows + int(threadIdx.x) / a.lanes;
+    const int col = (slice * a.lanes + (int(threadIdx.x) & (a.lanes - 1))) * 4;
+    if (row >= a.V || col >= a.d) continue;
+    const uint32_t s = a.bound[row], e = a.bound[row + 1];
+    if (OP == EMB_GRAD_ADD && s == e) continue;
+    const int64_t i = row * a.d + col;
+    f32x4_t w, m, v;
+    if constexpr (OP != EMB_GRAD) w = *reinterpret_cast<const f32x4_t*>(a.W + i);
+    if constexpr (ADAM || OP == EMB_SGDM) m = *reinterpret_cast<const f32x4_t*>(a.m + i);
+    if constexpr (ADAM) v = *reinterpret_cast<const f32x4_t*>(a.v + i);
+    f32x4_t g = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t c0 = (s + kSumChunk - 1) / kSumChunk, c1 = e / kSumChunk;
+    if (c0 < c1) {
+      add_tokens<BF16>(a, g, s, c0 * kSumChunk, col);
+      for (uint32_t c = c0; c < c1; ++c)
+        g = g + *reinterpret_cast<const f32x4_t*>(a.chunk + int64_t(c) * a.d + col);
+      add_tokens<BF16>(a, g, c1 * kSumChunk, e, col);
+    } else {
+      add_tokens<BF16>(a, g, s, e, col);
+    }
+    g = g * a.scale;
+    if constexpr (OP == EMB_GRAD) w = g;
+    if constexpr (OP == EMB_GRAD_ADD) w = w + g;
+    if constexpr (ADAM) adamw_vec4<OP == EMB_ADAMW_EXACT>(g, w, m, v, a.adam);
+    if constexpr (OP == EMB_SGDM) sgdm_vec4(g, w, m, a.sgd);
+    *reinterpret_cast<f32x4_t*>(a.W + i) = w;
+    if constexpr (ADAM || OP == EMB_SGDM) *reinterpret_cast<f32x4_t*>(a.m + i) = m;
+    if constexpr (ADAM) *reinterpret_cast<f32x4_t*>(a.v + i) = v;
+  }
+}
+
+struct LookupArgs {
+  IdSource src;
+  const void* table;
+  void* out;
+  int64_t T;
+  int32_t d, lanes, slices;
+  int64_t blocks;
+  float scale;
+};
+
+// 8 columns of one token per thread.
+template <bool TABLE_BF16, bool OUT_BF16>
+__global__ __launch_bounds__(256) void embedding_kernel(LookupArgs a) {
+  const int rows = 256 / a.lanes;
+  for (int64_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
+    const int64_t rb = b / a.slices;
+    const int slice = int(b - rb * a.slices);
+    const int64_t t = rb * rows + int(threadIdx.x) / a.lanes;
+    const int col = (slice * a.lanes + (int(threadIdx.x) & (a.lanes - 1))) * 8;
+    if (t >= a.T || col >= a.d) continue;
+    const uint32_t row = load_key(a.src, t);
+    f32x4_t x[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    if (row < a.src.V) {
+      const int64_t i = int64_t(row) * a.d + col;
+      if constexpr (TABLE_BF16) {
+        const u32x4_t raw = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.table) + i);
+        x[0] = unpack_bf16x4(u32x2_t{raw[0], raw[1]});
+        x[1] = unpack_bf16x4(u32x2_t{raw[2], raw[3]});
+      } else {
+        const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.table) + i);
+        x[0] = p[0];
+        x[1] = p[1];
+      }
+      x[0] = x[0] * a.scale;
+      x[1] = x[1] * a.scale;
+    }
+    const int64_t o = t * a.d + col;
+    if constexpr (OUT_BF16) {
+      const u32x2_t lo = pack_bf16x4(x[0]), hi = pack_bf16x4(x[1]);
+      *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.out) + o) = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+    } else {
+      f32x4_t* p = reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + o);
+      p[0] = x[0];
+      p[1] = x[1];
+    }
+  }
+}
+
+}  // namespace forge

@@ -1,0 +1,211 @@
+// Embedding lookup and gradient entry points of the forge C ABI.
+#include <algorithm>
+
+#include "embedding_kernels.hpp"
+#include "forge_ops.h"
+#include "host.hpp"
+#include "validate_ops.hpp"
+
+namespace forge {
+namespace {
+
+// Most workgroups of 256 threads of a launch; what is beyond loops.
+constexpr int64_t kMaxGrid = int64_t(1) << 22;
+
+int pow2_at_least(int64_t n, int most) {
+  int p = 1;
+  while (p < most && p < n) p *= 2;
+  return p;
+}
+
+// Threads across a row of `units` vectors, workgroups across it, and
+// workgroups in all for `rows` rows.
+template <class Args>
+void cut_rows(Args& a, int64_t rows, int64_t units) {
+  a.lanes = pow2_at_least(units, 256);
+  a.slices = int32_t((units + a.lanes - 1) / a.lanes);
+  const int64_t per = 256 / a.lanes;
+  a.blocks = (rows + per - 1) / per * a.slices;
+}
+
+dim3 grid_for(int64_t blocks) { return dim3(uint32_t(std::min(blocks, kMaxGrid))); }
+
+int bits_for(int64_t largest) {
+  int b = 1;
+  while ((int64_t(1) << b) <= largest) ++b;
+  return b;
+}
+
+// Sorts the tokens by row into a.keys, a.pos.
+forge_status launch_sort(const IdSource& src, const EmbeddingWorkspace& ws, char* base, int64_t T,
+                         EmbeddingArgs& a, hipStream_t s) {
+  uint32_t* const keys[2] = {reinterpret_cast<uint32_t*>(base + ws.keys[0]),
+                             reinterpret_cast<uint32_t*>(base + ws.keys[1])};
+  uint32_t* const pos[2] = {reinterpret_cast<uint32_t*>(base + ws.pos[0]),
+                            reinterpret_cast<uint32_t*>(base + ws.pos[1])};
+  a.keys = keys[0];
+  a.pos = pos[0];
+  const int key_bits = bits_for(src.V);
+  if (T <= kSortOne) {
+    hipLaunchKernelGGL(sort_one_kernel, dim3(1), dim3(kSortThreads), 0, s, src, int(T), key_bits,
+                       keys[0], pos[0]);
+    return launch_status();
+  }
+  const int passes = (key_bits + kDigitBits - 1) / kDigitBits;
+  SortPass p{};
+  p.src = src;
+  p.count = reinterpret_cast<uint32_t*>(base + ws.count);
+  p.T = T;
+  p.tiles = int32_t((T + kSortTile - 1) / kSortTile);
+  for (int k = 0; k < passes; ++k) {
+    p.keys_in = k ? keys[(k - 1) & 1] : nullptr;
+    p.pos_in = k ? pos[(k - 1) & 1] : nullptr;
+    p.keys_out = keys[k & 1];
+    p.pos_out = pos[k & 1];
+    p.shift = key_bits * k / passes;
+    p.bits = key_bits * (k + 1) / passes - p.shift;
+    hipLaunchKernelGGL(sort_count_kernel, dim3(p.tiles), dim3(kSortThreads), 0, s, p);
+    if (forge_status st = launch_status()) return st;
+    hipLaunchKernelGGL(sort_sum_kernel, dim3(1), dim3(kSortThreads), 0, s, p.count,
+                       int64_t(p.tiles) << p.bits);
+    if (forge_status st = launch_status()) return st;
+    hipLaunchKernelGGL(sort_scatter_kernel, dim3(p.tiles), dim3(kSortThreads), 0, s, p);
+    if (forge_status st = launch_status()) return st;
+  }
+  a.keys = p.keys_out;
+  a.pos = p.pos_out;
+  return FORGE_OK;
+}
+
+template <int OP, bool BF16>
+forge_status launch_gradient_t(EmbeddingArgs a, hipStream_t s) {
+  EmbeddingArgs b = a;
+  b.bound_blocks = (a.V + 256) / 256;
+  b.slices = (a.d / 4 + 255) / 256;
+  b.blocks = b.bound_blocks + a.T / kSumChunk * b.slices;
+  hipLaunchKernelGGL((embedding_bounds_kernel<BF16>), grid_for(b.blocks), dim3(256), 0, s, b);
+  if (forge_status st = launch_status()) return st;
+  cut_rows(a, a.V, a.d / 4);
+  hipLaunchKernelGGL((embedding_rows_kernel<OP, BF16>), grid_for(a.blocks), dim3(256), 0, s, a);
+  return launch_status();
+}
+
+template <int OP>
+forge_status launch_gradient(const void* ids, int32_t id_bytes, const void* dY, forge_dtype dY_dtype,
+                             EmbeddingArgs a, void* workspace, void* stream) {
+  if (forge_status s = check_device()) return s;
+  (void)hipGetLastError();
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const EmbeddingWorkspace ws = embedding_workspace(a.T, a.V, a.d);
+  char* const base = static_cast<char*>(workspace);
+  a.dY = dY;
+  a.bound = reinterpret_cast<uint32_t*>(base + ws.bound);
+  a.chunk = reinterpret_cast<float*>(base + ws.chunk);
+  if (forge_status s = launch_sort(IdSource{ids, id_bytes, uint32_t(a.V)}, ws, base, a.T, a, st))
+    return s;
+  return dY_dtype == FORGE_BF16 ? launch_gradient_t<OP, true>(a, st)
+                                : launch_gradient_t<OP, false>(a, st);
+}
+
+EmbeddingArgs gradient_args(float* W, float* m, float* v, int64_t T, int64_t V, int64_t d,
+                            double scale) {
+  EmbeddingArgs a{};
+  a.W = W;
+  a.m = m;
+  a.v = v;
+  a.T = T;
+  a.V = int32_t(V);
+  a.d = int32_t(d);
+  a.scale = float(scale);
+  return a;
+}
+
+}  // namespace
+}  // namespace forge
+
+using namespace forge;
+
+extern "C" {
+
+FORGE_API forge_status forge_embedding(const void* table, forge_dtype table_dtype,
+                                       const void* ids, int32_t id_bytes, void* out,
+                                       forge_dtype out_dtype, int64_t T, int64_t V, int64_t d,
+                                       double scale, void* stream) {
+  if (forge_status s = validate_embedding(table, table_dtype, ids, id_bytes, out, out_dtype, T, V,
+                                          d, scale))
+    return s;
+  if (T == 0 || d == 0) return FORGE_OK;
+  if (forge_status s = check_device()) return s;
+  (void)hipGetLastError();
+  LookupArgs a{};
+  a.src = IdSource{ids, id_bytes, uint32_t(V)};
+  a.table = table;
+  a.out = out;
+  a.T = T;
+  a.d = int32_t(d);
+  a.scale = float(scale);
+  cut_rows(a, T, d / 8);
+  const bool tb = table_dtype == FORGE_BF16, ob = out_dtype == FORGE_BF16;
+  const auto kernel = tb ? (ob ? embedding_kernel<true, true> : embedding_kernel<true, false>)
+                         : (ob ? embedding_kernel<false, true> : embedding_kernel<false, false>);
+  hipLaunchKernelGGL(kernel, grid_for(a.blocks), dim3(256), 0, static_cast<hipStream_t>(stream), a);
+  return launch_status();
+}
+
+FORGE_API int64_t forge_embedding_workspace(int64_t T, int64_t V, int64_t d) {
+  return embedding_sizes_ok(T, V, d) ? embedding_workspace(T, V, d).bytes : 0;
+}
+
+FORGE_API forge_status forge_embedding_grad(const void* ids, int32_t id_bytes, const void* dY,
+                                            forge_dtype dY_dtype, float* grad, int64_t T,
+                                            int64_t V, int64_t d, double scale,
+                                            int32_t accumulate, void* workspace,
+                                            int64_t workspace_bytes, void* stream) {
+  const void* outs[1] = {grad};
+  if (forge_status s = validate_embedding_grad(ids, id_bytes, dY, dY_dtype, outs, 1, T, V, d,
+                                               scale, workspace, workspace_bytes))
+    return s;
+  if (V == 0 || d == 0) return FORGE_OK;
+  const EmbeddingArgs a = gradient_args(grad, nullptr, nullptr, T, V, d, scale);
+  return accumulate
+             ? launch_gradient<EMB_GRAD_ADD>(ids, id_bytes, dY, dY_dtype, a, workspace, stream)
+             : launch_gradient<EMB_GRAD>(ids, id_bytes, dY, dY_dtype, a, workspace, stream);
+}
+
+FORGE_API forge_status forge_embedding_adamw(const void* ids, int32_t id_bytes, const void* dY,
+                                             forge_dtype dY_dtype, float* W, float* m, float* v,
+                                             int64_t T, int64_t V, int64_t d, double scale,
+                                             const forge_adamw_params* p, void* workspace,
+                                             int64_t workspace_bytes, void* stream) {
+  const void* outs[3] = {W, m, v};
+  if (!p) return FORGE_ERR_NULL;
+  if (forge_status s = validate_embedding_grad(ids, id_bytes, dY, dY_dtype, outs, 3, T, V, d,
+                                               scale, workspace, workspace_bytes))
+    return s;
+  if (forge_status s = check_adamw_params(p)) return s;
+  if (V == 0 || d == 0) return FORGE_OK;
+  EmbeddingArgs a = gradient_args(W, m, v, T, V, d, scale);
+  a.adam = make_adamw(*p);
+  return p->eps > 0.0
+             ? launch_gradient<EMB_ADAMW>(ids, id_bytes, dY, dY_dtype, a, workspace, stream)
+             : launch_gradient<EMB_ADAMW_EXACT>(ids, id_bytes, dY, dY_dtype, a, workspace, stream);
+}
+
+FORGE_API forge_status forge_embedding_sgdm(const void* ids, int32_t id_bytes, const void* dY,
+                                            forge_dtype dY_dtype, float* W, float* mom, int64_t T,
+                                            int64_t V, int64_t d, double scale,
+                                            const forge_sgdm_params* p, void* workspace,
+                                            int64_t workspace_bytes, void* stream) {
+  const void* outs[2] = {W, mom};
+  if (!p) return FORGE_ERR_NULL;
+  if (forge_status s = validate_embedding_grad(ids, id_bytes, dY, dY_dtype, outs, 2, T, V, d,
+                                               scale, workspace, workspace_bytes))
+    return s;
+  if (forge_status s = check_sgdm_params(p)) return s;
+  if (V == 0 || d == 0) return FORGE_OK;
+  EmbeddingArgs a = gradient_args(W, mom, nullptr, T, V, d, scale);
+  a.sgd = make_sgdm(*p);
+  return launch_gradient<EMB_SGDM>(ids, id_bytes, dY, dY_dtype, a, workspace, stream);
+}
+
+}  // extern "C"

@@ -143,4 +143,92 @@ forge_status validate_sgdm_clipped(const forge_tensor* tensors, int32_t count, c
   return check_sgdm_params(p);
 }
 
+bool embedding_sizes_ok(int64_t T, int64_t V, int64_t d) {
+  return T >= 0 && T <= kMaxTokens && V >= 0 && V <= kMaxDim && d >= 0 && d <= kMaxDim;
+}
+
+// Two copies of (key, position) for the sort's passes, its digit counts (512
+// for each tile of 4096 tokens), the rows' bounds, and the sums of chunks of 32
+// tokens.
+EmbeddingWorkspace embedding_workspace(int64_t T, int64_t V, int64_t d) {
+  EmbeddingWorkspace w{};
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t p = at;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  for (int k = 0; k < 2; ++k) {
+    w.keys[k] = take(4 * T);
+    w.pos[k] = take(4 * T);
+  }
+  w.count = take((T + 4095) / 4096 * 512 * 4);
+  w.bound = take(4 * (V + 1));
+  w.chunk = take(T / 32 * d * 4);
+  w.bytes = at;
+  return w;
+}
+
+namespace {
+
+bool ids_ok(int32_t id_bytes) { return id_bytes == 4 || id_bytes == 8; }
+bool aligned_ids(const void* p, int32_t id_bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & uintptr_t(id_bytes - 1)) == 0;
+}
+bool finite_scale(double scale) { return std::isfinite(scale) && std::isfinite(float(scale)); }
+
+}  // namespace
+
+forge_status validate_embedding(const void* table, forge_dtype table_dtype, const void* ids,
+                                int32_t id_bytes, const void* out, forge_dtype out_dtype,
+                                int64_t T, int64_t V, int64_t d, double scale) {
+  const int tb = dtype_bytes(table_dtype), ob = dtype_bytes(out_dtype);
+  if (tb == 0 || ob == 0 || !ids_ok(id_bytes)) return FORGE_ERR_DTYPE;
+  if (T > 0 && d > 0 && (!ids || !out || (V > 0 && !table))) return FORGE_ERR_NULL;
+  if (!embedding_sizes_ok(T, V, d)) return FORGE_ERR_SHAPE;
+  if (T > 0 && d > 0) {
+    if (d % 8 != 0 || !aligned16(out) || !aligned_ids(ids, id_bytes) || (V > 0 && !aligned16(table)))
+      return FORGE_ERR_ALIGN;
+    const Span so{out, uint64_t(T) * uint64_t(d) * uint64_t(ob)};
+    if (spans_overlap(so, Span{ids, uint64_t(T) * uint64_t(id_bytes)}) ||
+        spans_overlap(so, Span{table, uint64_t(V) * uint64_t(d) * uint64_t(tb)}))
+      return FORGE_ERR_ALIAS;
+  }
+  return finite_scale(scale) ? FORGE_OK : FORGE_ERR_HPARAM;
+}
+
+forge_status validate_embedding_grad(const void* ids, int32_t id_bytes, const void* dY,
+                                     forge_dtype dY_dtype, const void* const* outs, int n_outs,
+                                     int64_t T, int64_t V, int64_t d, double scale,
+                                     const void* workspace, int64_t workspace_bytes) {
+  const int yb = dtype_bytes(dY_dtype);
+  if (yb == 0 || !ids_ok(id_bytes)) return FORGE_ERR_DTYPE;
+  const bool work = V > 0 && d > 0;
+  if (work) {
+    if (!workspace || (T > 0 && (!ids || !dY))) return FORGE_ERR_NULL;
+    for (int k = 0; k < n_outs; ++k)
+      if (!outs[k]) return FORGE_ERR_NULL;
+  }
+  if (!embedding_sizes_ok(T, V, d)) return FORGE_ERR_SHAPE;
+  if (work) {
+    if (workspace_bytes < embedding_workspace(T, V, d).bytes) return FORGE_ERR_SHAPE;
+    if (d % 8 != 0 || !aligned16(workspace)) return FORGE_ERR_ALIGN;
+    if (T > 0 && (!aligned_ids(ids, id_bytes) || !aligned16(dY))) return FORGE_ERR_ALIGN;
+    Span spans[6] = {};
+    int n = 0;
+    for (int k = 0; k < n_outs; ++k) {
+      if (!aligned16(outs[k])) return FORGE_ERR_ALIGN;
+      spans[n++] = Span{outs[k], uint64_t(V) * uint64_t(d) * 4u};
+    }
+    spans[n++] = Span{workspace, uint64_t(workspace_bytes)};
+    const int written = n;
+    spans[n++] = Span{ids, uint64_t(T) * uint64_t(id_bytes)};
+    spans[n++] = Span{dY, uint64_t(T) * uint64_t(d) * uint64_t(yb)};
+    for (int k = 0; k < written; ++k)
+      for (int j = k + 1; j < n; ++j)
+        if (spans_overlap(spans[k], spans[j])) return FORGE_ERR_ALIAS;
+  }
+  return finite_scale(scale) ? FORGE_OK : FORGE_ERR_HPARAM;
+}
+
 }  // namespace forge

@@ -24,4 +24,19 @@ forge_status validate_adamw_clipped(const forge_tensor* tensors, int32_t count, 
 forge_status validate_sgdm_clipped(const forge_tensor* tensors, int32_t count, const float* coef,
                                    const forge_sgdm_params* p);
 
+// Byte offsets of the parts of the embedding gradient's workspace.
+struct EmbeddingWorkspace {
+  int64_t keys[2], pos[2], count, bound, chunk, bytes;
+};
+bool embedding_sizes_ok(int64_t T, int64_t V, int64_t d);
+EmbeddingWorkspace embedding_workspace(int64_t T, int64_t V, int64_t d);
+forge_status validate_embedding(const void* table, forge_dtype table_dtype, const void* ids,
+                                int32_t id_bytes, const void* out, forge_dtype out_dtype,
+                                int64_t T, int64_t V, int64_t d, double scale);
+// outs: the float32 arrays [V, d] that the call writes.
+forge_status validate_embedding_grad(const void* ids, int32_t id_bytes, const void* dY,
+                                     forge_dtype dY_dtype, const void* const* outs, int n_outs,
+                                     int64_t T, int64_t V, int64_t d, double scale,
+                                     const void* workspace, int64_t workspace_bytes);
+
 }  // namespace forge
