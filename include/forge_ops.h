@@ -1,7 +1,8 @@
 /*
  * forge_ops.h - C ABI of the operators around the fused weight-gradient step
  * (forge.h) for AMD Instinct MI355X (gfx950): the embedding's lookup and
- * gradient, and the global gradient norm with the clipped optimizer steps.
+ * gradient, the global gradient norm with the clipped optimizer steps, and
+ * microscaled 4-bit products.
  *
  * The conventions of forge.h hold here too: device pointers owned by the
  * caller, dense row-major arrays, 16-byte aligned pointers, nothing allocated,
@@ -31,7 +32,7 @@ extern "C" {
  * Exact global-norm clipping needs the norm of the whole gradient before any
  * weight moves, so it is refused by the fused steps
  * (FORGE_ERR_CLIP_NOT_FUSABLE). This is the path for it: gradients stored by
- * forge_wgrad, forge_wgrad_bf16, forge_wgrad_fp8 or
+ * forge_wgrad, forge_wgrad_bf16, forge_wgrad_fp8, forge_matmul_mxfp4 or
  * forge_embedding_grad, one pass for their norm, one for the step. */
 
 /*
@@ -154,6 +155,70 @@ FORGE_API forge_status forge_embedding_sgdm(const void* ids, int32_t id_bytes, c
                                   forge_dtype dY_dtype, float* W, float* mom, int64_t T,
                                   int64_t V, int64_t d, double scale, const forge_sgdm_params* p,
                                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit operands (OCP MX, MXFP4) and their product.
+ *
+ * Values along the contraction K are cut into blocks of 32. A block has one
+ * scale, a power of two 2^(s - 127) stored as the byte s (E8M0), and 32 codes
+ * of 4 bits (E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign bit). s is the
+ * biased float32 exponent of the block's largest magnitude minus 2, at least
+ * 0; values are rounded to the nearest code, ties to the even code, and
+ * magnitudes beyond 6 become 6. A block with a NaN or an infinity has s = 255
+ * (NaN), and every value of it is NaN.
+ *
+ * An operand of R rows and K columns, with Kp = FORGE_MXFP4_K(K):
+ *   codes  [R, Kp / 2] bytes, the even column in the low half of a byte;
+ *   scales [Kp / 128, R, 4] bytes: byte b of entry (g, r) is the scale of
+ *          row r's columns 128 g + 32 b .. + 31.
+ * Columns K .. Kp - 1 hold zero codes.
+ */
+#define FORGE_MXFP4_K(K) (((int64_t)(K) + 127) / 128 * 128)
+
+/* Largest padded contraction length. */
+#define FORGE_MXFP4_MAX_K 8388608
+
+/*
+ * Quantises x [R, C] (x_dtype FORGE_F32 or FORGE_BF16) into either or both of
+ *   row_codes, row_scales: the operand of R rows with K = C (blocks along a
+ *     row of x: the contraction runs over x's columns);
+ *   col_codes, col_scales: the operand of C rows with K = R (blocks along a
+ *     column of x, transposed: the contraction runs over x's rows, as the
+ *     tokens of a weight gradient).
+ * A pair is left out by two NULLs; one NULL of a pair, or both pairs left
+ * out, is FORGE_ERR_NULL. C % 8 == 0, any R. Both pairs read x once.
+ */
+FORGE_API forge_status forge_quantize_mxfp4(const void* x, forge_dtype x_dtype, int64_t R, int64_t C,
+                                  void* row_codes, void* row_scales, void* col_codes,
+                                  void* col_scales, void* stream);
+
+/*
+ * out [M, N] (FORGE_F32, or FORGE_BF16 rounded to nearest even) = A B^T for
+ * operands A of M rows and B of N rows, both of the padded length Kp
+ * (a multiple of 128, else FORGE_ERR_ALIGN). N % 8 == 0, any M.
+ * Kp == 0 writes zeros. Products are exact; they are accumulated in float32
+ * in ascending steps of 64 columns, so every tile gives the same bits.
+ *   Weight gradient   g = dY^T X:  A = dY by columns, B = X by columns.
+ *   Input gradient    dX = dY W:   A = dY by rows,    B = W by columns.
+ *   Layer output      Y = X W^T:   A = X by rows,     B = W by rows.
+ * tile: the ids of forge.h over [N, M].
+ */
+FORGE_API forge_status forge_matmul_mxfp4(const void* a_codes, const void* a_scales,
+                                const void* b_codes, const void* b_scales, void* out,
+                                forge_dtype out_dtype, int64_t M, int64_t N, int64_t Kp,
+                                forge_tile tile, void* stream);
+
+/*
+ * Weight gradient from microscaled operands, consumed by AdamW in the
+ * product's epilogue as in forge_wgrad_adamw: x the operand of d_in rows and
+ * dy the operand of d_out rows over the tokens (both quantised by columns),
+ * W, m, v [d_out, d_in] float32, in place. Kp == 0 takes a pure decay step.
+ * The result is bitwise forge_matmul_mxfp4 followed by forge_adamw.
+ */
+FORGE_API forge_status forge_wgrad_adamw_mxfp4(const void* x_codes, const void* x_scales,
+                                     const void* dy_codes, const void* dy_scales, float* W,
+                                     float* m, float* v, int64_t Kp, int64_t d_in, int64_t d_out,
+                                     const forge_adamw_params* p, forge_tile tile, void* stream);
 
 #ifdef __cplusplus
 }

@@ -295,3 +295,92 @@ def test_embedding_calls_reach_the_device_check(lib):
         assert f(lib, ws_bytes=need) == E_DEVICE and f(lib, ws_bytes=need - 1) == E_SHAPE
         assert f(lib, T=0, ids=NULL, dY=NULL) == E_DEVICE
     assert embgrad(lib, acc=1) == E_DEVICE
+
+
+# --------------------------------------------------------------------------
+# microscaled 4-bit operands
+# --------------------------------------------------------------------------
+def quantize(lib, x=A, dt=BF16, R=100, C=256, rc=B, rs=C, cc=D, cs=E):
+    return lib.forge_quantize_mxfp4(x, dt, R, C, rc, rs, cc, cs, None)
+
+
+def matmul(lib, ac=A, as_=B, bc=C, bs=D, out=E, ot=F32, M=40, N=64, K=256, tile=0):
+    return lib.forge_matmul_mxfp4(ac, as_, bc, bs, out, ot, M, N, K, tile, None)
+
+
+G = 7 << 33
+
+
+def wgrad_mx(lib, xc=A, xs=B, yc=C, ys=D, W=E, m=F, v=G, K=256, d_in=64, d_out=40, p=None,
+             tile=0):
+    return lib.forge_wgrad_adamw_mxfp4(xc, xs, yc, ys, W, m, v, K, d_in, d_out,
+                                       ctypes.byref(p or adam()), tile, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dt=2), E_DTYPE), (dict(x=NULL), E_NULL), (dict(rc=NULL), E_NULL), (dict(rs=NULL), E_NULL),
+    (dict(cc=NULL), E_NULL), (dict(cs=NULL), E_NULL),
+    (dict(rc=NULL, rs=NULL, cc=NULL, cs=NULL), E_NULL),
+    (dict(R=-1), E_SHAPE), (dict(C=-8), E_SHAPE), (dict(C=(1 << 23) + 8), E_SHAPE),
+    (dict(R=(1 << 23) + 1), E_SHAPE), (dict(R=(1 << 22) + 1), E_SHAPE),
+    (dict(C=100), E_ALIGN), (dict(x=A + 8), E_ALIGN), (dict(rc=B + 4), E_ALIGN),
+    (dict(rs=C + 1), E_ALIGN), (dict(cc=D + 2), E_ALIGN), (dict(cs=E + 8), E_ALIGN),
+    (dict(rc=A), E_ALIAS), (dict(cs=A + 100 * 256 * 2 - 16), E_ALIAS), (dict(rs=B + 16), E_ALIAS),
+    (dict(cc=B), E_ALIAS), (dict(cs=D + 256 * 64 - 16), E_ALIAS),
+    (dict(R=0, x=NULL), OK), (dict(C=0, x=NULL), OK),
+])
+def test_quantize_rejects(lib, kw, status):
+    assert quantize(lib, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(K=-128), E_SHAPE), (dict(K=(1 << 23) + 128), E_SHAPE), (dict(K=100), E_ALIGN),
+    (dict(tile=5), E_TILE), (dict(tile=-1), E_TILE), (dict(K=130), E_ALIGN),
+])
+def test_products_reject(lib, kw, status):
+    assert matmul(lib, **kw) == status and wgrad_mx(lib, **kw) == status
+
+
+def test_matmul_rejects(lib):
+    assert matmul(lib, ot=2) == E_DTYPE
+    for name in ("ac", "as_", "bc", "bs", "out"):
+        assert matmul(lib, **{name: NULL}) == E_NULL
+        assert matmul(lib, **{name: A + (1 << 32) + 8}) == E_ALIGN
+    assert matmul(lib, M=-1) == E_SHAPE and matmul(lib, N=-8) == E_SHAPE
+    assert matmul(lib, M=(1 << 22) + 1) == E_SHAPE and matmul(lib, N=(1 << 22) + 8) == E_SHAPE
+    assert matmul(lib, N=60) == E_ALIGN
+    assert matmul(lib, out=A) == E_ALIAS and matmul(lib, out=B) == E_ALIAS
+    assert matmul(lib, out=C + 64 * 128 - 16) == E_ALIAS and matmul(lib, out=D) == E_ALIAS
+    assert matmul(lib, M=0, out=NULL) == OK and matmul(lib, N=0) == OK
+
+
+def test_wgrad_adamw_mxfp4_rejects(lib):
+    for name in ("xc", "xs", "yc", "ys", "W", "m", "v"):
+        assert wgrad_mx(lib, **{name: NULL}) == E_NULL
+        assert wgrad_mx(lib, **{name: A + (1 << 32) + 4}) == E_ALIGN
+    assert wgrad_mx(lib, m=E) == E_ALIAS and wgrad_mx(lib, v=F + 40 * 64 * 4 - 16) == E_ALIAS
+    assert wgrad_mx(lib, W=C) == E_ALIAS
+    assert wgrad_mx(lib, d_in=60) == E_ALIGN
+    assert wgrad_mx(lib, p=adam(max_grad_norm=1.0)) == E_CLIP
+    assert wgrad_mx(lib, p=adam(eps=-1.0)) == E_HPARAM
+    assert lib.forge_wgrad_adamw_mxfp4(A, B, C, D, E, F, G, 256, 64, 40, None, 0, None) == E_NULL
+    assert wgrad_mx(lib, d_out=0) == OK
+
+
+def test_mxfp4_calls_reach_the_device_check(lib):
+    no_gpu()
+    assert quantize(lib) == E_DEVICE and quantize(lib, cc=NULL, cs=NULL) == E_DEVICE
+    assert quantize(lib, rc=NULL, rs=NULL, R=1 << 23) == E_DEVICE
+    assert quantize(lib, cs=D + 256 * 64) == E_DEVICE            # right behind the codes
+    assert matmul(lib) == E_DEVICE and matmul(lib, ot=BF16) == E_DEVICE
+    assert matmul(lib, ac=A, as_=B, bc=A, bs=B) == E_DEVICE      # an operand with itself
+    assert matmul(lib, K=0, ac=NULL, as_=NULL, bc=NULL, bs=NULL) == E_DEVICE
+    assert wgrad_mx(lib) == E_DEVICE
+
+
+def test_mxfp4_operand_shapes():
+    import weight_gradient_gemm_amd as wg
+    for rows, k, groups in ((3, 0, 0), (3, 1, 1), (5, 128, 1), (5, 129, 2), (8, 1000, 8)):
+        codes, scales = wg.forge_mxfp4_empty(rows, k, device="cpu")
+        assert tuple(codes.shape) == (rows, groups * 64)
+        assert tuple(scales.shape) == (groups, rows, 4)

@@ -51,5 +51,9 @@ from ._ops import (  # noqa: F401
     forge_embedding_grad,
     forge_embedding_sgdm,
     forge_grad_norm,
+    forge_matmul_mxfp4,
+    forge_mxfp4_empty,
+    forge_quantize_mxfp4,
     forge_sgdm_clipped,
+    forge_wgrad_adamw_mxfp4,
 )

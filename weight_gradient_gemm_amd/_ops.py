@@ -42,6 +42,10 @@ _SIGNATURES = {
                                      _adam_p, _vp, _i64, _vp]),
     "forge_embedding_sgdm": (None, [_vp, _i32, _vp, _i32, _vp, _vp, _i64, _i64, _i64, _d, _sgdm_p,
                                     _vp, _i64, _vp]),
+    "forge_quantize_mxfp4": (None, [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "forge_matmul_mxfp4": (None, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp]),
+    "forge_wgrad_adamw_mxfp4": (None, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                                       _adam_p, _i32, _vp]),
 }
 
 _DONE = None
@@ -245,3 +249,85 @@ def forge_embedding_sgdm(ids, dY, W, mom, *, scale=1.0, lr=1e-3, momentum=0.9, w
     _check(library().forge_embedding_sgdm(*head, _ptr(W), _ptr(mom), T, V, d, float(scale),
                                           ctypes.byref(p), _ptr(ws), ws.numel(),
                                           _stream(stream)), "forge_embedding_sgdm")
+
+
+# --------------------------------------------------------------------------
+# microscaled 4-bit operands
+# --------------------------------------------------------------------------
+def forge_mxfp4_empty(rows, k, device=None):
+    """(codes, scales), uninitialised, of an operand of `rows` rows and
+    contraction length k: uint8 [rows, Kp / 2] and [Kp / 128, rows, 4], Kp the
+    next multiple of 128."""
+    torch = _torch()
+    groups = (int(k) + 127) // 128
+    device = "cuda" if device is None else device
+    return (torch.empty((int(rows), groups * 64), dtype=torch.uint8, device=device),
+            torch.empty((groups, int(rows), 4), dtype=torch.uint8, device=device))
+
+
+def _operand(pair, name):
+    """Checked (codes, scales) of an operand; its rows and padded length."""
+    torch = _torch()
+    codes, scales = pair
+    _want(codes, torch.uint8, f"{name} codes")
+    _want(scales, torch.uint8, f"{name} scales")
+    rows, half = _lib._shape2(codes, f"{name} codes")
+    if half % 64:
+        raise ValueError(f"{name} codes must have a multiple of 64 columns, got {half}")
+    if tuple(scales.shape) != (half // 64, rows, 4):
+        raise ValueError(f"{name} scales must have shape {(half // 64, rows, 4)}, "
+                         f"got {tuple(scales.shape)}")
+    return rows, half * 2
+
+
+def forge_quantize_mxfp4(x, *, rows=None, cols=None, stream=None) -> None:
+    """Quantises x [R, C] (float32 or bfloat16) into the operands ``rows`` (R
+    rows, blocks along a row) and / or ``cols`` (C rows, blocks along a column:
+    transposed), each a pair as forge_mxfp4_empty makes."""
+    R, C = _lib._shape2(x, "x")
+    code = _rows_like(x, (R, C), "x")
+    ptrs = []
+    for name, pair, want in (("rows", rows, (R, C)), ("cols", cols, (C, R))):
+        if pair is None:
+            ptrs += [None, None]
+            continue
+        n, k = _operand(pair, name)
+        if (n, k) != (want[0], (want[1] + 127) // 128 * 128):
+            raise ValueError(f"{name} is an operand of {n} rows and padded length {k}, not of "
+                             f"{want[0]} rows and length {want[1]}")
+        if n and k:
+            ptrs += [_ptr(pair[0]), _ptr(pair[1])]
+        else:
+            return                           # x is empty: nothing to write
+    _check(library().forge_quantize_mxfp4(_ptr(x), code, R, C, *ptrs, _stream(stream)),
+           "forge_quantize_mxfp4")
+
+
+def forge_matmul_mxfp4(A, B, out, *, tile=_lib.FORGE_TILE_DEFAULT, stream=None) -> None:
+    """out [M, N] (float32 or bfloat16) <- A B^T for operands A of M rows and B
+    of N rows, each a (codes, scales) pair."""
+    M, k = _operand(A, "A")
+    N, k2 = _operand(B, "B")
+    if k != k2:
+        raise ValueError(f"A has padded length {k}, B has {k2}")
+    oc = _rows_like(out, (M, N), "out")
+    _check(library().forge_matmul_mxfp4(_ptr(A[0]), _ptr(A[1]), _ptr(B[0]), _ptr(B[1]), _ptr(out),
+                                        oc, M, N, k, int(tile), _stream(stream)),
+           "forge_matmul_mxfp4")
+
+
+def forge_wgrad_adamw_mxfp4(X, dY, W, m, v, *, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
+                            weight_decay=0.01, max_grad_norm=0.0, tile=_lib.FORGE_TILE_DEFAULT,
+                            stream=None) -> None:
+    """W, m, v <- AdamW(W, m, v, g = dY^T X), in place, g never stored, from the
+    operands X (d_in rows) and dY (d_out rows) over the tokens."""
+    d_in, k = _operand(X, "X")
+    d_out, k2 = _operand(dY, "dY")
+    if k != k2:
+        raise ValueError(f"X has padded length {k}, dY has {k2}")
+    _lib._state_like(W, (("m", m), ("v", v)), d_out, d_in)
+    p = _adamw(step, lr, beta1, beta2, eps, weight_decay, max_grad_norm)
+    _check(library().forge_wgrad_adamw_mxfp4(_ptr(X[0]), _ptr(X[1]), _ptr(dY[0]), _ptr(dY[1]),
+                                             _ptr(W), _ptr(m), _ptr(v), k, d_in, d_out,
+                                             ctypes.byref(p), int(tile), _stream(stream)),
+           "forge_wgrad_adamw_mxfp4")

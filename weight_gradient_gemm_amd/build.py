@@ -46,7 +46,7 @@ def _run(cmd, verbose):
 
 # HIP translation units (compiled in parallel) and the host-only validation.
 HIP_UNITS = ("host.hip", "forge.hip", "forge_dgrad.hip", "forge_fp8.hip", "forge_clip.hip",
-             "forge_embedding.hip")
+             "forge_embedding.hip", "forge_mxfp4.hip")
 CXX_UNITS = ("validate.cpp", "validate_ops.cpp")
 
 

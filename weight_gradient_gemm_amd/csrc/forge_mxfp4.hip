@@ -1,0 +1,112 @@
+// Microscaled 4-bit entry points of the forge C ABI.
+#include <algorithm>
+
+#include "forge_ops.h"
+#include "host.hpp"
+#include "mxfp4_kernels.hpp"
+#include "validate_ops.hpp"
+
+namespace forge {
+namespace {
+
+template <class C, int EPI>
+forge_status launch_mx_t(WgradArgs a, const MxArgs& x, hipStream_t s) {
+  set_grid<C>(a, 1);
+  hipLaunchKernelGGL((mxfp4_kernel<C, EPI>), dim3(a.num_tiles), dim3(C::THREADS), 0, s, a, x);
+  return launch_status();
+}
+
+template <int EPI>
+struct MxLaunch {
+  static forge_status run(WgradArgs a, const MxArgs& x, forge_tile tile, hipStream_t s) {
+    switch (tile) {
+      case FORGE_TILE_128x128: return launch_mx_t<Cfg128x128, EPI>(a, x, s);
+      case FORGE_TILE_256x128: return launch_mx_t<Cfg256x128, EPI>(a, x, s);
+      case FORGE_TILE_256x256: return launch_mx_t<Cfg256x256, EPI>(a, x, s);
+      case FORGE_TILE_PERSISTENT: {
+        const int grid = persistent_grid();
+        if (grid <= 0) return launch_mx_t<Cfg256x256, EPI>(a, x, s);
+        set_grid<Cfg256x256>(a, 1);
+        hipLaunchKernelGGL((mxfp4_persistent_kernel<Cfg256x256, Cfg256x128, EPI>), dim3(grid),
+                           dim3(Cfg256x256::THREADS), 0, s, a, x);
+        return launch_status();
+      }
+      default: return FORGE_ERR_TILE;
+    }
+  }
+};
+
+}  // namespace
+}  // namespace forge
+
+using namespace forge;
+
+extern "C" {
+
+FORGE_API forge_status forge_quantize_mxfp4(const void* x, forge_dtype x_dtype, int64_t R,
+                                            int64_t C, void* row_codes, void* row_scales,
+                                            void* col_codes, void* col_scales, void* stream) {
+  if (forge_status s = validate_quantize_mxfp4(x, x_dtype, R, C, row_codes, row_scales, col_codes,
+                                               col_scales))
+    return s;
+  if (R == 0 || C == 0) return FORGE_OK;
+  if (forge_status s = check_device()) return s;
+  (void)hipGetLastError();
+  QuantArgs a{};
+  a.x = x;
+  a.row_codes = static_cast<uint8_t*>(row_codes);
+  a.row_scales = static_cast<uint8_t*>(row_scales);
+  a.col_codes = static_cast<uint8_t*>(col_codes);
+  a.col_scales = static_cast<uint8_t*>(col_scales);
+  a.R = R;
+  a.C = C;
+  a.row_pitch = FORGE_MXFP4_K(C) / 2;
+  a.col_pitch = FORGE_MXFP4_K(R) / 2;
+  a.tiles_c = int32_t((C + kQuantTile - 1) / kQuantTile);
+  a.tiles = (R + kQuantTile - 1) / kQuantTile * a.tiles_c;
+  const dim3 grid(uint32_t(std::min<int64_t>(a.tiles, int64_t(1) << 22)));
+  const auto kernel = x_dtype == FORGE_BF16 ? quantize_mxfp4_kernel<true> : quantize_mxfp4_kernel<false>;
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, static_cast<hipStream_t>(stream), a);
+  return launch_status();
+}
+
+FORGE_API forge_status forge_matmul_mxfp4(const void* a_codes, const void* a_scales,
+                                          const void* b_codes, const void* b_scales, void* out,
+                                          forge_dtype out_dtype, int64_t M, int64_t N, int64_t Kp,
+                                          forge_tile tile, void* stream) {
+  if (forge_status s = validate_matmul_mxfp4(a_codes, a_scales, b_codes, b_scales, out, out_dtype,
+                                             M, N, Kp, tile))
+    return s;
+  if (M == 0 || N == 0) return FORGE_OK;
+  if (forge_status s = check_device()) return s;
+  tile = resolve_tile(tile, N, M, 1);
+  if (!grid_fits(N, M, tile, 1)) return FORGE_ERR_SHAPE;
+  (void)hipGetLastError();
+  const WgradArgs a = base_args(b_codes, a_codes, static_cast<float*>(out), nullptr, nullptr, Kp, N, M);
+  const MxArgs x{static_cast<const uint8_t*>(b_scales), static_cast<const uint8_t*>(a_scales), Kp};
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  return out_dtype == FORGE_BF16 ? MxLaunch<EPI_GRAD | EPI_BF16_OUT>::run(a, x, tile, st)
+                                 : MxLaunch<EPI_GRAD>::run(a, x, tile, st);
+}
+
+FORGE_API forge_status forge_wgrad_adamw_mxfp4(const void* x_codes, const void* x_scales,
+                                               const void* dy_codes, const void* dy_scales,
+                                               float* W, float* m, float* v, int64_t Kp,
+                                               int64_t d_in, int64_t d_out,
+                                               const forge_adamw_params* p, forge_tile tile,
+                                               void* stream) {
+  if (forge_status s = validate_wgrad_adamw_mxfp4(x_codes, x_scales, dy_codes, dy_scales, W, m, v,
+                                                  Kp, d_in, d_out, p, tile))
+    return s;
+  if (d_in == 0 || d_out == 0) return FORGE_OK;
+  if (forge_status s = check_device()) return s;
+  tile = resolve_tile(tile, d_in, d_out, 1);
+  if (!grid_fits(d_in, d_out, tile, 1)) return FORGE_ERR_SHAPE;
+  (void)hipGetLastError();
+  WgradArgs a = base_args(x_codes, dy_codes, W, m, v, Kp, d_in, d_out);
+  a.adam = make_adamw(*p);
+  const MxArgs x{static_cast<const uint8_t*>(x_scales), static_cast<const uint8_t*>(dy_scales), Kp};
+  return with_adamw_epi<MxLaunch>(*p, a, x, tile, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

@@ -231,4 +231,106 @@ forge_status validate_embedding_grad(const void* ids, int32_t id_bytes, const vo
   return finite_scale(scale) ? FORGE_OK : FORGE_ERR_HPARAM;
 }
 
+namespace {
+
+Span codes_span(const void* p, int64_t R, int64_t Kp) { return Span{p, uint64_t(R) * uint64_t(Kp / 2)}; }
+Span scales_span(const void* p, int64_t R, int64_t Kp) { return Span{p, uint64_t(R) * uint64_t(Kp / 32)}; }
+
+// The product of operands I (N rows) and O (M rows) into the outputs [M, N].
+forge_status check_product(const void* i_codes, const void* i_scales, const void* o_codes,
+                           const void* o_scales, const void* const* outs, const int* elem_bytes,
+                           int n_outs, int64_t N, int64_t M, int64_t Kp) {
+  if (M < 0 || N < 0 || Kp < 0) return FORGE_ERR_SHAPE;
+  const bool work = M > 0 && N > 0;
+  const void* const in[4] = {i_codes, i_scales, o_codes, o_scales};
+  if (work) {
+    for (int k = 0; k < n_outs; ++k)
+      if (!outs[k]) return FORGE_ERR_NULL;
+    for (const void* p : in)
+      if (Kp > 0 && !p) return FORGE_ERR_NULL;
+  }
+  if (M > kMaxDim || N > kMaxDim || Kp > FORGE_MXFP4_MAX_K || M * N > kMaxElems) return FORGE_ERR_SHAPE;
+  if (!work) return FORGE_OK;
+  if (N % 8 != 0 || Kp % 128 != 0) return FORGE_ERR_ALIGN;
+  Span spans[7] = {};
+  int n = 0;
+  for (int k = 0; k < n_outs; ++k) {
+    if (!aligned16(outs[k])) return FORGE_ERR_ALIGN;
+    spans[n++] = Span{outs[k], uint64_t(M) * uint64_t(N) * uint64_t(elem_bytes[k])};
+  }
+  if (Kp > 0)
+    for (const void* p : in)
+      if (!aligned16(p)) return FORGE_ERR_ALIGN;
+  spans[n++] = codes_span(i_codes, N, Kp);
+  spans[n++] = scales_span(i_scales, N, Kp);
+  spans[n++] = codes_span(o_codes, M, Kp);
+  spans[n++] = scales_span(o_scales, M, Kp);
+  for (int k = 0; k < n_outs; ++k)
+    for (int j = k + 1; j < n; ++j)
+      if (spans_overlap(spans[k], spans[j])) return FORGE_ERR_ALIAS;
+  return FORGE_OK;
+}
+
+}  // namespace
+
+forge_status validate_quantize_mxfp4(const void* x, forge_dtype x_dtype, int64_t R, int64_t C,
+                                     const void* row_codes, const void* row_scales,
+                                     const void* col_codes, const void* col_scales) {
+  const int xb = dtype_bytes(x_dtype);
+  if (xb == 0) return FORGE_ERR_DTYPE;
+  if (!row_codes != !row_scales || !col_codes != !col_scales || (!row_codes && !col_codes))
+    return FORGE_ERR_NULL;
+  if (R > 0 && C > 0 && !x) return FORGE_ERR_NULL;
+  if (R < 0 || C < 0 || R > kMaxTokens || C > kMaxTokens) return FORGE_ERR_SHAPE;
+  if ((row_codes && (C > FORGE_MXFP4_MAX_K || R > kMaxDim)) ||
+      (col_codes && (R > FORGE_MXFP4_MAX_K || C > kMaxDim)))
+    return FORGE_ERR_SHAPE;
+  if (R == 0 || C == 0) return FORGE_OK;
+  if (C % 8 != 0 || !aligned16(x)) return FORGE_ERR_ALIGN;
+  Span spans[5] = {};
+  int n = 0;
+  if (row_codes) {
+    if (!aligned16(row_codes) || !aligned16(row_scales)) return FORGE_ERR_ALIGN;
+    spans[n++] = codes_span(row_codes, R, FORGE_MXFP4_K(C));
+    spans[n++] = scales_span(row_scales, R, FORGE_MXFP4_K(C));
+  }
+  if (col_codes) {
+    if (!aligned16(col_codes) || !aligned16(col_scales)) return FORGE_ERR_ALIGN;
+    spans[n++] = codes_span(col_codes, C, FORGE_MXFP4_K(R));
+    spans[n++] = scales_span(col_scales, C, FORGE_MXFP4_K(R));
+  }
+  const int written = n;
+  spans[n++] = Span{x, uint64_t(R) * uint64_t(C) * uint64_t(xb)};
+  for (int k = 0; k < written; ++k)
+    for (int j = k + 1; j < n; ++j)
+      if (spans_overlap(spans[k], spans[j])) return FORGE_ERR_ALIAS;
+  return FORGE_OK;
+}
+
+forge_status validate_matmul_mxfp4(const void* a_codes, const void* a_scales, const void* b_codes,
+                                   const void* b_scales, const void* out, forge_dtype out_dtype,
+                                   int64_t M, int64_t N, int64_t Kp, forge_tile tile) {
+  const int ob[1] = {dtype_bytes(out_dtype)};
+  if (ob[0] == 0) return FORGE_ERR_DTYPE;
+  const void* outs[1] = {out};
+  if (forge_status s = check_product(b_codes, b_scales, a_codes, a_scales, outs, ob, 1, N, M, Kp))
+    return s;
+  return check_tile(tile);
+}
+
+forge_status validate_wgrad_adamw_mxfp4(const void* x_codes, const void* x_scales,
+                                        const void* dy_codes, const void* dy_scales,
+                                        const float* W, const float* m, const float* v, int64_t Kp,
+                                        int64_t d_in, int64_t d_out, const forge_adamw_params* p,
+                                        forge_tile tile) {
+  const int four[3] = {4, 4, 4};
+  const void* outs[3] = {W, m, v};
+  if (!p) return FORGE_ERR_NULL;
+  if (forge_status s = check_product(x_codes, x_scales, dy_codes, dy_scales, outs, four, 3, d_in,
+                                     d_out, Kp))
+    return s;
+  if (forge_status s = check_adamw_params(p)) return s;
+  return check_tile(tile);
+}
+
 }  // namespace forge

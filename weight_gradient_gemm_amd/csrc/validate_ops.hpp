@@ -39,4 +39,16 @@ forge_status validate_embedding_grad(const void* ids, int32_t id_bytes, const vo
                                      int64_t T, int64_t V, int64_t d, double scale,
                                      const void* workspace, int64_t workspace_bytes);
 
+forge_status validate_quantize_mxfp4(const void* x, forge_dtype x_dtype, int64_t R, int64_t C,
+                                     const void* row_codes, const void* row_scales,
+                                     const void* col_codes, const void* col_scales);
+forge_status validate_matmul_mxfp4(const void* a_codes, const void* a_scales, const void* b_codes,
+                                   const void* b_scales, const void* out, forge_dtype out_dtype,
+                                   int64_t M, int64_t N, int64_t Kp, forge_tile tile);
+forge_status validate_wgrad_adamw_mxfp4(const void* x_codes, const void* x_scales,
+                                        const void* dy_codes, const void* dy_scales,
+                                        const float* W, const float* m, const float* v, int64_t Kp,
+                                        int64_t d_in, int64_t d_out, const forge_adamw_params* p,
+                                        forge_tile tile);
+
 }  // namespace forge
