@@ -225,12 +225,14 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
   const uint8_t* gi = reinterpret_cast<const uint8_t*>(a.X) + int64_t(i0) * pitch;
   const uint8_t* go = reinterpret_cast<const uint8_t*>(a.dY) + int64_t(o0) * pitch;
   auto load_stage = [&](uint16_t* slot) {
-    // Stages past the last one load zeros.
-    const int64_t off = int64_t(g_stage) * RB;
-    const __amdgpu_buffer_rsrc_t ri =
-        window(gi + off, g_stage < nk ? int64_t(d_in - i0) * pitch - off : 0);
-    const __amdgpu_buffer_rsrc_t ro =
-        window(go + off, g_stage < nk ? int64_t(d_out - o0) * pitch - off : 0);
+    // Rows past the edge have an out-of-window offset, so the window only has
+    // to reach the tile's last row (256 pitch < 2^31), and nothing past the
+    // last stage, which loads zeros. No branches: the compiler would sink
+    // MFMAs below them, out of their stage.
+    const uint32_t bytes = g_stage < nk ? kOOB - 1u : 0u;
+    const __amdgpu_buffer_rsrc_t ri = window32(gi, bytes), ro = window32(go, bytes);
+    gi += RB;
+    go += RB;
     ++g_stage;
 #pragma unroll
     for (int i = 0; i < NQW; ++i) {
@@ -249,13 +251,13 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
 #pragma unroll
   for (int n = 0; n < TN; ++n) sv[TM + n] = uint32_t(o0 + wn * C::WN + n * 32 + l32) * 4u;
   int s_stage = 0;
+  const uint8_t *si = x.i_scales, *so = x.o_scales;
   uint32_t sc[4][NSC];
   auto load_scales = [&](int k) {
-    const int64_t s = s_stage < nk ? s_stage : 0;       // a window of no bytes past the last
-    const __amdgpu_buffer_rsrc_t ri =
-        window32(x.i_scales + s * d_in * 4, s_stage < nk ? uint32_t(d_in) * 4u : 0u);
-    const __amdgpu_buffer_rsrc_t ro =
-        window32(x.o_scales + s * d_out * 4, s_stage < nk ? uint32_t(d_out) * 4u : 0u);
+    const __amdgpu_buffer_rsrc_t ri = window32(si, s_stage < nk ? uint32_t(d_in) * 4u : 0u);
+    const __amdgpu_buffer_rsrc_t ro = window32(so, s_stage < nk ? uint32_t(d_out) * 4u : 0u);
+    si += int64_t(d_in) * 4;
+    so += int64_t(d_out) * 4;
     ++s_stage;
 #pragma unroll
     for (int t = 0; t < NSC; ++t)
