@@ -11,8 +11,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from ._lib import (SgdmParams, _adamw, _check, _dtype_code, _ptr, _stream,
-                   _torch, _want)
+from ._lib import FORGE_BF16, FORGE_F32, ForgeError, SgdmParams, _adamw, _torch, _want
 
 _i32, _i64, _vp, _d = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_double
 _adam_p = ctypes.POINTER(_lib.AdamWParams)
@@ -63,16 +62,66 @@ def library() -> ctypes.CDLL:
     return lib
 
 
-def _workspace(nbytes, workspace, stream):
-    """`workspace`, or one of nbytes that belongs to the stream the call runs on."""
+# The small calls here take the GPU a few microseconds, so the checks are kept
+# cheap: one look at the current device per call, and _lib's checks, which name
+# what is wrong, only for a tensor that does not pass a short one.
+def _check(status, where):
+    if status:
+        raise ForgeError(status, where)
+
+
+def _current(stream):
+    """(torch, current device, stream handle) of a call; stream None: the current one."""
     torch = _torch()
+    cur = torch.cuda.current_device()
+    if stream is None:
+        return torch, cur, torch._C._cuda_getCurrentRawStream(cur)
+    if stream.device.index != cur:
+        raise ValueError(f"stream is on {stream.device} but the current device is cuda:{cur}")
+    return torch, cur, stream.cuda_stream
+
+
+def _in(t, dtype, name, cur):
+    """The address of a contiguous tensor of `dtype` on device `cur` (None if empty)."""
+    try:
+        if t.dtype is dtype and t.get_device() == cur and t.is_contiguous():
+            return t.data_ptr() or None
+    except AttributeError:
+        pass
+    _want(t, dtype, name)
+    return t.data_ptr() or None
+
+
+def _real(torch, t, name):
+    """Type code of a float32 or bfloat16 tensor."""
+    dtype = getattr(t, "dtype", None)
+    if dtype is torch.float32:
+        return FORGE_F32
+    if dtype is torch.bfloat16:
+        return FORGE_BF16
+    raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+
+
+def _shaped(t, shape, name):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _two(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _workspace(torch, cur, nbytes, workspace, stream):
+    """`workspace`, or one of nbytes that belongs to the stream the call runs on."""
     if workspace is not None:
-        _want(workspace, torch.uint8, "workspace")
+        _in(workspace, torch.uint8, "workspace", cur)
         return workspace
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        return torch.empty(nbytes, dtype=torch.uint8, device=cur)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        return torch.empty(nbytes, dtype=torch.uint8, device=cur)
 
 
 # --------------------------------------------------------------------------
@@ -100,7 +149,7 @@ class ForgeTensorList:
         for row, g in zip(rows, grads):
             if not isinstance(g, torch.Tensor):
                 raise TypeError("grads must be torch.Tensors")
-            row.grad_dtype = _dtype_code(g, "grads")
+            row.grad_dtype = _real(torch, g, "grads")
             _want(g, g.dtype, "grads")
             row.grad, row.n = g.data_ptr() or None, g.numel()
         for name, ts in fields.items():
@@ -119,22 +168,21 @@ class ForgeTensorList:
         self.rows, self.count = rows, len(grads)
         self.device = grads[0].device.index if grads else None
 
-    def _args(self, *need):
+    def _args(self, cur, *need):
         for name in need:
             if name not in self.tensors:
                 raise ValueError(f"the list was built without {name}")
-        cur = _torch().cuda.current_device()
         if self.device not in (None, cur):
             raise ValueError(f"the list is on cuda:{self.device} but the current device is "
                              f"cuda:{cur} (select it with torch.cuda.device)")
         return self.rows, self.count
 
 
-def _norm2(norm):
-    _want(norm, _torch().float32, "norm")
+def _norm2(torch, cur, norm):
+    p = _in(norm, torch.float32, "norm", cur)
     if norm.numel() != 2:
         raise ValueError(f"norm must hold 2 elements (norm, coefficient), got {norm.numel()}")
-    return norm.data_ptr()
+    return p
 
 
 def forge_grad_norm(tensors, norm, *, max_norm, workspace=None, stream=None) -> None:
@@ -142,56 +190,52 @@ def forge_grad_norm(tensors, norm, *, max_norm, workspace=None, stream=None) -> 
     min(1, max_norm / (norm[0] + 1e-6)), the coefficient that clips to max_norm.
 
     ``norm`` is a float32 tensor of 2 elements; nothing is copied to the host."""
-    rows, count = tensors._args()
-    out = _norm2(norm)
+    torch, cur, st = _current(stream)
+    rows, count = tensors._args(cur)
+    out = _norm2(torch, cur, norm)
     lib = library()
-    ws = _workspace(lib.forge_grad_norm_workspace(count), workspace, stream)
-    _check(lib.forge_grad_norm(rows, count, float(max_norm), out, _ptr(ws), ws.numel(),
-                               _stream(stream)), "forge_grad_norm")
+    ws = _workspace(torch, cur, lib.forge_grad_norm_workspace(count), workspace, stream)
+    _check(lib.forge_grad_norm(rows, count, max_norm, out, ws.data_ptr(), ws.numel(), st),
+           "forge_grad_norm")
 
 
 def forge_clip_grads(tensors, norm, *, stream=None) -> None:
     """out <- norm[1] * grad for every tensor of the list."""
-    rows, count = tensors._args("out")
-    _check(library().forge_clip_grads(rows, count, _norm2(norm) + 4, _stream(stream)),
+    torch, cur, st = _current(stream)
+    rows, count = tensors._args(cur, "out")
+    _check(library().forge_clip_grads(rows, count, _norm2(torch, cur, norm) + 4, st),
            "forge_clip_grads")
 
 
 def forge_adamw_clipped(tensors, norm, *, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
                         weight_decay=0.01, max_grad_norm=0.0, stream=None) -> None:
     """AdamW on W, m, v of every tensor of the list from norm[1] * grad."""
-    rows, count = tensors._args("W", "m", "v")
+    torch, cur, st = _current(stream)
+    rows, count = tensors._args(cur, "W", "m", "v")
     p = _adamw(step, lr, beta1, beta2, eps, weight_decay, max_grad_norm)
-    _check(library().forge_adamw_clipped(rows, count, _norm2(norm) + 4, ctypes.byref(p),
-                                         _stream(stream)), "forge_adamw_clipped")
+    _check(library().forge_adamw_clipped(rows, count, _norm2(torch, cur, norm) + 4,
+                                         ctypes.byref(p), st), "forge_adamw_clipped")
 
 
 def forge_sgdm_clipped(tensors, norm, *, lr=1e-3, momentum=0.9, weight_decay=0.0,
                        max_grad_norm=0.0, stream=None) -> None:
     """SGD-momentum on W, mom of every tensor of the list from norm[1] * grad."""
-    rows, count = tensors._args("W", "m")
+    torch, cur, st = _current(stream)
+    rows, count = tensors._args(cur, "W", "m")
     p = SgdmParams(float(lr), float(momentum), float(weight_decay), float(max_grad_norm))
-    _check(library().forge_sgdm_clipped(rows, count, _norm2(norm) + 4, ctypes.byref(p),
-                                        _stream(stream)), "forge_sgdm_clipped")
+    _check(library().forge_sgdm_clipped(rows, count, _norm2(torch, cur, norm) + 4,
+                                        ctypes.byref(p), st), "forge_sgdm_clipped")
 
 
 # --------------------------------------------------------------------------
 # embedding
 # --------------------------------------------------------------------------
-def _ids(ids):
-    torch = _torch()
-    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64):
+def _ids(torch, cur, ids):
+    """Address, bytes of one id, and number of ids."""
+    dtype = getattr(ids, "dtype", None)
+    if dtype is not torch.int64 and dtype is not torch.int32:
         raise TypeError("ids must be a torch.Tensor of int32 or int64")
-    _want(ids, ids.dtype, "ids")
-    return ids.numel(), ids.element_size()
-
-
-def _rows_like(t, shape, name, dtype=None):
-    code = _dtype_code(t, name) if dtype is None else None
-    _want(t, dtype or t.dtype, name)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return code
+    return _in(ids, dtype, "ids", cur), 8 if dtype is torch.int64 else 4, ids.numel()
 
 
 def forge_embedding(table, ids, out, *, scale=1.0, stream=None) -> None:
@@ -199,33 +243,40 @@ def forge_embedding(table, ids, out, *, scale=1.0, stream=None) -> None:
 
     table [V, d] and out [*ids.shape, d] float32 or bfloat16, ids int32 or
     int64 of any shape."""
-    T, id_bytes = _ids(ids)
-    V, d = _lib._shape2(table, "table")
-    tc = _rows_like(table, (V, d), "table")
-    oc = _rows_like(out, (*ids.shape, d), "out")
-    _check(library().forge_embedding(_ptr(table), tc, _ptr(ids), id_bytes, _ptr(out), oc, T, V, d,
-                                     float(scale), _stream(stream)), "forge_embedding")
+    torch, cur, st = _current(stream)
+    ip, id_bytes, T = _ids(torch, cur, ids)
+    tc, oc = _real(torch, table, "table"), _real(torch, out, "out")
+    V, d = _two(table, "table")
+    _shaped(out, (*ids.shape, d), "out")
+    _check(library().forge_embedding(_in(table, table.dtype, "table", cur), tc, ip, id_bytes,
+                                     _in(out, out.dtype, "out", cur), oc, T, V, d, scale, st),
+           "forge_embedding")
 
 
 def _embedding_args(ids, dY, outs, workspace, stream):
-    """ids of any shape, dY [*ids.shape, d]; outs: (name, [V, d] float32) pairs."""
-    T, id_bytes = _ids(ids)
-    V, d = _lib._shape2(outs[0][1], outs[0][0])
-    yc = _rows_like(dY, (*ids.shape, d), "dY")
+    """ids of any shape, dY [*ids.shape, d]; outs: (name, [V, d] float32) pairs.
+    The leading arguments of the C calls, the outputs' addresses, sizes,
+    workspace and stream."""
+    torch, cur, st = _current(stream)
+    ip, id_bytes, T = _ids(torch, cur, ids)
+    V, d = _two(outs[0][1], outs[0][0])
+    yc = _real(torch, dY, "dY")
+    _shaped(dY, (*ids.shape, d), "dY")
+    ptrs = []
     for name, t in outs:
-        _rows_like(t, (V, d), name, _torch().float32)
-    ws = _workspace(library().forge_embedding_workspace(T, V, d), workspace, stream)
-    return (_ptr(ids), id_bytes, _ptr(dY), yc), (T, V, d), ws
+        ptrs.append(_in(t, torch.float32, name, cur))
+        _shaped(t, (V, d), name)
+    ws = _workspace(torch, cur, library().forge_embedding_workspace(T, V, d), workspace, stream)
+    return (ip, id_bytes, _in(dY, dY.dtype, "dY", cur), yc, *ptrs), (T, V, d), ws, st
 
 
 def forge_embedding_grad(ids, dY, grad, *, scale=1.0, accumulate=False, workspace=None,
                          stream=None) -> None:
     """grad[r] <- scale * the sum of dY[t] over the tokens with ids[t] == r (or
     += with ``accumulate``, which leaves rows without a token alone)."""
-    head, (T, V, d), ws = _embedding_args(ids, dY, (("grad", grad),), workspace, stream)
-    _check(library().forge_embedding_grad(*head, _ptr(grad), T, V, d, float(scale),
-                                          int(bool(accumulate)), _ptr(ws), ws.numel(),
-                                          _stream(stream)), "forge_embedding_grad")
+    head, size, ws, st = _embedding_args(ids, dY, (("grad", grad),), workspace, stream)
+    _check(library().forge_embedding_grad(*head, *size, scale, 1 if accumulate else 0,
+                                          ws.data_ptr(), ws.numel(), st), "forge_embedding_grad")
 
 
 def forge_embedding_adamw(ids, dY, W, m, v, *, step, scale=1.0, lr=1e-3, beta1=0.9, beta2=0.999,
@@ -233,22 +284,20 @@ def forge_embedding_adamw(ids, dY, W, m, v, *, step, scale=1.0, lr=1e-3, beta1=0
                           stream=None) -> None:
     """W, m, v <- AdamW on the embedding's gradient, in place, the gradient
     never stored; rows without a token take the step with a zero gradient."""
-    head, (T, V, d), ws = _embedding_args(ids, dY, (("W", W), ("m", m), ("v", v)), workspace,
-                                          stream)
+    head, size, ws, st = _embedding_args(ids, dY, (("W", W), ("m", m), ("v", v)), workspace,
+                                         stream)
     p = _adamw(step, lr, beta1, beta2, eps, weight_decay, max_grad_norm)
-    _check(library().forge_embedding_adamw(*head, _ptr(W), _ptr(m), _ptr(v), T, V, d,
-                                           float(scale), ctypes.byref(p), _ptr(ws), ws.numel(),
-                                           _stream(stream)), "forge_embedding_adamw")
+    _check(library().forge_embedding_adamw(*head, *size, scale, ctypes.byref(p), ws.data_ptr(),
+                                           ws.numel(), st), "forge_embedding_adamw")
 
 
 def forge_embedding_sgdm(ids, dY, W, mom, *, scale=1.0, lr=1e-3, momentum=0.9, weight_decay=0.0,
                          max_grad_norm=0.0, workspace=None, stream=None) -> None:
     """W, mom <- SGD-momentum on the embedding's gradient, in place."""
-    head, (T, V, d), ws = _embedding_args(ids, dY, (("W", W), ("mom", mom)), workspace, stream)
+    head, size, ws, st = _embedding_args(ids, dY, (("W", W), ("mom", mom)), workspace, stream)
     p = SgdmParams(float(lr), float(momentum), float(weight_decay), float(max_grad_norm))
-    _check(library().forge_embedding_sgdm(*head, _ptr(W), _ptr(mom), T, V, d, float(scale),
-                                          ctypes.byref(p), _ptr(ws), ws.numel(),
-                                          _stream(stream)), "forge_embedding_sgdm")
+    _check(library().forge_embedding_sgdm(*head, *size, scale, ctypes.byref(p), ws.data_ptr(),
+                                          ws.numel(), st), "forge_embedding_sgdm")
 
 
 # --------------------------------------------------------------------------
@@ -257,63 +306,62 @@ def forge_embedding_sgdm(ids, dY, W, mom, *, scale=1.0, lr=1e-3, momentum=0.9, w
 def forge_mxfp4_empty(rows, k, device=None):
     """(codes, scales), uninitialised, of an operand of `rows` rows and
     contraction length k: uint8 [rows, Kp / 2] and [Kp / 128, rows, 4], Kp the
-    next multiple of 128."""
+    next multiple of 128. Both are views of one allocation."""
     torch = _torch()
-    groups = (int(k) + 127) // 128
-    device = "cuda" if device is None else device
-    return (torch.empty((int(rows), groups * 64), dtype=torch.uint8, device=device),
-            torch.empty((groups, int(rows), 4), dtype=torch.uint8, device=device))
+    rows, groups = int(rows), (int(k) + 127) // 128
+    n = groups * 64 * rows
+    buf = torch.empty(n + groups * 4 * rows, dtype=torch.uint8,
+                      device="cuda" if device is None else device)
+    return buf[:n].view(rows, groups * 64), buf[n:].view(groups, rows, 4)
 
 
-def _operand(pair, name):
-    """Checked (codes, scales) of an operand; its rows and padded length."""
-    torch = _torch()
+def _operand(torch, cur, pair, name):
+    """Addresses of an operand's codes and scales, its rows and padded length."""
     codes, scales = pair
-    _want(codes, torch.uint8, f"{name} codes")
-    _want(scales, torch.uint8, f"{name} scales")
-    rows, half = _lib._shape2(codes, f"{name} codes")
+    cp = _in(codes, torch.uint8, f"{name} codes", cur)
+    sp = _in(scales, torch.uint8, f"{name} scales", cur)
+    rows, half = _two(codes, f"{name} codes")
     if half % 64:
         raise ValueError(f"{name} codes must have a multiple of 64 columns, got {half}")
-    if tuple(scales.shape) != (half // 64, rows, 4):
-        raise ValueError(f"{name} scales must have shape {(half // 64, rows, 4)}, "
-                         f"got {tuple(scales.shape)}")
-    return rows, half * 2
+    _shaped(scales, (half // 64, rows, 4), f"{name} scales")
+    return cp, sp, rows, half * 2
 
 
 def forge_quantize_mxfp4(x, *, rows=None, cols=None, stream=None) -> None:
     """Quantises x [R, C] (float32 or bfloat16) into the operands ``rows`` (R
     rows, blocks along a row) and / or ``cols`` (C rows, blocks along a column:
     transposed), each a pair as forge_mxfp4_empty makes."""
-    R, C = _lib._shape2(x, "x")
-    code = _rows_like(x, (R, C), "x")
+    torch, cur, st = _current(stream)
+    code = _real(torch, x, "x")
+    xp = _in(x, x.dtype, "x", cur)
+    R, C = _two(x, "x")
     ptrs = []
-    for name, pair, want in (("rows", rows, (R, C)), ("cols", cols, (C, R))):
+    for name, pair, n, k in (("rows", rows, R, C), ("cols", cols, C, R)):
         if pair is None:
-            ptrs += [None, None]
+            ptrs += (None, None)
             continue
-        n, k = _operand(pair, name)
-        if (n, k) != (want[0], (want[1] + 127) // 128 * 128):
-            raise ValueError(f"{name} is an operand of {n} rows and padded length {k}, not of "
-                             f"{want[0]} rows and length {want[1]}")
-        if n and k:
-            ptrs += [_ptr(pair[0]), _ptr(pair[1])]
-        else:
+        cp, sp, pn, pk = _operand(torch, cur, pair, name)
+        if pn != n or pk != (k + 127) // 128 * 128:
+            raise ValueError(f"{name} is an operand of {pn} rows and padded length {pk}, not of "
+                             f"{n} rows and length {k}")
+        if not (n and k):
             return                           # x is empty: nothing to write
-    _check(library().forge_quantize_mxfp4(_ptr(x), code, R, C, *ptrs, _stream(stream)),
-           "forge_quantize_mxfp4")
+        ptrs += (cp, sp)
+    _check(library().forge_quantize_mxfp4(xp, code, R, C, *ptrs, st), "forge_quantize_mxfp4")
 
 
 def forge_matmul_mxfp4(A, B, out, *, tile=_lib.FORGE_TILE_DEFAULT, stream=None) -> None:
     """out [M, N] (float32 or bfloat16) <- A B^T for operands A of M rows and B
     of N rows, each a (codes, scales) pair."""
-    M, k = _operand(A, "A")
-    N, k2 = _operand(B, "B")
+    torch, cur, st = _current(stream)
+    ac, as_, M, k = _operand(torch, cur, A, "A")
+    bc, bs, N, k2 = _operand(torch, cur, B, "B")
     if k != k2:
         raise ValueError(f"A has padded length {k}, B has {k2}")
-    oc = _rows_like(out, (M, N), "out")
-    _check(library().forge_matmul_mxfp4(_ptr(A[0]), _ptr(A[1]), _ptr(B[0]), _ptr(B[1]), _ptr(out),
-                                        oc, M, N, k, int(tile), _stream(stream)),
-           "forge_matmul_mxfp4")
+    oc = _real(torch, out, "out")
+    _shaped(out, (M, N), "out")
+    _check(library().forge_matmul_mxfp4(ac, as_, bc, bs, _in(out, out.dtype, "out", cur), oc, M,
+                                        N, k, tile, st), "forge_matmul_mxfp4")
 
 
 def forge_wgrad_adamw_mxfp4(X, dY, W, m, v, *, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
@@ -321,13 +369,16 @@ def forge_wgrad_adamw_mxfp4(X, dY, W, m, v, *, step, lr=1e-3, beta1=0.9, beta2=0
                             stream=None) -> None:
     """W, m, v <- AdamW(W, m, v, g = dY^T X), in place, g never stored, from the
     operands X (d_in rows) and dY (d_out rows) over the tokens."""
-    d_in, k = _operand(X, "X")
-    d_out, k2 = _operand(dY, "dY")
+    torch, cur, st = _current(stream)
+    xc, xs, d_in, k = _operand(torch, cur, X, "X")
+    yc, ys, d_out, k2 = _operand(torch, cur, dY, "dY")
     if k != k2:
         raise ValueError(f"X has padded length {k}, dY has {k2}")
-    _lib._state_like(W, (("m", m), ("v", v)), d_out, d_in)
+    ptrs = []
+    for name, t in (("W", W), ("m", m), ("v", v)):
+        ptrs.append(_in(t, torch.float32, name, cur))
+        _shaped(t, (d_out, d_in), name)
     p = _adamw(step, lr, beta1, beta2, eps, weight_decay, max_grad_norm)
-    _check(library().forge_wgrad_adamw_mxfp4(_ptr(X[0]), _ptr(X[1]), _ptr(dY[0]), _ptr(dY[1]),
-                                             _ptr(W), _ptr(m), _ptr(v), k, d_in, d_out,
-                                             ctypes.byref(p), int(tile), _stream(stream)),
+    _check(library().forge_wgrad_adamw_mxfp4(xc, xs, yc, ys, *ptrs, k, d_in, d_out,
+                                             ctypes.byref(p), tile, st),
            "forge_wgrad_adamw_mxfp4")
