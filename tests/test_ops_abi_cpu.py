@@ -108,8 +108,8 @@ def norm(lib, *ts, max_norm=1.0, out=F, ws=F + 4096, ws_bytes=1 << 20):
 def test_norm_workspace_sizes(lib):
     f = lib.forge_grad_norm_workspace
     assert f(-1) == 0 and f(65537) == 0
-    assert f(0) >= 16 and f(1) == f(128) == 2048 * 8 and f(129) == 2 * f(128)
-    assert f(65536) == 512 * f(1)
+    assert f(0) >= 16 and f(1) == f(256) == 2048 * 8 and f(257) == 2 * f(256)
+    assert f(65536) == 256 * f(1)
 
 
 @pytest.mark.parametrize("kw,status", [

@@ -26,44 +26,50 @@
 namespace forge {
 
 // Tensors in one launch: the tables stay under 4 KB of kernel arguments.
-constexpr int kNormTensors = 128;
-constexpr int kStepTensors = 72;
-constexpr int kNormChunk = 16384;    // elements of a chunk of the norm's pass
+constexpr int kNormTensors = 256;
+constexpr int kClipTensors = 128;    // three addresses a tensor
+constexpr int kAdamTensors = 100;    // four
+constexpr int kChunk = 4096;         // elements of a chunk
 constexpr int kNormGrid = 2048;      // most workgroups (and partial sums) of a norm launch
-constexpr int kStepChunk = 4096;     // elements of a chunk of the step's pass
+constexpr int kNormAlone = 16;       // chunks that one workgroup sums by itself
 
-struct NormTable {
-  const void* g[kNormTensors];
-  int64_t n[kNormTensors];
-  int32_t first[kNormTensors];       // first chunk of tensor t; INT32_MAX past the last tensor
-  uint8_t bf16[kNormTensors];
+// The tensors of one launch, A addresses each. Tensor t has the chunks
+// first[t] .. first[t + 1] - 1, the last of them with tail[t] & 8191 elements;
+// bit 15 of tail[t] marks a bf16 gradient.
+template <int N_, int A_>
+struct TensorTable {
+  static constexpr int N = N_, A = A_;
+  void* p[A][N];
+  int32_t first[N + 1];              // INT32_MAX past the last tensor's end
+  uint16_t tail[N];
   int32_t chunks;
 };
-
-struct StepTable {
-  const void* g[kStepTensors];
-  void* W[kStepTensors];             // the clipped gradient's place in forge_clip_grads
-  float* m[kStepTensors];
-  float* v[kStepTensors];
-  int64_t n[kStepTensors];
-  int32_t first[kStepTensors];
-  uint8_t bf16[kStepTensors];
-  int32_t chunks;
-};
-static_assert(sizeof(NormTable) <= 4000 && sizeof(StepTable) <= 4000, "kernel argument size");
+typedef TensorTable<kNormTensors, 1> NormTable;     // gradient
+typedef TensorTable<kClipTensors, 3> ClipTable;     // gradient, and its place or W and momentum
+typedef TensorTable<kAdamTensors, 4> AdamTable;     // gradient, W, m, v
+static_assert(sizeof(NormTable) <= 4000 && sizeof(ClipTable) <= 4000 && sizeof(AdamTable) <= 4000,
+              "kernel argument size");
 
 // The tensor of chunk c: the last one that starts at or before it. Every lane
 // of the wave takes part.
-template <int N>
-__device__ __forceinline__ int tensor_of(const int32_t (&first)[N], int c) {
+template <class Table>
+__device__ __forceinline__ int tensor_of(const Table& tab, int c) {
+  constexpr int N = Table::N;
   const int lane = threadIdx.x & 63;
   int t = -1;
 #pragma unroll
   for (int k = 0; k < N; k += 64) {
-    const bool below = k + lane < N && first[k + lane < N ? k + lane : N - 1] <= c;
+    const bool below = k + lane < N && tab.first[k + lane < N ? k + lane : N - 1] <= c;
     t += __popcll(__ballot(below));
   }
   return __builtin_amdgcn_readfirstlane(t);
+}
+
+// Elements of tensor t that lie before the end of its chunk c.
+template <class Table>
+__device__ __forceinline__ int64_t end_of(const Table& tab, int t, int c) {
+  const int64_t k = int64_t(c - tab.first[t]) * kChunk;
+  return k + (c + 1 == tab.first[t + 1] || c + 1 == tab.chunks ? tab.tail[t] & 8191 : kChunk);
 }
 
 // Sum of v over the workgroup, in thread 0. `part`: one double per wave.
@@ -115,13 +121,15 @@ __device__ __forceinline__ double square_sum(const void* g, int64_t k0, int64_t 
     }
   };
   const u32x4_t* p = reinterpret_cast<const u32x4_t*>(g);
-  // Four loads in flight per thread.
-  for (; k + 3 * int64_t(step) + E <= k1; k += 4 * int64_t(step)) {
-    u32x4_t r[4];
+  // Eight loads in flight per thread, past the caches' replacement: 6.75 TB/s
+  // against 5.8 without the hint (906 MB of float32).
+  constexpr int U = 8;
+  for (; k + (U - 1) * int64_t(step) + E <= k1; k += U * int64_t(step)) {
+    u32x4_t r[U];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = p[(k + j * int64_t(step)) / E];
+    for (int j = 0; j < U; ++j) r[j] = __builtin_nontemporal_load(&p[(k + j * int64_t(step)) / E]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) add(r[j]);
+    for (int j = 0; j < U; ++j) add(r[j]);
   }
   for (; k + E <= k1; k += step) add(p[k / E]);
   for (int64_t i = k; i < k1; ++i) {         // the thread that owns the partial vector
@@ -132,18 +140,32 @@ __device__ __forceinline__ double square_sum(const void* g, int64_t k0, int64_t 
   return s0 + s1;
 }
 
-// Workgroup b sums chunks b, b + grid, ... into part[b].
-__global__ __launch_bounds__(256) void norm_partial_kernel(NormTable tab, double* part) {
+// Workgroup b sums its share of the chunks, a run of them, into part[b]. ALONE:
+// one workgroup that stores the result itself.
+template <bool ALONE>
+__global__ __launch_bounds__(ALONE ? 1024 : 256) void norm_partial_kernel(NormTable tab, double* part,
+                                                                          double max_norm, float* out) {
   __shared__ double lds[16];
+  const int per = (tab.chunks + int(gridDim.x) - 1) / int(gridDim.x);
+  int c = int(blockIdx.x) * per;
+  const int c1 = c + per < tab.chunks ? c + per : tab.chunks;
   double s = 0.0;
-  for (int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-    const int t = tensor_of(tab.first, c);
-    const int64_t k0 = int64_t(c - tab.first[t]) * kNormChunk;
-    const int64_t n = tab.n[t], k1 = k0 + kNormChunk < n ? k0 + kNormChunk : n;
-    s += tab.bf16[t] ? square_sum<true>(tab.g[t], k0, k1) : square_sum<false>(tab.g[t], k0, k1);
+  if (c < c1) {
+    for (int t = tensor_of(tab, c); c < c1; ++t) {
+      const int last = (tab.first[t + 1] < c1 ? tab.first[t + 1] : c1) - 1;
+      const int64_t k0 = int64_t(c - tab.first[t]) * kChunk, k1 = end_of(tab, t, last);
+      s += tab.tail[t] >> 15 ? square_sum<true>(tab.p[0][t], k0, k1)
+                             : square_sum<false>(tab.p[0][t], k0, k1);
+      c = last + 1;
+    }
   }
   s = block_sum(s, lds);
-  if (threadIdx.x == 0) part[blockIdx.x] = s;
+  if (threadIdx.x == 0) {
+    if constexpr (ALONE)
+      store_norm(s, max_norm, out);
+    else
+      part[blockIdx.x] = s;
+  }
 }
 
 __global__ __launch_bounds__(1024) void norm_finish_kernel(const double* part, int64_t count,
@@ -158,55 +180,60 @@ __global__ __launch_bounds__(1024) void norm_finish_kernel(const double* part, i
 enum ClipOp : int { CLIP_SCALE = 0, CLIP_ADAMW = 1, CLIP_ADAMW_EXACT = 2, CLIP_SGDM = 3 };
 
 // One chunk of one tensor per workgroup: 4 groups of 4 elements per thread.
-template <int OP, bool BF16>
-__device__ __forceinline__ void clip_chunk(const StepTable& tab, int t, int64_t k0, float coef,
+// Everything is read and written once, so loads and stores carry the
+// non-temporal hint (AdamW on 226M elements: 5.8 TB/s against 5.4 without).
+template <int OP, bool BF16, class Table>
+__device__ __forceinline__ void clip_chunk(const Table& tab, int t, int c, float coef,
                                            const AdamWConsts& ac, const SgdmConsts& sc) {
-  typedef __bf16 bf16v4 __attribute__((ext_vector_type(4)));
   constexpr bool ADAM = OP == CLIP_ADAMW || OP == CLIP_ADAMW_EXACT;
-  constexpr int G = kStepChunk / (256 * 4);
-  const int64_t n = tab.n[t];
-  const void* const g_ = tab.g[t];
-  float* const W = static_cast<float*>(tab.W[t]);
-  float* const m = tab.m[t];
-  float* const v = tab.v[t];
+  constexpr int G = kChunk / (256 * 4);
+  const void* const g_ = tab.p[0][t];
+  float* const W = static_cast<float*>(tab.p[1][t]);
+  float* const m = OP == CLIP_SCALE ? nullptr : static_cast<float*>(tab.p[Table::A > 2 ? 2 : 0][t]);
+  float* const v = ADAM ? static_cast<float*>(tab.p[Table::A > 3 ? 3 : 0][t]) : nullptr;
+  const int64_t k0 = int64_t(c - tab.first[t]) * kChunk, n = end_of(tab, t, c);
   const int64_t k = k0 + int(threadIdx.x) * 4;
+  auto get4 = [](const float* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p));
+  };
+  auto set4 = [](float* p, const f32x4_t& x) {
+    __builtin_nontemporal_store(x, reinterpret_cast<f32x4_t*>(p));
+  };
   auto grad4 = [&](int64_t i) {
     if constexpr (BF16)
-      return __builtin_convertvector(*reinterpret_cast<const bf16v4*>(static_cast<const __bf16*>(g_) + i),
-                                     f32x4_t);
+      return unpack_bf16x4(__builtin_nontemporal_load(
+          reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(g_) + i)));
     else
-      return *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(g_) + i);
+      return get4(static_cast<const float*>(g_) + i);
   };
-  auto put4 = [&](int64_t i, const f32x4_t& g) {
-    if constexpr (BF16)
-      *reinterpret_cast<bf16v4*>(reinterpret_cast<__bf16*>(W) + i) = __builtin_convertvector(g, bf16v4);
-    else
-      *reinterpret_cast<f32x4_t*>(W + i) = g;
-  };
-  if (k0 + kStepChunk <= n) {
+  if (k0 + kChunk == n) {
     f32x4_t g[G], w[G], a[G], b[G];
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       g[j] = grad4(k + j * 1024);
       if constexpr (OP != CLIP_SCALE) {
-        w[j] = *reinterpret_cast<const f32x4_t*>(W + k + j * 1024);
-        a[j] = *reinterpret_cast<const f32x4_t*>(m + k + j * 1024);
+        w[j] = get4(W + k + j * 1024);
+        a[j] = get4(m + k + j * 1024);
       }
-      if constexpr (ADAM) b[j] = *reinterpret_cast<const f32x4_t*>(v + k + j * 1024);
+      if constexpr (ADAM) b[j] = get4(v + k + j * 1024);
     }
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       g[j] = g[j] * coef;
       if constexpr (OP == CLIP_SCALE) {
-        put4(k + j * 1024, g[j]);
+        if constexpr (BF16)
+          __builtin_nontemporal_store(pack_bf16x4(g[j]), reinterpret_cast<u32x2_t*>(
+                                                             reinterpret_cast<uint16_t*>(W) + k + j * 1024));
+        else
+          set4(W + k + j * 1024, g[j]);
       } else {
         if constexpr (ADAM)
           adamw_vec4<OP == CLIP_ADAMW_EXACT>(g[j], w[j], a[j], b[j], ac);
         else
           sgdm_vec4(g[j], w[j], a[j], sc);
-        *reinterpret_cast<f32x4_t*>(W + k + j * 1024) = w[j];
-        *reinterpret_cast<f32x4_t*>(m + k + j * 1024) = a[j];
-        if constexpr (ADAM) *reinterpret_cast<f32x4_t*>(v + k + j * 1024) = b[j];
+        set4(W + k + j * 1024, w[j]);
+        set4(m + k + j * 1024, a[j]);
+        if constexpr (ADAM) set4(v + k + j * 1024, b[j]);
       }
     }
     return;
@@ -235,16 +262,15 @@ __device__ __forceinline__ void clip_chunk(const StepTable& tab, int t, int64_t 
   }
 }
 
-template <int OP>
-__global__ __launch_bounds__(256) void clip_step_kernel(StepTable tab, const float* coef_,
+template <int OP, class Table>
+__global__ __launch_bounds__(256) void clip_step_kernel(Table tab, const float* coef_,
                                                         AdamWConsts ac, SgdmConsts sc) {
   const float coef = *coef_;
-  const int t = tensor_of(tab.first, blockIdx.x);
-  const int64_t k0 = int64_t(int(blockIdx.x) - tab.first[t]) * kStepChunk;
-  if (tab.bf16[t])
-    clip_chunk<OP, true>(tab, t, k0, coef, ac, sc);
+  const int c = blockIdx.x, t = tensor_of(tab, c);
+  if (tab.tail[t] >> 15)
+    clip_chunk<OP, true>(tab, t, c, coef, ac, sc);
   else
-    clip_chunk<OP, false>(tab, t, k0, coef, ac, sc);
+    clip_chunk<OP, false>(tab, t, c, coef, ac, sc);
 }
 
 }  // namespace forge

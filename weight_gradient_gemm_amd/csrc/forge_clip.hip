@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstring>
+#include <type_traits>
 
 #include "clip_kernels.hpp"
 #include "forge_ops.h"
@@ -12,9 +13,9 @@
 namespace forge {
 namespace {
 
-// Cuts the list into tables of at most N tensors and MAX_CHUNKS chunks and
-// hands each to `launch(table)`; a tensor of more chunks goes into several.
-template <class Table, int N, int CHUNK, int64_t MAX_CHUNKS, class Fill, class Launch>
+// Cuts the list into tables of at most Table::N tensors and MAX_CHUNKS chunks
+// and hands each to `launch(table)`; a tensor of more chunks goes into several.
+template <class Table, int64_t MAX_CHUNKS, class Fill, class Launch>
 forge_status for_tables(const forge_tensor* tensors, int32_t count, const Fill& fill,
                         const Launch& launch) {
   Table tab;
@@ -22,7 +23,7 @@ forge_status for_tables(const forge_tensor* tensors, int32_t count, const Fill& 
   int64_t chunks = 0;
   auto flush = [&]() -> forge_status {
     if (used == 0) return FORGE_OK;
-    for (int t = used; t < N; ++t) tab.first[t] = INT_MAX;
+    for (int t = used; t <= Table::N; ++t) tab.first[t] = INT_MAX;
     tab.chunks = int32_t(chunks);
     const forge_status s = launch(tab);
     used = 0;
@@ -32,43 +33,42 @@ forge_status for_tables(const forge_tensor* tensors, int32_t count, const Fill& 
   std::memset(&tab, 0, sizeof(tab));
   for (int32_t i = 0; i < count; ++i) {
     for (int64_t at = 0; at < tensors[i].n;) {
-      if (used == N || chunks == MAX_CHUNKS)
+      if (used == Table::N || chunks == MAX_CHUNKS)
         if (forge_status s = flush()) return s;
-      const int64_t room = (MAX_CHUNKS - chunks) * CHUNK;
-      const int64_t n = std::min(tensors[i].n - at, room);
+      const int64_t n = std::min(tensors[i].n - at, (MAX_CHUNKS - chunks) * kChunk);
       fill(tab, used, tensors[i], at);
-      tab.n[used] = n;
-      tab.bf16[used] = tensors[i].grad_dtype == FORGE_BF16;
+      tab.tail[used] = uint16_t((n - 1) % kChunk + 1) | (tensors[i].grad_dtype == FORGE_BF16 ? 0x8000 : 0);
       tab.first[used] = int32_t(chunks);
       ++used;
-      chunks += (n + CHUNK - 1) / CHUNK;
+      chunks += (n + kChunk - 1) / kChunk;
       at += n;
     }
   }
   return flush();
 }
 
-template <class T>
-T* advance(T* p, int64_t elems, int64_t bytes) {
-  return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + uint64_t(elems) * uint64_t(bytes));
+void* advance(const void* p, int64_t elems, int64_t bytes) {
+  return reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(p) + uint64_t(elems) * uint64_t(bytes));
 }
 
 template <int OP>
 forge_status launch_steps(const forge_tensor* tensors, int32_t count, const float* coef,
                           const AdamWConsts& ac, const SgdmConsts& sc, hipStream_t s) {
+  constexpr bool ADAM = OP == CLIP_ADAMW || OP == CLIP_ADAMW_EXACT;
+  typedef typename std::conditional<ADAM, AdamTable, ClipTable>::type Table;
   // One workgroup of 256 per chunk: the launch's work items stay below 2^32.
-  return for_tables<StepTable, kStepTensors, kStepChunk, (int64_t(1) << 23)>(
+  return for_tables<Table, (int64_t(1) << 23)>(
       tensors, count,
-      [](StepTable& tab, int k, const forge_tensor& t, int64_t at) {
+      [](Table& tab, int k, const forge_tensor& t, int64_t at) {
         const int gb = dtype_bytes(t.grad_dtype);
-        tab.g[k] = advance(t.grad, at, gb);
-        tab.W[k] = OP == CLIP_SCALE ? advance(t.out, at, gb) : advance(t.W, at, 4);
-        tab.m[k] = OP == CLIP_SCALE ? nullptr : advance(t.m, at, 4);
-        tab.v[k] = OP == CLIP_ADAMW || OP == CLIP_ADAMW_EXACT ? advance(t.v, at, 4) : nullptr;
+        tab.p[0][k] = advance(t.grad, at, gb);
+        tab.p[1][k] = OP == CLIP_SCALE ? advance(t.out, at, gb) : advance(t.W, at, 4);
+        if constexpr (OP != CLIP_SCALE) tab.p[2][k] = advance(t.m, at, 4);
+        if constexpr (ADAM) tab.p[3][k] = advance(t.v, at, 4);
       },
-      [&](const StepTable& tab) {
-        hipLaunchKernelGGL((clip_step_kernel<OP>), dim3(tab.chunks), dim3(256), 0, s, tab, coef,
-                           ac, sc);
+      [&](const Table& tab) {
+        hipLaunchKernelGGL((clip_step_kernel<OP, Table>), dim3(tab.chunks), dim3(256), 0, s, tab,
+                           coef, ac, sc);
         return launch_status();
       });
 }
@@ -99,18 +99,27 @@ FORGE_API forge_status forge_grad_norm(const forge_tensor* tensors, int32_t coun
   const hipStream_t st = static_cast<hipStream_t>(stream);
   double* const part = static_cast<double*>(workspace);
   int64_t parts = 0;
-  const forge_status s = for_tables<NormTable, kNormTensors, kNormChunk, kMaxListElems / kNormChunk + FORGE_MAX_TENSORS>(
+  bool alone = false;
+  const forge_status s = for_tables<NormTable, kMaxListElems / kChunk + FORGE_MAX_TENSORS>(
       tensors, count,
       [](NormTable& tab, int k, const forge_tensor& t, int64_t at) {
-        tab.g[k] = advance(t.grad, at, dtype_bytes(t.grad_dtype));
+        tab.p[0][k] = advance(t.grad, at, dtype_bytes(t.grad_dtype));
       },
       [&](const NormTable& tab) {
+        // A short list of few tensors: one workgroup, one launch.
+        alone = count <= kNormTensors && tab.chunks <= kNormAlone;
+        if (alone) {
+          hipLaunchKernelGGL((norm_partial_kernel<true>), dim3(1), dim3(1024), 0, st, tab, part,
+                             max_norm, norm_coef);
+          return launch_status();
+        }
         const int grid = std::min(int(tab.chunks), kNormGrid);
-        hipLaunchKernelGGL(norm_partial_kernel, dim3(grid), dim3(256), 0, st, tab, part + parts);
+        hipLaunchKernelGGL((norm_partial_kernel<false>), dim3(grid), dim3(256), 0, st, tab,
+                           part + parts, max_norm, norm_coef);
         parts += grid;
         return launch_status();
       });
-  if (s) return s;
+  if (s || alone) return s;
   hipLaunchKernelGGL(norm_finish_kernel, dim3(1), dim3(1024), 0, st, part, parts, max_norm,
                      norm_coef);
   return launch_status();

@@ -103,10 +103,10 @@ forge_status check_clipped(const forge_tensor* tensors, int32_t count, const flo
 
 }  // namespace
 
-// One launch takes 128 tensors and leaves at most 2048 float64 partial sums.
+// One launch takes 256 tensors and leaves at most 2048 float64 partial sums.
 int64_t grad_norm_workspace(int32_t count) {
   if (count < 0 || count > FORGE_MAX_TENSORS) return 0;
-  return std::max<int64_t>(16, (int64_t(count) + 127) / 128 * 2048 * 8);
+  return std::max<int64_t>(16, (int64_t(count) + 255) / 256 * 2048 * 8);
 }
 
 forge_status validate_grad_norm(const forge_tensor* tensors, int32_t count, double max_norm,
