@@ -31,7 +31,7 @@ constexpr int kClipTensors = 128;    // three addresses a tensor
 constexpr int kAdamTensors = 100;    // four
 constexpr int kChunk = 4096;         // elements of a chunk
 constexpr int kNormGrid = 2048;      // most workgroups (and partial sums) of a norm launch
-constexpr int kNormAlone = 16;       // chunks that one workgroup sums by itself
+constexpr int kNormAlone = 24;       // chunks that one workgroup sums by itself
 
 // The tensors of one launch, A addresses each. Tensor t has the chunks
 // first[t] .. first[t + 1] - 1, the last of them with tail[t] & 8191 elements;
@@ -92,15 +92,15 @@ __device__ __forceinline__ void store_norm(double sum, double max_norm, float* o
   out[1] = c >= 1.0 ? 1.0f : float(c);       // a NaN stays one
 }
 
-// Sum of squares of the elements [k0, k1) of a tensor by the workgroup, k0 a
-// multiple of 8: each thread's share, in float64.
+// Sum of squares of the elements [k0, k1) of a tensor, k0 a multiple of 8: the
+// share of thread `me` of `threads`, in float64.
 template <bool BF16>
-__device__ __forceinline__ double square_sum(const void* g, int64_t k0, int64_t k1) {
+__device__ __forceinline__ double square_sum(const void* g, int64_t k0, int64_t k1, int me, int threads) {
   typedef __bf16 bf16v8 __attribute__((ext_vector_type(8)));
   constexpr int E = BF16 ? 8 : 4;            // elements of a 16-byte load
-  const int step = int(blockDim.x) * E;
+  const int step = threads * E;
   double s0 = 0.0, s1 = 0.0;
-  int64_t k = k0 + int(threadIdx.x) * E;
+  int64_t k = k0 + me * E;
   auto add = [&](const u32x4_t& raw) {
     if constexpr (BF16) {
       const bf16v8 b = __builtin_bit_cast(bf16v8, raw);
@@ -140,12 +140,16 @@ __device__ __forceinline__ double square_sum(const void* g, int64_t k0, int64_t 
   return s0 + s1;
 }
 
-// Workgroup b sums its share of the chunks, a run of them, into part[b]. ALONE:
-// one workgroup that stores the result itself.
-template <bool ALONE>
-__global__ __launch_bounds__(ALONE ? 1024 : 256) void norm_partial_kernel(NormTable tab, double* part,
-                                                                          double max_norm, float* out) {
-  __shared__ double lds[16];
+template <class Table>
+__device__ __forceinline__ double tensor_square_sum(const Table& tab, int t, int64_t k0, int64_t k1, int me,
+                                                    int threads) {
+  return tab.tail[t] >> 15 ? square_sum<true>(tab.p[0][t], k0, k1, me, threads)
+                           : square_sum<false>(tab.p[0][t], k0, k1, me, threads);
+}
+
+// Workgroup b sums its share of the chunks, a run of them, into part[b].
+__global__ __launch_bounds__(256) void norm_partial_kernel(NormTable tab, double* part) {
+  __shared__ double lds[4];
   const int per = (tab.chunks + int(gridDim.x) - 1) / int(gridDim.x);
   int c = int(blockIdx.x) * per;
   const int c1 = c + per < tab.chunks ? c + per : tab.chunks;
@@ -153,19 +157,28 @@ __global__ __launch_bounds__(ALONE ? 1024 : 256) void norm_partial_kernel(NormTa
   if (c < c1) {
     for (int t = tensor_of(tab, c); c < c1; ++t) {
       const int last = (tab.first[t + 1] < c1 ? tab.first[t + 1] : c1) - 1;
-      const int64_t k0 = int64_t(c - tab.first[t]) * kChunk, k1 = end_of(tab, t, last);
-      s += tab.tail[t] >> 15 ? square_sum<true>(tab.p[0][t], k0, k1)
-                             : square_sum<false>(tab.p[0][t], k0, k1);
+      s += tensor_square_sum(tab, t, int64_t(c - tab.first[t]) * kChunk, end_of(tab, t, last),
+                             int(threadIdx.x), 256);
       c = last + 1;
     }
   }
   s = block_sum(s, lds);
-  if (threadIdx.x == 0) {
-    if constexpr (ALONE)
-      store_norm(s, max_norm, out);
-    else
-      part[blockIdx.x] = s;
+  if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+// A short list by one workgroup, a chunk to a wave at a time, and the result.
+// Up to kNormAlone chunks: 65536 elements take 4.4 us in one tensor and 4.9 in
+// twelve, where the two launches take 5.1-5.3; 131072 in one take 6.4.
+__global__ __launch_bounds__(1024) void norm_alone_kernel(NormTable tab, double max_norm, float* out) {
+  __shared__ double lds[16];
+  double s = 0.0;
+  for (int c = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)); c < tab.chunks; c += 16) {
+    const int t = tensor_of(tab, c);
+    s += tensor_square_sum(tab, t, int64_t(c - tab.first[t]) * kChunk, end_of(tab, t, c),
+                           int(threadIdx.x & 63), 64);
   }
+  s = block_sum(s, lds);
+  if (threadIdx.x == 0) store_norm(s, max_norm, out);
 }
 
 __global__ __launch_bounds__(1024) void norm_finish_kernel(const double* part, int64_t count,

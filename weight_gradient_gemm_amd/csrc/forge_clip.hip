@@ -109,13 +109,12 @@ FORGE_API forge_status forge_grad_norm(const forge_tensor* tensors, int32_t coun
         // A short list of few tensors: one workgroup, one launch.
         alone = count <= kNormTensors && tab.chunks <= kNormAlone;
         if (alone) {
-          hipLaunchKernelGGL((norm_partial_kernel<true>), dim3(1), dim3(1024), 0, st, tab, part,
-                             max_norm, norm_coef);
+          hipLaunchKernelGGL(norm_alone_kernel, dim3(1), dim3(1024), 0, st, tab, max_norm,
+                             norm_coef);
           return launch_status();
         }
         const int grid = std::min(int(tab.chunks), kNormGrid);
-        hipLaunchKernelGGL((norm_partial_kernel<false>), dim3(grid), dim3(256), 0, st, tab,
-                           part + parts, max_norm, norm_coef);
+        hipLaunchKernelGGL(norm_partial_kernel, dim3(grid), dim3(256), 0, st, tab, part + parts);
         parts += grid;
         return launch_status();
       });
