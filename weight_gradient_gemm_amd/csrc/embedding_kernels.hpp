@@ -281,10 +281,10 @@ struct EmbeddingArgs {
   float *W, *m, *v;                // W: the gradient, where it is stored
   int64_t T;
   int32_t V, d;
-  int32_t lanes;                   // threads across a row in a workgroup: a power of two
-  int32_t slices;                  // workgroups across a row
-  int32_t bound_blocks;            // workgroups of the bounds kernel that search
-  int64_t blocks;                  // workgroups of a pass (a launch may have fewer, and loop)
+  int32_t lanes_log2;              // threads across a row in a workgroup
+  uint32_t slices;                 // workgroups across a row
+  uint32_t bound_blocks;           // workgroups of the bounds kernel that search
+  uint32_t blocks;                 // workgroups of a pass (a launch may have fewer, and loop)
   float scale;
   AdamWConsts adam;
   SgdmConsts sgd;
@@ -317,14 +317,14 @@ __device__ __forceinline__ void add_tokens(const EmbeddingArgs& a, f32x4_t& acc,
 // the chunks that lie within one row (the others, one slice of a chunk each).
 template <bool BF16>
 __global__ __launch_bounds__(256) void embedding_bounds_kernel(EmbeddingArgs a) {
-  for (int64_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
+  for (uint32_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
     if (b < a.bound_blocks) {
-      const int64_t r = b * 256 + threadIdx.x;
-      if (r <= a.V) {
+      const uint32_t r = b * 256 + threadIdx.x;
+      if (r <= uint32_t(a.V)) {
         uint32_t lo = 0, hi = uint32_t(a.T);       // first place whose key is >= r
         while (lo < hi) {
           const uint32_t mid = lo + (hi - lo) / 2;
-          if (a.keys[mid] < uint32_t(r))
+          if (a.keys[mid] < r)
             lo = mid + 1;
           else
             hi = mid;
@@ -333,15 +333,14 @@ __global__ __launch_bounds__(256) void embedding_bounds_kernel(EmbeddingArgs a) 
       }
       continue;
     }
-    const int64_t c = (b - a.bound_blocks) / a.slices;
-    const int slice = int((b - a.bound_blocks) - c * a.slices);
-    const uint32_t s = uint32_t(c) * kSumChunk, key = a.keys[s];
+    const uint32_t c = (b - a.bound_blocks) / a.slices, slice = b - a.bound_blocks - c * a.slices;
+    const uint32_t s = c * kSumChunk, key = a.keys[s];
     if (key >= uint32_t(a.V) || a.keys[s + kSumChunk - 1] != key) continue;
-    const int col = (slice * 256 + int(threadIdx.x)) * 4;
+    const int col = int(slice * 256 + threadIdx.x) * 4;
     if (col < a.d) {
       f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
       add_tokens<BF16>(a, acc, s, s + kSumChunk, col);
-      *reinterpret_cast<f32x4_t*>(a.chunk + c * a.d + col) = acc;
+      *reinterpret_cast<f32x4_t*>(a.chunk + int64_t(c) * a.d + col) = acc;
     }
   }
 }
@@ -352,20 +351,27 @@ enum EmbOp : int { EMB_GRAD = 0, EMB_GRAD_ADD = 1, EMB_ADAMW = 2, EMB_ADAMW_EXAC
 template <int OP, bool BF16>
 __global__ __launch_bounds__(256) void embedding_rows_kernel(EmbeddingArgs a) {
   constexpr bool ADAM = OP == EMB_ADAMW || OP == EMB_ADAMW_EXACT;
-  const int rows = 256 / a.lanes;
-  for (int64_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
-    const int64_t rb = b / a.slices;
-    const int slice = int(b - rb * a.slices);
-    const int64_t row = rb * rows + int(threadIdx.x) / a.lanes;
-    const int col = (slice * a.lanes + (int(threadIdx.x) & (a.lanes - 1))) * 4;
+  // W and the state are read and written once: non-temporal, as in the clipped
+  // steps.
+  auto get4 = [](const float* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p));
+  };
+  auto set4 = [](float* p, const f32x4_t& x) {
+    __builtin_nontemporal_store(x, reinterpret_cast<f32x4_t*>(p));
+  };
+  const int lanes = 1 << a.lanes_log2;
+  for (uint32_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
+    const uint32_t rb = b / a.slices, slice = b - rb * a.slices;
+    const int row = int((rb << (8 - a.lanes_log2)) + (threadIdx.x >> a.lanes_log2));
+    const int col = (int(slice << a.lanes_log2) + (int(threadIdx.x) & (lanes - 1))) * 4;
     if (row >= a.V || col >= a.d) continue;
     const uint32_t s = a.bound[row], e = a.bound[row + 1];
     if (OP == EMB_GRAD_ADD && s == e) continue;
-    const int64_t i = row * a.d + col;
+    const int64_t i = int64_t(row) * a.d + col;
     f32x4_t w, m, v;
-    if constexpr (OP != EMB_GRAD) w = *reinterpret_cast<const f32x4_t*>(a.W + i);
-    if constexpr (ADAM || OP == EMB_SGDM) m = *reinterpret_cast<const f32x4_t*>(a.m + i);
-    if constexpr (ADAM) v = *reinterpret_cast<const f32x4_t*>(a.v + i);
+    if constexpr (OP != EMB_GRAD) w = get4(a.W + i);
+    if constexpr (ADAM || OP == EMB_SGDM) m = get4(a.m + i);
+    if constexpr (ADAM) v = get4(a.v + i);
     f32x4_t g = {0.0f, 0.0f, 0.0f, 0.0f};
     const uint32_t c0 = (s + kSumChunk - 1) / kSumChunk, c1 = e / kSumChunk;
     if (c0 < c1) {
@@ -381,9 +387,9 @@ __global__ __launch_bounds__(256) void embedding_rows_kernel(EmbeddingArgs a) {
     if constexpr (OP == EMB_GRAD_ADD) w = w + g;
     if constexpr (ADAM) adamw_vec4<OP == EMB_ADAMW_EXACT>(g, w, m, v, a.adam);
     if constexpr (OP == EMB_SGDM) sgdm_vec4(g, w, m, a.sgd);
-    *reinterpret_cast<f32x4_t*>(a.W + i) = w;
-    if constexpr (ADAM || OP == EMB_SGDM) *reinterpret_cast<f32x4_t*>(a.m + i) = m;
-    if constexpr (ADAM) *reinterpret_cast<f32x4_t*>(a.v + i) = v;
+    set4(a.W + i, w);
+    if constexpr (ADAM || OP == EMB_SGDM) set4(a.m + i, m);
+    if constexpr (ADAM) set4(a.v + i, v);
   }
 }
 
@@ -392,20 +398,19 @@ struct LookupArgs {
   const void* table;
   void* out;
   int64_t T;
-  int32_t d, lanes, slices;
-  int64_t blocks;
+  int32_t d, lanes_log2;
+  uint32_t slices, blocks;
   float scale;
 };
 
 // 8 columns of one token per thread.
 template <bool TABLE_BF16, bool OUT_BF16>
 __global__ __launch_bounds__(256) void embedding_kernel(LookupArgs a) {
-  const int rows = 256 / a.lanes;
-  for (int64_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
-    const int64_t rb = b / a.slices;
-    const int slice = int(b - rb * a.slices);
-    const int64_t t = rb * rows + int(threadIdx.x) / a.lanes;
-    const int col = (slice * a.lanes + (int(threadIdx.x) & (a.lanes - 1))) * 8;
+  const int lanes = 1 << a.lanes_log2;
+  for (uint32_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
+    const uint32_t rb = b / a.slices, slice = b - rb * a.slices;
+    const int64_t t = (rb << (8 - a.lanes_log2)) + (threadIdx.x >> a.lanes_log2);
+    const int col = (int(slice << a.lanes_log2) + (int(threadIdx.x) & (lanes - 1))) * 8;
     if (t >= a.T || col >= a.d) continue;
     const uint32_t row = load_key(a.src, t);
     f32x4_t x[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};

@@ -11,21 +11,20 @@ namespace {
 
 // Most workgroups of 256 threads of a launch; what is beyond loops.
 constexpr int64_t kMaxGrid = int64_t(1) << 22;
-
-int pow2_at_least(int64_t n, int most) {
-  int p = 1;
-  while (p < most && p < n) p *= 2;
-  return p;
-}
+constexpr int64_t kMaxBlocks = int64_t(1) << 31;
 
 // Threads across a row of `units` vectors, workgroups across it, and
-// workgroups in all for `rows` rows.
+// workgroups in all for `rows` rows. False if they do not fit 31 bits (far more
+// than memory holds).
 template <class Args>
-void cut_rows(Args& a, int64_t rows, int64_t units) {
-  a.lanes = pow2_at_least(units, 256);
-  a.slices = int32_t((units + a.lanes - 1) / a.lanes);
-  const int64_t per = 256 / a.lanes;
-  a.blocks = (rows + per - 1) / per * a.slices;
+bool cut_rows(Args& a, int64_t rows, int64_t units) {
+  a.lanes_log2 = 0;
+  while (a.lanes_log2 < 8 && (1 << a.lanes_log2) < units) ++a.lanes_log2;
+  const int64_t lanes = 1 << a.lanes_log2, per = 256 / lanes;
+  const int64_t slices = (units + lanes - 1) / lanes, blocks = (rows + per - 1) / per * slices;
+  a.slices = uint32_t(slices);
+  a.blocks = uint32_t(blocks);
+  return blocks < kMaxBlocks;
 }
 
 dim3 grid_for(int64_t blocks) { return dim3(uint32_t(std::min(blocks, kMaxGrid))); }
@@ -80,12 +79,11 @@ forge_status launch_sort(const IdSource& src, const EmbeddingWorkspace& ws, char
 template <int OP, bool BF16>
 forge_status launch_gradient_t(EmbeddingArgs a, hipStream_t s) {
   EmbeddingArgs b = a;
-  b.bound_blocks = (a.V + 256) / 256;
-  b.slices = (a.d / 4 + 255) / 256;
-  b.blocks = b.bound_blocks + a.T / kSumChunk * b.slices;
+  b.bound_blocks = uint32_t(a.V + 256) / 256;
+  b.slices = uint32_t(a.d / 4 + 255) / 256;
+  b.blocks = b.bound_blocks + uint32_t(a.T / kSumChunk) * b.slices;
   hipLaunchKernelGGL((embedding_bounds_kernel<BF16>), grid_for(b.blocks), dim3(256), 0, s, b);
   if (forge_status st = launch_status()) return st;
-  cut_rows(a, a.V, a.d / 4);
   hipLaunchKernelGGL((embedding_rows_kernel<OP, BF16>), grid_for(a.blocks), dim3(256), 0, s, a);
   return launch_status();
 }
@@ -95,6 +93,8 @@ forge_status launch_gradient(const void* ids, int32_t id_bytes, const void* dY, 
                              EmbeddingArgs a, void* workspace, void* stream) {
   if (forge_status s = check_device()) return s;
   (void)hipGetLastError();
+  if (!cut_rows(a, a.V, a.d / 4) || a.T / kSumChunk * (a.d / 1024 + 1) >= kMaxBlocks)
+    return FORGE_ERR_SHAPE;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const EmbeddingWorkspace ws = embedding_workspace(a.T, a.V, a.d);
   char* const base = static_cast<char*>(workspace);
@@ -144,7 +144,7 @@ FORGE_API forge_status forge_embedding(const void* table, forge_dtype table_dtyp
   a.T = T;
   a.d = int32_t(d);
   a.scale = float(scale);
-  cut_rows(a, T, d / 8);
+  if (!cut_rows(a, T, d / 8)) return FORGE_ERR_SHAPE;
   const bool tb = table_dtype == FORGE_BF16, ob = out_dtype == FORGE_BF16;
   const auto kernel = tb ? (ob ? embedding_kernel<true, true> : embedding_kernel<true, false>)
                          : (ob ? embedding_kernel<false, true> : embedding_kernel<false, false>);
