@@ -18,6 +18,8 @@ CASES = [
     (16384, 1000, 64, "zipf"), (16385, 1000, 64, "zipf"), (16384, 513, 8, "one"),
     (20000, 77, 128, "one"), (50001, 128256, 32, "zipf"), (70000, 70000, 16, "sorted"),
     (70000, 70000, 16, "reversed"), (300, 40, 4104, "none"), (40000, 600000, 8, "spread"),
+    (65536, 300, 8, "zipf"), (65537, 128256, 8, "zipf"), (262144, 5000, 8, "zipf"),
+    (262145, 128256, 8, "zipf"), (1000003, 999983, 8, "zipf"), (4097, 600, 64, "zipf"),
 ]
 
 

@@ -280,8 +280,8 @@ def test_embedding_workspace_sizes(lib):
         assert f(*bad) == 0
     assert f(0, 0, 0) >= 16
     need = f(4097, 1000, 64)
-    # keys and positions twice, two tiles' digit counts, bounds, 128 chunk sums
-    assert need >= 4 * 4 * 4097 + 2 * 512 * 4 + 4 * 1001 + 128 * 64 * 4
+    # keys and positions twice, five tiles' digit counts, bounds, 128 chunk sums
+    assert need >= 4 * 4 * 4097 + 5 * 512 * 4 + 4 * 1001 + 128 * 64 * 4
     assert f(1 << 30, 1 << 22, 1 << 22) > 0
 
 

@@ -27,14 +27,13 @@
 
 namespace forge {
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kDigitBits = 9;                        // largest digit of a pass
 constexpr int kDigits = 1 << kDigitBits;
-constexpr int kSortOneRounds = 16;                   // keys per thread of the one-workgroup sort
-constexpr int kSortOne = kSortThreads * kSortOneRounds;
-constexpr int kSortTileRounds = 4;                   // keys per thread of a tile of the larger sort
-constexpr int kSortTile = kSortThreads * kSortTileRounds;
+constexpr int kOneThreads = 1024;                    // the one-workgroup sort
+constexpr int kOneRounds = 4;                        // its keys per thread
+constexpr int kSortOne = kOneThreads * kOneRounds;
+constexpr int kTileThreads = 256;                    // a tile of the larger sort
+constexpr int kDirectTiles = 64;                     // tiles that sum their counts themselves
 constexpr int kSumChunk = 32;
 
 struct IdSource {
@@ -73,16 +72,17 @@ __device__ __forceinline__ void wave_order() {
   asm volatile("" ::: "memory");
 }
 
+template <int WAVES>
 struct SortLds {
-  uint32_t count[kSortWaves][kDigits];
-  uint32_t wave_total[kSortWaves];
+  uint32_t count[WAVES][kDigits];
+  uint32_t wave_total[WAVES];
 };
 
 // Ranks this wave's keys, `rounds` of 64 in ascending position: rank[j] is the
 // number of earlier keys of the wave with the same digit; count[wave] ends as
 // the wave's digit counts. The workgroup synchronises before and after.
-template <int R>
-__device__ __forceinline__ void rank_keys(SortLds& s, const uint32_t (&key)[R], uint32_t (&rank)[R],
+template <int WAVES, int R>
+__device__ __forceinline__ void rank_keys(SortLds<WAVES>& s, const uint32_t (&key)[R], uint32_t (&rank)[R],
                                           int rounds, int shift, int bits) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   for (int d = lane; d < (1 << bits); d += 64) s.count[wave][d] = 0;
@@ -103,8 +103,7 @@ __device__ __forceinline__ void rank_keys(SortLds& s, const uint32_t (&key)[R], 
   }
 }
 
-// Exclusive sum of one value per thread over the workgroup's first `n` threads
-// (a multiple of 64; the others pass 0).
+// Exclusive sum of one value per thread over the workgroup.
 __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* wave_total) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   uint32_t inc = v;
@@ -121,41 +120,38 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* wave_t
   return base + inc - v;
 }
 
-// Turns the waves' digit counts into each wave's first place per digit, from
-// `base(digit, total)`.
-template <class Base>
-__device__ __forceinline__ void place_waves(SortLds& s, int bits, const Base& base) {
-  const int d = threadIdx.x;
-  if (d < (1 << bits)) {
-    uint32_t at = base(d);
-    for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t c = s.count[w][d];
-      s.count[w][d] = at;
-      at += c;
-    }
+// Turns the waves' counts of digit d into each wave's first place, from `at` on.
+template <int WAVES>
+__device__ __forceinline__ void place_waves(SortLds<WAVES>& s, int d, uint32_t at) {
+  for (int w = 0; w < WAVES; ++w) {
+    const uint32_t c = s.count[w][d];
+    s.count[w][d] = at;
+    at += c;
   }
 }
 
-__device__ __forceinline__ uint32_t digit_total(const SortLds& s, int bits) {
+template <int WAVES>
+__device__ __forceinline__ uint32_t digit_total(const SortLds<WAVES>& s, int d) {
   uint32_t sum = 0;
-  if (int(threadIdx.x) < (1 << bits))
-    for (int w = 0; w < kSortWaves; ++w) sum += s.count[w][threadIdx.x];
+  for (int w = 0; w < WAVES; ++w) sum += s.count[w][d];
   return sum;
 }
 
-// Up to kSortOne tokens by one workgroup, in LDS.
-__global__ __launch_bounds__(kSortThreads) void sort_one_kernel(IdSource src, int T, int key_bits,
-                                                                uint32_t* keys, uint32_t* pos) {
-  __shared__ SortLds s;
+// Up to kSortOne tokens by one workgroup, in LDS (1021 tokens: 7.8 us).
+__global__ __launch_bounds__(kOneThreads) void sort_one_kernel(IdSource src, int T, int key_bits,
+                                                               uint32_t* keys, uint32_t* pos) {
+  constexpr int WAVES = kOneThreads / 64, R = kOneRounds;
+  __shared__ SortLds<WAVES> s;
   __shared__ uint32_t lk[kSortOne];
   __shared__ uint16_t lp[kSortOne];
   static_assert(kSortOne <= 65536, "positions are kept in 16 bits");
+  static_assert(kDigits <= kOneThreads, "a thread to a digit");
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int rounds = (T + kSortThreads - 1) / kSortThreads;
+  const int rounds = (T + kOneThreads - 1) / kOneThreads;
   const int first = wave * rounds * 64 + lane;
-  uint32_t key[kSortOneRounds], p[kSortOneRounds], rank[kSortOneRounds];
+  uint32_t key[R], p[R], rank[R];
 #pragma unroll
-  for (int j = 0; j < kSortOneRounds; ++j) {
+  for (int j = 0; j < R; ++j) {
     const int t = first + j * 64;
     // Past the last token: behind every key, in every pass.
     key[j] = j < rounds && t < T ? load_key(src, t) : 0xffffffffu;
@@ -166,12 +162,14 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(IdSource src, in
     const int shift = key_bits * k / passes, bits = key_bits * (k + 1) / passes - shift;
     rank_keys(s, key, rank, rounds, shift, bits);
     __syncthreads();
-    const uint32_t at = block_exclusive(digit_total(s, bits), s.wave_total);
-    place_waves(s, bits, [&](int) { return at; });
+    const int d = threadIdx.x;
+    const bool mine = d < (1 << bits);
+    const uint32_t at = block_exclusive(mine ? digit_total(s, d) : 0u, s.wave_total);
+    if (mine) place_waves(s, d, at);
     __syncthreads();
     const bool last = k + 1 == passes;
 #pragma unroll
-    for (int j = 0; j < kSortOneRounds; ++j) {
+    for (int j = 0; j < R; ++j) {
       if (j < rounds) {
         const uint32_t to = s.count[wave][(key[j] >> shift) & ((1u << bits) - 1u)] + rank[j];
         if (!last) {
@@ -186,7 +184,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(IdSource src, in
     if (!last) {
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kSortOneRounds; ++j)
+      for (int j = 0; j < R; ++j)
         if (j < rounds) {
           key[j] = lk[first + j * 64];
           p[j] = lp[first + j * 64];
@@ -196,23 +194,27 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(IdSource src, in
   }
 }
 
-// The larger sort: per pass, the tiles' digit counts, their sums, the scatter.
+// The larger sort, per pass: the digit counts of tiles of 256 R keys, and the
+// scatter. Up to kDirectTiles tiles, a tile adds up the counts that precede its
+// own itself (one launch less, and the counts come from L2); beyond, a launch
+// between the two turns them into places. R is 4 up to 65536 tokens (16384:
+// 21 us, where one workgroup took 38) and 16 beyond.
 // keys_in == nullptr: the first pass, from the ids.
 struct SortPass {
   IdSource src;
   const uint32_t *keys_in, *pos_in;
   uint32_t *keys_out, *pos_out;
-  uint32_t* count;     // [digits][tiles]
+  uint32_t* count;     // direct: [tiles][kDigits]; else [digits][tiles]
   int64_t T;
   int32_t tiles, shift, bits;
 };
 
-__device__ __forceinline__ void load_tile(const SortPass& a, uint32_t (&key)[kSortTileRounds],
-                                          uint32_t (&p)[kSortTileRounds]) {
+template <int R>
+__device__ __forceinline__ void load_tile(const SortPass& a, uint32_t (&key)[R], uint32_t (&p)[R]) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t first = int64_t(blockIdx.x) * kSortTile + wave * kSortTileRounds * 64 + lane;
+  const int64_t first = int64_t(blockIdx.x) * (kTileThreads * R) + wave * R * 64 + lane;
 #pragma unroll
-  for (int j = 0; j < kSortTileRounds; ++j) {
+  for (int j = 0; j < R; ++j) {
     const int64_t t = first + j * 64;
     const bool in = t < a.T;
     key[j] = !in ? 0xffffffffu : a.keys_in ? a.keys_in[t] : load_key(a.src, t);
@@ -220,22 +222,25 @@ __device__ __forceinline__ void load_tile(const SortPass& a, uint32_t (&key)[kSo
   }
 }
 
-__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortPass a) {
-  __shared__ SortLds s;
-  uint32_t key[kSortTileRounds], p[kSortTileRounds], rank[kSortTileRounds];
+template <int R, bool DIRECT>
+__global__ __launch_bounds__(kTileThreads) void sort_count_kernel(SortPass a) {
+  __shared__ SortLds<kTileThreads / 64> s;
+  uint32_t key[R], p[R], rank[R];
   load_tile(a, key, p);
-  rank_keys(s, key, rank, kSortTileRounds, a.shift, a.bits);
+  rank_keys(s, key, rank, R, a.shift, a.bits);
   __syncthreads();
-  const uint32_t total = digit_total(s, a.bits);
-  if (int(threadIdx.x) < (1 << a.bits)) a.count[int64_t(threadIdx.x) * a.tiles + blockIdx.x] = total;
+  for (int d = threadIdx.x; d < (1 << a.bits); d += kTileThreads) {
+    const int64_t at = DIRECT ? int64_t(blockIdx.x) * kDigits + d : int64_t(d) * a.tiles + blockIdx.x;
+    a.count[at] = digit_total(s, d);
+  }
 }
 
 // Exclusive sum of n counts, in place, by one workgroup.
-__global__ __launch_bounds__(kSortThreads) void sort_sum_kernel(uint32_t* count, int64_t n) {
-  __shared__ uint32_t wave_total[kSortWaves];
-  constexpr int E = 8;
+__global__ __launch_bounds__(kOneThreads) void sort_sum_kernel(uint32_t* count, int64_t n) {
+  constexpr int WAVES = kOneThreads / 64, E = 8;
+  __shared__ uint32_t wave_total[WAVES];
   uint32_t carry = 0;
-  for (int64_t k = 0; k < n; k += kSortThreads * E) {
+  for (int64_t k = 0; k < n; k += kOneThreads * E) {
     uint32_t v[E], sum = 0;
     const int64_t at = k + int64_t(threadIdx.x) * E;
 #pragma unroll
@@ -244,7 +249,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_sum_kernel(uint32_t* count,
       sum += v[j];
     }
     uint32_t before = carry + block_exclusive(sum, wave_total);
-    for (int w = 0; w < kSortWaves; ++w) carry += wave_total[w];
+    for (int w = 0; w < WAVES; ++w) carry += wave_total[w];
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < E; ++j) {
@@ -254,17 +259,47 @@ __global__ __launch_bounds__(kSortThreads) void sort_sum_kernel(uint32_t* count,
   }
 }
 
-__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortPass a) {
-  __shared__ SortLds s;
-  uint32_t key[kSortTileRounds], p[kSortTileRounds], rank[kSortTileRounds];
+template <int R, bool DIRECT>
+__global__ __launch_bounds__(kTileThreads) void sort_scatter_kernel(SortPass a) {
+  __shared__ SortLds<kTileThreads / 64> s;
+  uint32_t key[R], p[R], rank[R];
   load_tile(a, key, p);
-  rank_keys(s, key, rank, kSortTileRounds, a.shift, a.bits);
+  rank_keys(s, key, rank, R, a.shift, a.bits);
   __syncthreads();
-  place_waves(s, a.bits, [&](int d) { return a.count[int64_t(d) * a.tiles + blockIdx.x]; });
+  // A thread takes the digits 2 t and 2 t + 1.
+  static_assert(kDigits == 2 * kTileThreads, "two digits to a thread");
+  const int d = 2 * int(threadIdx.x);
+  const bool mine = d < (1 << a.bits);     // bits >= 1: both digits or none
+  uint32_t at[2] = {0u, 0u};
+  if constexpr (DIRECT) {
+    uint32_t total[2] = {0u, 0u};
+    if (mine) {
+#pragma unroll 8
+      for (int t = 0; t < a.tiles; ++t) {
+        const u32x2_t c = *reinterpret_cast<const u32x2_t*>(a.count + int64_t(t) * kDigits + d);
+        total[0] += c[0];
+        total[1] += c[1];
+        if (t < int(blockIdx.x)) {
+          at[0] += c[0];
+          at[1] += c[1];
+        }
+      }
+    }
+    const uint32_t base = block_exclusive(total[0] + total[1], s.wave_total);
+    at[0] += base;
+    at[1] += base + total[0];
+  } else if (mine) {
+    at[0] = a.count[int64_t(d) * a.tiles + blockIdx.x];
+    at[1] = a.count[int64_t(d + 1) * a.tiles + blockIdx.x];
+  }
+  if (mine) {
+    place_waves(s, d, at[0]);
+    place_waves(s, d + 1, at[1]);
+  }
   __syncthreads();
   const int wave = threadIdx.x >> 6;
 #pragma unroll
-  for (int j = 0; j < kSortTileRounds; ++j) {
+  for (int j = 0; j < R; ++j) {
     const uint32_t to = s.count[wave][(key[j] >> a.shift) & ((1u << a.bits) - 1u)] + rank[j];
     if (int64_t(to) < a.T) {       // keys past the last token come last
       a.keys_out[to] = key[j];
@@ -299,18 +334,27 @@ __device__ __forceinline__ f32x4_t load_dy4(const void* dY, int64_t i) {
     return *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(dY) + i);
 }
 
-// acc += the tokens at sorted places [s, e), in order, four loads in flight.
+// acc += term(s) + ... + term(e - 1), one after the other, eight loads in flight.
+template <class Term>
+__device__ __forceinline__ void add_terms(f32x4_t& acc, uint32_t s, uint32_t e, const Term& term) {
+  constexpr int U = 8;
+  for (; s + U <= e; s += U) {
+    f32x4_t r[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) r[j] = term(s + j);
+#pragma unroll
+    for (int j = 0; j < U; ++j) acc = acc + r[j];
+  }
+  for (; s < e; ++s) acc = acc + term(s);
+}
+
+// acc += the tokens at sorted places [s, e).
 template <bool BF16>
 __device__ __forceinline__ void add_tokens(const EmbeddingArgs& a, f32x4_t& acc, uint32_t s,
                                            uint32_t e, int col) {
-  for (; s + 4 <= e; s += 4) {
-    f32x4_t r[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = load_dy4<BF16>(a.dY, int64_t(a.pos[s + j]) * a.d + col);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc = acc + r[j];
-  }
-  for (; s < e; ++s) acc = acc + load_dy4<BF16>(a.dY, int64_t(a.pos[s]) * a.d + col);
+  add_terms(acc, s, e, [&](uint32_t k) {
+    return load_dy4<BF16>(a.dY, int64_t(a.pos[k]) * a.d + col);
+  });
 }
 
 // The rows' bounds (the first workgroups, one row per thread), and the sums of
@@ -376,8 +420,9 @@ __global__ __launch_bounds__(256) void embedding_rows_kernel(EmbeddingArgs a) {
     const uint32_t c0 = (s + kSumChunk - 1) / kSumChunk, c1 = e / kSumChunk;
     if (c0 < c1) {
       add_tokens<BF16>(a, g, s, c0 * kSumChunk, col);
-      for (uint32_t c = c0; c < c1; ++c)
-        g = g + *reinterpret_cast<const f32x4_t*>(a.chunk + int64_t(c) * a.d + col);
+      add_terms(g, c0, c1, [&](uint32_t c) {
+        return *reinterpret_cast<const f32x4_t*>(a.chunk + int64_t(c) * a.d + col);
+      });
       add_tokens<BF16>(a, g, c1 * kSumChunk, e, col);
     } else {
       add_tokens<BF16>(a, g, s, e, col);

@@ -35,6 +35,20 @@ int bits_for(int64_t largest) {
   return b;
 }
 
+template <int R, bool DIRECT>
+forge_status launch_sort_pass(const SortPass& p, hipStream_t s) {
+  const dim3 grid(p.tiles), threads(kTileThreads);
+  hipLaunchKernelGGL((sort_count_kernel<R, DIRECT>), grid, threads, 0, s, p);
+  if (forge_status st = launch_status()) return st;
+  if (!DIRECT) {
+    hipLaunchKernelGGL(sort_sum_kernel, dim3(1), dim3(kOneThreads), 0, s, p.count,
+                       int64_t(p.tiles) << p.bits);
+    if (forge_status st = launch_status()) return st;
+  }
+  hipLaunchKernelGGL((sort_scatter_kernel<R, DIRECT>), grid, threads, 0, s, p);
+  return launch_status();
+}
+
 // Sorts the tokens by row into a.keys, a.pos.
 forge_status launch_sort(const IdSource& src, const EmbeddingWorkspace& ws, char* base, int64_t T,
                          EmbeddingArgs& a, hipStream_t s) {
@@ -46,16 +60,18 @@ forge_status launch_sort(const IdSource& src, const EmbeddingWorkspace& ws, char
   a.pos = pos[0];
   const int key_bits = bits_for(src.V);
   if (T <= kSortOne) {
-    hipLaunchKernelGGL(sort_one_kernel, dim3(1), dim3(kSortThreads), 0, s, src, int(T), key_bits,
+    hipLaunchKernelGGL(sort_one_kernel, dim3(1), dim3(kOneThreads), 0, s, src, int(T), key_bits,
                        keys[0], pos[0]);
     return launch_status();
   }
   const int passes = (key_bits + kDigitBits - 1) / kDigitBits;
+  const int64_t small = kTileThreads * 4, large = kTileThreads * 16;
+  const int64_t tile = T <= small * kDirectTiles ? small : large;
   SortPass p{};
   p.src = src;
   p.count = reinterpret_cast<uint32_t*>(base + ws.count);
   p.T = T;
-  p.tiles = int32_t((T + kSortTile - 1) / kSortTile);
+  p.tiles = int32_t((T + tile - 1) / tile);
   for (int k = 0; k < passes; ++k) {
     p.keys_in = k ? keys[(k - 1) & 1] : nullptr;
     p.pos_in = k ? pos[(k - 1) & 1] : nullptr;
@@ -63,13 +79,10 @@ forge_status launch_sort(const IdSource& src, const EmbeddingWorkspace& ws, char
     p.pos_out = pos[k & 1];
     p.shift = key_bits * k / passes;
     p.bits = key_bits * (k + 1) / passes - p.shift;
-    hipLaunchKernelGGL(sort_count_kernel, dim3(p.tiles), dim3(kSortThreads), 0, s, p);
-    if (forge_status st = launch_status()) return st;
-    hipLaunchKernelGGL(sort_sum_kernel, dim3(1), dim3(kSortThreads), 0, s, p.count,
-                       int64_t(p.tiles) << p.bits);
-    if (forge_status st = launch_status()) return st;
-    hipLaunchKernelGGL(sort_scatter_kernel, dim3(p.tiles), dim3(kSortThreads), 0, s, p);
-    if (forge_status st = launch_status()) return st;
+    const forge_status st = tile == small              ? launch_sort_pass<4, true>(p, s)
+                            : p.tiles <= kDirectTiles ? launch_sort_pass<16, true>(p, s)
+                                                      : launch_sort_pass<16, false>(p, s);
+    if (st) return st;
   }
   a.keys = p.keys_out;
   a.pos = p.pos_out;
