@@ -36,6 +36,12 @@ struct MxLaunch {
   }
 };
 
+template <bool BF16>
+void (*quantize_kernel(const QuantArgs& a))(QuantArgs) {
+  if (!a.row_codes) return quantize_mxfp4_kernel<BF16, false, true>;
+  return a.col_codes ? quantize_mxfp4_kernel<BF16, true, true> : quantize_mxfp4_kernel<BF16, true, false>;
+}
+
 }  // namespace
 }  // namespace forge
 
@@ -65,7 +71,7 @@ FORGE_API forge_status forge_quantize_mxfp4(const void* x, forge_dtype x_dtype, 
   a.tiles_c = int32_t((C + kQuantTile - 1) / kQuantTile);
   a.tiles = (R + kQuantTile - 1) / kQuantTile * a.tiles_c;
   const dim3 grid(uint32_t(std::min<int64_t>(a.tiles, int64_t(1) << 22)));
-  const auto kernel = x_dtype == FORGE_BF16 ? quantize_mxfp4_kernel<true> : quantize_mxfp4_kernel<false>;
+  const auto kernel = x_dtype == FORGE_BF16 ? quantize_kernel<true>(a) : quantize_kernel<false>(a);
   hipLaunchKernelGGL(kernel, grid, dim3(256), 0, static_cast<hipStream_t>(stream), a);
   return launch_status();
 }

@@ -74,36 +74,41 @@ __device__ __forceinline__ uint32_t abs_bits(float x) {
 // LDS: a row is 128 float32 or 64 words of two bf16; word w of row r is kept at
 // w ^ 16 (r / 32 mod 4), which puts the four blocks of 16 neighbouring words,
 // read by one wave at a time, on 64 different banks.
-template <bool BF16>
+template <bool BF16, bool ROWS, bool COLS>
 __global__ __launch_bounds__(256) void quantize_mxfp4_kernel(QuantArgs a) {
   constexpr int WPR = BF16 ? 64 : 128;       // words of a row
-  __shared__ __attribute__((aligned(16))) uint32_t lds[kQuantTile * WPR];
+  constexpr int L = BF16 ? 1 : 2;            // 16-byte loads of 8 columns
+  __shared__ __attribute__((aligned(16))) uint32_t lds[COLS ? kQuantTile * WPR : 4];
   const int tid = threadIdx.x;
   for (int64_t b = blockIdx.x; b < a.tiles; b += gridDim.x) {
     const int64_t tr = b / a.tiles_c;
     const int64_t r0 = tr * kQuantTile, c0 = (b - tr * a.tiles_c) * kQuantTile;
     const int j = tid & 15;
     const int64_t col = c0 + 8 * j;
+    u32x4_t raw[8][L];
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      const int64_t row = r0 + it * 16 + (tid >> 4);
+      const bool in = row < a.R && col < a.C;
+      const u32x4_t* p = reinterpret_cast<const u32x4_t*>(
+          static_cast<const char*>(a.x) + (row * a.C + col) * (BF16 ? 2 : 4));
+#pragma unroll
+      for (int k = 0; k < L; ++k)
+        raw[it][k] = in ? __builtin_nontemporal_load(p + k) : u32x4_t{0u, 0u, 0u, 0u};
+    }
 #pragma unroll
     for (int it = 0; it < 8; ++it) {
       const int r = it * 16 + (tid >> 4);
-      const int64_t row = r0 + r;
-      f32x4_t lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
-      u32x4_t raw = {0u, 0u, 0u, 0u};
-      if (row < a.R && col < a.C) {
+      if constexpr (ROWS) {
+        const int64_t row = r0 + r;
+        f32x4_t lo, hi;
         if constexpr (BF16) {
-          raw = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.x) + row * a.C + col);
+          lo = unpack_bf16x4(u32x2_t{raw[it][0][0], raw[it][0][1]});
+          hi = unpack_bf16x4(u32x2_t{raw[it][0][2], raw[it][0][3]});
         } else {
-          const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.x) + row * a.C + col);
-          lo = p[0];
-          hi = p[1];
+          lo = __builtin_bit_cast(f32x4_t, raw[it][0]);
+          hi = __builtin_bit_cast(f32x4_t, raw[it][L - 1]);
         }
-      }
-      if constexpr (BF16) {
-        lo = unpack_bf16x4(u32x2_t{raw[0], raw[1]});
-        hi = unpack_bf16x4(u32x2_t{raw[2], raw[3]});
-      }
-      if (a.row_codes) {
         uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) top = max(top, max(abs_bits(lo[k]), abs_bits(hi[k])));
@@ -117,17 +122,14 @@ __global__ __launch_bounds__(256) void quantize_mxfp4_kernel(QuantArgs a) {
             a.row_scales[((c0 / kQuantTile) * a.R + row) * 4 + (j >> 2)] = uint8_t(s);
         }
       }
-      if (a.col_codes) {
+      if constexpr (COLS) {
         const int swz = ((r >> 5) & 3) << 4;
-        if constexpr (BF16) {
-          *reinterpret_cast<u32x4_t*>(&lds[r * WPR + ((4 * j) ^ swz)]) = raw;
-        } else {
-          *reinterpret_cast<f32x4_t*>(&lds[r * WPR + ((8 * j) ^ swz)]) = lo;
-          *reinterpret_cast<f32x4_t*>(&lds[r * WPR + ((8 * j + 4) ^ swz)]) = hi;
-        }
+#pragma unroll
+        for (int k = 0; k < L; ++k)
+          *reinterpret_cast<u32x4_t*>(&lds[r * WPR + ((4 * L * j + 4 * k) ^ swz)]) = raw[it][k];
       }
     }
-    if (!a.col_codes) continue;
+    if constexpr (!COLS) continue;
     __syncthreads();
     // Thread: block `blk` of word column `w` (two columns of x for bf16).
     const int blk = tid & 3;
