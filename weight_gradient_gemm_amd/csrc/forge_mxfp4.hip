@@ -68,11 +68,16 @@ FORGE_API forge_status forge_quantize_mxfp4(const void* x, forge_dtype x_dtype, 
   a.C = C;
   a.row_pitch = FORGE_MXFP4_K(C) / 2;
   a.col_pitch = FORGE_MXFP4_K(R) / 2;
-  a.tiles_c = int32_t((C + kQuantTile - 1) / kQuantTile);
-  a.tiles = (R + kQuantTile - 1) / kQuantTile * a.tiles_c;
-  const dim3 grid(uint32_t(std::min<int64_t>(a.tiles, int64_t(1) << 22)));
+  // Padding columns of the codes along rows belong to tiles too.
+  const int64_t tc = x_dtype == FORGE_BF16 ? kQuantCols<true> : kQuantCols<false>;
+  const int64_t across = ((row_codes ? FORGE_MXFP4_K(C) : C) + tc - 1) / tc;
+  const int64_t tiles = (R + kQuantRows - 1) / kQuantRows * across;
+  if (tiles >= int64_t(1) << 31) return FORGE_ERR_SHAPE;
+  a.tiles_c = uint32_t(across);
+  a.tiles = uint32_t(tiles);
+  const dim3 grid(std::min(a.tiles, kQuantGrid));
   const auto kernel = x_dtype == FORGE_BF16 ? quantize_kernel<true>(a) : quantize_kernel<false>(a);
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, static_cast<hipStream_t>(stream), a);
+  hipLaunchKernelGGL(kernel, grid, dim3(kQuantThreads), 0, static_cast<hipStream_t>(stream), a);
   return launch_status();
 }
 

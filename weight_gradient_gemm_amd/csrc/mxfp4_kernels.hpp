@@ -27,141 +27,175 @@ struct QuantArgs {
   uint8_t *row_codes, *row_scales, *col_codes, *col_scales;
   int64_t R, C;
   int64_t row_pitch, col_pitch;    // bytes of a row of codes
-  int32_t tiles_c;                 // tiles of 128 columns
-  int64_t tiles;
+  uint32_t tiles_c;                // tiles across
+  uint32_t tiles;
 };
 
-constexpr int kQuantTile = 128;
+constexpr int kQuantRows = 128;    // a tile: 128 rows of kQuantWords words (2 bf16 or 1 float32)
+constexpr int kQuantWords = 128;
+constexpr int kQuantThreads = 4 * kQuantWords;
+constexpr uint32_t kQuantGrid = 2048;        // most workgroups of a launch
+template <bool BF16>
+constexpr int kQuantCols = BF16 ? 2 * kQuantWords : kQuantWords;
 
-// The scale byte of a block from the largest magnitude's float32 bits: its
-// biased exponent less 2 (so that the largest lands in [4, 8), the top two
-// codes' range), at least 0; 255 for a NaN or an infinity.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
-  const uint32_t e = amax_bits >> 23;
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+// The scale byte of a block from its largest magnitude's biased exponent: 2
+// less (so that the largest lands in [4, 8), the top two codes' range), at least
+// 0; 255 for a NaN or an infinity.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t e) {
   return e == 255u ? 255u : e > 2u ? e - 2u : 0u;
 }
 
-// 8 values to 8 codes (the first in the low half of the first byte), rounded
+// 4 values to 4 codes (the first in the low half of the first byte), rounded
 // to nearest even and saturated by the conversion instruction. It takes the
 // scale as a float32 power of two; blocks whose scale (or values) come near
 // float32's denormals are multiplied by 2^64 first, exactly.
-__device__ __forceinline__ uint32_t codes8(const f32x4_t& lo, const f32x4_t& hi, uint32_t s) {
-  if (s == 255u) return 0u;
-  uint32_t r = 0;
-  f32x4_t a = lo, b = hi;
+__device__ __forceinline__ uint32_t codes4(const f32x4_t& x, uint32_t s) {
+  f32x4_t a = x;
   uint32_t e = s;
   if (s < 32u) {
     a = a * 0x1p64f;
-    b = b * 0x1p64f;
     e = s + 64u;
   }
   const float scale = __builtin_bit_cast(float, e << 23);
+  uint32_t r = 0;
   r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, a[0], a[1], scale, 0);
   r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, a[2], a[3], scale, 1);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, b[0], b[1], scale, 2);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, b[2], b[3], scale, 3);
-  return r;
+  return s == 255u ? 0u : r;
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float x) {
-  return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+// 8 codes from 8 bf16 values in four words, the earlier one in the low half.
+__device__ __forceinline__ uint32_t codes8(const uint32_t (&w)[4], uint32_t s) {
+  if (s < 32u)
+    return codes4(unpack_bf16x4(u32x2_t{w[0], w[1]}), s) |
+           codes4(unpack_bf16x4(u32x2_t{w[2], w[3]}), s) << 16;
+  const float scale = __builtin_bit_cast(float, s << 23);
+  uint32_t r = 0;
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2_t, w[0]), scale, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2_t, w[1]), scale, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2_t, w[2]), scale, 2);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2_t, w[3]), scale, 3);
+  return s == 255u ? 0u : r;
 }
 
-// One 128 x 128 tile of x per workgroup. Loads are row-major, 8 columns to a
-// thread, which is what the codes along rows need (4 lanes share a block); the
-// codes along columns are formed from a copy of the tile in LDS, one 32-row
-// block of a column (of a pair of columns for bf16) to a thread.
-// LDS: a row is 128 float32 or 64 words of two bf16; word w of row r is kept at
-// w ^ 16 (r / 32 mod 4), which puts the four blocks of 16 neighbouring words,
-// read by one wave at a time, on 64 different banks.
+__device__ __forceinline__ uint32_t abs_bits(uint32_t x) { return x & 0x7fffffffu; }
+// The larger magnitude's bits in each half.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t top, uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(
+      __builtin_bit_cast(u16x2_t, top), __builtin_bit_cast(u16x2_t, w & 0x7fff7fffu)));
+}
+
+// A workgroup goes from tile to tile. Loads are row-major, 16 bytes (8 bf16 or
+// 4 float32 columns) to a thread, which is what the codes along rows need (4 or
+// 8 lanes share a block); the codes along columns are formed from a copy of the
+// tile in LDS, one 32-row block of a word's column (a pair of columns for bf16)
+// to a thread. Word w of row r is kept at w ^ 16 (r / 32 mod 4), which puts the
+// four blocks of 16 neighbouring words, read by one wave at a time, on 64
+// different banks. The next tile's loads are in flight while a tile's codes
+// along columns are formed and stored.
+//
+// Bound by HBM. bf16 8192 x 14336: 55 us by columns (297 MB, 5.4 TB/s), 52 by
+// rows, 70 for both (360 MB); float32 4096 x 14336 48 us by columns (60 when a
+// thread's two loads were neighbours instead of a wave's). Rows of 64 words and
+// 32 KB of LDS: 61 and 52 us.
 template <bool BF16, bool ROWS, bool COLS>
-__global__ __launch_bounds__(256) void quantize_mxfp4_kernel(QuantArgs a) {
-  constexpr int WPR = BF16 ? 64 : 128;       // words of a row
-  constexpr int L = BF16 ? 1 : 2;            // 16-byte loads of 8 columns
-  __shared__ __attribute__((aligned(16))) uint32_t lds[COLS ? kQuantTile * WPR : 4];
+__global__ __launch_bounds__(kQuantThreads) void quantize_mxfp4_kernel(QuantArgs a) {
+  constexpr int WPR = kQuantWords;
+  constexpr int TC = kQuantCols<BF16>;
+  constexpr int CPT = BF16 ? 8 : 4;          // columns of a load
+  constexpr int TPR = WPR / 4;               // threads of a row
+  constexpr int RPI = kQuantThreads / TPR, NIT = kQuantRows / RPI;
+  __shared__ __attribute__((aligned(16))) uint32_t lds[COLS ? kQuantRows * WPR : 4];
   const int tid = threadIdx.x;
-  for (int64_t b = blockIdx.x; b < a.tiles; b += gridDim.x) {
-    const int64_t tr = b / a.tiles_c;
-    const int64_t r0 = tr * kQuantTile, c0 = (b - tr * a.tiles_c) * kQuantTile;
-    const int j = tid & 15;
-    const int64_t col = c0 + 8 * j;
-    u32x4_t raw[8][L];
+  const int j = tid % TPR, rt = tid / TPR;
+  u32x4_t raw[NIT];
+  auto load = [&](uint32_t b) {
+    const uint32_t tr = b / a.tiles_c;
+    const int64_t col = int64_t(b - tr * a.tiles_c) * TC + CPT * j;
 #pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      const int64_t row = r0 + it * 16 + (tid >> 4);
-      const bool in = row < a.R && col < a.C;
-      const u32x4_t* p = reinterpret_cast<const u32x4_t*>(
-          static_cast<const char*>(a.x) + (row * a.C + col) * (BF16 ? 2 : 4));
-#pragma unroll
-      for (int k = 0; k < L; ++k)
-        raw[it][k] = in ? __builtin_nontemporal_load(p + k) : u32x4_t{0u, 0u, 0u, 0u};
+    for (int it = 0; it < NIT; ++it) {
+      const int64_t row = int64_t(tr) * kQuantRows + it * RPI + rt;
+      const u32x4_t* p = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.x) +
+                                                          (row * a.C + col) * (BF16 ? 2 : 4));
+      raw[it] = row < a.R && col < a.C ? __builtin_nontemporal_load(p) : u32x4_t{0u, 0u, 0u, 0u};
     }
+  };
+  load(blockIdx.x);
+  for (uint32_t b = blockIdx.x; b < a.tiles; b += gridDim.x) {
+    const uint32_t tr = b / a.tiles_c;
+    const int64_t r0 = int64_t(tr) * kQuantRows, c0 = int64_t(b - tr * a.tiles_c) * TC;
+    const int64_t col = c0 + CPT * j;
 #pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      const int r = it * 16 + (tid >> 4);
+    for (int it = 0; it < NIT; ++it) {
+      const int r = it * RPI + rt;
+      if constexpr (COLS)
+        *reinterpret_cast<u32x4_t*>(&lds[r * WPR + ((4 * j) ^ (((r >> 5) & 3) << 4))]) = raw[it];
       if constexpr (ROWS) {
         const int64_t row = r0 + r;
-        f32x4_t lo, hi;
-        if constexpr (BF16) {
-          lo = unpack_bf16x4(u32x2_t{raw[it][0][0], raw[it][0][1]});
-          hi = unpack_bf16x4(u32x2_t{raw[it][0][2], raw[it][0][3]});
-        } else {
-          lo = __builtin_bit_cast(f32x4_t, raw[it][0]);
-          hi = __builtin_bit_cast(f32x4_t, raw[it][L - 1]);
-        }
         uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) top = max(top, max(abs_bits(lo[k]), abs_bits(hi[k])));
+        for (int k = 0; k < 4; ++k)
+          top = BF16 ? max_abs2(top, raw[it][k]) : max(top, abs_bits(raw[it][k]));
+        if constexpr (BF16) top = max(top & 0xffffu, top >> 16) << 16;
         top = max(top, uint32_t(__shfl_xor(int(top), 1)));
         top = max(top, uint32_t(__shfl_xor(int(top), 2)));
-        const uint32_t s = scale_byte(top);
-        const uint32_t codes = codes8(lo, hi, s);
-        if (row < a.R) {
-          *reinterpret_cast<uint32_t*>(a.row_codes + row * a.row_pitch + c0 / 2 + 4 * j) = codes;
-          if ((j & 3) == 0)
-            a.row_scales[((c0 / kQuantTile) * a.R + row) * 4 + (j >> 2)] = uint8_t(s);
+        if constexpr (!BF16) top = max(top, uint32_t(__shfl_xor(int(top), 4)));
+        const uint32_t s = scale_byte(top >> 23);
+        if (row < a.R && col < 2 * a.row_pitch) {
+          uint8_t* const out = a.row_codes + row * a.row_pitch + col / 2;
+          if constexpr (BF16) {
+            const uint32_t w[4] = {raw[it][0], raw[it][1], raw[it][2], raw[it][3]};
+            *reinterpret_cast<uint32_t*>(out) = codes8(w, s);
+          } else {
+            *reinterpret_cast<uint16_t*>(out) = uint16_t(codes4(__builtin_bit_cast(f32x4_t, raw[it]), s));
+          }
+          if (j % (32 / CPT) == 0)
+            a.row_scales[((col >> 7) * a.R + row) * 4 + ((col >> 5) & 3)] = uint8_t(s);
         }
-      }
-      if constexpr (COLS) {
-        const int swz = ((r >> 5) & 3) << 4;
-#pragma unroll
-        for (int k = 0; k < L; ++k)
-          *reinterpret_cast<u32x4_t*>(&lds[r * WPR + ((4 * L * j + 4 * k) ^ swz)]) = raw[it][k];
       }
     }
+    if (a.tiles - b > gridDim.x) load(b + gridDim.x);
     if constexpr (!COLS) continue;
     __syncthreads();
-    // Thread: block `blk` of word column `w` (two columns of x for bf16).
-    const int blk = tid & 3;
+    // Thread: block `blk` of word column `w`.
+    const int blk = tid & 3, w = tid >> 2;
+    uint32_t v[32], top = 0;
 #pragma unroll
-    for (int w = tid >> 2; w < WPR; w += 64) {
-      constexpr int NC = BF16 ? 2 : 1;
-      float v[NC][32];
-      uint32_t top[NC] = {};
+    for (int i = 0; i < 32; ++i) {
+      v[i] = lds[(blk * 32 + i) * WPR + (w ^ (blk << 4))];
+      top = BF16 ? max_abs2(top, v[i]) : max(top, abs_bits(v[i]));
+    }
+    constexpr int NC = BF16 ? 2 : 1;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const uint32_t word = lds[(blk * 32 + i) * WPR + (w ^ (blk << 4))];
-        if constexpr (BF16) {
-          v[0][i] = __builtin_bit_cast(float, word << 16);
-          v[1][i] = __builtin_bit_cast(float, word & 0xffff0000u);
-        } else {
-          v[0][i] = __builtin_bit_cast(float, word);
-        }
-#pragma unroll
-        for (int c = 0; c < NC; ++c) top[c] = max(top[c], abs_bits(v[c][i]));
-      }
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int64_t column = c0 + w * NC + c;
-        if (column >= a.C) continue;
-        const uint32_t s = scale_byte(top[c]);
+    for (int c = 0; c < NC; ++c) {
+      const int64_t column = c0 + w * NC + c;
+      if (column < a.C) {
+        const uint32_t s = scale_byte(BF16 ? (top >> (16 * c + 7)) & 255u : top >> 23);
         u32x4_t out;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          out[k] = codes8(f32x4_t{v[c][8 * k], v[c][8 * k + 1], v[c][8 * k + 2], v[c][8 * k + 3]},
-                          f32x4_t{v[c][8 * k + 4], v[c][8 * k + 5], v[c][8 * k + 6], v[c][8 * k + 7]}, s);
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (BF16) {
+            uint32_t pair[4];                // the column's values of two rows in a word
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t e = v[8 * k + 2 * q], o = v[8 * k + 2 * q + 1];
+              pair[q] = c == 0 ? (e & 0xffffu) | (o << 16) : (e >> 16) | (o & 0xffff0000u);
+            }
+            out[k] = codes8(pair, s);
+          } else {
+            f32x4_t lo, hi;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              lo[q] = __builtin_bit_cast(float, v[8 * k + q]);
+              hi[q] = __builtin_bit_cast(float, v[8 * k + 4 + q]);
+            }
+            out[k] = codes4(lo, s) | codes4(hi, s) << 16;
+          }
+        }
         *reinterpret_cast<u32x4_t*>(a.col_codes + column * a.col_pitch + r0 / 2 + 16 * blk) = out;
-        a.col_scales[((r0 / kQuantTile) * a.C + column) * 4 + blk] = uint8_t(s);
+        a.col_scales[(int64_t(tr) * a.C + column) * 4 + blk] = uint8_t(s);
       }
     }
     __syncthreads();                         // the next tile reuses the LDS
