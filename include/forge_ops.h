@@ -168,15 +168,16 @@ FORGE_API forge_status forge_embedding_sgdm(const void* ids, int32_t id_bytes, c
  * (NaN), and every value of it is NaN.
  *
  * An operand of R rows and K columns, with Kp = FORGE_MXFP4_K(K):
- *   codes  [R, Kp / 2] bytes, the even column in the low half of a byte;
+ *   codes  [Kp / 128, R, 64] bytes: entry (g, r) holds row r's columns
+ *          128 g .. 128 g + 127, the even one in the low half of a byte;
  *   scales [Kp / 128, R, 4] bytes: byte b of entry (g, r) is the scale of
  *          row r's columns 128 g + 32 b .. + 31.
  * Columns K .. Kp - 1 hold zero codes.
  */
 #define FORGE_MXFP4_K(K) (((int64_t)(K) + 127) / 128 * 128)
 
-/* Largest padded contraction length. */
-#define FORGE_MXFP4_MAX_K 8388608
+/* Largest padded contraction length; an operand has at most 2^22 rows. */
+#define FORGE_MXFP4_MAX_K 1073741824
 
 /*
  * Quantises x [R, C] (x_dtype FORGE_F32 or FORGE_BF16) into either or both of

@@ -45,6 +45,7 @@ def reference(torch, x):
 def decode(torch, operand):
     """The values of an operand, and its scale bytes by row and block."""
     codes, scales = (t.cpu() for t in operand)
+    codes = codes.permute(1, 0, 2).reshape(codes.shape[1], -1)
     R, half = codes.shape
     table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
     table = torch.cat([table, -table])
@@ -248,7 +249,7 @@ def test_wgrad_adamw(env, T, d_in, d_out):
     wg.forge_quantize_mxfp4(X, cols=xo)
     wg.forge_quantize_mxfp4(dY, cols=yo)
     # an output count that is no multiple of 8: the operand's first rows
-    yo = (yo[0][:d_out].contiguous(), yo[1][:, :d_out].contiguous())
+    yo = (yo[0][:, :d_out].contiguous(), yo[1][:, :d_out].contiguous())
     W, m = torch.randn(d_out, d_in, device="cuda"), torch.randn(d_out, d_in, device="cuda")
     v = torch.rand(d_out, d_in, device="cuda") + 0.1
     grad = torch.empty(d_out, d_in, device="cuda")

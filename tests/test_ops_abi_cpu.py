@@ -321,8 +321,10 @@ def wgrad_mx(lib, xc=A, xs=B, yc=C, ys=D, W=E, m=F, v=G, K=256, d_in=64, d_out=4
     (dict(dt=2), E_DTYPE), (dict(x=NULL), E_NULL), (dict(rc=NULL), E_NULL), (dict(rs=NULL), E_NULL),
     (dict(cc=NULL), E_NULL), (dict(cs=NULL), E_NULL),
     (dict(rc=NULL, rs=NULL, cc=NULL, cs=NULL), E_NULL),
-    (dict(R=-1), E_SHAPE), (dict(C=-8), E_SHAPE), (dict(C=(1 << 23) + 8), E_SHAPE),
-    (dict(R=(1 << 23) + 1), E_SHAPE), (dict(R=(1 << 22) + 1), E_SHAPE),
+    (dict(R=-1), E_SHAPE), (dict(C=-8), E_SHAPE), (dict(C=(1 << 22) + 8), E_SHAPE),
+    (dict(R=(1 << 30) + 1), E_SHAPE), (dict(R=(1 << 22) + 1), E_SHAPE),
+    (dict(R=(1 << 30) + 1, rc=NULL, rs=NULL), E_SHAPE),
+    (dict(C=(1 << 30) + 8, cc=NULL, cs=NULL), E_SHAPE),
     (dict(C=100), E_ALIGN), (dict(x=A + 8), E_ALIGN), (dict(rc=B + 4), E_ALIGN),
     (dict(rs=C + 1), E_ALIGN), (dict(cc=D + 2), E_ALIGN), (dict(cs=E + 8), E_ALIGN),
     (dict(rc=A), E_ALIAS), (dict(cs=A + 100 * 256 * 2 - 16), E_ALIAS), (dict(rs=B + 16), E_ALIAS),
@@ -334,7 +336,7 @@ def test_quantize_rejects(lib, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(K=-128), E_SHAPE), (dict(K=(1 << 23) + 128), E_SHAPE), (dict(K=100), E_ALIGN),
+    (dict(K=-128), E_SHAPE), (dict(K=(1 << 30) + 128), E_SHAPE), (dict(K=100), E_ALIGN),
     (dict(tile=5), E_TILE), (dict(tile=-1), E_TILE), (dict(K=130), E_ALIGN),
 ])
 def test_products_reject(lib, kw, status):
@@ -382,5 +384,5 @@ def test_mxfp4_operand_shapes():
     import weight_gradient_gemm_amd as wg
     for rows, k, groups in ((3, 0, 0), (3, 1, 1), (5, 128, 1), (5, 129, 2), (8, 1000, 8)):
         codes, scales = wg.forge_mxfp4_empty(rows, k, device="cpu")
-        assert tuple(codes.shape) == (rows, groups * 64)
+        assert tuple(codes.shape) == (groups, rows, 64)
         assert tuple(scales.shape) == (groups, rows, 4)

@@ -305,14 +305,14 @@ def forge_embedding_sgdm(ids, dY, W, mom, *, scale=1.0, lr=1e-3, momentum=0.9, w
 # --------------------------------------------------------------------------
 def forge_mxfp4_empty(rows, k, device=None):
     """(codes, scales), uninitialised, of an operand of `rows` rows and
-    contraction length k: uint8 [rows, Kp / 2] and [Kp / 128, rows, 4], Kp the
-    next multiple of 128. Both are views of one allocation."""
+    contraction length k: uint8 [Kp / 128, rows, 64] and [Kp / 128, rows, 4],
+    Kp the next multiple of 128. Both are views of one allocation."""
     torch = _torch()
     rows, groups = int(rows), (int(k) + 127) // 128
     n = groups * 64 * rows
     buf = torch.empty(n + groups * 4 * rows, dtype=torch.uint8,
                       device="cuda" if device is None else device)
-    return buf[:n].view(rows, groups * 64), buf[n:].view(groups, rows, 4)
+    return buf[:n].view(groups, rows, 64), buf[n:].view(groups, rows, 4)
 
 
 def _operand(torch, cur, pair, name):
@@ -320,11 +320,12 @@ def _operand(torch, cur, pair, name):
     codes, scales = pair
     cp = _in(codes, torch.uint8, f"{name} codes", cur)
     sp = _in(scales, torch.uint8, f"{name} scales", cur)
-    rows, half = _two(codes, f"{name} codes")
-    if half % 64:
-        raise ValueError(f"{name} codes must have a multiple of 64 columns, got {half}")
-    _shaped(scales, (half // 64, rows, 4), f"{name} scales")
-    return cp, sp, rows, half * 2
+    if codes.dim() != 3 or codes.shape[2] != 64:
+        raise ValueError(f"{name} codes must have shape (groups, rows, 64), "
+                         f"got {tuple(codes.shape)}")
+    groups, rows, _ = codes.shape
+    _shaped(scales, (groups, rows, 4), f"{name} scales")
+    return cp, sp, rows, groups * 128
 
 
 def forge_quantize_mxfp4(x, *, rows=None, cols=None, stream=None) -> None:

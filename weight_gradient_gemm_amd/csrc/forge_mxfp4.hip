@@ -66,8 +66,7 @@ FORGE_API forge_status forge_quantize_mxfp4(const void* x, forge_dtype x_dtype, 
   a.col_scales = static_cast<uint8_t*>(col_scales);
   a.R = R;
   a.C = C;
-  a.row_pitch = FORGE_MXFP4_K(C) / 2;
-  a.col_pitch = FORGE_MXFP4_K(R) / 2;
+  a.padded_c = FORGE_MXFP4_K(C);
   // Padding columns of the codes along rows belong to tiles too.
   const int64_t tc = x_dtype == FORGE_BF16 ? kQuantCols<true> : kQuantCols<false>;
   const int64_t across = ((row_codes ? FORGE_MXFP4_K(C) : C) + tc - 1) / tc;

@@ -3,10 +3,11 @@
 // two operands by v_mfma_scale_f32_32x32x64_f8f6f4, which takes both blocks'
 // scales with their codes.
 //
-// An operand of R rows and padded length Kp holds codes [R][Kp / 2] and scales
-// [Kp / 128][R][4]: the scales of 128 columns of one row are one 32-bit word,
-// and the words of neighbouring rows are neighbours, so the matrix kernel's
-// lanes (a row each) load them from whole lines and pick a byte in registers.
+// An operand of R rows and padded length Kp holds codes [Kp / 128][R][64] and
+// scales [Kp / 128][R][4]: what one stage of the product takes of neighbouring
+// rows is contiguous. With rows of Kp / 2 bytes instead, a stage's 64 bytes of
+// each row were half lines at one distance, for a power of two all on one
+// channel of the L2 (MLP-down's product: ROWLAYOUT).
 #pragma once
 
 #include <type_traits>
@@ -26,7 +27,7 @@ struct QuantArgs {
   const void* x;
   uint8_t *row_codes, *row_scales, *col_codes, *col_scales;
   int64_t R, C;
-  int64_t row_pitch, col_pitch;    // bytes of a row of codes
+  int64_t padded_c;                // padded length of the operand along rows
   uint32_t tiles_c;                // tiles across
   uint32_t tiles;
 };
@@ -143,8 +144,9 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_mxfp4_kernel(QuantArgs
         top = max(top, uint32_t(__shfl_xor(int(top), 2)));
         if constexpr (!BF16) top = max(top, uint32_t(__shfl_xor(int(top), 4)));
         const uint32_t s = scale_byte(top >> 23);
-        if (row < a.R && col < 2 * a.row_pitch) {
-          uint8_t* const out = a.row_codes + row * a.row_pitch + col / 2;
+        if (row < a.R && col < a.padded_c) {
+          const int64_t at = (col >> 7) * a.R + row;
+          uint8_t* const out = a.row_codes + at * 64 + (col & 127) / 2;
           if constexpr (BF16) {
             const uint32_t w[4] = {raw[it][0], raw[it][1], raw[it][2], raw[it][3]};
             *reinterpret_cast<uint32_t*>(out) = codes8(w, s);
@@ -152,7 +154,7 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_mxfp4_kernel(QuantArgs
             *reinterpret_cast<uint16_t*>(out) = uint16_t(codes4(__builtin_bit_cast(f32x4_t, raw[it]), s));
           }
           if (j % (32 / CPT) == 0)
-            a.row_scales[((col >> 7) * a.R + row) * 4 + ((col >> 5) & 3)] = uint8_t(s);
+            a.row_scales[at * 4 + ((col >> 5) & 3)] = uint8_t(s);
         }
       }
     }
@@ -194,8 +196,9 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_mxfp4_kernel(QuantArgs
             out[k] = codes4(lo, s) | codes4(hi, s) << 16;
           }
         }
-        *reinterpret_cast<u32x4_t*>(a.col_codes + column * a.col_pitch + r0 / 2 + 16 * blk) = out;
-        a.col_scales[(int64_t(tr) * a.C + column) * 4 + blk] = uint8_t(s);
+        const int64_t at = int64_t(tr) * a.C + column;
+        *reinterpret_cast<u32x4_t*>(a.col_codes + at * 64 + 16 * blk) = out;
+        a.col_scales[at * 4 + blk] = uint8_t(s);
       }
     }
     __syncthreads();                         // the next tile reuses the LDS
@@ -210,20 +213,33 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_mxfp4_kernel(QuantArgs
 // wgrad_kernels.hpp) I is X and O is dY, both already K-major, so an MFMA
 // operand (32 columns of one row: one block) is 16 consecutive bytes.
 //
-// Mainloop: stages of 128 columns, rows of 64 bytes, straight from memory into
-// a ring of 4 LDS slots, as the bf16 kernel (same bytes per stage and tile).
-// 16-byte chunk c of row r is kept at chunk c ^ (r / 2 mod 4): the 8 rows that
-// LDS serves at a time then fall on different banks. The scale words go from
-// memory to registers, three stages ahead. Per stage, two k-steps of 64:
+// Mainloop: stages of 128 columns, rows of 64 bytes and then their scale words,
+// straight from memory into a ring of 4 LDS slots, as the bf16 kernel (the same
+// bytes of operands per stage and tile). 16-byte chunk c of row r is kept at
+// chunk c ^ (r / 4 mod 4), which puts 16 neighbouring rows' reads on different
+// banks. Per stage, two k-steps of 64:
 //   step 0: MFMAs; read step 1's operands from this slot.
 //   wait for this wave's LDS reads and for its loads of the next stage; barrier.
-//   step 1: request the scales of stage s + 3 and the codes of stage s + 4;
-//   MFMAs; read step 0's operands from the next slot.
+//   step 1: request stage s + 4 into this slot; MFMAs; read the scales and
+//   step 0's operands from the next slot.
 // Columns enter each element in ascending steps of 64, whatever the tile.
 struct MxArgs {
   const uint8_t *i_scales, *o_scales;
   int64_t kp;
 };
+
+// 16-bit elements of a slot: a stage's codes and scale words.
+template <class C>
+__host__ __device__ constexpr int mx_slot() {
+  return C::STAGE + 2 * (C::BM + C::BN);
+}
+
+// 4 bytes per lane from a buffer window straight into LDS: lane t writes at
+// dst + 4 t (see load16_to_lds).
+__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, uint16_t* dst, uint32_t voff) {
+  typedef __attribute__((address_space(3))) void lds_void;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 4, voff, 0, 0, 0);
+}
 
 template <class C, int EPI>
 __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, int tile_m,
@@ -232,7 +248,9 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
   constexpr int RB = 64;                                // bytes of a row in a stage
   constexpr int QX = BM * RB / 1024, QY = BN * RB / 1024;
   constexpr int NQW = (QX + QY) / C::WAVES;             // 1 KB loads per wave and stage
-  constexpr int NSC = TM + TN;                          // scale words per lane and stage
+  constexpr int SI = BM / 64, SO = BN / 64;             // 256-byte loads of scale words
+  constexpr int NSW = (SI + SO + C::WAVES - 1) / C::WAVES;
+  constexpr int kScales = RB * (BM + BN);               // their place in a slot
   static_assert((QX + QY) % C::WAVES == 0, "stage loads split evenly over the waves");
   static_assert(RB * (BM + BN) <= C::STAGE * 2, "stage exceeds a slot");
 
@@ -241,73 +259,66 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
   const int wm = wave % C::WAVES_M, wn = wave / C::WAVES_M;
   const int d_in = a.d_in, d_out = a.d_out;
   const int i0 = tile_m * BM, o0 = tile_n * BN;
-  const int pitch = int(x.kp / 2);
   const int nk = int(x.kp / 128);
 
-  // Loads: instruction q covers 16 rows of I (q < QX) or O; lane t fills row
-  // t / 4, physical chunk t % 4.
-  uint32_t voff[NQW];
-  int soff[NQW];
+  // Loads: instruction q covers 16 rows of I (q < QX) or O, 1 KB on end; lane t
+  // fills row t / 4, physical chunk t % 4. Rows past the edge lie past the end
+  // of the window, and stages past the last have a window of no bytes: both
+  // read zeros. No branches: the compiler would sink MFMAs below them, out of
+  // their stage.
+  uint32_t voff[NQW], soff[NSW];
 #pragma unroll
   for (int i = 0; i < NQW; ++i) {
     const int q = wave * NQW + i;
-    const bool isx = q < QX;
-    const int row0 = (isx ? q : q - QX) * 16, lrow = lane >> 2;
-    const int ch = (lane & 3) ^ ((lrow >> 1) & 3);
-    voff[i] = (isx ? i0 : o0) + row0 + lrow < (isx ? d_in : d_out) ? uint32_t(lrow * pitch + 16 * ch) : kOOB;
-    soff[i] = row0 * pitch;
+    voff[i] = uint32_t((q < QX ? q : q - QX) * 1024 + (lane >> 2) * RB +
+                       (((lane & 3) ^ ((lane >> 4) & 3)) * 16));
   }
+#pragma unroll
+  for (int i = 0; i < NSW; ++i) {
+    // With 6 loads for 4 waves, two of them are made twice: the same bytes.
+    const int q = (wave * NSW + i) % (SI + SO);
+    soff[i] = uint32_t((q < SI ? q : q - SI) * 256 + lane * 4);
+  }
+  const uint32_t left_i = uint32_t(d_in - i0), left_o = d_out > o0 ? uint32_t(d_out - o0) : 0u;
+  const uint8_t* gi = reinterpret_cast<const uint8_t*>(a.X) + int64_t(i0) * RB;
+  const uint8_t* go = reinterpret_cast<const uint8_t*>(a.dY) + int64_t(o0) * RB;
+  const uint8_t* si = x.i_scales + int64_t(i0) * 4;
+  const uint8_t* so = x.o_scales + int64_t(o0) * 4;
   int g_stage = 0;
-  const uint8_t* gi = reinterpret_cast<const uint8_t*>(a.X) + int64_t(i0) * pitch;
-  const uint8_t* go = reinterpret_cast<const uint8_t*>(a.dY) + int64_t(o0) * pitch;
   auto load_stage = [&](uint16_t* slot) {
-    // Rows past the edge have an out-of-window offset, so the window only has
-    // to reach the tile's last row (256 pitch < 2^31), and nothing past the
-    // last stage, which loads zeros. No branches: the compiler would sink
-    // MFMAs below them, out of their stage.
-    const uint32_t bytes = g_stage < nk ? kOOB - 1u : 0u;
-    const __amdgpu_buffer_rsrc_t ri = window32(gi, bytes), ro = window32(go, bytes);
-    gi += RB;
-    go += RB;
+    const uint32_t ni = g_stage < nk ? left_i : 0u, no = g_stage < nk ? left_o : 0u;
+    const __amdgpu_buffer_rsrc_t ri = window32(gi, ni * RB), ro = window32(go, no * RB);
+    const __amdgpu_buffer_rsrc_t qi = window32(si, ni * 4u), qo = window32(so, no * 4u);
+    gi += int64_t(d_in) * RB;
+    go += int64_t(d_out) * RB;
+    si += int64_t(d_in) * 4;
+    so += int64_t(d_out) * 4;
     ++g_stage;
+#pragma unroll
+    for (int i = 0; i < NSW; ++i) {
+      const int q = (wave * NSW + i) % (SI + SO);
+      load4_to_lds(q < SI ? qi : qo, slot + kScales / 2 + q * 128, soff[i]);
+    }
 #pragma unroll
     for (int i = 0; i < NQW; ++i) {
       const int q = wave * NQW + i;
-      load16_to_lds(q < QX ? ri : ro, slot + q * 512, voff[i], soff[i]);
+      load16_to_lds(q < QX ? ri : ro, slot + q * 512, voff[i], 0);
     }
   };
 
-  // Scale words: the four blocks of this lane's row in a stage; the lane's half
-  // h of the wave takes blocks 2 kk + h, so the word is shifted by h bytes once
-  // and step kk picks byte 2 kk.
-  const int l32 = lane & 31, h = lane >> 5;
-  uint32_t sv[NSC];
-#pragma unroll
-  for (int m = 0; m < TM; ++m) sv[m] = uint32_t(i0 + wm * C::WM + m * 32 + l32) * 4u;
-#pragma unroll
-  for (int n = 0; n < TN; ++n) sv[TM + n] = uint32_t(o0 + wn * C::WN + n * 32 + l32) * 4u;
-  int s_stage = 0;
-  const uint8_t *si = x.i_scales, *so = x.o_scales;
-  uint32_t sc[4][NSC];
-  auto load_scales = [&](int k) {
-    const __amdgpu_buffer_rsrc_t ri = window32(si, s_stage < nk ? uint32_t(d_in) * 4u : 0u);
-    const __amdgpu_buffer_rsrc_t ro = window32(so, s_stage < nk ? uint32_t(d_out) * 4u : 0u);
-    si += int64_t(d_in) * 4;
-    so += int64_t(d_out) * 4;
-    ++s_stage;
-#pragma unroll
-    for (int t = 0; t < NSC; ++t)
-      sc[k][t] = __builtin_amdgcn_raw_buffer_load_b32(t < TM ? ri : ro, int(sv[t]), 0, 0);
-  };
-
   // Operand addresses in a slot for step 0; step 1 is 32 bytes away (chunk
-  // 2 + h, and the swizzle is an exclusive or).
+  // 2 + h, and the swizzle is an exclusive or). A scale word holds the four
+  // blocks of a row in a stage; this lane's half h of the wave takes blocks
+  // 2 kk + h, so the word is shifted by h bytes once and step kk picks byte 2 kk.
+  const int l32 = lane & 31, h = lane >> 5;
   uint32_t fa[TM], fb[TN];
-  const uint32_t ch0 = uint32_t((h ^ ((l32 >> 1) & 3)) * 16);
+  const uint32_t ch0 = uint32_t((h ^ ((l32 >> 2) & 3)) * 16);
 #pragma unroll
   for (int m = 0; m < TM; ++m) fa[m] = uint32_t((wm * C::WM + m * 32 + l32) * RB) + ch0;
 #pragma unroll
   for (int n = 0; n < TN; ++n) fb[n] = uint32_t((BM + wn * C::WN + n * 32 + l32) * RB) + ch0;
+  const uint32_t sa = uint32_t(kScales + (wm * C::WM + l32) * 4);
+  const uint32_t sb = uint32_t(kScales + (BM + wn * C::WN + l32) * 4);
   i32x4_t frag[2][TM + TN];
   auto read_frags = [&](int f, const uint16_t* slot, int kk) {
     const char* base = reinterpret_cast<const char*>(slot);
@@ -318,6 +329,19 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
     for (int n = 0; n < TN; ++n)
       frag[f][TM + n] = *reinterpret_cast<const i32x4_t*>(base + (fb[n] ^ (32u * kk)));
   };
+  uint32_t sc[TM + TN], now[TM + TN];
+  auto read_scales = [&](const uint16_t* slot) {
+    const char* base = reinterpret_cast<const char*>(slot);
+#pragma unroll
+    for (int m = 0; m < TM; ++m) sc[m] = *reinterpret_cast<const uint32_t*>(base + sa + m * 128);
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+      sc[TM + n] = *reinterpret_cast<const uint32_t*>(base + sb + n * 128);
+  };
+  auto shift_scales = [&]() {
+#pragma unroll
+    for (int t = 0; t < TM + TN; ++t) now[t] = sc[t] >> (8 * h);
+  };
   f32x16_t acc[TM][TN];
 #pragma unroll
   for (int m = 0; m < TM; ++m)
@@ -326,11 +350,6 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.0f;
   auto wide = [](const i32x4_t& v) { return i32x8_t{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; };
-  uint32_t now[NSC];
-  auto shift_scales = [&](int k) {
-#pragma unroll
-    for (int t = 0; t < NSC; ++t) now[t] = sc[k][t] >> (8 * h);
-  };
   constexpr int kFp4 = 4;                               // operand format code of the instruction
   auto mfmas0 = [&]() {
 #pragma unroll
@@ -350,19 +369,17 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
             wide(frag[1][m]), wide(frag[1][TM + n]), acc[m][n], kFp4, kFp4, 2, int(now[m]), 2,
             int(now[TM + n]));
   };
-  auto interleave = [&](int loads) {
+  auto interleave = [&](int reads, int loads) {
 #pragma unroll
     for (int i = 0; i < TM * TN; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                       // MFMA
-      if (i < TM + TN) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);      // DS read
+      if (i < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);        // DS read
       if (i < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);        // VMEM read
     }
   };
-  // Requests in order: codes 0, codes 1, scales 0, codes 2, scales 1, codes 3,
-  // scales 2, then per stage s: scales s + 3, codes s + 4. At stage s the codes
-  // of stage s + 1 have landed once at most two stages' requests are left.
-  constexpr int kWaitMid = waitcnt_imm(2 * (NQW + NSC), 0);
-  constexpr int kWaitFirst = waitcnt_imm(3 * (NQW + NSC), 15);
+  constexpr int NL = NQW + NSW;
+  constexpr int kWaitMid = waitcnt_imm(2 * NL, 0);
+  constexpr int kWaitFirst = waitcnt_imm(3 * NL, 15);
 #define FORGE_MX_BARRIER(IMM)                 \
   do {                                        \
     __builtin_amdgcn_sched_barrier(0);        \
@@ -372,37 +389,35 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
     asm volatile("" ::: "memory");            \
     __builtin_amdgcn_sched_barrier(0);        \
   } while (0)
-  auto stage = [&](uint16_t* cur, uint16_t* nxt, int k) {
-    shift_scales(k);
+  auto stage = [&](uint16_t* cur, uint16_t* nxt) {
+    shift_scales();
     read_frags(1, cur, 1);
     mfmas0();
-    interleave(0);
+    interleave(TM + TN, 0);
     FORGE_MX_BARRIER(kWaitMid);
-    load_scales((k + 3) & 3);
     load_stage(cur);                             // stage s + 4 into the freed slot
+    read_scales(nxt);
     read_frags(0, nxt, 0);
     mfmas1();
-    interleave(NQW + NSC);
+    interleave(2 * (TM + TN), NL);
     __builtin_amdgcn_sched_barrier(0);
   };
   if (nk > 0) {
     load_stage(sl.s0);
     load_stage(sl.s1);
-    load_scales(0);
     load_stage(sl.s2);
-    load_scales(1);
     load_stage(sl.s3);
-    load_scales(2);
     FORGE_MX_BARRIER(kWaitFirst);
+    read_scales(sl.s0);
     read_frags(0, sl.s0, 0);
     // Whole rounds of 4 stages: the accumulators keep their registers. Stages
     // past the last add products of zero codes and zero scale bytes: exactly +0.
     const int rounds = (nk + 3) / 4;
     for (int r = 0; r < rounds; ++r) {
-      stage(sl.s0, sl.s1, 0);
-      stage(sl.s1, sl.s2, 1);
-      stage(sl.s2, sl.s3, 2);
-      stage(sl.s3, sl.s0, 3);
+      stage(sl.s0, sl.s1);
+      stage(sl.s1, sl.s2);
+      stage(sl.s2, sl.s3);
+      stage(sl.s3, sl.s0);
     }
   }
 #undef FORGE_MX_BARRIER
@@ -413,7 +428,7 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
 template <class C, int EPI>
 __global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(C::OCC, C::OCC)))
 void mxfp4_kernel(WgradArgs a, MxArgs x) {
-  FORGE_DECLARE_SLOTS(C::STAGE);
+  FORGE_DECLARE_SLOTS(mx_slot<C>());
   int e, tm, tn;
   map_tile(blockIdx.x, a.num_tiles, a.tiles_m, a.tiles_n, a.group_m, e, tm, tn);
   mxfp4_tile<C, EPI>(a, x, tm, tn, ring);
@@ -425,7 +440,7 @@ __global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(1, 
 void mxfp4_persistent_kernel(WgradArgs a, MxArgs x) {
   static_assert(CF::THREADS == CH::THREADS && CF::BM == CH::BM && CF::BN == 2 * CH::BN,
                 "half tiles must split the full tile's columns");
-  FORGE_DECLARE_SLOTS(CF::STAGE);
+  FORGE_DECLARE_SLOTS(mx_slot<CF>());
   const int b = blockIdx.x, xcd = b & 7, j = b >> 3, nw = gridDim.x >> 3;
   const int per = a.num_tiles >> 3, rem = a.num_tiles & 7;
   const int start = xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per;
