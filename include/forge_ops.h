@@ -202,7 +202,8 @@ FORGE_API forge_status forge_quantize_mxfp4(const void* x, forge_dtype x_dtype, 
  *   Weight gradient   g = dY^T X:  A = dY by columns, B = X by columns.
  *   Input gradient    dX = dY W:   A = dY by rows,    B = W by columns.
  *   Layer output      Y = X W^T:   A = X by rows,     B = W by rows.
- * tile: the ids of forge.h over [N, M].
+ * tile: the ids of forge.h over [N, M]; the default may also take smaller
+ * tiles, for outputs that would leave most of the chip idle.
  */
 FORGE_API forge_status forge_matmul_mxfp4(const void* a_codes, const void* a_scales,
                                 const void* b_codes, const void* b_scales, void* out,

@@ -44,7 +44,7 @@ def reference(torch, x):
 
 def decode(torch, operand):
     """The values of an operand, and its scale bytes by row and block."""
-    codes, scales = (t.cpu() for t in operand)
+    codes, scales = operand.codes.cpu(), operand.scales.cpu()
     codes = codes.permute(1, 0, 2).reshape(codes.shape[1], -1)
     R, half = codes.shape
     table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
@@ -66,8 +66,9 @@ def same(torch, operand, x):
 def both(torch, wg, x):
     R, C = x.shape
     rows, cols = wg.forge_mxfp4_empty(R, C), wg.forge_mxfp4_empty(C, R)
-    for t in (*rows, *cols):
-        t.fill_(0xA5)
+    for op in (rows, cols):
+        op.codes.fill_(0xA5)
+        op.scales.fill_(0xA5)
     wg.forge_quantize_mxfp4(x, rows=rows, cols=cols)
     return rows, cols
 
@@ -87,8 +88,8 @@ def test_quantize(env, R, C, dtype):
     one, two = wg.forge_mxfp4_empty(R, C), wg.forge_mxfp4_empty(C, R)
     wg.forge_quantize_mxfp4(x, rows=one)
     wg.forge_quantize_mxfp4(x, cols=two)
-    for a, b in zip((*rows, *cols), (*one, *two)):
-        assert torch.equal(a, b)
+    for a, b in ((rows, one), (cols, two)):
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
@@ -249,7 +250,7 @@ def test_wgrad_adamw(env, T, d_in, d_out):
     wg.forge_quantize_mxfp4(X, cols=xo)
     wg.forge_quantize_mxfp4(dY, cols=yo)
     # an output count that is no multiple of 8: the operand's first rows
-    yo = (yo[0][:, :d_out].contiguous(), yo[1][:, :d_out].contiguous())
+    yo = wg.ForgeMxfp4(yo.codes[:, :d_out].contiguous(), yo.scales[:, :d_out].contiguous())
     W, m = torch.randn(d_out, d_in, device="cuda"), torch.randn(d_out, d_in, device="cuda")
     v = torch.rand(d_out, d_in, device="cuda") + 0.1
     grad = torch.empty(d_out, d_in, device="cuda")
@@ -334,7 +335,9 @@ def test_binding_refuses(env):
     with pytest.raises(ValueError, match="padded length"):
         wg.forge_matmul_mxfp4(op, wg.forge_mxfp4_empty(32, 200), out)
     with pytest.raises(ValueError, match="scales must have shape"):
-        wg.forge_matmul_mxfp4((op[0], op[1][:, :16].contiguous()), op, out)
+        wg.forge_matmul_mxfp4((op.codes, op.scales[:, :16].contiguous()), op, out)
+    with pytest.raises(ValueError, match="on the GPU"):
+        wg.forge_matmul_mxfp4(wg.forge_mxfp4_empty(32, 64, device="cpu"), op, out)
     with pytest.raises(wg.ForgeError, match="TILE"):
         wg.forge_matmul_mxfp4(op, op, out, tile=9)
     with pytest.raises(wg.ForgeError, match="CLIP"):

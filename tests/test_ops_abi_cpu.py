@@ -383,6 +383,15 @@ def test_mxfp4_calls_reach_the_device_check(lib):
 def test_mxfp4_operand_shapes():
     import weight_gradient_gemm_amd as wg
     for rows, k, groups in ((3, 0, 0), (3, 1, 1), (5, 128, 1), (5, 129, 2), (8, 1000, 8)):
-        codes, scales = wg.forge_mxfp4_empty(rows, k, device="cpu")
-        assert tuple(codes.shape) == (groups, rows, 64)
-        assert tuple(scales.shape) == (groups, rows, 4)
+        op = wg.forge_mxfp4_empty(rows, k, device="cpu")
+        assert (op.rows, op.k) == (rows, groups * 128)
+        assert tuple(op.codes.shape) == (groups, rows, 64)
+        assert tuple(op.scales.shape) == (groups, rows, 4)
+        again = wg.ForgeMxfp4(op.codes, op.scales)
+        assert (again.rows, again.k, again.ptrs) == (op.rows, op.k, op.ptrs)
+    with pytest.raises(ValueError, match="shape"):
+        wg.ForgeMxfp4(op.codes, op.scales[:1])
+    with pytest.raises(TypeError, match="uint8"):
+        wg.ForgeMxfp4(op.codes.int(), op.scales)
+    with pytest.raises(ValueError, match="contiguous"):
+        wg.ForgeMxfp4(op.codes.transpose(0, 1), op.scales)

@@ -43,6 +43,7 @@ from ._lib import (  # noqa: F401
     library_path,
 )
 from ._ops import (  # noqa: F401
+    ForgeMxfp4,
     ForgeTensorList,
     forge_adamw_clipped,
     forge_clip_grads,

@@ -303,47 +303,86 @@ def forge_embedding_sgdm(ids, dY, W, mom, *, scale=1.0, lr=1e-3, momentum=0.9, w
 # --------------------------------------------------------------------------
 # microscaled 4-bit operands
 # --------------------------------------------------------------------------
-def forge_mxfp4_empty(rows, k, device=None):
-    """(codes, scales), uninitialised, of an operand of `rows` rows and
-    contraction length k: uint8 [Kp / 128, rows, 64] and [Kp / 128, rows, 4],
-    Kp the next multiple of 128. Both are views of one allocation."""
+class ForgeMxfp4:
+    """A microscaled 4-bit operand of ``rows`` rows and padded contraction
+    length ``k``: uint8 ``codes`` [k / 128, rows, 64] and ``scales`` [k / 128,
+    rows, 4], k a multiple of 128. It keeps its tensors alive and counts on
+    them staying where they are."""
+
+    def __init__(self, codes, scales):
+        torch = _torch()
+        for t, name in ((codes, "codes"), (scales, "scales")):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
+                raise TypeError(f"{name} must be a torch.Tensor of uint8")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if codes.dim() != 3 or codes.shape[2] != 64:
+            raise ValueError("codes must have shape (groups, rows, 64), "
+                             f"got {tuple(codes.shape)}")
+        groups, rows, _ = codes.shape
+        _shaped(scales, (groups, rows, 4), "scales")
+        if scales.device != codes.device:
+            raise ValueError(f"codes are on {codes.device}, scales on {scales.device}")
+        self._hold, self._codes, self._scales = None, codes, scales
+        self.rows, self.k, self.device = rows, groups * 128, codes.get_device()
+        self.ptrs = (codes.data_ptr() or None, scales.data_ptr() or None)
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            n = self.rows * self.k // 2
+            self._codes = self._hold[:n].view(self.k // 128, self.rows, 64)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            n = self.rows * self.k // 2
+            self._scales = self._hold[n:].view(self.k // 128, self.rows, 4)
+        return self._scales
+
+
+def forge_mxfp4_empty(rows, k, device=None) -> ForgeMxfp4:
+    """An uninitialised operand of `rows` rows and contraction length k (padded
+    to the next multiple of 128), codes and scales in one allocation."""
     torch = _torch()
-    rows, groups = int(rows), (int(k) + 127) // 128
-    n = groups * 64 * rows
-    buf = torch.empty(n + groups * 4 * rows, dtype=torch.uint8,
-                      device="cuda" if device is None else device)
-    return buf[:n].view(groups, rows, 64), buf[n:].view(groups, rows, 4)
+    op = ForgeMxfp4.__new__(ForgeMxfp4)
+    op.rows, op.k = int(rows), (int(k) + 127) // 128 * 128
+    n = op.rows * op.k // 2
+    op._hold = t = torch.empty(n + n // 16, dtype=torch.uint8,
+                               device="cuda" if device is None else device)
+    op._codes = op._scales = None
+    op.device = t.get_device()
+    p = t.data_ptr()
+    op.ptrs = (p, p + n) if n else (None, None)
+    return op
 
 
-def _operand(torch, cur, pair, name):
+def _operand(cur, op, name):
     """Addresses of an operand's codes and scales, its rows and padded length."""
-    codes, scales = pair
-    cp = _in(codes, torch.uint8, f"{name} codes", cur)
-    sp = _in(scales, torch.uint8, f"{name} scales", cur)
-    if codes.dim() != 3 or codes.shape[2] != 64:
-        raise ValueError(f"{name} codes must have shape (groups, rows, 64), "
-                         f"got {tuple(codes.shape)}")
-    groups, rows, _ = codes.shape
-    _shaped(scales, (groups, rows, 4), f"{name} scales")
-    return cp, sp, rows, groups * 128
+    if not isinstance(op, ForgeMxfp4):
+        op = ForgeMxfp4(*op)
+    if op.device != cur:
+        raise ValueError(f"{name} must be on the GPU and the current device, cuda:{cur}")
+    return *op.ptrs, op.rows, op.k
 
 
 def forge_quantize_mxfp4(x, *, rows=None, cols=None, stream=None) -> None:
     """Quantises x [R, C] (float32 or bfloat16) into the operands ``rows`` (R
     rows, blocks along a row) and / or ``cols`` (C rows, blocks along a column:
-    transposed), each a pair as forge_mxfp4_empty makes."""
+    transposed)."""
     torch, cur, st = _current(stream)
     code = _real(torch, x, "x")
     xp = _in(x, x.dtype, "x", cur)
     R, C = _two(x, "x")
     ptrs = []
-    for name, pair, n, k in (("rows", rows, R, C), ("cols", cols, C, R)):
-        if pair is None:
+    for name, op, n, k in (("rows", rows, R, C), ("cols", cols, C, R)):
+        if op is None:
             ptrs += (None, None)
             continue
-        cp, sp, pn, pk = _operand(torch, cur, pair, name)
-        if pn != n or pk != (k + 127) // 128 * 128:
-            raise ValueError(f"{name} is an operand of {pn} rows and padded length {pk}, not of "
+        cp, sp, on, ok = _operand(cur, op, name)
+        if on != n or ok != (k + 127) // 128 * 128:
+            raise ValueError(f"{name} is an operand of {on} rows and padded length {ok}, not of "
                              f"{n} rows and length {k}")
         if not (n and k):
             return                           # x is empty: nothing to write
@@ -353,10 +392,10 @@ def forge_quantize_mxfp4(x, *, rows=None, cols=None, stream=None) -> None:
 
 def forge_matmul_mxfp4(A, B, out, *, tile=_lib.FORGE_TILE_DEFAULT, stream=None) -> None:
     """out [M, N] (float32 or bfloat16) <- A B^T for operands A of M rows and B
-    of N rows, each a (codes, scales) pair."""
+    of N rows."""
     torch, cur, st = _current(stream)
-    ac, as_, M, k = _operand(torch, cur, A, "A")
-    bc, bs, N, k2 = _operand(torch, cur, B, "B")
+    ac, as_, M, k = _operand(cur, A, "A")
+    bc, bs, N, k2 = _operand(cur, B, "B")
     if k != k2:
         raise ValueError(f"A has padded length {k}, B has {k2}")
     oc = _real(torch, out, "out")
@@ -371,8 +410,8 @@ def forge_wgrad_adamw_mxfp4(X, dY, W, m, v, *, step, lr=1e-3, beta1=0.9, beta2=0
     """W, m, v <- AdamW(W, m, v, g = dY^T X), in place, g never stored, from the
     operands X (d_in rows) and dY (d_out rows) over the tokens."""
     torch, cur, st = _current(stream)
-    xc, xs, d_in, k = _operand(torch, cur, X, "X")
-    yc, ys, d_out, k2 = _operand(torch, cur, dY, "dY")
+    xc, xs, d_in, k = _operand(cur, X, "X")
+    yc, ys, d_out, k2 = _operand(cur, dY, "dY")
     if k != k2:
         raise ValueError(f"X has padded length {k}, dY has {k2}")
     ptrs = []

@@ -1,5 +1,6 @@
 // Microscaled 4-bit entry points of the forge C ABI.
 #include <algorithm>
+#include <cmath>
 
 #include "forge_ops.h"
 #include "host.hpp"
@@ -8,6 +9,49 @@
 
 namespace forge {
 namespace {
+
+// Tiles of the library's own choice, beside the public ids.
+enum : forge_tile { MX_TILE_128x64 = FORGE_TILE_COUNT, MX_TILE_64x64 };
+
+// The library's choice of tile: the least estimated time in microseconds, from
+// times measured on this kernel. A stage (128 columns) of a tile takes `alone`
+// where a CU has nothing else to do, and a CU with `slots` of them finishes one
+// every `full`; `ends` is what a round of tiles adds at its two ends. The
+// persistent schedule runs 256x256 tiles, its rounds counted in full tiles.
+// Sizes from 1 x 14336 x 4096 to 8191 x 14336 x 4096: within 12% of the fastest.
+forge_tile choose_tile(int64_t N, int64_t M, int64_t Kp) {
+  struct Kind {
+    forge_tile id;
+    int bm, bn, slots;
+    double alone, full, ends;
+  };
+  static const Kind kinds[] = {{FORGE_TILE_256x256, 256, 256, 1, 0.595, 0.94, 7.1},
+                               {FORGE_TILE_256x128, 256, 128, 1, 0.367, 0.59, 5.0},
+                               {FORGE_TILE_128x128, 128, 128, 2, 0.24, 0.304, 3.6},
+                               {MX_TILE_128x64, 128, 64, 3, 0.205, 0.187, 3.2},
+                               {MX_TILE_64x64, 64, 64, 4, 0.171, 0.12, 2.8}};
+  const double stages = double((Kp / 128 + 3) / 4 * 4);     // whole rounds of 4
+  auto round = [&](const Kind& k, int64_t tiles) {
+    if (tiles == 0) return 0.0;
+    const double load = double(tiles) / 256.0;
+    return stages * std::max(k.alone, (load <= 1.0 ? load : std::ceil(load)) * k.full) + k.ends;
+  };
+  forge_tile best = FORGE_TILE_256x256;
+  double least = 0.0;
+  for (const Kind& k : kinds) {
+    const int64_t tiles = count_tiles(N, M, TileShape{k.bm, k.bn}), slots = 256 * k.slots;
+    const double t = double(tiles / slots) * round(k, slots) + round(k, tiles % slots);
+    if (least == 0.0 || t < least) {
+      least = t;
+      best = k.id;
+    }
+  }
+  const int grid = persistent_grid();
+  const int64_t tiles = count_tiles(N, M, TileShape{256, 256});
+  if (grid > 0 && tiles >= grid && persistent_makespan(tiles, grid) * (stages * 0.9 + 7.1) < least)
+    best = FORGE_TILE_PERSISTENT;
+  return best;
+}
 
 template <class C, int EPI>
 forge_status launch_mx_t(WgradArgs a, const MxArgs& x, hipStream_t s) {
@@ -20,6 +64,8 @@ template <int EPI>
 struct MxLaunch {
   static forge_status run(WgradArgs a, const MxArgs& x, forge_tile tile, hipStream_t s) {
     switch (tile) {
+      case MX_TILE_64x64: return launch_mx_t<Mx64x64, EPI>(a, x, s);
+      case MX_TILE_128x64: return launch_mx_t<Mx128x64, EPI>(a, x, s);
       case FORGE_TILE_128x128: return launch_mx_t<Cfg128x128, EPI>(a, x, s);
       case FORGE_TILE_256x128: return launch_mx_t<Cfg256x128, EPI>(a, x, s);
       case FORGE_TILE_256x256: return launch_mx_t<Cfg256x256, EPI>(a, x, s);
@@ -89,8 +135,8 @@ FORGE_API forge_status forge_matmul_mxfp4(const void* a_codes, const void* a_sca
     return s;
   if (M == 0 || N == 0) return FORGE_OK;
   if (forge_status s = check_device()) return s;
-  tile = resolve_tile(tile, N, M, 1);
-  if (!grid_fits(N, M, tile, 1)) return FORGE_ERR_SHAPE;
+  if (!grid_fits(N, M, FORGE_TILE_128x128, 1)) return FORGE_ERR_SHAPE;
+  if (tile == FORGE_TILE_DEFAULT) tile = choose_tile(N, M, Kp);
   (void)hipGetLastError();
   const WgradArgs a = base_args(b_codes, a_codes, static_cast<float*>(out), nullptr, nullptr, Kp, N, M);
   const MxArgs x{static_cast<const uint8_t*>(b_scales), static_cast<const uint8_t*>(a_scales), Kp};
@@ -110,8 +156,8 @@ FORGE_API forge_status forge_wgrad_adamw_mxfp4(const void* x_codes, const void* 
     return s;
   if (d_in == 0 || d_out == 0) return FORGE_OK;
   if (forge_status s = check_device()) return s;
-  tile = resolve_tile(tile, d_in, d_out, 1);
-  if (!grid_fits(d_in, d_out, tile, 1)) return FORGE_ERR_SHAPE;
+  if (!grid_fits(d_in, d_out, FORGE_TILE_128x128, 1)) return FORGE_ERR_SHAPE;
+  if (tile == FORGE_TILE_DEFAULT) tile = choose_tile(d_in, d_out, Kp);
   (void)hipGetLastError();
   WgradArgs a = base_args(x_codes, dy_codes, W, m, v, Kp, d_in, d_out);
   a.adam = make_adamw(*p);

@@ -228,6 +228,19 @@ struct MxArgs {
   int64_t kp;
 };
 
+// Tiles smaller than the other kernels have, for outputs that do not fill the
+// chip: fields as TileCfg.
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int OCC_>
+struct SmallTileCfg {
+  static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, BK = 32, OCC = OCC_;
+  static constexpr int WAVES = WAVES_M * WAVES_N, THREADS = 64 * WAVES;
+  static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 32, TN = WN / 32;
+  static constexpr int STAGE = BK * (BM + BN);
+  static_assert(WAVES == 4 && TM >= 1 && TN >= 1, "4 waves of whole MFMA blocks");
+};
+using Mx128x64 = SmallTileCfg<128, 64, 2, 2, 3>;
+using Mx64x64 = SmallTileCfg<64, 64, 2, 2, 4>;
+
 // 16-bit elements of a slot: a stage's codes and scale words.
 template <class C>
 __host__ __device__ constexpr int mx_slot() {
