@@ -262,3 +262,11 @@ def test_binding_refuses(env):
         wg.forge_embedding_adamw(ids, out, table, table.clone(), table.clone(), step=1,
                                  max_grad_norm=1.0)
     assert bool((table == 0).all())
+
+
+def test_lookup_in_an_empty_table(env):
+    torch, wg = env
+    out = torch.full((3, 8), 5.0, device="cuda")
+    ids = torch.tensor([0, -1, 4], device="cuda")
+    wg.forge_embedding(torch.empty(0, 8, device="cuda"), ids, out)
+    assert bool((out == 0).all())
