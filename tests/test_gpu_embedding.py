@@ -20,6 +20,9 @@ CASES = [
     (70000, 70000, 16, "reversed"), (300, 40, 4104, "none"), (40000, 600000, 8, "spread"),
     (65536, 300, 8, "zipf"), (65537, 128256, 8, "zipf"), (262144, 5000, 8, "zipf"),
     (262145, 128256, 8, "zipf"), (1000003, 999983, 8, "zipf"), (4097, 600, 64, "zipf"),
+    (1024, 900, 512, "one"), (1024, 3, 1032, "zipf"), (1025, 3, 1032, "zipf"), (900, 1, 4104, "one"),
+    (777, 5000, 24, "zipf"), (255, 5000, 24, "zipf"), (256, 70, 1032, "zipf"), (256, 900, 512, "one"),
+    (257, 900, 512, "one"), (256, 200000, 16, "uniform"), (100, 1000, 4104, "zipf"),
 ]
 
 

@@ -35,6 +35,8 @@ constexpr int kSortOne = kOneThreads * kOneRounds;
 constexpr int kTileThreads = 256;                    // a tile of the larger sort
 constexpr int kDirectTiles = 64;                     // tiles that sum their counts themselves
 constexpr int kSumChunk = 32;
+constexpr int kScanTokens = 256;                     // tokens that are looked through, not sorted
+constexpr int kScanRows = 64;                        // most rows of a workgroup then
 
 struct IdSource {
   const void* ids;
@@ -320,6 +322,7 @@ struct EmbeddingArgs {
   uint32_t slices;                 // workgroups across a row
   uint32_t bound_blocks;           // workgroups of the bounds kernel that search
   uint32_t blocks;                 // workgroups of a pass (a launch may have fewer, and loop)
+  int32_t scan_rows;               // rows of a workgroup that looks through the ids
   float scale;
   AdamWConsts adam;
   SgdmConsts sgd;
@@ -334,10 +337,13 @@ __device__ __forceinline__ f32x4_t load_dy4(const void* dY, int64_t i) {
     return *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(dY) + i);
 }
 
-// acc += term(s) + ... + term(e - 1), one after the other, eight loads in flight.
-template <class Term>
+// acc += term(s) + ... + term(e - 1), one after the other. Loads go U at a
+// time, the last ones four at a time, where places past the end repeat the last
+// term and are not added. U costs registers: 8 where a row is only written (V
+// 128256 x 512, 1025 tokens: 50 us against 65 with 16), 16 where it is read too
+// (AdamW, 128256 x 4096: 2.15 ms against 2.22 with 8).
+template <int U, class Term>
 __device__ __forceinline__ void add_terms(f32x4_t& acc, uint32_t s, uint32_t e, const Term& term) {
-  constexpr int U = 8;
   for (; s + U <= e; s += U) {
     f32x4_t r[U];
 #pragma unroll
@@ -345,14 +351,23 @@ __device__ __forceinline__ void add_terms(f32x4_t& acc, uint32_t s, uint32_t e, 
 #pragma unroll
     for (int j = 0; j < U; ++j) acc = acc + r[j];
   }
-  for (; s < e; ++s) acc = acc + term(s);
+  for (; s < e; s += 4) {
+    f32x4_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = term(s + j < e ? s + j : e - 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f32x4_t sum = acc + r[j];
+      acc = s + j < e ? sum : acc;
+    }
+  }
 }
 
 // acc += the tokens at sorted places [s, e).
-template <bool BF16>
+template <int U, bool BF16>
 __device__ __forceinline__ void add_tokens(const EmbeddingArgs& a, f32x4_t& acc, uint32_t s,
                                            uint32_t e, int col) {
-  add_terms(acc, s, e, [&](uint32_t k) {
+  add_terms<U>(acc, s, e, [&](uint32_t k) {
     return load_dy4<BF16>(a.dY, int64_t(a.pos[k]) * a.d + col);
   });
 }
@@ -383,7 +398,7 @@ __global__ __launch_bounds__(256) void embedding_bounds_kernel(EmbeddingArgs a) 
     const int col = int(slice * 256 + threadIdx.x) * 4;
     if (col < a.d) {
       f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-      add_tokens<BF16>(a, acc, s, s + kSumChunk, col);
+      add_tokens<16, BF16>(a, acc, s, s + kSumChunk, col);
       *reinterpret_cast<f32x4_t*>(a.chunk + int64_t(c) * a.d + col) = acc;
     }
   }
@@ -391,18 +406,40 @@ __global__ __launch_bounds__(256) void embedding_bounds_kernel(EmbeddingArgs a) 
 
 enum EmbOp : int { EMB_GRAD = 0, EMB_GRAD_ADD = 1, EMB_ADAMW = 2, EMB_ADAMW_EXACT = 3, EMB_SGDM = 4 };
 
-// One row (or several short ones) per workgroup, 4 columns per thread.
-template <int OP, bool BF16>
-__global__ __launch_bounds__(256) void embedding_rows_kernel(EmbeddingArgs a) {
+// One row's gradient g (unscaled) at 4 columns, stored or consumed: `sum(g)`
+// adds the row's tokens, after W and the state have been requested. They are
+// read and written once: non-temporal, as in the clipped steps.
+template <int OP, class Sum>
+__device__ __forceinline__ void row_step(const EmbeddingArgs& a, int64_t i, const Sum& sum) {
   constexpr bool ADAM = OP == EMB_ADAMW || OP == EMB_ADAMW_EXACT;
-  // W and the state are read and written once: non-temporal, as in the clipped
-  // steps.
   auto get4 = [](const float* p) {
     return __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p));
   };
   auto set4 = [](float* p, const f32x4_t& x) {
     __builtin_nontemporal_store(x, reinterpret_cast<f32x4_t*>(p));
   };
+  f32x4_t w, m, v;
+  if constexpr (OP != EMB_GRAD) w = get4(a.W + i);
+  if constexpr (ADAM || OP == EMB_SGDM) m = get4(a.m + i);
+  if constexpr (ADAM) v = get4(a.v + i);
+  f32x4_t g = {0.0f, 0.0f, 0.0f, 0.0f};
+  sum(g);
+  g = g * a.scale;
+  if constexpr (OP == EMB_GRAD) w = g;
+  if constexpr (OP == EMB_GRAD_ADD) w = w + g;
+  if constexpr (ADAM) adamw_vec4<OP == EMB_ADAMW_EXACT>(g, w, m, v, a.adam);
+  if constexpr (OP == EMB_SGDM) sgdm_vec4(g, w, m, a.sgd);
+  set4(a.W + i, w);
+  if constexpr (ADAM || OP == EMB_SGDM) set4(a.m + i, m);
+  if constexpr (ADAM) set4(a.v + i, v);
+}
+
+// One row (or several short ones) per workgroup, 4 columns per thread.
+// 16384 tokens into 128256 x 4096 with AdamW: 2.2 ms, 12.7 GB (5.8 TB/s, what a
+// stream of reads and writes reaches).
+template <int OP, bool BF16>
+__global__ __launch_bounds__(256) void embedding_rows_kernel(EmbeddingArgs a) {
+  constexpr int U = OP == EMB_GRAD || OP == EMB_GRAD_ADD ? 8 : 16;
   const int lanes = 1 << a.lanes_log2;
   for (uint32_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
     const uint32_t rb = b / a.slices, slice = b - rb * a.slices;
@@ -411,30 +448,86 @@ __global__ __launch_bounds__(256) void embedding_rows_kernel(EmbeddingArgs a) {
     if (row >= a.V || col >= a.d) continue;
     const uint32_t s = a.bound[row], e = a.bound[row + 1];
     if (OP == EMB_GRAD_ADD && s == e) continue;
-    const int64_t i = int64_t(row) * a.d + col;
-    f32x4_t w, m, v;
-    if constexpr (OP != EMB_GRAD) w = get4(a.W + i);
-    if constexpr (ADAM || OP == EMB_SGDM) m = get4(a.m + i);
-    if constexpr (ADAM) v = get4(a.v + i);
-    f32x4_t g = {0.0f, 0.0f, 0.0f, 0.0f};
-    const uint32_t c0 = (s + kSumChunk - 1) / kSumChunk, c1 = e / kSumChunk;
-    if (c0 < c1) {
-      add_tokens<BF16>(a, g, s, c0 * kSumChunk, col);
-      add_terms(g, c0, c1, [&](uint32_t c) {
-        return *reinterpret_cast<const f32x4_t*>(a.chunk + int64_t(c) * a.d + col);
-      });
-      add_tokens<BF16>(a, g, c1 * kSumChunk, e, col);
-    } else {
-      add_tokens<BF16>(a, g, s, e, col);
+    row_step<OP>(a, int64_t(row) * a.d + col, [&](f32x4_t& g) {
+      const uint32_t c0 = (s + kSumChunk - 1) / kSumChunk, c1 = e / kSumChunk;
+      if (c0 < c1) {
+        add_tokens<U, BF16>(a, g, s, c0 * kSumChunk, col);
+        add_terms<U>(g, c0, c1, [&](uint32_t c) {
+          return *reinterpret_cast<const f32x4_t*>(a.chunk + int64_t(c) * a.d + col);
+        });
+        add_tokens<U, BF16>(a, g, c1 * kSumChunk, e, col);
+      } else {
+        add_tokens<U, BF16>(a, g, s, e, col);
+      }
+    });
+  }
+}
+
+// Few tokens: no sort. A workgroup takes a.scan_rows rows of one slice of
+// columns, looks through all ids for its own, and lists its rows' tokens in
+// ascending order in LDS: one launch instead of three. 256 tokens into 5003 x
+// 512: 5.7 us, where the sort and its successors take 13.3 for 257; all of one
+// row: 16.4 against 11.6. With the limit at 1024 the latter were 94 against 14.
+template <int OP, bool BF16>
+__global__ __launch_bounds__(kScanTokens) void embedding_scan_kernel(EmbeddingArgs a, IdSource src) {
+  constexpr int U = OP == EMB_GRAD || OP == EMB_GRAD_ADD ? 8 : 16;
+  constexpr int WAVES = kScanTokens / 64;
+  // Found tokens, each with its row in bits 16 and up, and four behind the last.
+  __shared__ __attribute__((aligned(16))) uint32_t found[kScanTokens + 4];
+  __shared__ uint16_t list[kScanTokens];               // tokens by row, ascending
+  __shared__ uint32_t count[WAVES], first[kScanRows + 1];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  for (uint32_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
+    const uint32_t rb = b / a.slices, slice = b - rb * a.slices;
+    const uint32_t r0 = rb * uint32_t(a.scan_rows);
+    const int rows = int(min(uint32_t(a.V) - r0, uint32_t(a.scan_rows)));
+    // A key of V (nobody's) lies past the last row's workgroup.
+    const uint32_t key = tid < a.T ? load_key(src, tid) - r0 : ~0u;
+    const uint64_t mine = __ballot(key < uint32_t(rows));
+    if (lane == 0) count[wave] = __popcll(mine);
+    __syncthreads();
+    uint32_t total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      if (w < wave) before += count[w];
+      total += count[w];
     }
-    g = g * a.scale;
-    if constexpr (OP == EMB_GRAD) w = g;
-    if constexpr (OP == EMB_GRAD_ADD) w = w + g;
-    if constexpr (ADAM) adamw_vec4<OP == EMB_ADAMW_EXACT>(g, w, m, v, a.adam);
-    if constexpr (OP == EMB_SGDM) sgdm_vec4(g, w, m, a.sgd);
-    set4(a.W + i, w);
-    if constexpr (ADAM || OP == EMB_SGDM) set4(a.m + i, m);
-    if constexpr (ADAM) set4(a.v + i, v);
+    if (total > 0) {
+      if (key < uint32_t(rows))
+        found[before + __popcll(mine & ((uint64_t(1) << lane) - 1))] = uint32_t(tid) | key << 16;
+      if (tid < 4) found[total + tid] = ~0u;
+      __syncthreads();
+      // An entry's place is the number of smaller ones, a row's first place the
+      // number of entries of the rows before it.
+      auto smaller = [&](uint32_t than) {
+        uint32_t n = 0;
+#pragma unroll 4
+        for (uint32_t k = 0; k < total; k += 4) {
+          const u32x4_t f = *reinterpret_cast<const u32x4_t*>(&found[k]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) n += f[j] < than;
+        }
+        return n;
+      };
+      if (uint32_t(tid) < total) list[smaller(found[tid])] = uint16_t(found[tid]);
+      if (tid <= rows) first[tid] = smaller(uint32_t(tid) << 16);
+    } else if (tid <= rows) {
+      first[tid] = 0;
+    }
+    __syncthreads();
+    const int lanes = 1 << a.lanes_log2;
+    const int col = (int(slice << a.lanes_log2) + (tid & (lanes - 1))) * 4;
+    if (col < a.d)
+      for (int r = tid >> a.lanes_log2; r < rows; r += 256 >> a.lanes_log2) {
+        const uint32_t s = first[r], e = first[r + 1];
+        if (OP == EMB_GRAD_ADD && s == e) continue;
+        row_step<OP>(a, (int64_t(r0) + r) * a.d + col, [&](f32x4_t& g) {
+          add_terms<U>(g, s, e, [&](uint32_t k) {
+            return load_dy4<BF16>(a.dY, int64_t(list[k]) * a.d + col);
+          });
+        });
+      }
+    __syncthreads();                                   // the next rows reuse the LDS
   }
 }
 

@@ -101,23 +101,39 @@ forge_status launch_gradient_t(EmbeddingArgs a, hipStream_t s) {
   return launch_status();
 }
 
+// Few tokens: rows enough to a workgroup that looking through the ids is small
+// beside its rows' traffic, but not so many that the chip stands idle.
+template <int OP, bool BF16>
+forge_status launch_scan(EmbeddingArgs a, const IdSource& src, hipStream_t s) {
+  const int64_t wide = std::min<int64_t>(a.d, 1024);
+  a.scan_rows = int32_t(std::max<int64_t>(
+      1, std::min<int64_t>({int64_t(kScanRows), 4096 / wide, int64_t(a.V) * a.slices / 1024})));
+  a.blocks = uint32_t((a.V + a.scan_rows - 1) / a.scan_rows) * a.slices;
+  hipLaunchKernelGGL((embedding_scan_kernel<OP, BF16>), grid_for(a.blocks), dim3(kScanTokens), 0, s,
+                     a, src);
+  return launch_status();
+}
+
 template <int OP>
 forge_status launch_gradient(const void* ids, int32_t id_bytes, const void* dY, forge_dtype dY_dtype,
                              EmbeddingArgs a, void* workspace, void* stream) {
   if (forge_status s = check_device()) return s;
   (void)hipGetLastError();
-  if (!cut_rows(a, a.V, a.d / 4) || a.T / kSumChunk * (a.d / 1024 + 1) >= kMaxBlocks)
+  if (!cut_rows(a, a.V, a.d / 4) || int64_t(a.V) * a.slices >= kMaxBlocks ||
+      a.T / kSumChunk * (a.d / 1024 + 1) >= kMaxBlocks)
     return FORGE_ERR_SHAPE;
   const hipStream_t st = static_cast<hipStream_t>(stream);
+  const IdSource src{ids, id_bytes, uint32_t(a.V)};
+  a.dY = dY;
+  const bool bf16 = dY_dtype == FORGE_BF16;
+  if (a.T <= kScanTokens)
+    return bf16 ? launch_scan<OP, true>(a, src, st) : launch_scan<OP, false>(a, src, st);
   const EmbeddingWorkspace ws = embedding_workspace(a.T, a.V, a.d);
   char* const base = static_cast<char*>(workspace);
-  a.dY = dY;
   a.bound = reinterpret_cast<uint32_t*>(base + ws.bound);
   a.chunk = reinterpret_cast<float*>(base + ws.chunk);
-  if (forge_status s = launch_sort(IdSource{ids, id_bytes, uint32_t(a.V)}, ws, base, a.T, a, st))
-    return s;
-  return dY_dtype == FORGE_BF16 ? launch_gradient_t<OP, true>(a, st)
-                                : launch_gradient_t<OP, false>(a, st);
+  if (forge_status s = launch_sort(src, ws, base, a.T, a, st)) return s;
+  return bf16 ? launch_gradient_t<OP, true>(a, st) : launch_gradient_t<OP, false>(a, st);
 }
 
 EmbeddingArgs gradient_args(float* W, float* m, float* v, int64_t T, int64_t V, int64_t d,
