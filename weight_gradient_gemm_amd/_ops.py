@@ -70,9 +70,15 @@ def _check(status, where):
         raise ForgeError(status, where)
 
 
+_TORCH = None
+
+
 def _current(stream):
     """(torch, current device, stream handle) of a call; stream None: the current one."""
-    torch = _torch()
+    global _TORCH
+    if _TORCH is None:
+        _TORCH = _torch()
+    torch = _TORCH
     cur = torch.cuda.current_device()
     if stream is None:
         return torch, cur, torch._C._cuda_getCurrentRawStream(cur)
