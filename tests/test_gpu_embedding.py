@@ -273,3 +273,16 @@ def test_lookup_in_an_empty_table(env):
     ids = torch.tensor([0, -1, 4], device="cuda")
     wg.forge_embedding(torch.empty(0, 8, device="cuda"), ids, out)
     assert bool((out == 0).all())
+
+
+@pytest.mark.parametrize("types", ["f32-f32", "f32-bf16", "bf16-f32", "bf16-bf16"])
+def test_lookup_of_an_output_past_the_cache(env, types):
+    torch, wg = env
+    tt, ot = ({"f32": torch.float32, "bf16": torch.bfloat16}[k] for k in types.split("-"))
+    T, V, d = (1 << 27) // 1032 // (4 if ot == torch.float32 else 2) + 1, 50, 1032
+    table = torch.randn(V, d, device="cuda").to(tt)
+    ids = torch.arange(T, device="cuda", dtype=torch.int32) % (V + 1)
+    out = torch.empty(T, d, device="cuda", dtype=ot)
+    wg.forge_embedding(table, ids, out, scale=3.0)
+    want = torch.cat([table.float() * 3.0, torch.zeros(1, d, device="cuda")]).to(ot)
+    assert torch.equal(out, want[ids.long()])

@@ -541,9 +541,18 @@ struct LookupArgs {
   float scale;
 };
 
-// 8 columns of one token per thread.
-template <bool TABLE_BF16, bool OUT_BF16>
+// 8 columns of one token per thread. STREAM: stores with the non-temporal hint,
+// for outputs that would fill the 256 MB cache anyway. 16384 x 4096 bf16 (134
+// MB): 45 us against 52, with a reader behind it 76 against 75; 4096 tokens (34
+// MB): 13.0 against 14.2, and 22.6 against 22.3.
+template <bool TABLE_BF16, bool OUT_BF16, bool STREAM>
 __global__ __launch_bounds__(256) void embedding_kernel(LookupArgs a) {
+  auto put = [](const auto& v, auto* p) {
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(v, p);
+    else
+      *p = v;
+  };
   const int lanes = 1 << a.lanes_log2;
   for (uint32_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
     const uint32_t rb = b / a.slices, slice = b - rb * a.slices;
@@ -569,11 +578,11 @@ __global__ __launch_bounds__(256) void embedding_kernel(LookupArgs a) {
     const int64_t o = t * a.d + col;
     if constexpr (OUT_BF16) {
       const u32x2_t lo = pack_bf16x4(x[0]), hi = pack_bf16x4(x[1]);
-      *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.out) + o) = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+      put(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.out) + o));
     } else {
       f32x4_t* p = reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + o);
-      p[0] = x[0];
-      p[1] = x[1];
+      put(x[0], p);
+      put(x[1], p + 1);
     }
   }
 }

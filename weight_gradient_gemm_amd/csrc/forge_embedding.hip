@@ -12,6 +12,8 @@ namespace {
 // Most workgroups of 256 threads of a launch; what is beyond loops.
 constexpr int64_t kMaxGrid = int64_t(1) << 22;
 constexpr int64_t kMaxBlocks = int64_t(1) << 31;
+// Lookups of so many bytes do not leave their output in the caches.
+constexpr int64_t kStreamBytes = int64_t(1) << 27;
 
 // Threads across a row of `units` vectors, workgroups across it, and
 // workgroups in all for `rows` rows. False if they do not fit 31 bits (far more
@@ -136,6 +138,13 @@ forge_status launch_gradient(const void* ids, int32_t id_bytes, const void* dY, 
   return bf16 ? launch_gradient_t<OP, true>(a, st) : launch_gradient_t<OP, false>(a, st);
 }
 
+template <bool STREAM>
+void (*lookup_kernel(forge_dtype table, forge_dtype out))(LookupArgs) {
+  if (table == FORGE_BF16)
+    return out == FORGE_BF16 ? embedding_kernel<true, true, STREAM> : embedding_kernel<true, false, STREAM>;
+  return out == FORGE_BF16 ? embedding_kernel<false, true, STREAM> : embedding_kernel<false, false, STREAM>;
+}
+
 EmbeddingArgs gradient_args(float* W, float* m, float* v, int64_t T, int64_t V, int64_t d,
                             double scale) {
   EmbeddingArgs a{};
@@ -174,9 +183,9 @@ FORGE_API forge_status forge_embedding(const void* table, forge_dtype table_dtyp
   a.d = int32_t(d);
   a.scale = float(scale);
   if (!cut_rows(a, T, d / 8)) return FORGE_ERR_SHAPE;
-  const bool tb = table_dtype == FORGE_BF16, ob = out_dtype == FORGE_BF16;
-  const auto kernel = tb ? (ob ? embedding_kernel<true, true> : embedding_kernel<true, false>)
-                         : (ob ? embedding_kernel<false, true> : embedding_kernel<false, false>);
+  const bool stream_out = T * d * dtype_bytes(out_dtype) >= kStreamBytes;
+  const auto kernel = stream_out ? lookup_kernel<true>(table_dtype, out_dtype)
+                                 : lookup_kernel<false>(table_dtype, out_dtype);
   hipLaunchKernelGGL(kernel, grid_for(a.blocks), dim3(256), 0, static_cast<hipStream_t>(stream), a);
   return launch_status();
 }
