@@ -29,14 +29,15 @@ namespace forge {
 
 constexpr int kDigitBits = 9;                        // largest digit of a pass
 constexpr int kDigits = 1 << kDigitBits;
-constexpr int kOneThreads = 1024;                    // the one-workgroup sort
-constexpr int kOneRounds = 4;                        // its keys per thread
-constexpr int kSortOne = kOneThreads * kOneRounds;
+constexpr int kRankTokens = 8192;                   // tokens that are ranked by comparing all pairs
+constexpr int kRankKeys = 32;                        // of a workgroup then, 8 threads to a key
+constexpr int kSumThreads = 1024;
 constexpr int kTileThreads = 256;                    // a tile of the larger sort
 constexpr int kDirectTiles = 64;                     // tiles that sum their counts themselves
 constexpr int kSumChunk = 32;
 constexpr int kScanTokens = 256;                     // tokens that are looked through, not sorted
-constexpr int kScanRows = 64;                        // most rows of a workgroup then
+constexpr int kScanUnits = 4;                        // most 256-unit pieces of a workgroup then
+constexpr int kScanRows = kScanUnits * 256 / 2 + 1;  // and rows: two units or more, cut at both ends
 
 struct IdSource {
   const void* ids;
@@ -53,6 +54,32 @@ __device__ __forceinline__ int64_t load_id(const IdSource& src, int64_t t) {
 __device__ __forceinline__ uint32_t load_key(const IdSource& src, int64_t t) {
   const int64_t id = load_id(src, t);
   return id >= 0 && id < int64_t(src.V) ? uint32_t(id) : src.V;
+}
+
+// Sort keys of the tokens first, first + step, ... (N of them), ~0 past the
+// last: all loads in flight at once, behind one look at the ids' type.
+template <int N>
+__device__ __forceinline__ void load_keys(const IdSource& src, int64_t first, int64_t step, int64_t T,
+                                          uint32_t (&key)[N]) {
+  int64_t id[N];
+  if (src.bytes == 8) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int64_t t = first + j * step;
+      id[j] = static_cast<const int64_t*>(src.ids)[t < T ? t : T - 1];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int64_t t = first + j * step;
+      id[j] = static_cast<const int32_t*>(src.ids)[t < T ? t : T - 1];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t k = id[j] >= 0 && id[j] < int64_t(src.V) ? uint32_t(id[j]) : src.V;
+    key[j] = first + j * step < T ? k : ~0u;
+  }
 }
 
 // Lanes of this wave whose digit equals this lane's.
@@ -80,28 +107,26 @@ struct SortLds {
   uint32_t wave_total[WAVES];
 };
 
-// Ranks this wave's keys, `rounds` of 64 in ascending position: rank[j] is the
+// Ranks this wave's keys, R times 64 in ascending position: rank[j] is the
 // number of earlier keys of the wave with the same digit; count[wave] ends as
 // the wave's digit counts. The workgroup synchronises before and after.
 template <int WAVES, int R>
 __device__ __forceinline__ void rank_keys(SortLds<WAVES>& s, const uint32_t (&key)[R], uint32_t (&rank)[R],
-                                          int rounds, int shift, int bits) {
+                                          int shift, int bits) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   for (int d = lane; d < (1 << bits); d += 64) s.count[wave][d] = 0;
   const uint64_t lower = (uint64_t(1) << lane) - 1;
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    if (j < rounds) {
-      const uint32_t digit = (key[j] >> shift) & ((1u << bits) - 1u);
-      const uint64_t same = match_digit(digit, bits);
-      // One wave's LDS operations complete in order; wave_order() keeps the
-      // compiler's order the same.
-      wave_order();
-      const uint32_t before = s.count[wave][digit];
-      wave_order();
-      if ((same & lower) == 0) s.count[wave][digit] = before + __popcll(same);
-      rank[j] = before + __popcll(same & lower);
-    }
+    const uint32_t digit = (key[j] >> shift) & ((1u << bits) - 1u);
+    const uint64_t same = match_digit(digit, bits);
+    // One wave's LDS operations complete in order; wave_order() keeps the
+    // compiler's order the same.
+    wave_order();
+    const uint32_t before = s.count[wave][digit];
+    wave_order();
+    if ((same & lower) == 0) s.count[wave][digit] = before + __popcll(same);
+    rank[j] = before + __popcll(same & lower);
   }
 }
 
@@ -139,68 +164,49 @@ __device__ __forceinline__ uint32_t digit_total(const SortLds<WAVES>& s, int d) 
   return sum;
 }
 
-// Up to kSortOne tokens by one workgroup, in LDS (1021 tokens: 7.8 us).
-__global__ __launch_bounds__(kOneThreads) void sort_one_kernel(IdSource src, int T, int key_bits,
-                                                               uint32_t* keys, uint32_t* pos) {
-  constexpr int WAVES = kOneThreads / 64, R = kOneRounds;
-  __shared__ SortLds<WAVES> s;
-  __shared__ uint32_t lk[kSortOne];
-  __shared__ uint16_t lp[kSortOne];
-  static_assert(kSortOne <= 65536, "positions are kept in 16 bits");
-  static_assert(kDigits <= kOneThreads, "a thread to a digit");
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int rounds = (T + kOneThreads - 1) / kOneThreads;
-  const int first = wave * rounds * 64 + lane;
-  uint32_t key[R], p[R], rank[R];
+// Up to kRankTokens tokens in one launch: a token's place is the number of
+// smaller (key, position) pairs, counted by 8 threads that go through all keys
+// in LDS. T^2 comparisons are cheap beside the launches of a radix sort:
+// 1021 tokens 4.6 us, 6175 14.8; the tiles below take 21.
+__global__ __launch_bounds__(8 * kRankKeys) void rank_kernel(IdSource src, int T, uint32_t* keys,
+                                                             uint32_t* pos) {
+  __shared__ __attribute__((aligned(16))) uint32_t lk[kRankTokens];
+  const int tid = threadIdx.x, part = tid & 7;
+  const int padded = (T + 31) & ~31;                   // behind the last: larger than any key
+  for (int t0 = tid; t0 < padded; t0 += 8 * 8 * kRankKeys) {
+    uint32_t k[8];
+    load_keys(src, t0, 8 * kRankKeys, T, k);
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const int t = first + j * 64;
-    // Past the last token: behind every key, in every pass.
-    key[j] = j < rounds && t < T ? load_key(src, t) : 0xffffffffu;
-    p[j] = t;
+    for (int j = 0; j < 8; ++j)
+      if (t0 + j * 8 * kRankKeys < padded) lk[t0 + j * 8 * kRankKeys] = k[j];
   }
-  const int passes = (key_bits + kDigitBits - 1) / kDigitBits;
-  for (int k = 0; k < passes; ++k) {
-    const int shift = key_bits * k / passes, bits = key_bits * (k + 1) / passes - shift;
-    rank_keys(s, key, rank, rounds, shift, bits);
-    __syncthreads();
-    const int d = threadIdx.x;
-    const bool mine = d < (1 << bits);
-    const uint32_t at = block_exclusive(mine ? digit_total(s, d) : 0u, s.wave_total);
-    if (mine) place_waves(s, d, at);
-    __syncthreads();
-    const bool last = k + 1 == passes;
+  __syncthreads();
+  const int i = int(blockIdx.x) * kRankKeys + (tid >> 3);
+  if (i >= T) return;
+  const uint32_t key = lk[i];
+  const int own = i >> 2;                              // the group of four that holds i
+  uint32_t n = 0;
+#pragma unroll 4
+  for (int v = part; v < padded / 4; v += 8) {
+    const u32x4_t k = *reinterpret_cast<const u32x4_t*>(&lk[4 * v]);
+    const uint32_t than = v < own ? key + 1u : key;    // equal keys count where they come first
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (j < rounds) {
-        const uint32_t to = s.count[wave][(key[j] >> shift) & ((1u << bits) - 1u)] + rank[j];
-        if (!last) {
-          lk[to] = key[j];
-          lp[to] = uint16_t(p[j]);
-        } else if (to < uint32_t(T)) {
-          keys[to] = key[j];
-          pos[to] = p[j];
-        }
-      }
-    }
-    if (!last) {
-      __syncthreads();
+    for (int j = 0; j < 4; ++j) n += k[j] < than;
+  }
+  if (part == (own & 7))
+    for (int j = own * 4; j < i; ++j) n += lk[j] == key;
 #pragma unroll
-      for (int j = 0; j < R; ++j)
-        if (j < rounds) {
-          key[j] = lk[first + j * 64];
-          p[j] = lp[first + j * 64];
-        }
-      __syncthreads();
-    }
+  for (int d = 1; d < 8; d <<= 1) n += uint32_t(__shfl_xor(int(n), d));
+  if (part == 0) {
+    keys[n] = key;
+    pos[n] = uint32_t(i);
   }
 }
 
 // The larger sort, per pass: the digit counts of tiles of 256 R keys, and the
 // scatter. Up to kDirectTiles tiles, a tile adds up the counts that precede its
 // own itself (one launch less, and the counts come from L2); beyond, a launch
-// between the two turns them into places. R is 4 up to 65536 tokens (16384:
-// 21 us, where one workgroup took 38) and 16 beyond.
+// between the two turns them into places. R is 4 up to 65536 tokens and 16 beyond.
 // keys_in == nullptr: the first pass, from the ids.
 struct SortPass {
   IdSource src;
@@ -215,13 +221,21 @@ template <int R>
 __device__ __forceinline__ void load_tile(const SortPass& a, uint32_t (&key)[R], uint32_t (&p)[R]) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t first = int64_t(blockIdx.x) * (kTileThreads * R) + wave * R * 64 + lane;
+  if (!a.keys_in) {
+    load_keys(a.src, first, 64, a.T, key);
+#pragma unroll
+    for (int j = 0; j < R; ++j) p[j] = uint32_t(first + j * 64);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    const int64_t t = first + j * 64;
-    const bool in = t < a.T;
-    key[j] = !in ? 0xffffffffu : a.keys_in ? a.keys_in[t] : load_key(a.src, t);
-    p[j] = !in ? 0u : a.keys_in ? a.pos_in[t] : uint32_t(t);
+    const int64_t t = first + j * 64 < a.T ? first + j * 64 : a.T - 1;
+    key[j] = a.keys_in[t];
+    p[j] = a.pos_in[t];
   }
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+    if (first + j * 64 >= a.T) key[j] = ~0u;
 }
 
 template <int R, bool DIRECT>
@@ -229,7 +243,7 @@ __global__ __launch_bounds__(kTileThreads) void sort_count_kernel(SortPass a) {
   __shared__ SortLds<kTileThreads / 64> s;
   uint32_t key[R], p[R], rank[R];
   load_tile(a, key, p);
-  rank_keys(s, key, rank, R, a.shift, a.bits);
+  rank_keys(s, key, rank, a.shift, a.bits);
   __syncthreads();
   for (int d = threadIdx.x; d < (1 << a.bits); d += kTileThreads) {
     const int64_t at = DIRECT ? int64_t(blockIdx.x) * kDigits + d : int64_t(d) * a.tiles + blockIdx.x;
@@ -238,11 +252,11 @@ __global__ __launch_bounds__(kTileThreads) void sort_count_kernel(SortPass a) {
 }
 
 // Exclusive sum of n counts, in place, by one workgroup.
-__global__ __launch_bounds__(kOneThreads) void sort_sum_kernel(uint32_t* count, int64_t n) {
-  constexpr int WAVES = kOneThreads / 64, E = 8;
+__global__ __launch_bounds__(kSumThreads) void sort_sum_kernel(uint32_t* count, int64_t n) {
+  constexpr int WAVES = kSumThreads / 64, E = 8;
   __shared__ uint32_t wave_total[WAVES];
   uint32_t carry = 0;
-  for (int64_t k = 0; k < n; k += kOneThreads * E) {
+  for (int64_t k = 0; k < n; k += kSumThreads * E) {
     uint32_t v[E], sum = 0;
     const int64_t at = k + int64_t(threadIdx.x) * E;
 #pragma unroll
@@ -266,7 +280,7 @@ __global__ __launch_bounds__(kTileThreads) void sort_scatter_kernel(SortPass a) 
   __shared__ SortLds<kTileThreads / 64> s;
   uint32_t key[R], p[R], rank[R];
   load_tile(a, key, p);
-  rank_keys(s, key, rank, R, a.shift, a.bits);
+  rank_keys(s, key, rank, a.shift, a.bits);
   __syncthreads();
   // A thread takes the digits 2 t and 2 t + 1.
   static_assert(kDigits == 2 * kTileThreads, "two digits to a thread");
@@ -310,6 +324,30 @@ __global__ __launch_bounds__(kTileThreads) void sort_scatter_kernel(SortPass a) 
   }
 }
 
+// Work in units of a few columns, counted through all rows on end: workgroups
+// of 256 units then write whole lines and have no idle threads, whatever d is.
+// (With a workgroup to a row, or a slice of one, 112822 rows of 1384 float32
+// were written at 4.5 TB/s, rows of 1024 at 7.2.)
+struct Rows {
+  uint32_t units;      // of a row
+  uint32_t magic;      // ceil(2^20 / units), for units < 256
+};
+
+// Row and unit of place q < units + 256 of row `row`. Fewer than 512 units are
+// divided by multiplying: units * 512 < 2^20 makes it exact.
+__device__ __forceinline__ void carry(const Rows& r, uint32_t q, uint32_t& row, uint32_t& unit) {
+  const uint32_t over = r.units >= 256 ? uint32_t(q >= r.units) : (q * r.magic) >> 20;
+  row += over;
+  unit = q - over * r.units;
+}
+
+// Row and unit of the thread `tid` < 256 behind `first` units.
+__device__ __forceinline__ void locate(const Rows& r, uint64_t first, uint32_t tid, uint32_t& row,
+                                       uint32_t& unit) {
+  row = first >> 32 ? uint32_t(first / r.units) : uint32_t(first) / r.units;
+  carry(r, uint32_t(first - uint64_t(row) * r.units) + tid, row, unit);
+}
+
 struct EmbeddingArgs {
   const uint32_t *keys, *pos;      // sorted
   uint32_t* bound;                 // [V + 1]: first sorted place of each row
@@ -318,11 +356,11 @@ struct EmbeddingArgs {
   float *W, *m, *v;                // W: the gradient, where it is stored
   int64_t T;
   int32_t V, d;
-  int32_t lanes_log2;              // threads across a row in a workgroup
-  uint32_t slices;                 // workgroups across a row
+  Rows rows;                       // of 4-column units
+  uint32_t slices;                 // 1024-column slices of a row (chunk sums)
   uint32_t bound_blocks;           // workgroups of the bounds kernel that search
   uint32_t blocks;                 // workgroups of a pass (a launch may have fewer, and loop)
-  int32_t scan_rows;               // rows of a workgroup that looks through the ids
+  uint32_t scan_units;             // 256-unit pieces of a workgroup that looks through the ids
   float scale;
   AdamWConsts adam;
   SgdmConsts sgd;
@@ -434,18 +472,23 @@ __device__ __forceinline__ void row_step(const EmbeddingArgs& a, int64_t i, cons
   if constexpr (ADAM) set4(a.v + i, v);
 }
 
-// One row (or several short ones) per workgroup, 4 columns per thread.
-// 16384 tokens into 128256 x 4096 with AdamW: 2.2 ms, 12.7 GB (5.8 TB/s, what a
-// stream of reads and writes reaches).
+// Waves per SIMD that the rows' passes are compiled for: rows that are only
+// written need many in flight (128256 x 4096: 354 us with 8, 374 with 7). Four
+// pieces of 256 units to a workgroup instead of one took 395.
+template <int OP>
+constexpr int kRowWaves = OP == EMB_GRAD ? 8 : OP == EMB_GRAD_ADD ? 7 : 4;
+
+// 4 columns of one row per thread.
+// 16384 tokens into 128256 x 4096 with AdamW: 2.0-2.2 ms, 12.7 GB (5.9-6.2 TB/s,
+// what a stream of reads and writes reaches).
 template <int OP, bool BF16>
-__global__ __launch_bounds__(256) void embedding_rows_kernel(EmbeddingArgs a) {
+__global__ __launch_bounds__(256, kRowWaves<OP>) void embedding_rows_kernel(EmbeddingArgs a) {
   constexpr int U = OP == EMB_GRAD || OP == EMB_GRAD_ADD ? 8 : 16;
-  const int lanes = 1 << a.lanes_log2;
   for (uint32_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
-    const uint32_t rb = b / a.slices, slice = b - rb * a.slices;
-    const int row = int((rb << (8 - a.lanes_log2)) + (threadIdx.x >> a.lanes_log2));
-    const int col = (int(slice << a.lanes_log2) + (int(threadIdx.x) & (lanes - 1))) * 4;
-    if (row >= a.V || col >= a.d) continue;
+    uint32_t row, unit;
+    locate(a.rows, uint64_t(b) * 256, threadIdx.x, row, unit);
+    if (row >= uint32_t(a.V)) continue;
+    const int col = int(unit) * 4;
     const uint32_t s = a.bound[row], e = a.bound[row + 1];
     if (OP == EMB_GRAD_ADD && s == e) continue;
     row_step<OP>(a, int64_t(row) * a.d + col, [&](f32x4_t& g) {
@@ -463,8 +506,8 @@ __global__ __launch_bounds__(256) void embedding_rows_kernel(EmbeddingArgs a) {
   }
 }
 
-// Few tokens: no sort. A workgroup takes a.scan_rows rows of one slice of
-// columns, looks through all ids for its own, and lists its rows' tokens in
+// Few tokens: no sort. A workgroup takes a.scan_units * 256 units, looks
+// through all ids for those of its rows, and lists its rows' tokens in
 // ascending order in LDS: one launch instead of three. 256 tokens into 5003 x
 // 512: 5.7 us, where the sort and its successors take 13.3 for 257; all of one
 // row: 16.4 against 11.6. With the limit at 1024 the latter were 94 against 14.
@@ -472,16 +515,19 @@ template <int OP, bool BF16>
 __global__ __launch_bounds__(kScanTokens) void embedding_scan_kernel(EmbeddingArgs a, IdSource src) {
   constexpr int U = OP == EMB_GRAD || OP == EMB_GRAD_ADD ? 8 : 16;
   constexpr int WAVES = kScanTokens / 64;
+  static_assert(kScanTokens == 256, "an id to a thread");
   // Found tokens, each with its row in bits 16 and up, and four behind the last.
   __shared__ __attribute__((aligned(16))) uint32_t found[kScanTokens + 4];
   __shared__ uint16_t list[kScanTokens];               // tokens by row, ascending
   __shared__ uint32_t count[WAVES], first[kScanRows + 1];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   for (uint32_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
-    const uint32_t rb = b / a.slices, slice = b - rb * a.slices;
-    const uint32_t r0 = rb * uint32_t(a.scan_rows);
-    const int rows = int(min(uint32_t(a.V) - r0, uint32_t(a.scan_rows)));
-    // A key of V (nobody's) lies past the last row's workgroup.
+    const uint64_t unit0 = uint64_t(b) * a.scan_units * 256;
+    uint32_t r0, r1, unit;
+    locate(a.rows, unit0, 0, r0, unit);
+    locate(a.rows, unit0 + (a.scan_units - 1) * 256, 255, r1, unit);
+    const int rows = int(min(r1 + 1, uint32_t(a.V)) - r0);
+    // A key of V (nobody's) lies past the last row.
     const uint32_t key = tid < a.T ? load_key(src, tid) - r0 : ~0u;
     const uint64_t mine = __ballot(key < uint32_t(rows));
     if (lane == 0) count[wave] = __popcll(mine);
@@ -510,23 +556,24 @@ __global__ __launch_bounds__(kScanTokens) void embedding_scan_kernel(EmbeddingAr
         return n;
       };
       if (uint32_t(tid) < total) list[smaller(found[tid])] = uint16_t(found[tid]);
-      if (tid <= rows) first[tid] = smaller(uint32_t(tid) << 16);
-    } else if (tid <= rows) {
-      first[tid] = 0;
+      for (int r = tid; r <= rows; r += 256) first[r] = smaller(uint32_t(r) << 16);
+    } else {
+      for (int r = tid; r <= rows; r += 256) first[r] = 0;
     }
     __syncthreads();
-    const int lanes = 1 << a.lanes_log2;
-    const int col = (int(slice << a.lanes_log2) + (tid & (lanes - 1))) * 4;
-    if (col < a.d)
-      for (int r = tid >> a.lanes_log2; r < rows; r += 256 >> a.lanes_log2) {
-        const uint32_t s = first[r], e = first[r + 1];
-        if (OP == EMB_GRAD_ADD && s == e) continue;
-        row_step<OP>(a, (int64_t(r0) + r) * a.d + col, [&](f32x4_t& g) {
-          add_terms<U>(g, s, e, [&](uint32_t k) {
-            return load_dy4<BF16>(a.dY, int64_t(list[k]) * a.d + col);
-          });
+    for (uint32_t k = 0; k < a.scan_units; ++k) {
+      uint32_t row;
+      locate(a.rows, unit0 + k * 256, tid, row, unit);
+      if (row >= uint32_t(a.V)) break;
+      const int col = int(unit) * 4;
+      const uint32_t s = first[row - r0], e = first[row - r0 + 1];
+      if (OP == EMB_GRAD_ADD && s == e) continue;
+      row_step<OP>(a, int64_t(row) * a.d + col, [&](f32x4_t& g) {
+        add_terms<U>(g, s, e, [&](uint32_t t) {
+          return load_dy4<BF16>(a.dY, int64_t(list[t]) * a.d + col);
         });
-      }
+      });
+    }
     __syncthreads();                                   // the next rows reuse the LDS
   }
 }
@@ -536,8 +583,9 @@ struct LookupArgs {
   const void* table;
   void* out;
   int64_t T;
-  int32_t d, lanes_log2;
-  uint32_t slices, blocks;
+  int32_t d;
+  Rows rows;           // of 8-column units
+  uint32_t blocks;
   float scale;
 };
 
@@ -553,12 +601,11 @@ __global__ __launch_bounds__(256) void embedding_kernel(LookupArgs a) {
     else
       *p = v;
   };
-  const int lanes = 1 << a.lanes_log2;
   for (uint32_t b = blockIdx.x; b < a.blocks; b += gridDim.x) {
-    const uint32_t rb = b / a.slices, slice = b - rb * a.slices;
-    const int64_t t = (rb << (8 - a.lanes_log2)) + (threadIdx.x >> a.lanes_log2);
-    const int col = (int(slice << a.lanes_log2) + (int(threadIdx.x) & (lanes - 1))) * 8;
-    if (t >= a.T || col >= a.d) continue;
+    uint32_t t, unit;
+    locate(a.rows, uint64_t(b) * 256, threadIdx.x, t, unit);
+    if (t >= a.T) continue;
+    const int col = int(unit) * 8;
     const uint32_t row = load_key(a.src, t);
     f32x4_t x[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
     if (row < a.src.V) {
@@ -575,7 +622,7 @@ __global__ __launch_bounds__(256) void embedding_kernel(LookupArgs a) {
       x[0] = x[0] * a.scale;
       x[1] = x[1] * a.scale;
     }
-    const int64_t o = t * a.d + col;
+    const int64_t o = int64_t(t) * a.d + col;
     if constexpr (OUT_BF16) {
       const u32x2_t lo = pack_bf16x4(x[0]), hi = pack_bf16x4(x[1]);
       put(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.out) + o));

@@ -15,16 +15,13 @@ constexpr int64_t kMaxBlocks = int64_t(1) << 31;
 // Lookups of so many bytes do not leave their output in the caches.
 constexpr int64_t kStreamBytes = int64_t(1) << 27;
 
-// Threads across a row of `units` vectors, workgroups across it, and
-// workgroups in all for `rows` rows. False if they do not fit 31 bits (far more
-// than memory holds).
+// `count` rows of `units` each, and their workgroups of 256 * pieces units.
+// False if they do not fit 31 bits (far more than memory holds).
 template <class Args>
-bool cut_rows(Args& a, int64_t rows, int64_t units) {
-  a.lanes_log2 = 0;
-  while (a.lanes_log2 < 8 && (1 << a.lanes_log2) < units) ++a.lanes_log2;
-  const int64_t lanes = 1 << a.lanes_log2, per = 256 / lanes;
-  const int64_t slices = (units + lanes - 1) / lanes, blocks = (rows + per - 1) / per * slices;
-  a.slices = uint32_t(slices);
+bool cut_rows(Args& a, int64_t count, int64_t units, int64_t pieces = 1) {
+  a.rows.units = uint32_t(units);
+  a.rows.magic = uint32_t(((int64_t(1) << 20) + units - 1) / units);
+  const int64_t blocks = (count * units + 256 * pieces - 1) / (256 * pieces);
   a.blocks = uint32_t(blocks);
   return blocks < kMaxBlocks;
 }
@@ -43,7 +40,7 @@ forge_status launch_sort_pass(const SortPass& p, hipStream_t s) {
   hipLaunchKernelGGL((sort_count_kernel<R, DIRECT>), grid, threads, 0, s, p);
   if (forge_status st = launch_status()) return st;
   if (!DIRECT) {
-    hipLaunchKernelGGL(sort_sum_kernel, dim3(1), dim3(kOneThreads), 0, s, p.count,
+    hipLaunchKernelGGL(sort_sum_kernel, dim3(1), dim3(kSumThreads), 0, s, p.count,
                        int64_t(p.tiles) << p.bits);
     if (forge_status st = launch_status()) return st;
   }
@@ -61,9 +58,9 @@ forge_status launch_sort(const IdSource& src, const EmbeddingWorkspace& ws, char
   a.keys = keys[0];
   a.pos = pos[0];
   const int key_bits = bits_for(src.V);
-  if (T <= kSortOne) {
-    hipLaunchKernelGGL(sort_one_kernel, dim3(1), dim3(kOneThreads), 0, s, src, int(T), key_bits,
-                       keys[0], pos[0]);
+  if (T <= kRankTokens) {
+    hipLaunchKernelGGL(rank_kernel, dim3(uint32_t(T + kRankKeys - 1) / kRankKeys), dim3(8 * kRankKeys),
+                       0, s, src, int(T), keys[0], pos[0]);
     return launch_status();
   }
   const int passes = (key_bits + kDigitBits - 1) / kDigitBits;
@@ -103,14 +100,12 @@ forge_status launch_gradient_t(EmbeddingArgs a, hipStream_t s) {
   return launch_status();
 }
 
-// Few tokens: rows enough to a workgroup that looking through the ids is small
-// beside its rows' traffic, but not so many that the chip stands idle.
+// Few tokens: up to four pieces to a workgroup, so that looking through the ids
+// is small beside its rows' traffic, but not so many that the chip stands idle.
 template <int OP, bool BF16>
 forge_status launch_scan(EmbeddingArgs a, const IdSource& src, hipStream_t s) {
-  const int64_t wide = std::min<int64_t>(a.d, 1024);
-  a.scan_rows = int32_t(std::max<int64_t>(
-      1, std::min<int64_t>({int64_t(kScanRows), 4096 / wide, int64_t(a.V) * a.slices / 1024})));
-  a.blocks = uint32_t((a.V + a.scan_rows - 1) / a.scan_rows) * a.slices;
+  a.scan_units = uint32_t(std::max<int64_t>(1, std::min<int64_t>(kScanUnits, a.blocks / 1024)));
+  (void)cut_rows(a, a.V, a.d / 4, a.scan_units);
   hipLaunchKernelGGL((embedding_scan_kernel<OP, BF16>), grid_for(a.blocks), dim3(kScanTokens), 0, s,
                      a, src);
   return launch_status();
@@ -121,8 +116,7 @@ forge_status launch_gradient(const void* ids, int32_t id_bytes, const void* dY, 
                              EmbeddingArgs a, void* workspace, void* stream) {
   if (forge_status s = check_device()) return s;
   (void)hipGetLastError();
-  if (!cut_rows(a, a.V, a.d / 4) || int64_t(a.V) * a.slices >= kMaxBlocks ||
-      a.T / kSumChunk * (a.d / 1024 + 1) >= kMaxBlocks)
+  if (!cut_rows(a, a.V, a.d / 4) || a.T / kSumChunk * (a.d / 1024 + 1) >= kMaxBlocks)
     return FORGE_ERR_SHAPE;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const IdSource src{ids, id_bytes, uint32_t(a.V)};
