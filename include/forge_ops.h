@@ -8,8 +8,9 @@
  * caller, dense row-major arrays, 16-byte aligned pointers, nothing allocated,
  * no state between calls, validation before anything is launched,
  * asynchronous and ordered on `stream`, current device gfx950. Outputs must
- * not overlap each other or an input, unless said otherwise. Sums are float32 or wider and no call uses atomics, so
- * every result is bitwise the same from run to run.
+ * not overlap each other or an input, unless said otherwise. Sums are float32
+ * or wider and no call uses atomics, so every result is bitwise the same from
+ * run to run.
  *
  * Workspaces. Where a call takes `workspace`, it is caller-owned device memory
  * of at least the stated size, 16-byte aligned, overlapping nothing else; its
@@ -104,11 +105,11 @@ FORGE_API forge_status forge_sgdm_clipped(const forge_tensor* tensors, int32_t c
  * The embedding is the weight whose gradient is a sum over tokens without a
  * matrix product: g[r] = scale * sum over t with ids[t] == r of dY[t].
  *   ids [T] int32 or int64 (id_bytes 4 or 8, else FORGE_ERR_DTYPE), on the
- *   device. An id outside [0, V) is nobody's row: its lookup is a row of
+ *   device, aligned as such integers are. An id outside [0, V) is nobody's row: its lookup is a row of
  *   zeros and it adds to no gradient (padding, or the tokens of another
  *   shard of the vocabulary).
  *   scale: finite (else FORGE_ERR_HPARAM), rounded to float32.
- *   0 <= T < 2^30, 0 <= V <= 2^22, d a multiple of 8 up to 2^22. T == 0, V == 0
+ *   0 <= T <= 2^30, 0 <= V <= 2^22, d a multiple of 8 up to 2^22. T == 0, V == 0
  *   and d == 0 are allowed.
  */
 

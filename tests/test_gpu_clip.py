@@ -248,6 +248,8 @@ def test_binding_refuses(env):
         wg.forge_grad_norm(wg.ForgeTensorList([g[1:]]), norm, max_norm=1.0)
     with pytest.raises(wg.ForgeError, match="HPARAM"):
         wg.forge_grad_norm(wg.ForgeTensorList([g]), norm, max_norm=-1.0)
+    with pytest.raises(TypeError, match="ForgeTensorList"):
+        wg.forge_grad_norm([g], norm, max_norm=1.0)
     with pytest.raises(ValueError, match="2 elements"):
         wg.forge_grad_norm(wg.ForgeTensorList([g]), g, max_norm=1.0)
     small = torch.empty(64, dtype=torch.uint8, device="cuda")

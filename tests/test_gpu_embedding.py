@@ -257,6 +257,8 @@ def test_binding_refuses(env):
     with pytest.raises(wg.ForgeError, match="SHAPE"):
         wg.forge_embedding_grad(ids, out, table,
                                 workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(wg.ForgeError, match="SHAPE"):                # 2^22 rows are the most
+        wg.forge_embedding_grad(ids, out, torch.empty((1 << 22) + 1, 8, device="cuda"))
     with pytest.raises(wg.ForgeError, match="HPARAM"):
         wg.forge_embedding(table, ids, out, scale=math.nan)
     with pytest.raises(wg.ForgeError, match="ALIGN"):

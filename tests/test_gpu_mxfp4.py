@@ -325,8 +325,11 @@ def test_binding_refuses(env):
     op = wg.forge_mxfp4_empty(32, 64)
     with pytest.raises(ValueError, match="operand of 32 rows"):
         wg.forge_quantize_mxfp4(x, cols=op)
-    with pytest.raises(wg.ForgeError, match="NULL"):
-        wg.forge_quantize_mxfp4(x)
+    with pytest.raises(ValueError, match="operand of 32 rows"):
+        wg.forge_quantize_mxfp4(x[:0], rows=wg.forge_mxfp4_empty(0, 64), cols=op)
+    for v in (x, x[:0]):
+        with pytest.raises(wg.ForgeError, match="NULL"):
+            wg.forge_quantize_mxfp4(v)
     with pytest.raises(wg.ForgeError, match="ALIGN"):
         wg.forge_quantize_mxfp4(torch.zeros(32, 60, device="cuda"), rows=op)
     with pytest.raises(TypeError, match="float32 or bfloat16"):
@@ -343,4 +346,14 @@ def test_binding_refuses(env):
     with pytest.raises(wg.ForgeError, match="CLIP"):
         wg.forge_wgrad_adamw_mxfp4(op, op, out, out.clone(), out.clone(), step=1,
                                    max_grad_norm=1.0)
+    assert bool((out == 0).all())
+
+
+def test_quantise_nothing(env):
+    torch, wg = env
+    x = torch.empty(0, 64, device="cuda")
+    rows, cols = wg.forge_mxfp4_empty(0, 64), wg.forge_mxfp4_empty(64, 0)
+    wg.forge_quantize_mxfp4(x, rows=rows, cols=cols)
+    out = torch.ones(64, 64, device="cuda")
+    wg.forge_matmul_mxfp4(cols, cols, out)
     assert bool((out == 0).all())

@@ -120,14 +120,15 @@ def _two(t, name):
 
 
 def _workspace(torch, cur, nbytes, workspace, stream):
-    """`workspace`, or one of nbytes that belongs to the stream the call runs on."""
+    """`workspace`, or one of nbytes that belongs to the stream the call runs on
+    (of 16 where the sizes are out of range, for the library to say so)."""
     if workspace is not None:
         _in(workspace, torch.uint8, "workspace", cur)
         return workspace
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=cur)
+        return torch.empty(nbytes or 16, dtype=torch.uint8, device=cur)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=cur)
+        return torch.empty(nbytes or 16, dtype=torch.uint8, device=cur)
 
 
 # --------------------------------------------------------------------------
@@ -174,14 +175,18 @@ class ForgeTensorList:
         self.rows, self.count = rows, len(grads)
         self.device = grads[0].device.index if grads else None
 
-    def _args(self, cur, *need):
-        for name in need:
-            if name not in self.tensors:
-                raise ValueError(f"the list was built without {name}")
-        if self.device not in (None, cur):
-            raise ValueError(f"the list is on cuda:{self.device} but the current device is "
-                             f"cuda:{cur} (select it with torch.cuda.device)")
-        return self.rows, self.count
+
+def _listed(tensors, cur, *need):
+    """The C array of a list that has the fields `need`, and its length."""
+    if not isinstance(tensors, ForgeTensorList):
+        raise TypeError(f"tensors must be a ForgeTensorList, got {type(tensors).__name__}")
+    for name in need:
+        if name not in tensors.tensors:
+            raise ValueError(f"the list was built without {name}")
+    if tensors.device not in (None, cur):
+        raise ValueError(f"the list is on cuda:{tensors.device} but the current device is "
+                         f"cuda:{cur} (select it with torch.cuda.device)")
+    return tensors.rows, tensors.count
 
 
 def _norm2(torch, cur, norm):
@@ -197,7 +202,7 @@ def forge_grad_norm(tensors, norm, *, max_norm, workspace=None, stream=None) -> 
 
     ``norm`` is a float32 tensor of 2 elements; nothing is copied to the host."""
     torch, cur, st = _current(stream)
-    rows, count = tensors._args(cur)
+    rows, count = _listed(tensors, cur)
     out = _norm2(torch, cur, norm)
     lib = library()
     ws = _workspace(torch, cur, lib.forge_grad_norm_workspace(count), workspace, stream)
@@ -208,7 +213,7 @@ def forge_grad_norm(tensors, norm, *, max_norm, workspace=None, stream=None) -> 
 def forge_clip_grads(tensors, norm, *, stream=None) -> None:
     """out <- norm[1] * grad for every tensor of the list."""
     torch, cur, st = _current(stream)
-    rows, count = tensors._args(cur, "out")
+    rows, count = _listed(tensors, cur, "out")
     _check(library().forge_clip_grads(rows, count, _norm2(torch, cur, norm) + 4, st),
            "forge_clip_grads")
 
@@ -217,7 +222,7 @@ def forge_adamw_clipped(tensors, norm, *, step, lr=1e-3, beta1=0.9, beta2=0.999,
                         weight_decay=0.01, max_grad_norm=0.0, stream=None) -> None:
     """AdamW on W, m, v of every tensor of the list from norm[1] * grad."""
     torch, cur, st = _current(stream)
-    rows, count = tensors._args(cur, "W", "m", "v")
+    rows, count = _listed(tensors, cur, "W", "m", "v")
     p = _adamw(step, lr, beta1, beta2, eps, weight_decay, max_grad_norm)
     _check(library().forge_adamw_clipped(rows, count, _norm2(torch, cur, norm) + 4,
                                          ctypes.byref(p), st), "forge_adamw_clipped")
@@ -227,7 +232,7 @@ def forge_sgdm_clipped(tensors, norm, *, lr=1e-3, momentum=0.9, weight_decay=0.0
                        max_grad_norm=0.0, stream=None) -> None:
     """SGD-momentum on W, mom of every tensor of the list from norm[1] * grad."""
     torch, cur, st = _current(stream)
-    rows, count = tensors._args(cur, "W", "m")
+    rows, count = _listed(tensors, cur, "W", "m")
     p = SgdmParams(float(lr), float(momentum), float(weight_decay), float(max_grad_norm))
     _check(library().forge_sgdm_clipped(rows, count, _norm2(torch, cur, norm) + 4,
                                         ctypes.byref(p), st), "forge_sgdm_clipped")
@@ -390,10 +395,9 @@ def forge_quantize_mxfp4(x, *, rows=None, cols=None, stream=None) -> None:
         if on != n or ok != (k + 127) // 128 * 128:
             raise ValueError(f"{name} is an operand of {on} rows and padded length {ok}, not of "
                              f"{n} rows and length {k}")
-        if not (n and k):
-            return                           # x is empty: nothing to write
         ptrs += (cp, sp)
-    _check(library().forge_quantize_mxfp4(xp, code, R, C, *ptrs, st), "forge_quantize_mxfp4")
+    if ptrs != [None] * 4 or (rows is None and cols is None):    # else x is empty
+        _check(library().forge_quantize_mxfp4(xp, code, R, C, *ptrs, st), "forge_quantize_mxfp4")
 
 
 def forge_matmul_mxfp4(A, B, out, *, tile=_lib.FORGE_TILE_DEFAULT, stream=None) -> None:

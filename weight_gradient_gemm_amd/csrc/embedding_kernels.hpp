@@ -15,7 +15,9 @@
 // own; the row's pass then adds such sums, and the tokens before and after
 // them, in ascending order. A row of n tokens costs its pass at most
 // 2 (kSumChunk - 1) + n / kSumChunk additions in a row, and the order of
-// additions depends on the ids alone.
+// additions depends on the ids alone. Up to kRankTokens tokens a token's place
+// is counted instead (rank_kernel), up to kScanTokens nothing is sorted
+// (embedding_scan_kernel).
 //
 // No atomics: a wave ranks its 64 keys with ballots (lanes of equal digit),
 // and the lowest lane of each group advances the wave's own counter.

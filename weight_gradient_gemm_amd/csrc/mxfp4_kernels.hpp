@@ -7,7 +7,7 @@
 // scales [Kp / 128][R][4]: what one stage of the product takes of neighbouring
 // rows is contiguous. With rows of Kp / 2 bytes instead, a stage's 64 bytes of
 // each row were half lines at one distance, for a power of two all on one
-// channel of the L2 (MLP-down's product: ROWLAYOUT).
+// channel of the L2 (MLP-down's product at K 32768: 986 us against 845).
 #pragma once
 
 #include <type_traits>
