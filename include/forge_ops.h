@@ -51,7 +51,8 @@ typedef struct {
   forge_dtype grad_dtype; /* FORGE_F32 or FORGE_BF16                    */
 } forge_tensor;
 
-/* Most tensors of one list. */
+/* Most tensors of one list. Their addresses are below 2^52, as every device
+ * address is (else FORGE_ERR_ALIGN). */
 #define FORGE_MAX_TENSORS 65536
 
 /* Bytes of forge_grad_norm's workspace for `count` tensors, at least 16; 0 if

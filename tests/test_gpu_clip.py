@@ -166,6 +166,32 @@ def test_clipped_steps(env, name, dtypes):
             assert bool(((got[k].double().cpu() - w).abs() <= t).all()), (k, LISTS[name][k])
 
 
+@pytest.mark.parametrize("count", [63, 64, 65, 127, 128, 129, 160, 161, 257, 320, 321, 645])
+def test_lists_of_any_length(env, count):
+    # However the list is cut into launches, each tensor gets what it gets alone.
+    torch, wg = env
+    sizes = [1 + (k * 7919) % 6011 for k in range(count)]
+    grads, W, m, v = make(torch, sizes, "both", 41)
+    norm = torch.empty(2, device="cuda")
+    wg.forge_grad_norm(wg.ForgeTensorList(grads), norm, max_norm=0.5)
+    check_norm(norm, norm64(grads), 0.5)
+    st, one = ([[t.clone() for t in ts] for ts in (W, m, v)] for _ in range(2))
+    out, alone = [torch.full_like(g, 9.0) for g in grads], [torch.full_like(g, 9.0) for g in grads]
+    wg.forge_adamw_clipped(wg.ForgeTensorList(grads, W=st[0], m=st[1], v=st[2]), norm, **ADAM)
+    wg.forge_sgdm_clipped(wg.ForgeTensorList(grads, W=st[0], mom=st[1]), norm, **SGDM)
+    wg.forge_clip_grads(wg.ForgeTensorList(grads, out=out), norm)
+    for k in range(count):
+        tensors = wg.ForgeTensorList(grads[k:k + 1], out=alone[k:k + 1], W=one[0][k:k + 1],
+                                     m=one[1][k:k + 1], v=one[2][k:k + 1])
+        wg.forge_adamw_clipped(tensors, norm, **ADAM)
+        wg.forge_sgdm_clipped(tensors, norm, **SGDM)
+        wg.forge_clip_grads(tensors, norm)
+    torch.cuda.synchronize()
+    for k in range(count):
+        assert torch.equal(out[k], alone[k]), k
+        assert all(torch.equal(a[k], b[k]) for a, b in zip(st, one)), k
+
+
 @pytest.mark.parametrize("eps", [1e-8, 0.0])
 def test_coefficient_one_is_the_unclipped_step(env, eps):
     torch, wg = env

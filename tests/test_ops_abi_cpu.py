@@ -115,7 +115,7 @@ def test_norm_workspace_sizes(lib):
 @pytest.mark.parametrize("kw,status", [
     (dict(n=-1), E_SHAPE), (dict(n=(1 << 40) + 1), E_SHAPE), (dict(grad_dtype=2), E_DTYPE),
     (dict(grad=NULL), E_NULL), (dict(grad=A + 4), E_ALIGN), (dict(grad_dtype=-1), E_DTYPE),
-    (dict(grad=F), E_ALIAS), (dict(grad=F + 4096 - 16), E_ALIAS),
+    (dict(grad=F), E_ALIAS), (dict(grad=F + 4096 - 16), E_ALIAS), (dict(grad=1 << 52), E_ALIGN),
 ])
 def test_norm_rejects_tensors(lib, kw, status):
     assert norm(lib, tensor(), tensor(**kw)) == status

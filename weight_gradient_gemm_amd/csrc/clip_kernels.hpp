@@ -26,23 +26,49 @@
 namespace forge {
 
 // Tensors in one launch: the tables stay under 4 KB of kernel arguments.
-constexpr int kNormTensors = 256;
-constexpr int kClipTensors = 128;    // three addresses a tensor
-constexpr int kAdamTensors = 100;    // four
+constexpr int kNormTensors = 320;
+constexpr int kClipTensors = 160;    // three addresses a tensor
+constexpr int kAdamTensors = 128;    // four
 constexpr int kChunk = 4096;         // elements of a chunk
 constexpr int kNormGrid = 2048;      // most workgroups (and partial sums) of a norm launch
 constexpr int kNormAlone = 24;       // chunks that one workgroup sums by itself
 
-// The tensors of one launch, A addresses each. Tensor t has the chunks
-// first[t] .. first[t + 1] - 1, the last of them with tail[t] & 8191 elements;
-// bit 15 of tail[t] marks a bf16 gradient.
+// N 16-bit numbers, two to a word, so that they come by scalar loads.
+template <int N>
+struct Halves {
+  static_assert(N % 2 == 0, "two to a word");
+  uint32_t w[N / 2];
+  __host__ __device__ uint32_t operator[](int k) const { return w[k >> 1] >> (16 * (k & 1)) & 0xffffu; }
+  void set(int k, uint32_t v) {
+    const int s = 16 * (k & 1);
+    w[k >> 1] = (w[k >> 1] & ~(0xffffu << s)) | v << s;
+  }
+};
+
+// The tensors of one launch, A addresses each (of 16-byte aligned arrays below
+// 2^52: 6 bytes). Tensor t has the chunks first[t] .. first[t + 1] - 1, the last
+// of them with tail[t] & 8191 elements; bit 15 of tail[t] marks a bf16 gradient.
+// A list of 300 tensors takes one launch for the norm and two for an
+// SGD-momentum step; with 8-byte addresses it took two and three, and 24M
+// elements 100 us instead of 94 (and one tensor's norm and clip 201 instead of 203).
 template <int N_, int A_>
 struct TensorTable {
   static constexpr int N = N_, A = A_;
-  void* p[A][N];
+  uint32_t low[A][N];
+  Halves<N> high[A];
   int32_t first[N + 1];              // INT32_MAX past the last tensor's end
-  uint16_t tail[N];
+  Halves<N> tail;
   int32_t chunks;
+  __device__ __forceinline__ void* p(int a, int t) const {
+    // By way of the global address space, so that its accesses are global ones.
+    typedef __attribute__((address_space(1))) void global_void;
+    return (void*)(global_void*)((uint64_t(high[a][t]) << 32 | low[a][t]) << 4);
+  }
+  void set(int a, int t, const void* at, int64_t bytes) {
+    const uint64_t u = (reinterpret_cast<uintptr_t>(at) + uint64_t(bytes)) >> 4;
+    low[a][t] = uint32_t(u);
+    high[a].set(t, uint32_t(u >> 32));
+  }
 };
 typedef TensorTable<kNormTensors, 1> NormTable;     // gradient
 typedef TensorTable<kClipTensors, 3> ClipTable;     // gradient, and its place or W and momentum
@@ -160,8 +186,8 @@ __device__ __forceinline__ double square_sum(const void* g, int64_t k0, int64_t 
 template <class Table>
 __device__ __forceinline__ double tensor_square_sum(const Table& tab, int t, int64_t k0, int64_t k1, int me,
                                                     int threads) {
-  return tab.tail[t] >> 15 ? square_sum<true>(tab.p[0][t], k0, k1, me, threads)
-                           : square_sum<false>(tab.p[0][t], k0, k1, me, threads);
+  return tab.tail[t] >> 15 ? square_sum<true>(tab.p(0, t), k0, k1, me, threads)
+                           : square_sum<false>(tab.p(0, t), k0, k1, me, threads);
 }
 
 // Workgroup b sums its share of the chunks, a run of them, into part[b].
@@ -217,10 +243,10 @@ __device__ __forceinline__ void clip_chunk(const Table& tab, int t, int c, float
                                            const AdamWConsts& ac, const SgdmConsts& sc) {
   constexpr bool ADAM = OP == CLIP_ADAMW || OP == CLIP_ADAMW_EXACT;
   constexpr int G = kChunk / (256 * 4);
-  const void* const g_ = tab.p[0][t];
-  float* const W = static_cast<float*>(tab.p[1][t]);
-  float* const m = OP == CLIP_SCALE ? nullptr : static_cast<float*>(tab.p[Table::A > 2 ? 2 : 0][t]);
-  float* const v = ADAM ? static_cast<float*>(tab.p[Table::A > 3 ? 3 : 0][t]) : nullptr;
+  const void* const g_ = tab.p(0, t);
+  float* const W = static_cast<float*>(tab.p(1, t));
+  float* const m = OP == CLIP_SCALE ? nullptr : static_cast<float*>(tab.p(Table::A > 2 ? 2 : 0, t));
+  float* const v = ADAM ? static_cast<float*>(tab.p(Table::A > 3 ? 3 : 0, t)) : nullptr;
   const int64_t k0 = int64_t(c - tab.first[t]) * kChunk, n = end_of(tab, t, c);
   const int64_t k = k0 + int(threadIdx.x) * 4;
   auto get4 = [](const float* p) {

@@ -37,7 +37,7 @@ forge_status for_tables(const forge_tensor* tensors, int32_t count, const Fill& 
         if (forge_status s = flush()) return s;
       const int64_t n = std::min(tensors[i].n - at, (MAX_CHUNKS - chunks) * kChunk);
       fill(tab, used, tensors[i], at);
-      tab.tail[used] = uint16_t((n - 1) % kChunk + 1) | (tensors[i].grad_dtype == FORGE_BF16 ? 0x8000 : 0);
+      tab.tail.set(used, uint32_t((n - 1) % kChunk + 1) | (tensors[i].grad_dtype == FORGE_BF16 ? 0x8000u : 0u));
       tab.first[used] = int32_t(chunks);
       ++used;
       chunks += (n + kChunk - 1) / kChunk;
@@ -45,10 +45,6 @@ forge_status for_tables(const forge_tensor* tensors, int32_t count, const Fill& 
     }
   }
   return flush();
-}
-
-void* advance(const void* p, int64_t elems, int64_t bytes) {
-  return reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(p) + uint64_t(elems) * uint64_t(bytes));
 }
 
 template <int OP>
@@ -60,11 +56,14 @@ forge_status launch_steps(const forge_tensor* tensors, int32_t count, const floa
   return for_tables<Table, (int64_t(1) << 23)>(
       tensors, count,
       [](Table& tab, int k, const forge_tensor& t, int64_t at) {
-        const int gb = dtype_bytes(t.grad_dtype);
-        tab.p[0][k] = advance(t.grad, at, gb);
-        tab.p[1][k] = OP == CLIP_SCALE ? advance(t.out, at, gb) : advance(t.W, at, 4);
-        if constexpr (OP != CLIP_SCALE) tab.p[2][k] = advance(t.m, at, 4);
-        if constexpr (ADAM) tab.p[3][k] = advance(t.v, at, 4);
+        const int64_t gb = at * dtype_bytes(t.grad_dtype);
+        tab.set(0, k, t.grad, gb);
+        if constexpr (OP == CLIP_SCALE) tab.set(1, k, t.out, gb);
+        if constexpr (OP != CLIP_SCALE) {
+          tab.set(1, k, t.W, at * 4);
+          tab.set(2, k, t.m, at * 4);
+        }
+        if constexpr (ADAM) tab.set(3, k, t.v, at * 4);
       },
       [&](const Table& tab) {
         hipLaunchKernelGGL((clip_step_kernel<OP, Table>), dim3(tab.chunks), dim3(256), 0, s, tab,
@@ -103,7 +102,7 @@ FORGE_API forge_status forge_grad_norm(const forge_tensor* tensors, int32_t coun
   const forge_status s = for_tables<NormTable, kMaxListElems / kChunk + FORGE_MAX_TENSORS>(
       tensors, count,
       [](NormTable& tab, int k, const forge_tensor& t, int64_t at) {
-        tab.p[0][k] = advance(t.grad, at, dtype_bytes(t.grad_dtype));
+        tab.set(0, k, t.grad, at * dtype_bytes(t.grad_dtype));
       },
       [&](const NormTable& tab) {
         // A short list of few tensors: one workgroup, one launch.

@@ -48,6 +48,9 @@ class Ranges {
   int64_t n_ = 0;
 };
 
+// An array of a list: its table holds addresses below 2^52 (which all are).
+bool aligned_entry(const void* p) { return aligned16(p) && uint64_t(reinterpret_cast<uintptr_t>(p)) >> 52 == 0; }
+
 // Which of a tensor's fields a call uses, beside grad, n and grad_dtype.
 enum : int { USE_OUT = 1, USE_W_M = 2, USE_V = 4 };
 
@@ -63,9 +66,9 @@ forge_status check_list(const forge_tensor* tensors, int32_t count, int use) {
     if (!t.grad || ((use & USE_OUT) && !t.out) || ((use & USE_W_M) && (!t.W || !t.m)) ||
         ((use & USE_V) && !t.v))
       return FORGE_ERR_NULL;
-    if (!aligned16(t.grad) || ((use & USE_OUT) && !aligned16(t.out)) ||
-        ((use & USE_W_M) && (!aligned16(t.W) || !aligned16(t.m))) ||
-        ((use & USE_V) && !aligned16(t.v)))
+    if (!aligned_entry(t.grad) || ((use & USE_OUT) && !aligned_entry(t.out)) ||
+        ((use & USE_W_M) && (!aligned_entry(t.W) || !aligned_entry(t.m))) ||
+        ((use & USE_V) && !aligned_entry(t.v)))
       return FORGE_ERR_ALIGN;
     total += t.n;
     if (total > kMaxListElems) return FORGE_ERR_SHAPE;
@@ -103,7 +106,7 @@ forge_status check_clipped(const forge_tensor* tensors, int32_t count, const flo
 
 }  // namespace
 
-// One launch takes 256 tensors and leaves at most 2048 float64 partial sums.
+// A launch takes at least 256 tensors and leaves at most 2048 float64 partial sums.
 int64_t grad_norm_workspace(int32_t count) {
   if (count < 0 || count > FORGE_MAX_TENSORS) return 0;
   return std::max<int64_t>(16, (int64_t(count) + 255) / 256 * 2048 * 8);
