@@ -181,6 +181,42 @@ def test_matmul(env, M, N, K, dtype):
     assert all(torch.equal(outs[0], o) for o in outs[1:])
 
 
+def test_matmul_of_nan_in_the_last_rows(env):
+    # The rows past a tile's edge repeat the last one.
+    torch, wg = env
+    A, B = operands(torch, wg, 70, 136, 700, 3)
+    A.scales[2, 69, 1] = 255
+    out = torch.empty(70, 136, device="cuda")
+    for tile in TILES:
+        wg.forge_matmul_mxfp4(A, B, out, tile=tile)
+        assert bool(torch.isnan(out[69]).all()) and bool(torch.isfinite(out[:69]).all())
+
+
+def test_matmul_of_an_operand_beyond_31_bits(env):
+    # 2.7 GB of codes: rows of the large operand give what they give in a small one.
+    torch, wg = env
+    N, K, M = (1 << 21) + 8, 2560, 3
+    g = torch.Generator(device="cuda").manual_seed(4)
+
+    def random(R):
+        codes = torch.randint(0, 256, (K // 128, R, 64), dtype=torch.uint8, device="cuda", generator=g)
+        scales = torch.randint(120, 130, (K // 128, R, 4), dtype=torch.uint8, device="cuda",
+                               generator=g)
+        return codes, scales
+
+    A, (codes, scales) = random(M), random(N)
+    out = torch.empty(M, N, device="cuda")
+    wg.forge_matmul_mxfp4(A, (codes, scales), out)
+    for r in (0, 64, N // 2 - 8, N - 200, N - 72):
+        rows = slice(r, r + 72)
+        some = torch.empty(M, 72, device="cuda")
+        wg.forge_matmul_mxfp4(A, (codes[:, rows].contiguous(), scales[:, rows].contiguous()), some)
+        assert torch.equal(out[:, rows], some)
+    want, size, _ = product64(torch, wg.ForgeMxfp4(*A), wg.ForgeMxfp4(
+        codes[:, rows].contiguous(), scales[:, rows].contiguous()))
+    assert bool(((some.double().cpu() - want).abs() <= (K / 8 + K / 64 + 2) * 2 * U * size).all())
+
+
 def test_matmul_scales_by_block(env):
     """Blocks of very different scales: each lane's block takes its own scale."""
     torch, wg = env

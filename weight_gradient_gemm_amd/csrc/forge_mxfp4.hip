@@ -10,31 +10,34 @@
 namespace forge {
 namespace {
 
-// Tiles of the library's own choice, beside the public ids.
-enum : forge_tile { MX_TILE_128x64 = FORGE_TILE_COUNT, MX_TILE_64x64 };
+// Tiles of the library's own choice, beside the public ids. 64x64x2: slots of
+// two stages, more in flight for long contractions of few tiles.
+enum : forge_tile { MX_TILE_128x64 = FORGE_TILE_COUNT, MX_TILE_64x64, MX_TILE_64x64x2 };
 
 // The library's choice of tile: the least estimated time in microseconds, from
 // times measured on this kernel. A stage (128 columns) of a tile takes `alone`
 // where a CU has nothing else to do, and a CU with `slots` of them finishes one
 // every `full`; `ends` is what a round of tiles adds at its two ends. The
 // persistent schedule runs 256x256 tiles, its rounds counted in full tiles.
-// Sizes from 1 x 14336 x 4096 to 8191 x 14336 x 4096: within 12% of the fastest.
+// 23 sizes from 64 x 1024 x 128 to 4096 x 8192 x 8192: one 14% behind the fastest,
+// the others within 5%.
 forge_tile choose_tile(int64_t N, int64_t M, int64_t Kp) {
   struct Kind {
     forge_tile id;
-    int bm, bn, slots;
+    int bm, bn, slots, ring;       // ring: stages of a round of its LDS slots
     double alone, full, ends;
   };
-  static const Kind kinds[] = {{FORGE_TILE_256x256, 256, 256, 1, 0.595, 0.94, 7.1},
-                               {FORGE_TILE_256x128, 256, 128, 1, 0.367, 0.59, 5.0},
-                               {FORGE_TILE_128x128, 128, 128, 2, 0.24, 0.304, 3.6},
-                               {MX_TILE_128x64, 128, 64, 3, 0.205, 0.187, 3.2},
-                               {MX_TILE_64x64, 64, 64, 4, 0.171, 0.12, 2.8}};
-  const double stages = double((Kp / 128 + 3) / 4 * 4);     // whole rounds of 4
+  static const Kind kinds[] = {{FORGE_TILE_256x256, 256, 256, 1, 4, 0.47, 0.92, 8.5},
+                               {FORGE_TILE_256x128, 256, 128, 1, 4, 0.267, 0.48, 5.2},
+                               {FORGE_TILE_128x128, 128, 128, 2, 4, 0.175, 0.28, 3.8},
+                               {MX_TILE_128x64, 128, 64, 3, 4, 0.152, 0.17, 3.2},
+                               {MX_TILE_64x64, 64, 64, 4, 4, 0.115, 0.118, 2.8},
+                               {MX_TILE_64x64x2, 64, 64, 2, 8, 0.098, 0.108, 3.1}};
+  auto stages = [&](int ring) { return double((Kp / 128 + ring - 1) / ring * ring); };
   auto round = [&](const Kind& k, int64_t tiles) {
     if (tiles == 0) return 0.0;
     const double load = double(tiles) / 256.0;
-    return stages * std::max(k.alone, (load <= 1.0 ? load : std::ceil(load)) * k.full) + k.ends;
+    return stages(k.ring) * std::max(k.alone, (load <= 1.0 ? load : std::ceil(load)) * k.full) + k.ends;
   };
   forge_tile best = FORGE_TILE_256x256;
   double least = 0.0;
@@ -48,7 +51,7 @@ forge_tile choose_tile(int64_t N, int64_t M, int64_t Kp) {
   }
   const int grid = persistent_grid();
   const int64_t tiles = count_tiles(N, M, TileShape{256, 256});
-  if (grid > 0 && tiles >= grid && persistent_makespan(tiles, grid) * (stages * 0.9 + 7.1) < least)
+  if (grid > 0 && tiles >= grid && persistent_makespan(tiles, grid) * (stages(4) * 0.84 + 7.1) < least)
     best = FORGE_TILE_PERSISTENT;
   return best;
 }
@@ -65,6 +68,7 @@ struct MxLaunch {
   static forge_status run(WgradArgs a, const MxArgs& x, forge_tile tile, hipStream_t s) {
     switch (tile) {
       case MX_TILE_64x64: return launch_mx_t<Mx64x64, EPI>(a, x, s);
+      case MX_TILE_64x64x2: return launch_mx_t<Mx64x64x2, EPI>(a, x, s);
       case MX_TILE_128x64: return launch_mx_t<Mx128x64, EPI>(a, x, s);
       case FORGE_TILE_128x128: return launch_mx_t<Cfg128x128, EPI>(a, x, s);
       case FORGE_TILE_256x128: return launch_mx_t<Cfg256x128, EPI>(a, x, s);

@@ -217,12 +217,13 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_mxfp4_kernel(QuantArgs
 // straight from memory into a ring of 4 LDS slots, as the bf16 kernel (the same
 // bytes of operands per stage and tile). 16-byte chunk c of row r is kept at
 // chunk c ^ (r / 4 mod 4), which puts 16 neighbouring rows' reads on different
-// banks. Per stage, two k-steps of 64:
-//   step 0: request the second half of stage s + 3 into the previous slot; MFMAs;
+// banks. Per slot of one stage, two k-steps of 64:
+//   step 0: request the second half of slot s + 3 into the previous one; MFMAs;
 //   read step 1's operands from this slot.
-//   wait for this wave's LDS reads and for its loads of the next stage; barrier.
-//   step 1: request the first half of stage s + 4 into this slot; MFMAs; read the
+//   wait for this wave's LDS reads and for its loads of the next slot; barrier.
+//   step 1: request the first half of slot s + 4 into this one; MFMAs; read the
 //   scales and step 0's operands from the next slot.
+// Slots of two stages have four such steps, and the wait before the last.
 // Loads that queue up hold back the wave that issues them: with all of a stage's
 // in step 1, MLP-down's product took 222 us against 217, K 32768 805 against 785.
 // Columns enter each element in ascending steps of 64, whatever the tile.
@@ -233,28 +234,40 @@ struct MxArgs {
 
 // Tiles smaller than the other kernels have, for outputs that do not fill the
 // chip: fields as TileCfg.
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int OCC_>
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int OCC_, int KS_>
 struct SmallTileCfg {
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, BK = 32, OCC = OCC_;
+  static constexpr int KS = KS_;                        // stages of a slot
   static constexpr int WAVES = WAVES_M * WAVES_N, THREADS = 64 * WAVES;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 32, TN = WN / 32;
   static constexpr int STAGE = BK * (BM + BN);
   static_assert(WAVES == 4 && TM >= 1 && TN >= 1, "4 waves of whole MFMA blocks");
 };
-using Mx128x64 = SmallTileCfg<128, 64, 2, 2, 3>;
-using Mx64x64 = SmallTileCfg<64, 64, 2, 2, 4>;
+using Mx128x64 = SmallTileCfg<128, 64, 2, 2, 3, 1>;
+using Mx64x64 = SmallTileCfg<64, 64, 2, 2, 4, 1>;
+using Mx64x64x2 = SmallTileCfg<64, 64, 2, 2, 2, 2>;
 
-// 16-bit elements of a slot: a stage's codes and scale words.
+// Stages of a slot.
+template <class C, class = void>
+constexpr int mx_stages = 1;
+template <class C>
+constexpr int mx_stages<C, std::void_t<decltype(C::KS)>> = C::KS;
+
+// 16-bit elements of a stage's codes and scale words, and of a slot.
+template <class C>
+__host__ __device__ constexpr int mx_stage() {
+  return C::STAGE + 2 * (C::BM + C::BN);
+}
 template <class C>
 __host__ __device__ constexpr int mx_slot() {
-  return C::STAGE + 2 * (C::BM + C::BN);
+  return mx_stages<C> * mx_stage<C>();
 }
 
 // 4 bytes per lane from a buffer window straight into LDS: lane t writes at
 // dst + 4 t (see load16_to_lds).
-__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, uint16_t* dst, uint32_t voff) {
+__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, uint16_t* dst, uint32_t voff, int soff) {
   typedef __attribute__((address_space(3))) void lds_void;
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 4, voff, 0, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 4, voff, soff, 0, 0);
 }
 
 template <class C, int EPI>
@@ -266,8 +279,13 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
   constexpr int NQW = (QX + QY) / C::WAVES;             // 1 KB loads per wave and stage
   constexpr int SI = BM / 64, SO = BN / 64;             // 256-byte loads of scale words
   constexpr int NSW = (SI + SO + C::WAVES - 1) / C::WAVES;
-  constexpr int NL = NQW + NSW;                         // loads per wave and stage
-  constexpr int H = NL / 2 > NSW ? NL / 2 - NSW : 1;    // NSW + H of them are the first half
+  constexpr int KS = mx_stages<C>;
+  static_assert(KS <= 2, "a slot's halves are its stages");
+  constexpr int NL = KS * (NQW + NSW);                  // loads per wave and slot
+  // The first half of a slot's loads: its first stage, or the scales and H of the
+  // codes of its only one.
+  constexpr int H = KS > 1 ? NQW : NL / 2 > NSW ? NL / 2 - NSW : 1;
+  constexpr int NL0 = NSW + H, NL1 = NL - NL0;
   constexpr int kScales = RB * (BM + BN);               // their place in a slot
   static_assert((QX + QY) % C::WAVES == 0, "stage loads split evenly over the waves");
   static_assert(RB * (BM + BN) <= C::STAGE * 2, "stage exceeds a slot");
@@ -280,53 +298,78 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
   const int nk = int(x.kp / 128);
 
   // Loads: instruction q covers 16 rows of I (q < QX) or O, 1 KB on end; lane t
-  // fills row t / 4, physical chunk t % 4. Rows past the edge lie past the end
-  // of the window, and stages past the last have a window of no bytes: both
-  // read zeros. No branches: the compiler would sink MFMAs below them, out of
-  // their stage.
+  // fills row t / 4, physical chunk t % 4. Tiles with as many rows of I as of O
+  // have waves for each, others give every wave its share of both. Rows past the
+  // edge repeat the last one (their products are not stored). A window reaches
+  // from the tile's first row to the operand's end, so that stages past the last
+  // lie past its end and read zeros; a stage is an offset to it, and it moves on
+  // every round of slots. This keeps the scalar instructions few, of which a wave
+  // issues one every 8 cycles or so: with windows built for each stage, 1 x 4096 x
+  // 14336 took 18.8 us against 14.4, MLP-down's product with K 32768 785 against 769.
+  constexpr bool SIDES = QX == QY;
+  constexpr int NF = SIDES ? 1 : 2, QXW = SIDES ? NQW : QX / C::WAVES;
+  static_assert(SIDES ? QX % NQW == 0 : QX % C::WAVES == 0 && QY % C::WAVES == 0, "whole loads");
+  static_assert(SI % NSW == 0 && SO % NSW == 0, "a wave's scale loads are of one side");
+  const int left_i = d_in - i0, left_o = d_out > o0 ? d_out - o0 : 1;
+  const int row_o = d_out > o0 ? o0 : d_out - 1;        // a half tile may lie past the edge
+  struct Feed {
+    const uint8_t* p;
+    int64_t left, stage;                                // bytes to the end, and of a stage
+    __amdgpu_buffer_rsrc_t window;
+    __device__ __forceinline__ void open() {
+      window = window32(p, left < 0 ? 0u : uint32_t(left < 0x7fffffff ? left : 0x7fffffff));
+    }
+    __device__ __forceinline__ void advance(int stages) {
+      p += stage * stages;
+      left -= stage * stages;
+      open();
+    }
+  };
+  auto feed = [&](bool o_side, const void* i_base, const void* o_base, int row_bytes) {
+    const int rows = o_side ? d_out : d_in, row0 = o_side ? row_o : i0;
+    Feed f;
+    f.p = static_cast<const uint8_t*>(o_side ? o_base : i_base) + int64_t(row0) * row_bytes;
+    f.stage = int64_t(rows) * row_bytes;
+    f.left = f.stage * nk - int64_t(row0) * row_bytes;
+    f.open();
+    return f;
+  };
+  const int sq0 = wave * NSW % (SI + SO);               // with 6 loads for 4 waves, two are made twice
+  Feed codes[NF], scales = feed(sq0 >= SI, x.i_scales, x.o_scales, 4);
+  codes[0] = feed(SIDES && wave >= C::WAVES / 2, a.X, a.dY, RB);
+  if constexpr (!SIDES) codes[1] = feed(true, a.X, a.dY, RB);
   uint32_t voff[NQW], soff[NSW];
+  auto load_of = [&](int i) { return i < QXW ? wave * QXW + i : QX + wave * (NQW - QXW) + i - QXW; };
 #pragma unroll
   for (int i = 0; i < NQW; ++i) {
-    const int q = wave * NQW + i;
-    voff[i] = uint32_t((q < QX ? q : q - QX) * 1024 + (lane >> 2) * RB +
-                       (((lane & 3) ^ ((lane >> 4) & 3)) * 16));
+    const int q = load_of(i);
+    const int row = (q < QX ? q : q - QX) * 16 + (lane >> 2);
+    voff[i] = uint32_t(min(row, (q < QX ? left_i : left_o) - 1) * RB + ((lane & 3) ^ ((lane >> 4) & 3)) * 16);
   }
 #pragma unroll
   for (int i = 0; i < NSW; ++i) {
-    // With 6 loads for 4 waves, two of them are made twice: the same bytes.
-    const int q = (wave * NSW + i) % (SI + SO);
-    soff[i] = uint32_t((q < SI ? q : q - SI) * 256 + lane * 4);
+    const int q = sq0 + i;
+    soff[i] = uint32_t(min((q < SI ? q : q - SI) * 64 + lane, (q < SI ? left_i : left_o) - 1) * 4);
   }
-  const uint32_t left_i = uint32_t(d_in - i0), left_o = d_out > o0 ? uint32_t(d_out - o0) : 0u;
-  const uint8_t* gi = reinterpret_cast<const uint8_t*>(a.X) + int64_t(i0) * RB;
-  const uint8_t* go = reinterpret_cast<const uint8_t*>(a.dY) + int64_t(o0) * RB;
-  const uint8_t* si = x.i_scales + int64_t(i0) * 4;
-  const uint8_t* so = x.o_scales + int64_t(o0) * 4;
-  int g_stage = 0;
-  auto load_half = [&](uint16_t* slot, auto second) {
+  // The first or second half of slot j of a round.
+  auto load_half = [&](uint16_t* slot, int j, auto second) {
     constexpr bool SECOND = decltype(second)::value;
-    const uint32_t ni = g_stage < nk ? left_i : 0u, no = g_stage < nk ? left_o : 0u;
-    const __amdgpu_buffer_rsrc_t ri = window32(gi, ni * RB), ro = window32(go, no * RB);
-    if constexpr (!SECOND) {
-      const __amdgpu_buffer_rsrc_t qi = window32(si, ni * 4u), qo = window32(so, no * 4u);
+    const int u = KS * j + (SECOND && KS > 1);
+    if constexpr (SECOND && KS > 1) slot += mx_stage<C>();
+    if constexpr (!SECOND || KS > 1)
 #pragma unroll
-      for (int i = 0; i < NSW; ++i) {
-        const int q = (wave * NSW + i) % (SI + SO);
-        load4_to_lds(q < SI ? qi : qo, slot + kScales / 2 + q * 128, soff[i]);
-      }
-    }
+      for (int i = 0; i < NSW; ++i)
+        load4_to_lds(scales.window, slot + kScales / 2 + (sq0 + i) * 128, soff[i], int(scales.stage) * u);
 #pragma unroll
-    for (int i = SECOND ? H : 0; i < (SECOND ? NQW : H); ++i) {
-      const int q = wave * NQW + i;
-      load16_to_lds(q < QX ? ri : ro, slot + q * 512, voff[i], 0);
+    for (int i = SECOND && KS == 1 ? H : 0; i < (SECOND ? NQW : H); ++i) {
+      const Feed& f = codes[i < QXW ? 0 : NF - 1];
+      load16_to_lds(f.window, slot + load_of(i) * 512, voff[i], int(f.stage) * u);
     }
-    if constexpr (SECOND) {
-      gi += int64_t(d_in) * RB;
-      go += int64_t(d_out) * RB;
-      si += int64_t(d_in) * 4;
-      so += int64_t(d_out) * 4;
-      ++g_stage;
-    }
+  };
+  auto advance = [&]() {
+#pragma unroll
+    for (int k = 0; k < NF; ++k) codes[k].advance(4 * KS);
+    scales.advance(4 * KS);
   };
   const std::false_type first_half{};
   const std::true_type second_half{};
@@ -403,7 +446,7 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
     }
   };
   constexpr int kWaitMid = waitcnt_imm(2 * NL, 0);
-  constexpr int kWaitFirst = waitcnt_imm(2 * NL + NSW + H, 15);
+  constexpr int kWaitFirst = waitcnt_imm(2 * NL + NL0, 15);
 #define FORGE_MX_BARRIER(IMM)                 \
   do {                                        \
     __builtin_amdgcn_sched_barrier(0);        \
@@ -413,37 +456,53 @@ __device__ __forceinline__ void mxfp4_tile(const WgradArgs& a, const MxArgs& x, 
     asm volatile("" ::: "memory");            \
     __builtin_amdgcn_sched_barrier(0);        \
   } while (0)
-  auto stage = [&](uint16_t* prv, uint16_t* cur, uint16_t* nxt) {
+  // Slot j of a round of four.
+  auto run_slot = [&](uint16_t* prv, uint16_t* cur, uint16_t* nxt, int j) {
     shift_scales();
-    load_half(prv, second_half);                 // of stage s + 3
+    load_half(prv, (j + 3) % 4, second_half);    // of slot s + 3
+    if (j == 0) advance();
     read_frags(1, cur, 1);
     mfmas0();
-    interleave(TM + TN, NQW - H);
+    interleave(TM + TN, NL1);
+    if constexpr (KS > 1) {                      // its second stage
+      __builtin_amdgcn_sched_barrier(0);
+      const uint16_t* const two = cur + mx_stage<C>();
+      read_scales(two);
+      read_frags(0, two, 0);
+      mfmas1();
+      interleave(2 * (TM + TN), 0);
+      __builtin_amdgcn_sched_barrier(0);
+      shift_scales();
+      read_frags(1, two, 1);
+      mfmas0();
+      interleave(TM + TN, 0);
+    }
     FORGE_MX_BARRIER(kWaitMid);
-    load_half(cur, first_half);                  // of stage s + 4, into the freed slot
+    load_half(cur, j, first_half);               // of slot s + 4, into the freed one
     read_scales(nxt);
     read_frags(0, nxt, 0);
     mfmas1();
-    interleave(2 * (TM + TN), NSW + H);
+    interleave(2 * (TM + TN), NL0);
     __builtin_amdgcn_sched_barrier(0);
   };
   if (nk > 0) {
-    for (uint16_t* slot : {sl.s0, sl.s1, sl.s2}) {
-      load_half(slot, first_half);
-      load_half(slot, second_half);
+    for (int j = 0; j < 3; ++j) {
+      uint16_t* const slot = j == 0 ? sl.s0 : j == 1 ? sl.s1 : sl.s2;
+      load_half(slot, j, first_half);
+      load_half(slot, j, second_half);
     }
-    load_half(sl.s3, first_half);
+    load_half(sl.s3, 3, first_half);
     FORGE_MX_BARRIER(kWaitFirst);
     read_scales(sl.s0);
     read_frags(0, sl.s0, 0);
-    // Whole rounds of 4 stages: the accumulators keep their registers. Stages
+    // Whole rounds of 4 slots: the accumulators keep their registers. Stages
     // past the last add products of zero codes and zero scale bytes: exactly +0.
-    const int rounds = (nk + 3) / 4;
+    const int rounds = (nk + 4 * KS - 1) / (4 * KS);
     for (int r = 0; r < rounds; ++r) {
-      stage(sl.s3, sl.s0, sl.s1);
-      stage(sl.s0, sl.s1, sl.s2);
-      stage(sl.s1, sl.s2, sl.s3);
-      stage(sl.s2, sl.s3, sl.s0);
+      run_slot(sl.s3, sl.s0, sl.s1, 0);
+      run_slot(sl.s0, sl.s1, sl.s2, 1);
+      run_slot(sl.s1, sl.s2, sl.s3, 2);
+      run_slot(sl.s2, sl.s3, sl.s0, 3);
     }
   }
 #undef FORGE_MX_BARRIER
