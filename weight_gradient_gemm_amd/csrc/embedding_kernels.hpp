@@ -10,11 +10,11 @@
 // the gradient or steps the optimizer at once. Ids outside [0, V) get the key
 // V and end up behind the last row.
 //
-// Frequent ids: the sorted order is cut into chunks of kSumChunk tokens. A
-// chunk that lies within one row is summed beforehand by workgroups of its
+// Frequent ids: the sorted order is cut into chunks of C = 32 tokens (128 or
+// 256 of many: see embedding_chunk_bits). A chunk that lies within one row is summed beforehand by workgroups of its
 // own; the row's pass then adds such sums, and the tokens before and after
 // them, in ascending order. A row of n tokens costs its pass at most
-// 2 (kSumChunk - 1) + n / kSumChunk additions in a row, and the order of
+// 2 (C - 1) + n / C additions in a row, and the order of
 // additions depends on the ids alone. Up to kRankTokens tokens a token's place
 // is counted instead (rank_kernel), up to kScanTokens nothing is sorted
 // (embedding_scan_kernel).
@@ -36,7 +36,6 @@ constexpr int kRankKeys = 32;                        // of a workgroup then, 8 t
 constexpr int kSumThreads = 1024;
 constexpr int kTileThreads = 256;                    // a tile of the larger sort
 constexpr int kDirectTiles = 64;                     // tiles that sum their counts themselves
-constexpr int kSumChunk = 32;
 constexpr int kScanTokens = 256;                     // tokens that are looked through, not sorted
 constexpr int kScanUnits = 4;                        // most 256-unit pieces of a workgroup then
 constexpr int kScanRows = kScanUnits * 256 / 2 + 1;  // and rows: two units or more, cut at both ends
@@ -353,11 +352,11 @@ __device__ __forceinline__ void locate(const Rows& r, uint64_t first, uint32_t t
 struct EmbeddingArgs {
   const uint32_t *keys, *pos;      // sorted
   uint32_t* bound;                 // [V + 1]: first sorted place of each row
-  float* chunk;                    // [T / kSumChunk, d]: sums of chunks within one row
+  float* chunk;                    // [T >> chunk_bits, d]: sums of chunks within one row
   const void* dY;
   float *W, *m, *v;                // W: the gradient, where it is stored
   int64_t T;
-  int32_t V, d;
+  int32_t V, d, chunk_bits;
   Rows rows;                       // of 4-column units
   uint32_t slices;                 // 1024-column slices of a row (chunk sums)
   uint32_t bound_blocks;           // workgroups of the bounds kernel that search
@@ -433,12 +432,12 @@ __global__ __launch_bounds__(256) void embedding_bounds_kernel(EmbeddingArgs a) 
       continue;
     }
     const uint32_t c = (b - a.bound_blocks) / a.slices, slice = b - a.bound_blocks - c * a.slices;
-    const uint32_t s = c * kSumChunk, key = a.keys[s];
-    if (key >= uint32_t(a.V) || a.keys[s + kSumChunk - 1] != key) continue;
+    const uint32_t s = c << a.chunk_bits, e = s + (1u << a.chunk_bits), key = a.keys[s];
+    if (key >= uint32_t(a.V) || a.keys[e - 1] != key) continue;
     const int col = int(slice * 256 + threadIdx.x) * 4;
     if (col < a.d) {
       f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-      add_tokens<16, BF16>(a, acc, s, s + kSumChunk, col);
+      add_tokens<16, BF16>(a, acc, s, e, col);
       *reinterpret_cast<f32x4_t*>(a.chunk + int64_t(c) * a.d + col) = acc;
     }
   }
@@ -494,13 +493,13 @@ __global__ __launch_bounds__(256, kRowWaves<OP>) void embedding_rows_kernel(Embe
     const uint32_t s = a.bound[row], e = a.bound[row + 1];
     if (OP == EMB_GRAD_ADD && s == e) continue;
     row_step<OP>(a, int64_t(row) * a.d + col, [&](f32x4_t& g) {
-      const uint32_t c0 = (s + kSumChunk - 1) / kSumChunk, c1 = e / kSumChunk;
+      const uint32_t c0 = (s + (1u << a.chunk_bits) - 1) >> a.chunk_bits, c1 = e >> a.chunk_bits;
       if (c0 < c1) {
-        add_tokens<U, BF16>(a, g, s, c0 * kSumChunk, col);
+        add_tokens<U, BF16>(a, g, s, c0 << a.chunk_bits, col);
         add_terms<U>(g, c0, c1, [&](uint32_t c) {
           return *reinterpret_cast<const f32x4_t*>(a.chunk + int64_t(c) * a.d + col);
         });
-        add_tokens<U, BF16>(a, g, c1 * kSumChunk, e, col);
+        add_tokens<U, BF16>(a, g, c1 << a.chunk_bits, e, col);
       } else {
         add_tokens<U, BF16>(a, g, s, e, col);
       }

@@ -93,7 +93,7 @@ forge_status launch_gradient_t(EmbeddingArgs a, hipStream_t s) {
   EmbeddingArgs b = a;
   b.bound_blocks = uint32_t(a.V + 256) / 256;
   b.slices = uint32_t(a.d / 4 + 255) / 256;
-  b.blocks = b.bound_blocks + uint32_t(a.T / kSumChunk) * b.slices;
+  b.blocks = b.bound_blocks + uint32_t(a.T >> a.chunk_bits) * b.slices;
   hipLaunchKernelGGL((embedding_bounds_kernel<BF16>), grid_for(b.blocks), dim3(256), 0, s, b);
   if (forge_status st = launch_status()) return st;
   hipLaunchKernelGGL((embedding_rows_kernel<OP, BF16>), grid_for(a.blocks), dim3(256), 0, s, a);
@@ -116,7 +116,7 @@ forge_status launch_gradient(const void* ids, int32_t id_bytes, const void* dY, 
                              EmbeddingArgs a, void* workspace, void* stream) {
   if (forge_status s = check_device()) return s;
   (void)hipGetLastError();
-  if (!cut_rows(a, a.V, a.d / 4) || a.T / kSumChunk * (a.d / 1024 + 1) >= kMaxBlocks)
+  if (!cut_rows(a, a.V, a.d / 4) || (a.T >> a.chunk_bits) * (a.d / 1024 + 1) >= kMaxBlocks)
     return FORGE_ERR_SHAPE;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const IdSource src{ids, id_bytes, uint32_t(a.V)};
@@ -148,6 +148,7 @@ EmbeddingArgs gradient_args(float* W, float* m, float* v, int64_t T, int64_t V, 
   a.T = T;
   a.V = int32_t(V);
   a.d = int32_t(d);
+  a.chunk_bits = embedding_chunk_bits(T);
   a.scale = float(scale);
   return a;
 }

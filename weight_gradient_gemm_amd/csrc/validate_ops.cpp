@@ -151,7 +151,7 @@ bool embedding_sizes_ok(int64_t T, int64_t V, int64_t d) {
 }
 
 // Two copies of (key, position) for the sort's passes, its digit counts (512
-// for each tile of 1024 tokens), the rows' bounds, and the sums of chunks of 32
+// for each tile of 1024 tokens), the rows' bounds, and the sums of chunks of
 // tokens.
 EmbeddingWorkspace embedding_workspace(int64_t T, int64_t V, int64_t d) {
   EmbeddingWorkspace w{};
@@ -167,7 +167,7 @@ EmbeddingWorkspace embedding_workspace(int64_t T, int64_t V, int64_t d) {
   }
   w.count = take((T + 1023) / 1024 * 512 * 4);
   w.bound = take(4 * (V + 1));
-  w.chunk = take(T / 32 * d * 4);
+  w.chunk = take((T >> embedding_chunk_bits(T)) * d * 4);
   w.bytes = at;
   return w;
 }

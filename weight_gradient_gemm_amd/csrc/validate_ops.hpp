@@ -28,6 +28,14 @@ forge_status validate_sgdm_clipped(const forge_tensor* tensors, int32_t count, c
 struct EmbeddingWorkspace {
   int64_t keys[2], pos[2], count, bound, chunk, bytes;
 };
+// Tokens whose sum is formed ahead of a row's, as a power of two. A row of n
+// tokens adds up at most 2 (C - 1) + n / C terms one after the other: 32 serve
+// frequent ids of thousands of tokens, more those of tens of thousands. Of
+// 262144 tokens into 32000 x 1024 with 71500 of one id: 352 us with 32, 207 with
+// 128 (spread evenly 190 with both). Of 1048576 into 32000 x 512 with 286000: 1085
+// with 32, 548 with 128, 458 with 256, 461 with 512; evenly into 300 rows 408, -,
+// 445 and 502.
+inline int embedding_chunk_bits(int64_t T) { return T <= 32768 ? 5 : T <= 524288 ? 7 : 8; }
 bool embedding_sizes_ok(int64_t T, int64_t V, int64_t d);
 EmbeddingWorkspace embedding_workspace(int64_t T, int64_t V, int64_t d);
 forge_status validate_embedding(const void* table, forge_dtype table_dtype, const void* ids,
