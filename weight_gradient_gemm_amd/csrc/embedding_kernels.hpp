@@ -33,8 +33,9 @@ constexpr int kDigitBits = 9;                        // largest digit of a pass
 constexpr int kDigits = 1 << kDigitBits;
 constexpr int kRankTokens = 8192;                   // tokens that are ranked by comparing all pairs
 constexpr int kRankKeys = 32;                        // of a workgroup then, 8 threads to a key
-constexpr int kSumThreads = 1024;
 constexpr int kTileThreads = 256;                    // a tile of the larger sort
+constexpr int kTileR = 4;                            // keys of a thread
+constexpr int kTileKeys = kTileThreads * kTileR;
 constexpr int kDirectTiles = 64;                     // tiles that sum their counts themselves
 constexpr int kScanTokens = 256;                     // tokens that are looked through, not sorted
 constexpr int kScanUnits = 4;                        // most 256-unit pieces of a workgroup then
@@ -204,24 +205,25 @@ __global__ __launch_bounds__(8 * kRankKeys) void rank_kernel(IdSource src, int T
   }
 }
 
-// The larger sort, per pass: the digit counts of tiles of 256 R keys, and the
-// scatter. Up to kDirectTiles tiles, a tile adds up the counts that precede its
-// own itself (one launch less, and the counts come from L2); beyond, a launch
-// between the two turns them into places. R is 4 up to 65536 tokens and 16 beyond.
+// The larger sort, per pass: the digit counts of tiles of 1024 keys, and the
+// scatter. Up to kDirectTiles tiles a tile adds up the counts that precede its
+// own itself (65536 tokens: 12.9 us a pass); beyond, a launch between the two
+// forms the sums (262144 tokens: 17 us; 31 with direct tiles of 4096 keys).
 // keys_in == nullptr: the first pass, from the ids.
 struct SortPass {
   IdSource src;
   const uint32_t *keys_in, *pos_in;
   uint32_t *keys_out, *pos_out;
   uint32_t* count;     // direct: [tiles][kDigits]; else [digits][tiles]
+  uint32_t* total;     // else: of each digit
   int64_t T;
   int32_t tiles, shift, bits;
 };
 
-template <int R>
-__device__ __forceinline__ void load_tile(const SortPass& a, uint32_t (&key)[R], uint32_t (&p)[R]) {
+__device__ __forceinline__ void load_tile(const SortPass& a, uint32_t (&key)[kTileR], uint32_t (&p)[kTileR]) {
+  constexpr int R = kTileR;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t first = int64_t(blockIdx.x) * (kTileThreads * R) + wave * R * 64 + lane;
+  const int64_t first = int64_t(blockIdx.x) * kTileKeys + wave * R * 64 + lane;
   if (!a.keys_in) {
     load_keys(a.src, first, 64, a.T, key);
 #pragma unroll
@@ -239,10 +241,10 @@ __device__ __forceinline__ void load_tile(const SortPass& a, uint32_t (&key)[R],
     if (first + j * 64 >= a.T) key[j] = ~0u;
 }
 
-template <int R, bool DIRECT>
+template <bool DIRECT>
 __global__ __launch_bounds__(kTileThreads) void sort_count_kernel(SortPass a) {
   __shared__ SortLds<kTileThreads / 64> s;
-  uint32_t key[R], p[R], rank[R];
+  uint32_t key[kTileR], p[kTileR], rank[kTileR];
   load_tile(a, key, p);
   rank_keys(s, key, rank, a.shift, a.bits);
   __syncthreads();
@@ -252,34 +254,27 @@ __global__ __launch_bounds__(kTileThreads) void sort_count_kernel(SortPass a) {
   }
 }
 
-// Exclusive sum of n counts, in place, by one workgroup.
-__global__ __launch_bounds__(kSumThreads) void sort_sum_kernel(uint32_t* count, int64_t n) {
-  constexpr int WAVES = kSumThreads / 64, E = 8;
-  __shared__ uint32_t wave_total[WAVES];
+// A digit's counts over the tiles, by a workgroup: their exclusive sums, in place,
+// and the digit's total.
+__global__ __launch_bounds__(kTileThreads) void sort_sum_kernel(SortPass a) {
+  __shared__ uint32_t wave_total[kTileThreads / 64];
+  uint32_t* const count = a.count + int64_t(blockIdx.x) * a.tiles;
   uint32_t carry = 0;
-  for (int64_t k = 0; k < n; k += kSumThreads * E) {
-    uint32_t v[E], sum = 0;
-    const int64_t at = k + int64_t(threadIdx.x) * E;
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      v[j] = at + j < n ? count[at + j] : 0;
-      sum += v[j];
-    }
-    uint32_t before = carry + block_exclusive(sum, wave_total);
-    for (int w = 0; w < WAVES; ++w) carry += wave_total[w];
+  for (int k = 0; k < a.tiles; k += kTileThreads) {
+    const int at = k + int(threadIdx.x);
+    const uint32_t v = at < a.tiles ? count[at] : 0;
+    const uint32_t before = carry + block_exclusive(v, wave_total);
+    for (int w = 0; w < kTileThreads / 64; ++w) carry += wave_total[w];
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      if (at + j < n) count[at + j] = before;
-      before += v[j];
-    }
+    if (at < a.tiles) count[at] = before;
   }
+  if (threadIdx.x == 0) a.total[blockIdx.x] = carry;
 }
 
-template <int R, bool DIRECT>
+template <bool DIRECT>
 __global__ __launch_bounds__(kTileThreads) void sort_scatter_kernel(SortPass a) {
   __shared__ SortLds<kTileThreads / 64> s;
-  uint32_t key[R], p[R], rank[R];
+  uint32_t key[kTileR], p[kTileR], rank[kTileR];
   load_tile(a, key, p);
   rank_keys(s, key, rank, a.shift, a.bits);
   __syncthreads();
@@ -287,9 +282,8 @@ __global__ __launch_bounds__(kTileThreads) void sort_scatter_kernel(SortPass a) 
   static_assert(kDigits == 2 * kTileThreads, "two digits to a thread");
   const int d = 2 * int(threadIdx.x);
   const bool mine = d < (1 << a.bits);     // bits >= 1: both digits or none
-  uint32_t at[2] = {0u, 0u};
+  uint32_t at[2] = {0u, 0u}, total[2] = {0u, 0u};
   if constexpr (DIRECT) {
-    uint32_t total[2] = {0u, 0u};
     if (mine) {
 #pragma unroll 8
       for (int t = 0; t < a.tiles; ++t) {
@@ -302,13 +296,15 @@ __global__ __launch_bounds__(kTileThreads) void sort_scatter_kernel(SortPass a) 
         }
       }
     }
-    const uint32_t base = block_exclusive(total[0] + total[1], s.wave_total);
-    at[0] += base;
-    at[1] += base + total[0];
   } else if (mine) {
-    at[0] = a.count[int64_t(d) * a.tiles + blockIdx.x];
-    at[1] = a.count[int64_t(d + 1) * a.tiles + blockIdx.x];
+    for (int k = 0; k < 2; ++k) {
+      total[k] = a.total[d + k];
+      at[k] = a.count[int64_t(d + k) * a.tiles + blockIdx.x];
+    }
   }
+  const uint32_t base = block_exclusive(total[0] + total[1], s.wave_total);
+  at[0] += base;
+  at[1] += base + total[0];
   if (mine) {
     place_waves(s, d, at[0]);
     place_waves(s, d + 1, at[1]);
@@ -316,7 +312,7 @@ __global__ __launch_bounds__(kTileThreads) void sort_scatter_kernel(SortPass a) 
   __syncthreads();
   const int wave = threadIdx.x >> 6;
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
+  for (int j = 0; j < kTileR; ++j) {
     const uint32_t to = s.count[wave][(key[j] >> a.shift) & ((1u << a.bits) - 1u)] + rank[j];
     if (int64_t(to) < a.T) {       // keys past the last token come last
       a.keys_out[to] = key[j];

@@ -34,17 +34,16 @@ int bits_for(int64_t largest) {
   return b;
 }
 
-template <int R, bool DIRECT>
+template <bool DIRECT>
 forge_status launch_sort_pass(const SortPass& p, hipStream_t s) {
   const dim3 grid(p.tiles), threads(kTileThreads);
-  hipLaunchKernelGGL((sort_count_kernel<R, DIRECT>), grid, threads, 0, s, p);
+  hipLaunchKernelGGL((sort_count_kernel<DIRECT>), grid, threads, 0, s, p);
   if (forge_status st = launch_status()) return st;
   if (!DIRECT) {
-    hipLaunchKernelGGL(sort_sum_kernel, dim3(1), dim3(kSumThreads), 0, s, p.count,
-                       int64_t(p.tiles) << p.bits);
+    hipLaunchKernelGGL(sort_sum_kernel, dim3(1u << p.bits), threads, 0, s, p);
     if (forge_status st = launch_status()) return st;
   }
-  hipLaunchKernelGGL((sort_scatter_kernel<R, DIRECT>), grid, threads, 0, s, p);
+  hipLaunchKernelGGL((sort_scatter_kernel<DIRECT>), grid, threads, 0, s, p);
   return launch_status();
 }
 
@@ -64,13 +63,12 @@ forge_status launch_sort(const IdSource& src, const EmbeddingWorkspace& ws, char
     return launch_status();
   }
   const int passes = (key_bits + kDigitBits - 1) / kDigitBits;
-  const int64_t small = kTileThreads * 4, large = kTileThreads * 16;
-  const int64_t tile = T <= small * kDirectTiles ? small : large;
   SortPass p{};
   p.src = src;
   p.count = reinterpret_cast<uint32_t*>(base + ws.count);
   p.T = T;
-  p.tiles = int32_t((T + tile - 1) / tile);
+  p.tiles = int32_t((T + kTileKeys - 1) / kTileKeys);
+  p.total = p.count + int64_t(p.tiles) * kDigits;
   for (int k = 0; k < passes; ++k) {
     p.keys_in = k ? keys[(k - 1) & 1] : nullptr;
     p.pos_in = k ? pos[(k - 1) & 1] : nullptr;
@@ -78,9 +76,8 @@ forge_status launch_sort(const IdSource& src, const EmbeddingWorkspace& ws, char
     p.pos_out = pos[k & 1];
     p.shift = key_bits * k / passes;
     p.bits = key_bits * (k + 1) / passes - p.shift;
-    const forge_status st = tile == small              ? launch_sort_pass<4, true>(p, s)
-                            : p.tiles <= kDirectTiles ? launch_sort_pass<16, true>(p, s)
-                                                      : launch_sort_pass<16, false>(p, s);
+    const forge_status st =
+        p.tiles <= kDirectTiles ? launch_sort_pass<true>(p, s) : launch_sort_pass<false>(p, s);
     if (st) return st;
   }
   a.keys = p.keys_out;

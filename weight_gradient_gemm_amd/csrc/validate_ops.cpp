@@ -151,7 +151,7 @@ bool embedding_sizes_ok(int64_t T, int64_t V, int64_t d) {
 }
 
 // Two copies of (key, position) for the sort's passes, its digit counts (512
-// for each tile of 1024 tokens), the rows' bounds, and the sums of chunks of
+// for each tile of 1024 tokens, and in all), the rows' bounds, and the sums of chunks of
 // tokens.
 EmbeddingWorkspace embedding_workspace(int64_t T, int64_t V, int64_t d) {
   EmbeddingWorkspace w{};
@@ -165,7 +165,7 @@ EmbeddingWorkspace embedding_workspace(int64_t T, int64_t V, int64_t d) {
     w.keys[k] = take(4 * T);
     w.pos[k] = take(4 * T);
   }
-  w.count = take((T + 1023) / 1024 * 512 * 4);
+  w.count = take(((T + 1023) / 1024 + 1) * 512 * 4);
   w.bound = take(4 * (V + 1));
   w.chunk = take((T >> embedding_chunk_bits(T)) * d * 4);
   w.bytes = at;

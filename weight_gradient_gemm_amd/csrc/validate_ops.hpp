@@ -33,8 +33,9 @@ struct EmbeddingWorkspace {
 // frequent ids of thousands of tokens, more those of tens of thousands. Of
 // 262144 tokens into 32000 x 1024 with 71500 of one id: 352 us with 32, 207 with
 // 128 (spread evenly 190 with both). Of 1048576 into 32000 x 512 with 286000: 1085
-// with 32, 548 with 128, 458 with 256, 461 with 512; evenly into 300 rows 408, -,
-// 445 and 502.
+// with 32, 548 with 128, 458 with 256, 461 with 512, and spread evenly over 300
+// rows 408, 445 with 256 and 502 with 512 (all of them with a sort that took 95 us
+// longer than now).
 inline int embedding_chunk_bits(int64_t T) { return T <= 32768 ? 5 : T <= 524288 ? 7 : 8; }
 bool embedding_sizes_ok(int64_t T, int64_t V, int64_t d);
 EmbeddingWorkspace embedding_workspace(int64_t T, int64_t V, int64_t d);
