@@ -282,3 +282,73 @@ def test_binding_refuses(env):
     with pytest.raises(wg.ForgeError, match="SHAPE"):
         wg.forge_grad_norm(wg.ForgeTensorList([g]), norm, max_norm=1.0, workspace=small)
     assert bool((g == 1).all()) and bool((norm == 1).all())
+
+
+def test_moved_tensors_are_refused_before_anything_runs(env):
+    torch, wg = env
+    sizes = [5000, 0, 77, 1]
+
+    def data(t):
+        t.data = t.clone()
+
+    def grown(t):
+        t.untyped_storage().resize_(4 * t.untyped_storage().nbytes() + (4 << 20))
+
+    for move in (data, grown):
+        for k in (0, 2, 3):
+            for name, calls in (("grads", "nsac"), ("out", "c"), ("W", "sa"), ("m", "sa"), ("v", "a")):
+                grads, W, m, v = make(torch, sizes, "f32", 7)
+                fields = dict(grads=grads, out=[torch.ones_like(g) for g in grads], W=W, m=m, v=v)
+                tensors = wg.ForgeTensorList(**fields)
+                norm = torch.ones(2, device="cuda")
+                move(fields[name][k])
+                keep = {n: [t.clone() for t in ts] for n, ts in fields.items()}
+                run = dict(n=lambda: wg.forge_grad_norm(tensors, norm, max_norm=1.0),
+                           c=lambda: wg.forge_clip_grads(tensors, norm),
+                           s=lambda: wg.forge_sgdm_clipped(tensors, norm, **SGDM),
+                           a=lambda: wg.forge_adamw_clipped(tensors, norm, **ADAM))
+                for call in calls:
+                    with pytest.raises(ValueError, match=r"\[%d\] of the list is not where" % k):
+                        run[call]()
+                assert bool((norm == 1).all())
+                for n, ts in fields.items():
+                    assert all(torch.equal(a, b) for a, b in zip(ts, keep[n])), n
+
+
+def test_list_over_a_training_loop(env):
+    """A list built from the parameters' own gradients, over steps that clear
+    them in place; gradients that backward made anew are refused."""
+    torch, wg = env
+    g = torch.Generator(device="cuda").manual_seed(3)
+    layer = torch.nn.Linear(40, 24, device="cuda")
+    W = list(layer.parameters())
+    m, v = ([torch.zeros_like(w) for w in W] for _ in range(2))
+    norm = torch.empty(2, device="cuda")
+
+    def backward():
+        x = torch.randn(9, 40, generator=g, device="cuda")
+        layer(x).square().mean().backward()
+
+    backward()
+    tensors = wg.ForgeTensorList([w.grad for w in W], W=W, m=m, v=v)
+    for step in range(1, 4):
+        if step > 1:
+            layer.zero_grad(set_to_none=False)
+            backward()
+        old = [[t.detach().double().cpu() for t in ts] for ts in (W, m, v)]
+        wg.forge_grad_norm(tensors, norm, max_norm=0.01)
+        wg.forge_adamw_clipped(tensors, norm, **dict(ADAM, step=step))
+        check_norm(norm, norm64([w.grad for w in W]), 0.01)
+        for k, w in enumerate(W):
+            g64 = (w.grad * norm[1]).double().cpu()
+            want, tol = adamw64(g64, *(ts[k] for ts in old), **dict(ADAM, step=step))
+            for got, x, t in zip((w, m[k], v[k]), want, tol):
+                assert bool(((got.detach().double().cpu() - x).abs() <= t).all()), (step, k)
+    layer.zero_grad()
+    backward()
+    keep = [w.detach().clone() for w in W]
+    for call in (lambda: wg.forge_grad_norm(tensors, norm, max_norm=0.01),
+                 lambda: wg.forge_adamw_clipped(tensors, norm, **ADAM)):
+        with pytest.raises(ValueError, match="another gradient"):
+            call()
+    assert all(torch.equal(a, b) for a, b in zip(W, keep))

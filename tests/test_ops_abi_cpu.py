@@ -201,6 +201,96 @@ def test_tensor_list_checks():
         wg.ForgeTensorList([], W=[g])
 
 
+@pytest.fixture
+def host_lists(monkeypatch):
+    """Lists of CPU tensors, which no call could take, for what a call looks at first."""
+    monkeypatch.setattr(_ops, "_want", lambda t, dtype, name: None)
+
+
+def listed(tensors, *need):
+    import torch
+    try:
+        return _ops._listed(torch, tensors, None, *need)
+    except ValueError as e:
+        return str(e)
+
+
+def test_a_list_whose_tensors_moved_is_refused(host_lists):
+    import torch
+    import weight_gradient_gemm_amd as wg
+
+    def make():
+        # flat storages of several tensors, as well as tensors of their own, one of them empty
+        return [torch.ones(n) for n in (64, 0, 7)] + list(torch.ones(96).split(32))
+
+    def data(t):
+        t.data = torch.ones_like(t)
+
+    def resized(t):
+        n = t.untyped_storage().nbytes()
+        t.untyped_storage().resize_(4 * n + 1024)
+
+    def freed(t):
+        t.untyped_storage().resize_(0)
+
+    fields = dict(out=make, W=make, m=make, v=make)
+    names = ("grad", *fields)
+    for move in (data, resized, freed):
+        for name in names:
+            for k in (0, 2, 4):
+                grads, rest = make(), {n: f() for n, f in fields.items()}
+                tensors = wg.ForgeTensorList(grads, **rest)
+                assert listed(tensors, "out") == listed(tensors, "W", "m", "v") == (tensors.rows, 6)
+                move((grads if name == "grad" else rest[name])[k])
+                for need in ((), ("out",), ("W", "m"), ("W", "m", "v")):
+                    got = listed(tensors, *need)
+                    if name == "grad" or name in need:
+                        assert "build the list again" in got and name in got, (move, name, k, need)
+                    else:                                   # a field that the call does not use
+                        assert got == (tensors.rows, 6)
+
+
+def test_a_list_holds_its_memory(host_lists):
+    # With the old storage alive nothing else can come to lie at the list's address.
+    import torch
+    import weight_gradient_gemm_amd as wg
+    p = torch.ones(1 << 16)
+    at = p.data_ptr()
+    tensors = wg.ForgeTensorList([p])
+    p.data = torch.empty(0)
+    assert all(torch.empty(1 << 16).data_ptr() != at for _ in range(8))
+    assert "build the list again" in listed(tensors)
+
+
+def test_a_list_of_gradients_that_backward_replaced_is_refused(host_lists):
+    import torch
+    import weight_gradient_gemm_amd as wg
+    W = [torch.ones(8, requires_grad=True), torch.ones(3, requires_grad=True)]
+
+    def backward():
+        sum(w.sum() for w in W).backward()
+
+    def build(**kw):
+        return wg.ForgeTensorList([w.grad for w in W], W=W, m=[torch.ones_like(w) for w in W], **kw)
+
+    backward()
+    tensors = build()
+    opt = torch.optim.SGD(W)
+    for again in (False, True):
+        opt.zero_grad(set_to_none=False)
+        backward()
+        assert listed(tensors, "W", "m") == (tensors.rows, 2)        # the same gradients
+    opt.zero_grad()
+    assert listed(tensors, "W", "m") == (tensors.rows, 2)            # the list's are all there are
+    backward()
+    assert "another gradient" in listed(tensors, "W", "m") and "another" in listed(tensors)
+    assert listed(build(), "W", "m")[1] == 2
+    # gradients of the program's own, beside what autograd keeps
+    own = wg.ForgeTensorList([torch.ones_like(w) for w in W], W=W, m=[w.grad for w in W])
+    W[0].grad = torch.zeros(8)
+    assert listed(own, "W")[1] == 2
+
+
 # --------------------------------------------------------------------------
 # embedding
 # --------------------------------------------------------------------------

@@ -137,12 +137,18 @@ def _workspace(torch, cur, nbytes, workspace, stream):
 class ForgeTensorList:
     """Gradients, and what goes with each, of one training step: built once and
     passed to forge_grad_norm, forge_clip_grads, forge_adamw_clipped and
-    forge_sgdm_clipped as often as the tensors stay where they are.
+    forge_sgdm_clipped as often as the tensors stay where they are. A call
+    raises ValueError where one of the tensors that it uses has moved
+    (``p.data = ...``, a resized storage). After ``zero_grad(set_to_none=True)``,
+    torch's default, backward makes new gradients, which a list of the old ones
+    does not see: clear with ``set_to_none=False``, or build the list after
+    every backward. A list built with weights ``W`` and their own ``grad`` as
+    gradients raises where such a weight has come to another one.
 
     ``grads``: float32 or bfloat16 tensors of any shape, contiguous. ``out``:
     the clipped gradients' places (the gradients themselves: in place), of the
     gradients' types. ``W`` and ``m``, ``v`` (AdamW) or ``mom`` (SGD-momentum):
-    float32. The list keeps the tensors alive.
+    float32. The list keeps the tensors and their memory alive.
     """
 
     def __init__(self, grads, *, out=None, W=None, m=None, v=None, mom=None):
@@ -174,9 +180,27 @@ class ForgeTensorList:
             self.tensors[name] = ts
         self.rows, self.count = rows, len(grads)
         self.device = grads[0].device.index if grads else None
+        # Where the tensors are. The storages are held, so that no other tensor
+        # can come to lie at an address of the list.
+        self._at = {name: (tuple(ts), _addresses(torch, ts)) for name, ts in self.tensors.items()}
+        self._storages = [t.untyped_storage() for ts in self.tensors.values() for t in ts]
+        self._own_grads = [(w, g) for w, g in zip(self.tensors.get("W", ()), grads)
+                           if w.requires_grad and w.is_leaf and w.grad is g]
 
 
-def _listed(tensors, cur, *need):
+def _addresses(torch, ts):
+    return list(map(torch.Tensor.data_ptr, ts))
+
+
+def _moved(torch, tensors, name):
+    """What is wrong with a field of a list whose addresses do not hold any more."""
+    ts, at = tensors._at[name]
+    k = next(k for k, t in enumerate(ts) if t.data_ptr() != at[k])
+    return ValueError(f"{name}[{k}] of the list is not where it was when the list was built "
+                      "(its data was replaced or its storage resized): build the list again")
+
+
+def _listed(torch, tensors, cur, *need):
     """The C array of a list that has the fields `need`, and its length."""
     if not isinstance(tensors, ForgeTensorList):
         raise TypeError(f"tensors must be a ForgeTensorList, got {type(tensors).__name__}")
@@ -186,6 +210,15 @@ def _listed(tensors, cur, *need):
     if tensors.device not in (None, cur):
         raise ValueError(f"the list is on cuda:{tensors.device} but the current device is "
                          f"cuda:{cur} (select it with torch.cuda.device)")
+    for name in ("grad", *need):
+        ts, at = tensors._at[name]
+        if _addresses(torch, ts) != at:
+            raise _moved(torch, tensors, name)
+    for w, g in tensors._own_grads:
+        now = w.grad
+        if now is not g and now is not None and now.data_ptr() != g.data_ptr():
+            raise ValueError("a weight of the list has another gradient than when the list was "
+                             "built (zero_grad(set_to_none=True)?): build the list again")
     return tensors.rows, tensors.count
 
 
@@ -202,7 +235,7 @@ def forge_grad_norm(tensors, norm, *, max_norm, workspace=None, stream=None) -> 
 
     ``norm`` is a float32 tensor of 2 elements; nothing is copied to the host."""
     torch, cur, st = _current(stream)
-    rows, count = _listed(tensors, cur)
+    rows, count = _listed(torch, tensors, cur)
     out = _norm2(torch, cur, norm)
     lib = library()
     ws = _workspace(torch, cur, lib.forge_grad_norm_workspace(count), workspace, stream)
@@ -213,7 +246,7 @@ def forge_grad_norm(tensors, norm, *, max_norm, workspace=None, stream=None) -> 
 def forge_clip_grads(tensors, norm, *, stream=None) -> None:
     """out <- norm[1] * grad for every tensor of the list."""
     torch, cur, st = _current(stream)
-    rows, count = _listed(tensors, cur, "out")
+    rows, count = _listed(torch, tensors, cur, "out")
     _check(library().forge_clip_grads(rows, count, _norm2(torch, cur, norm) + 4, st),
            "forge_clip_grads")
 
@@ -222,7 +255,7 @@ def forge_adamw_clipped(tensors, norm, *, step, lr=1e-3, beta1=0.9, beta2=0.999,
                         weight_decay=0.01, max_grad_norm=0.0, stream=None) -> None:
     """AdamW on W, m, v of every tensor of the list from norm[1] * grad."""
     torch, cur, st = _current(stream)
-    rows, count = _listed(tensors, cur, "W", "m", "v")
+    rows, count = _listed(torch, tensors, cur, "W", "m", "v")
     p = _adamw(step, lr, beta1, beta2, eps, weight_decay, max_grad_norm)
     _check(library().forge_adamw_clipped(rows, count, _norm2(torch, cur, norm) + 4,
                                          ctypes.byref(p), st), "forge_adamw_clipped")
@@ -232,7 +265,7 @@ def forge_sgdm_clipped(tensors, norm, *, lr=1e-3, momentum=0.9, weight_decay=0.0
                        max_grad_norm=0.0, stream=None) -> None:
     """SGD-momentum on W, mom of every tensor of the list from norm[1] * grad."""
     torch, cur, st = _current(stream)
-    rows, count = _listed(tensors, cur, "W", "m")
+    rows, count = _listed(torch, tensors, cur, "W", "m")
     p = SgdmParams(float(lr), float(momentum), float(weight_decay), float(max_grad_norm))
     _check(library().forge_sgdm_clipped(rows, count, _norm2(torch, cur, norm) + 4,
                                         ctypes.byref(p), st), "forge_sgdm_clipped")
