@@ -393,3 +393,29 @@ def test_quantise_nothing(env):
     out = torch.ones(64, 64, device="cuda")
     wg.forge_matmul_mxfp4(cols, cols, out)
     assert bool((out == 0).all())
+
+
+def test_moved_operands_are_refused_before_anything_runs(env):
+    torch, wg = env
+
+    def resized(t):
+        t.untyped_storage().resize_(t.untyped_storage().nbytes() + (4 << 20))
+
+    def data(t):
+        t.data = t.clone()
+
+    x = torch.randn(64, 256, device="cuda")
+    A, B = operands(torch, wg, 64, 72, 256, 5)
+    W = torch.full((64, 72), 3.0, device="cuda")
+    for own, move in ((True, resized), (False, resized), (False, data)):
+        for k in range(2):
+            op = (wg.forge_mxfp4_empty(64, 256) if own else
+                  wg.ForgeMxfp4(torch.zeros_like(A.codes), torch.zeros_like(A.scales)))
+            move((op.codes, op.scales)[k])
+            for call in (lambda: wg.forge_quantize_mxfp4(x, rows=op),
+                         lambda: wg.forge_matmul_mxfp4(op, B, W),
+                         lambda: wg.forge_matmul_mxfp4(B, op, W.t().contiguous()),
+                         lambda: wg.forge_wgrad_adamw_mxfp4(B, op, W, W.clone(), W.clone(), **ADAM)):
+                with pytest.raises(ValueError, match="make the operand again"):
+                    call()
+    assert bool((W == 3).all())

@@ -485,3 +485,24 @@ def test_mxfp4_operand_shapes():
         wg.ForgeMxfp4(op.codes.int(), op.scales)
     with pytest.raises(ValueError, match="contiguous"):
         wg.ForgeMxfp4(op.codes.transpose(0, 1), op.scales)
+
+
+def test_an_operand_whose_tensors_moved_is_refused():
+    import torch
+    import weight_gradient_gemm_amd as wg
+    for make in (lambda: wg.forge_mxfp4_empty(8, 300, device="cpu"),
+                 lambda: wg.ForgeMxfp4(torch.zeros(3, 8, 64, dtype=torch.uint8),
+                                       torch.zeros(3, 8, 4, dtype=torch.uint8))):
+        for move in ("codes", "scales"):
+            op = make()
+            assert _ops._operand(-1, op, "A") == (*op.ptrs, 8, 384)
+            t = getattr(op, move)
+            t.untyped_storage().resize_(1 << 20)
+            with pytest.raises(ValueError, match="make the operand again"):
+                _ops._operand(-1, op, "A")
+    op, c = make(), torch.zeros(3, 8, 64, dtype=torch.uint8)
+    op.codes.data = c
+    with pytest.raises(ValueError, match="make the operand again"):
+        _ops._operand(-1, op, "A")
+    empty = wg.forge_mxfp4_empty(8, 0, device="cpu")
+    assert _ops._operand(-1, empty, "A") == (None, None, 8, 0)

@@ -350,8 +350,9 @@ def forge_embedding_sgdm(ids, dY, W, mom, *, scale=1.0, lr=1e-3, momentum=0.9, w
 class ForgeMxfp4:
     """A microscaled 4-bit operand of ``rows`` rows and padded contraction
     length ``k``: uint8 ``codes`` [k / 128, rows, 64] and ``scales`` [k / 128,
-    rows, 4], k a multiple of 128. It keeps its tensors alive and counts on
-    them staying where they are."""
+    rows, 4], k a multiple of 128. It keeps its tensors and their memory alive;
+    a call raises ValueError where they have moved (``codes.data = ...``, a
+    resized storage)."""
 
     def __init__(self, codes, scales):
         torch = _torch()
@@ -370,6 +371,13 @@ class ForgeMxfp4:
         self._hold, self._codes, self._scales = None, codes, scales
         self.rows, self.k, self.device = rows, groups * 128, codes.get_device()
         self.ptrs = (codes.data_ptr() or None, scales.data_ptr() or None)
+        self._storages = codes.untyped_storage(), scales.untyped_storage()
+
+    def _here(self):
+        """Whether codes and scales are where the addresses point."""
+        if self._hold is not None:
+            return (self._hold.data_ptr() or None) == self.ptrs[0]
+        return (self._codes.data_ptr() or None, self._scales.data_ptr() or None) == self.ptrs
 
     @property
     def codes(self):
@@ -408,6 +416,9 @@ def _operand(cur, op, name):
         op = ForgeMxfp4(*op)
     if op.device != cur:
         raise ValueError(f"{name} must be on the GPU and the current device, cuda:{cur}")
+    if not op._here():
+        raise ValueError(f"{name}'s codes or scales are not where they were when the operand was "
+                         "made (data replaced or storage resized): make the operand again")
     return *op.ptrs, op.rows, op.k
 
 
