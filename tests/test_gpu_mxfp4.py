@@ -419,3 +419,49 @@ def test_moved_operands_are_refused_before_anything_runs(env):
                 with pytest.raises(ValueError, match="make the operand again"):
                     call()
     assert bool((W == 3).all())
+
+
+def every_epilogue(torch, wg, A, B, tiles):
+    """Product and AdamW step of A B^T at each tile id, all bitwise the same; the product."""
+    M, N = A.rows, B.rows
+    g = torch.Generator(device="cuda").manual_seed(8)
+    W, m = (torch.randn(M, N, generator=g, device="cuda") for _ in range(2))
+    v = torch.rand(M, N, generator=g, device="cuda") + 0.1
+    first = {}
+    for tile in tiles:
+        for dtype in (torch.float32, torch.bfloat16):
+            guard = torch.full((M * N + 64,), 7.0, dtype=dtype, device="cuda")
+            wg.forge_matmul_mxfp4(A, B, guard[:M * N].view(M, N), tile=tile)
+            assert bool((guard[M * N:] == 7).all())
+            assert torch.equal(first.setdefault(dtype, guard), guard), (tile, dtype)
+        st = [t.clone() for t in (W, m, v)]
+        wg.forge_wgrad_adamw_mxfp4(B, A, *st, tile=tile, **ADAM)
+        for a, b in zip(first.setdefault("adamw", st), st):
+            assert torch.equal(a, b), tile
+    out = first[torch.float32][:M * N].view(M, N)
+    wg.forge_adamw(out, W, m, v, **ADAM)
+    assert all(torch.equal(a, b) for a, b in zip(first["adamw"], (W, m, v)))
+    assert torch.equal(first[torch.bfloat16][:M * N].view(M, N), out.to(torch.bfloat16))
+    return out
+
+
+@pytest.mark.parametrize("M,N,K", [(4104, 4360, 1100), (4104, 8712, 333)])
+def test_more_tiles_than_workgroups(env, M, N, K):
+    """306 and 595 tiles of 256x256: the persistent schedule's workers go from full to half tiles,
+    from half to full ones, and through two full ones on end."""
+    torch, wg = env
+    A, B = operands(torch, wg, M, N, K, 12)
+    out = every_epilogue(torch, wg, A, B, (4, 1, 2, 3))
+    rows = sorted({0, M - 1, *range(0, M, 256), *range(255, M, 256), *range(70, M, 611)})
+    some = wg.ForgeMxfp4(A.codes[:, rows].contiguous(), A.scales[:, rows].contiguous())
+    check_product(torch, out[rows], some, B)
+
+
+@pytest.mark.parametrize("M,N,K", [(2300, 776, 640), (520, 2056, 1100),      # 128x64 by default
+                                   (300, 1032, 5000), (64, 1032, 4000),      # 64x64, slots of two stages
+                                   (700, 1032, 333), (257, 520, 641)])       # 64x64
+def test_tiles_of_the_librarys_own(env, M, N, K):
+    torch, wg = env
+    A, B = operands(torch, wg, M, N, K, 13)
+    out = every_epilogue(torch, wg, A, B, (0, 2))
+    check_product(torch, out, A, B)
