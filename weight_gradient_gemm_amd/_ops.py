@@ -182,19 +182,16 @@ class ForgeTensorList:
         self.device = grads[0].device.index if grads else None
         # Where the tensors are. The storages are held, so that no other tensor
         # can come to lie at an address of the list.
-        self._at = {name: (tuple(ts), _addresses(torch, ts)) for name, ts in self.tensors.items()}
+        self._at = {name: (tuple(ts), [t.data_ptr() for t in ts])
+                    for name, ts in self.tensors.items()}
         self._storages = [t.untyped_storage() for ts in self.tensors.values() for t in ts]
         self._own_grads = [(w, g) for w, g in zip(self.tensors.get("W", ()), grads)
                            if w.requires_grad and w.is_leaf and w.grad is g]
+        self._norm_bytes = library().forge_grad_norm_workspace(self.count)
 
 
-def _addresses(torch, ts):
-    return list(map(torch.Tensor.data_ptr, ts))
-
-
-def _moved(torch, tensors, name):
-    """What is wrong with a field of a list whose addresses do not hold any more."""
-    ts, at = tensors._at[name]
+def _moved(name, ts, at):
+    """What is wrong with a list's tensors whose addresses do not hold any more."""
     k = next(k for k, t in enumerate(ts) if t.data_ptr() != at[k])
     return ValueError(f"{name}[{k}] of the list is not where it was when the list was built "
                       "(its data was replaced or its storage resized): build the list again")
@@ -204,16 +201,17 @@ def _listed(torch, tensors, cur, *need):
     """The C array of a list that has the fields `need`, and its length."""
     if not isinstance(tensors, ForgeTensorList):
         raise TypeError(f"tensors must be a ForgeTensorList, got {type(tensors).__name__}")
+    fields = tensors._at
     for name in need:
-        if name not in tensors.tensors:
+        if name not in fields:
             raise ValueError(f"the list was built without {name}")
     if tensors.device not in (None, cur):
         raise ValueError(f"the list is on cuda:{tensors.device} but the current device is "
                          f"cuda:{cur} (select it with torch.cuda.device)")
     for name in ("grad", *need):
-        ts, at = tensors._at[name]
-        if _addresses(torch, ts) != at:
-            raise _moved(torch, tensors, name)
+        ts, at = fields[name]
+        if list(map(torch.Tensor.data_ptr, ts)) != at:
+            raise _moved(name, ts, at)
     for w, g in tensors._own_grads:
         now = w.grad
         if now is not g and now is not None and now.data_ptr() != g.data_ptr():
@@ -238,7 +236,7 @@ def forge_grad_norm(tensors, norm, *, max_norm, workspace=None, stream=None) -> 
     rows, count = _listed(torch, tensors, cur)
     out = _norm2(torch, cur, norm)
     lib = library()
-    ws = _workspace(torch, cur, lib.forge_grad_norm_workspace(count), workspace, stream)
+    ws = _workspace(torch, cur, tensors._norm_bytes, workspace, stream)
     _check(lib.forge_grad_norm(rows, count, max_norm, out, ws.data_ptr(), ws.numel(), st),
            "forge_grad_norm")
 
