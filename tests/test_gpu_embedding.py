@@ -288,3 +288,38 @@ def test_lookup_of_an_output_past_the_cache(env, types):
     wg.forge_embedding(table, ids, out, scale=3.0)
     want = torch.cat([table.float() * 3.0, torch.zeros(1, d, device="cuda")]).to(ot)
     assert torch.equal(out, want[ids.long()])
+
+
+def test_outputs_of_more_workgroups_than_a_launch(env):
+    """2^22 rows of 1026 units: beyond 2^32 units and 2^22 workgroups (also with four pieces to
+    one), so that every kernel goes round its loop and the row of a unit takes 64 bits."""
+    torch, wg = env
+    V, d, part = 1 << 22, 4104, 1 << 18
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("69 GB of output and its comparison do not fit")
+    big = torch.empty(V, d, device="cuda")
+    # Rows at both ends and around places 2^22 workgroups and 2^32 units in.
+    rows = [0, 1, V - 1, V - 2, *((p // 1026 + k) for p in (1 << 30, 1 << 32) for k in (-2, -1, 0, 1, 2))]
+    assert all(0 <= r < V for r in rows)
+    for T in (200, 300):                    # looked through, and sorted
+        ids = torch.tensor([rows[k % len(rows)] for k in range(T)], device="cuda")
+        dY = torch.randn(T, d, device="cuda")
+        small = torch.unique(ids)           # the same gradient over the rows with tokens alone
+        want = torch.empty(len(small), d, device="cuda")
+        wg.forge_embedding_grad(torch.searchsorted(small, ids), dY, want, scale=1.5)
+        big.fill_(7.0)
+        wg.forge_embedding_grad(ids, dY, big, scale=1.5)
+        assert torch.equal(big[small], want)
+        wg.forge_embedding_grad(ids, dY, big, scale=1.5, accumulate=True)
+        assert torch.equal(big[small], want + want)
+        big[small] = 0
+        assert not any(bool(big[r:r + part].any()) for r in range(0, V, part))
+    table = torch.randn(37, 2 * d, device="cuda")
+    ids = torch.arange(V, device="cuda", dtype=torch.int32) % 38          # one of them nobody's
+    out = big.view(torch.bfloat16)
+    wg.forge_embedding(table, ids, out, scale=3.0)
+    want = torch.cat([table * 3.0, torch.zeros(1, 2 * d, device="cuda")]).to(torch.bfloat16)
+    for r in range(0, V, part // 4):
+        assert torch.equal(out[r:r + part // 4], want[ids[r:r + part // 4].long()]), r
+    del big, out
+    torch.cuda.empty_cache()
