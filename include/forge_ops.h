@@ -37,8 +37,9 @@ extern "C" {
  * forge_embedding_grad, one pass for their norm, one for the step. */
 
 /*
- * One tensor of a list. n elements, any n >= 0; a tensor of n == 0 is skipped
- * and its pointers are not looked at. Each call names the fields that it uses
+ * One tensor of a list. n elements, 0 <= n <= 2^40 and at most 2^42 in the
+ * list (else FORGE_ERR_SHAPE); a tensor of n == 0 is skipped and its pointers
+ * are not looked at. Each call names the fields that it uses
  * and does not look at the others.
  */
 typedef struct {
@@ -178,7 +179,8 @@ FORGE_API forge_status forge_embedding_sgdm(const void* ids, int32_t id_bytes, c
  */
 #define FORGE_MXFP4_K(K) (((int64_t)(K) + 127) / 128 * 128)
 
-/* Largest padded contraction length; an operand has at most 2^22 rows. */
+/* Largest padded contraction length; an operand has at most 2^22 rows and a
+ * product at most 2^40 elements (else FORGE_ERR_SHAPE). */
 #define FORGE_MXFP4_MAX_K 1073741824
 
 /*

@@ -169,8 +169,9 @@ __device__ __forceinline__ uint32_t digit_total(const SortLds<WAVES>& s, int d) 
 
 // Up to kRankTokens tokens in one launch: a token's place is the number of
 // smaller (key, position) pairs, counted by 8 threads that go through all keys
-// in LDS. T^2 comparisons are cheap beside the launches of a radix sort:
-// 1021 tokens 4.6 us, 6175 14.8; the tiles below take 21.
+// in LDS. T^2 comparisons are cheap beside the launches of a radix sort: the
+// whole gradient of 1021 tokens into 5003 x 512 takes 14.1 us, with the tiles below
+// 23.1; of 4096 21.1 and 28.4; of 8192 into 32000 x 512 35.1 and 35.4.
 __global__ __launch_bounds__(8 * kRankKeys) void rank_kernel(IdSource src, int T, uint32_t* keys,
                                                              uint32_t* pos) {
   __shared__ __attribute__((aligned(16))) uint32_t lk[kRankTokens];
@@ -208,8 +209,9 @@ __global__ __launch_bounds__(8 * kRankKeys) void rank_kernel(IdSource src, int T
 
 // The larger sort, per pass: the digit counts of tiles of 1024 keys, and the
 // scatter. Up to kDirectTiles tiles a tile adds up the counts that precede its
-// own itself (65536 tokens: 12.9 us a pass); beyond, a launch between the two
-// forms the sums (262144 tokens: 17 us; 31 with direct tiles of 4096 keys).
+// own itself; beyond, a launch between the two forms the sums. The gradient of
+// 16384 tokens into 32000 x 64 takes 34.4 us with the former and 38.3 with the
+// latter, of 65536 57.3 and 56.4, of 131072 83 and 76, of 262144 105 and 85.
 // keys_in == nullptr: the first pass, from the ids.
 struct SortPass {
   IdSource src;
@@ -352,8 +354,9 @@ __device__ __forceinline__ f32x4_t load_dy4(const void* dY, int64_t i) {
 // acc += term(s) + ... + term(e - 1), one after the other. Loads go U at a
 // time, the last ones four at a time, where places past the end repeat the last
 // term and are not added. U costs registers: 8 where a row is only written (V
-// 128256 x 512, 1025 tokens: 50 us against 65 with 16), 16 where it is read too
-// (AdamW, 128256 x 4096: 2.15 ms against 2.22 with 8).
+// 128256 x 512, 1025 tokens: 49 us against 74 with 16), 16 where it is stepped
+// (AdamW, 16384 tokens into 32000 x 1024: 151 us against 157 with 8; into 128256 x
+// 4096 runs differ by more, 2.05-2.20 ms with either).
 template <int U, class Term>
 __device__ __forceinline__ void add_terms(f32x4_t& acc, uint32_t s, uint32_t e, const Term& term) {
   for (; s + U <= e; s += U) {
@@ -447,8 +450,8 @@ __device__ __forceinline__ void row_step(const EmbeddingArgs& a, int64_t i, cons
 }
 
 // Waves per SIMD that the rows' passes are compiled for: rows that are only
-// written need many in flight (128256 x 4096: 354 us with 8, 374 with 7). Four
-// pieces of 256 units to a workgroup instead of one took 395.
+// written keep to the 64 registers that eight need. (Compiled for 4 or 7 they take
+// 64 as well, and the same 327 us for 16384 tokens into 128256 x 4096.)
 template <int OP>
 constexpr int kRowWaves = OP == EMB_GRAD ? 8 : OP == EMB_GRAD_ADD ? 7 : 4;
 
@@ -482,9 +485,9 @@ __global__ __launch_bounds__(256, kRowWaves<OP>) void embedding_rows_kernel(Embe
 
 // Few tokens: no sort. A workgroup takes a.scan_units * 256 units, looks
 // through all ids for those of its rows, and lists its rows' tokens in
-// ascending order in LDS: one launch instead of three. 256 tokens into 5003 x
-// 512: 5.7 us, where the sort and its successors take 13.3 for 257; all of one
-// row: 16.4 against 11.6. With the limit at 1024 the latter were 94 against 14.
+// ascending order in LDS: one launch instead of three. 255 tokens into 5003 x
+// 512: 6.3 us, where the ranking and its successors take 11.4; all of one row: 19.1
+// against 12.6, and of 64 tokens 8.2 against 10.7.
 template <int OP, bool BF16>
 __global__ __launch_bounds__(kScanTokens) void embedding_scan_kernel(EmbeddingArgs a, IdSource src) {
   constexpr int U = OP == EMB_GRAD || OP == EMB_GRAD_ADD ? 8 : 16;
@@ -565,8 +568,8 @@ struct LookupArgs {
 
 // 8 columns of one token per thread. STREAM: stores with the non-temporal hint,
 // for outputs that would fill the 256 MB cache anyway. 16384 x 4096 bf16 (134
-// MB): 45 us against 52, with a reader behind it 76 against 75; 4096 tokens (34
-// MB): 13.0 against 14.2, and 22.6 against 22.3.
+// MB): 44 us against 47, with a reader behind it 77 against 76; 4096 tokens (34
+// MB): 13.4 against 13.8, but with the reader 28.7 against 25.5.
 template <bool TABLE_BF16, bool OUT_BF16, bool STREAM>
 __global__ __launch_bounds__(256) void embedding_kernel(LookupArgs a) {
   auto put = [](const auto& v, auto* p) {

@@ -19,8 +19,10 @@ enum : forge_tile { MX_TILE_128x64 = FORGE_TILE_COUNT, MX_TILE_64x64, MX_TILE_64
 // where a CU has nothing else to do, and a CU with `slots` of them finishes one
 // every `full`; `ends` is what a round of tiles adds at its two ends. The
 // persistent schedule runs 256x256 tiles, its rounds counted in full tiles.
-// 23 sizes from 64 x 1024 x 128 to 4096 x 8192 x 8192: one 14% behind the fastest,
-// the others within 5%.
+// Of 23 sizes from 64 x 1024 x 128 to 4096 x 8192 x 8192 and 1 x 4096 x 14336 one is
+// 11% behind the fastest tile and the others within 6% (1024 x 4096 x 8192: 21 us at
+// 128x128, 26 to 40 at the others; 1 x 4096 x 14336: 15 at 64x64 with slots of two
+// stages, 16 to 61). All with a float32 store: which epilogue follows does not enter.
 forge_tile choose_tile(int64_t N, int64_t M, int64_t Kp) {
   struct Kind {
     forge_tile id;

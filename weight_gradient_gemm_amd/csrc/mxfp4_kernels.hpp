@@ -228,10 +228,12 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_mxfp4_kernel(QuantArgs
 // in step 1, MLP-down's product took 222 us against 217, K 32768 805 against 785.
 // Columns enter each element in ascending steps of 64, whatever the tile.
 //
-// Bound by the board's power limit: MLP-down (4096 x 14336 x 8192) takes 209 us,
-// 4.6 PFLOP/s, with the matrix cores busy in 64% of the cycles of a clock that
-// the limit holds at 1.73 GHz; K 32768 769 us, 5.0 PFLOP/s. Small outputs are
-// bound by what a wave issues in a stage: 0.1 us of it for 64x64 tiles.
+// Held back by the board's power limit: MLP-down (4096 x 14336 x 8192) takes
+// 204-228 us on different boards, 4.2-4.7 PFLOP/s, at 1400 W and a clock of 1.68-1.73
+// GHz instead of 2.4, with the matrix cores busy in 64% of the cycles; K 32768
+// 769-826 us, 4.7-5.0 PFLOP/s. The limit is not the only thing: fewer cycles per
+// stage bought half of their share in time. Small outputs are bound by what a wave
+// issues in a stage: 0.1 us of it for 64x64 tiles.
 struct MxArgs {
   const uint8_t *i_scales, *o_scales;
   int64_t kp;

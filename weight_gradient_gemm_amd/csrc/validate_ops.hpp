@@ -30,12 +30,11 @@ struct EmbeddingWorkspace {
 };
 // Tokens whose sum is formed ahead of a row's, as a power of two. A row of n
 // tokens adds up at most 2 (C - 1) + n / C terms one after the other: 32 serve
-// frequent ids of thousands of tokens, more those of tens of thousands. Of
-// 262144 tokens into 32000 x 1024 with 71500 of one id: 352 us with 32, 207 with
-// 128 (spread evenly 190 with both). Of 1048576 into 32000 x 512 with 286000: 1085
-// with 32, 548 with 128, 458 with 256, 461 with 512, and spread evenly over 300
-// rows 408, 445 with 256 and 502 with 512 (all of them with a sort that took 95 us
-// longer than now).
+// frequent ids of thousands of tokens, more those of tens of thousands. Of 16384
+// tokens into 32000 x 1024 with 4400 of one id: 52 us with 32, 64 with 128. Of
+// 262144 with 71500 of one id: 320 us with 32, 191 with 128, 209 with 256 (spread
+// evenly 162 with each). Of 1048576 into 32000 x 512 with 286000: 991 with 32, 441
+// with 128, 354 with 256, and spread evenly over 300 rows 304, 315 and 338.
 inline int embedding_chunk_bits(int64_t T) { return T <= 32768 ? 5 : T <= 524288 ? 7 : 8; }
 bool embedding_sizes_ok(int64_t T, int64_t V, int64_t d);
 EmbeddingWorkspace embedding_workspace(int64_t T, int64_t V, int64_t d);
