@@ -1,8 +1,8 @@
 /*
  * forge_ops.h - C ABI of the operators around the fused weight-gradient step
  * (forge.h) for AMD Instinct MI355X (gfx950): the embedding's lookup and
- * gradient, the global gradient norm with the clipped optimizer steps, and
- * microscaled 4-bit products.
+ * gradient, the global gradient norm with the clipped optimizer steps,
+ * microscaled 4-bit products, and layer norm with its weight's gradient.
  *
  * The conventions of forge.h hold here too: device pointers owned by the
  * caller, dense row-major arrays, 16-byte aligned pointers, nothing allocated,
@@ -225,6 +225,50 @@ FORGE_API forge_status forge_wgrad_adamw_mxfp4(const void* x_codes, const void* 
                                      const void* dy_codes, const void* dy_scales, float* W,
                                      float* m, float* v, int64_t Kp, int64_t d_in, int64_t d_out,
                                      const forge_adamw_params* p, forge_tile tile, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm over the rows of x [T, d], and its backward pass.
+ *
+ *   mean = sum x / d,  rstd = 1 / sqrt(sum (x - mean)^2 / d + eps),
+ *   y = (x - mean) rstd gamma + beta
+ *
+ * and, with n = (x - mean) rstd and a = dY gamma,
+ *
+ *   dX = rstd (a - sum a / d - n sum (a n) / d),
+ *   dgamma = sum over rows of dY n,   dbeta = sum over rows of dY.
+ *
+ * x and dX are of x_dtype, y and dY of y_dtype, each FORGE_F32 or FORGE_BF16;
+ * gamma, beta, dgamma, dbeta [d] and mean, rstd [T] are float32. mean and rstd
+ * need the alignment of a float only. All arithmetic is float32, each result is
+ * rounded once. 0 <= T <= 2^30, d a multiple of 8 up to FORGE_LAYERNORM_MAX_D,
+ * T d <= 2^40. d == 0 does nothing.
+ */
+#define FORGE_LAYERNORM_MAX_D 65536
+
+/*
+ * y from x. beta may be NULL (no bias); mean and rstd, which the backward pass
+ * takes, may each be NULL. eps >= 0 and finite, rounded to float32 (else
+ * FORGE_ERR_HPARAM). With eps == 0 a row of equal values gives NaN, as the
+ * formula does.
+ */
+FORGE_API forge_status forge_layernorm(const void* x, forge_dtype x_dtype, const float* gamma,
+                             const float* beta, void* y, forge_dtype y_dtype, float* mean,
+                             float* rstd, int64_t T, int64_t d, double eps, void* stream);
+
+/* Bytes of the workspace of forge_layernorm_backward, at least 16; 0 if a size is
+ * out of range. */
+FORGE_API int64_t forge_layernorm_workspace(int64_t T, int64_t d);
+
+/*
+ * dX, dgamma and dbeta (which may be NULL) from dY, x and the forward pass's
+ * mean and rstd, all overwritten. dX may be dY itself where x_dtype ==
+ * y_dtype. T == 0 writes zeros to dgamma and dbeta.
+ */
+FORGE_API forge_status forge_layernorm_backward(const void* dY, forge_dtype y_dtype, const void* x,
+                                      forge_dtype x_dtype, const float* gamma,
+                                      const float* mean, const float* rstd, void* dX,
+                                      float* dgamma, float* dbeta, int64_t T, int64_t d,
+                                      void* workspace, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

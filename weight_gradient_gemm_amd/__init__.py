@@ -52,6 +52,8 @@ from ._ops import (  # noqa: F401
     forge_embedding_grad,
     forge_embedding_sgdm,
     forge_grad_norm,
+    forge_layernorm,
+    forge_layernorm_backward,
     forge_matmul_mxfp4,
     forge_mxfp4_empty,
     forge_quantize_mxfp4,

@@ -45,6 +45,10 @@ _SIGNATURES = {
     "forge_matmul_mxfp4": (None, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp]),
     "forge_wgrad_adamw_mxfp4": (None, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
                                        _adam_p, _i32, _vp]),
+    "forge_layernorm": (None, [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _i64, _i64, _d, _vp]),
+    "forge_layernorm_workspace": (_i64, [_i64, _i64]),
+    "forge_layernorm_backward": (None, [_vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                        _i64, _vp, _i64, _vp]),
 }
 
 _DONE = None
@@ -474,3 +478,71 @@ def forge_wgrad_adamw_mxfp4(X, dY, W, m, v, *, step, lr=1e-3, beta1=0.9, beta2=0
     _check(library().forge_wgrad_adamw_mxfp4(xc, xs, yc, ys, *ptrs, k, d_in, d_out,
                                              ctypes.byref(p), tile, st),
            "forge_wgrad_adamw_mxfp4")
+
+
+# --------------------------------------------------------------------------
+# layer norm
+# --------------------------------------------------------------------------
+def _float_or_none(torch, cur, t, shape, name):
+    """Address of an optional float32 tensor of `shape`."""
+    if t is None:
+        return None
+    p = _in(t, torch.float32, name, cur)
+    _shaped(t, shape, name)
+    return p
+
+
+def _given(t, name):
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+
+
+def forge_layernorm(x, gamma, beta, y, mean=None, rstd=None, *, eps=1e-5, stream=None) -> None:
+    """y <- the layer norm of x over its last dimension, times gamma, plus beta.
+
+    x and y of one shape [..., d], each float32 or bfloat16; gamma [d] and beta
+    [d] (or None) float32. ``mean`` and ``rstd`` [...] float32 receive what
+    forge_layernorm_backward needs."""
+    torch, cur, st = _current(stream)
+    xc, yc = _real(torch, x, "x"), _real(torch, y, "y")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    rows, d = x.shape[:-1], x.shape[-1]
+    xp, yp = _in(x, x.dtype, "x", cur), _in(y, y.dtype, "y", cur)
+    _shaped(y, x.shape, "y")
+    _given(gamma, "gamma")
+    _check(library().forge_layernorm(
+        xp, xc, _float_or_none(torch, cur, gamma, (d,), "gamma"),
+        _float_or_none(torch, cur, beta, (d,), "beta"), yp, yc,
+        _float_or_none(torch, cur, mean, rows, "mean"),
+        _float_or_none(torch, cur, rstd, rows, "rstd"), rows.numel(), d, eps, st),
+        "forge_layernorm")
+
+
+def forge_layernorm_backward(dY, x, gamma, mean, rstd, dX, dgamma, dbeta=None, *, workspace=None,
+                             stream=None) -> None:
+    """dX, dgamma and dbeta <- the gradients of forge_layernorm's x, gamma and beta
+    from its output's dY and the mean and rstd that it stored.
+
+    dY, x and dX of one shape [..., d], dX of x's type (and dY itself, if that is
+    of x's type too); the others float32."""
+    torch, cur, st = _current(stream)
+    xc, yc = _real(torch, x, "x"), _real(torch, dY, "dY")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    rows, d = x.shape[:-1], x.shape[-1]
+    T = rows.numel()
+    ptrs = [_in(dY, dY.dtype, "dY", cur), _in(x, x.dtype, "x", cur), _in(dX, x.dtype, "dX", cur)]
+    _shaped(dY, x.shape, "dY")
+    _shaped(dX, x.shape, "dX")
+    for t, name in ((gamma, "gamma"), (mean, "mean"), (rstd, "rstd"), (dgamma, "dgamma")):
+        _given(t, name)
+    lib = library()
+    ws = _workspace(torch, cur, lib.forge_layernorm_workspace(T, d), workspace, stream)
+    _check(lib.forge_layernorm_backward(
+        ptrs[0], yc, ptrs[1], xc, _float_or_none(torch, cur, gamma, (d,), "gamma"),
+        _float_or_none(torch, cur, mean, rows, "mean"),
+        _float_or_none(torch, cur, rstd, rows, "rstd"), ptrs[2],
+        _float_or_none(torch, cur, dgamma, (d,), "dgamma"),
+        _float_or_none(torch, cur, dbeta, (d,), "dbeta"), T, d, ws.data_ptr(), ws.numel(), st),
+        "forge_layernorm_backward")

@@ -336,4 +336,77 @@ forge_status validate_wgrad_adamw_mxfp4(const void* x_codes, const void* x_scale
   return check_tile(tile);
 }
 
+// --------------------------------------------------------------------------
+// layer norm
+// --------------------------------------------------------------------------
+namespace {
+
+bool layernorm_sizes_ok(int64_t T, int64_t d) {
+  return T >= 0 && T <= kMaxTokens && d >= 0 && d <= FORGE_LAYERNORM_MAX_D && T * d <= kMaxElems;
+}
+
+// Whether one of the first `written` spans overlaps another one; `may` is a pair
+// of them that may be the same.
+bool any_overlap(const Span* spans, int written, int n, int may_a = -1, int may_b = -1) {
+  for (int k = 0; k < written; ++k)
+    for (int j = k + 1; j < n; ++j)
+      if (!(k == may_a && j == may_b && spans[k].p == spans[j].p) && spans_overlap(spans[k], spans[j]))
+        return true;
+  return false;
+}
+
+}  // namespace
+
+// The sums of dY n and dY over each workgroup's rows.
+int64_t layernorm_workspace(int64_t T, int64_t d) {
+  if (!layernorm_sizes_ok(T, d)) return 0;
+  return std::max<int64_t>(16, std::min(T, kLayernormParts) * 2 * d * 4);
+}
+
+forge_status validate_layernorm(const void* x, forge_dtype x_dtype, const float* gamma,
+                                const float* beta, const void* y, forge_dtype y_dtype,
+                                const float* mean, const float* rstd, int64_t T, int64_t d,
+                                double eps) {
+  const int xb = dtype_bytes(x_dtype), yb = dtype_bytes(y_dtype);
+  if (xb == 0 || yb == 0) return FORGE_ERR_DTYPE;
+  const bool work = T > 0 && d > 0;
+  if (work && (!x || !gamma || !y)) return FORGE_ERR_NULL;
+  if (!layernorm_sizes_ok(T, d)) return FORGE_ERR_SHAPE;
+  if (work) {
+    if (d % 8 != 0 || !aligned16(x) || !aligned16(gamma) || !aligned16(beta) || !aligned16(y) ||
+        !aligned4(mean) || !aligned4(rstd))
+      return FORGE_ERR_ALIGN;
+    const uint64_t n = uint64_t(T) * uint64_t(d), row = uint64_t(d) * 4u, col = uint64_t(T) * 4u;
+    const Span spans[6] = {{y, n * uint64_t(yb)}, {mean, mean ? col : 0}, {rstd, rstd ? col : 0},
+                           {x, n * uint64_t(xb)}, {gamma, row}, {beta, beta ? row : 0}};
+    if (any_overlap(spans, 3, 6)) return FORGE_ERR_ALIAS;
+  }
+  return std::isfinite(eps) && std::isfinite(float(eps)) && eps >= 0.0 ? FORGE_OK : FORGE_ERR_HPARAM;
+}
+
+forge_status validate_layernorm_backward(const void* dY, forge_dtype y_dtype, const void* x,
+                                         forge_dtype x_dtype, const float* gamma,
+                                         const float* mean, const float* rstd, const void* dX,
+                                         const float* dgamma, const float* dbeta, int64_t T,
+                                         int64_t d, const void* workspace,
+                                         int64_t workspace_bytes) {
+  const int xb = dtype_bytes(x_dtype), yb = dtype_bytes(y_dtype);
+  if (xb == 0 || yb == 0) return FORGE_ERR_DTYPE;
+  if (d > 0 && (!dgamma || !workspace || (T > 0 && (!dY || !x || !gamma || !mean || !rstd || !dX))))
+    return FORGE_ERR_NULL;
+  if (!layernorm_sizes_ok(T, d)) return FORGE_ERR_SHAPE;
+  if (d == 0) return FORGE_OK;
+  if (workspace_bytes < layernorm_workspace(T, d)) return FORGE_ERR_SHAPE;
+  if (d % 8 != 0 || !aligned16(dgamma) || !aligned16(dbeta) || !aligned16(workspace))
+    return FORGE_ERR_ALIGN;
+  if (T > 0 && (!aligned16(dY) || !aligned16(x) || !aligned16(gamma) || !aligned16(dX) ||
+                !aligned4(mean) || !aligned4(rstd)))
+    return FORGE_ERR_ALIGN;
+  const uint64_t n = uint64_t(T) * uint64_t(d), row = uint64_t(d) * 4u, col = uint64_t(T) * 4u;
+  const Span spans[9] = {{dX, n * uint64_t(xb)}, {dgamma, row}, {dbeta, dbeta ? row : 0},
+                         {workspace, uint64_t(workspace_bytes)}, {dY, n * uint64_t(yb)},
+                         {x, n * uint64_t(xb)}, {gamma, T > 0 ? row : 0}, {mean, col}, {rstd, col}};
+  return any_overlap(spans, 4, 9, xb == yb ? 0 : -1, 4) ? FORGE_ERR_ALIAS : FORGE_OK;
+}
+
 }  // namespace forge

@@ -59,4 +59,18 @@ forge_status validate_wgrad_adamw_mxfp4(const void* x_codes, const void* x_scale
                                         int64_t d_in, int64_t d_out, const forge_adamw_params* p,
                                         forge_tile tile);
 
+// Most partial sums of the layer norm's weight gradients (one workgroup each).
+constexpr int64_t kLayernormParts = 512;
+int64_t layernorm_workspace(int64_t T, int64_t d);
+forge_status validate_layernorm(const void* x, forge_dtype x_dtype, const float* gamma,
+                                const float* beta, const void* y, forge_dtype y_dtype,
+                                const float* mean, const float* rstd, int64_t T, int64_t d,
+                                double eps);
+forge_status validate_layernorm_backward(const void* dY, forge_dtype y_dtype, const void* x,
+                                         forge_dtype x_dtype, const float* gamma,
+                                         const float* mean, const float* rstd, const void* dX,
+                                         const float* dgamma, const float* dbeta, int64_t T,
+                                         int64_t d, const void* workspace,
+                                         int64_t workspace_bytes);
+
 }  // namespace forge
