@@ -2,7 +2,8 @@
  * forge_ops.h - C ABI of the operators around the fused weight-gradient step
  * (forge.h) for AMD Instinct MI355X (gfx950): the embedding's lookup and
  * gradient, the global gradient norm with the clipped optimizer steps,
- * microscaled 4-bit products, and layer norm with its weight's gradient.
+ * microscaled 4-bit products, layer norm with its weight's gradient, and
+ * distillation from a teacher's top logits.
  *
  * The conventions of forge.h hold here too: device pointers owned by the
  * caller, dense row-major arrays, 16-byte aligned pointers, nothing allocated,
@@ -269,6 +270,48 @@ FORGE_API forge_status forge_layernorm_backward(const void* dY, forge_dtype y_dt
                                       const float* mean, const float* rstd, void* dX,
                                       float* dgamma, float* dbeta, int64_t T, int64_t d,
                                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Distillation from a teacher's top logits: each row's loss, and the gradient
+ * of the student's logits.
+ *
+ * Row t has the student's logits z [V] and K entries of the teacher, each an id
+ * and a logit. An entry whose id is outside [0, V), or whose logit is -infinity,
+ * is not there. With q the softmax of the row's entries over the temperature
+ * tau, p the softmax of z over tau, and w the row's weight,
+ *
+ *   loss[t]    = scale w tau^2 sum over entries with q_j > 0 of q_j (log q_j - log p[id_j]),
+ *   grad[t, i] = scale w tau (p[i] - sum of the q_j with id_j == i),
+ *
+ * which is d loss[t] / d z[i]. A row of weight 0 or without entries has loss 0
+ * and a gradient of zeros, whatever its logits are. Otherwise NaN and infinities
+ * go through as in the formulas; a logit of -infinity (a column that is masked)
+ * has p = 0.
+ *   logits [T, ld] of z_dtype; columns V .. ld - 1 (a padded vocabulary) are
+ *     not looked at. ld a multiple of 8 (else FORGE_ERR_ALIGN), V <= ld.
+ *   teacher [T, K] of teacher_dtype, ids [T, K] int32 or int64 (id_bytes 4 or 8).
+ *     An id may recur in a row: each entry counts by itself.
+ *   weight [T] float32, or NULL: 1 for every row. loss [T] float32. These four
+ *     need the alignment of their elements only.
+ *   grad [T, ld] of grad_dtype, overwritten (columns past V with zeros), ready
+ *     as dY of the weight-gradient calls; NULL: the loss alone. It may be logits
+ *     itself where z_dtype == grad_dtype.
+ * The element types are FORGE_F32 or FORGE_BF16. Arithmetic is float32.
+ * temperature > 0 and scale: finite, as float32 too, and so 1 / temperature
+ * (else FORGE_ERR_HPARAM). 0 <= T <= 2^30, 0 <= V <= ld <= 2^22, T ld <= 2^40,
+ * 0 <= K <= FORGE_DISTILL_MAX_K.
+ */
+#define FORGE_DISTILL_MAX_K 1024
+
+/* Bytes of forge_distill's workspace, at least 16; 0 if a size is out of range. */
+FORGE_API int64_t forge_distill_workspace(int64_t T, int64_t V, int64_t K);
+
+FORGE_API forge_status forge_distill(const void* logits, forge_dtype z_dtype, int64_t ld,
+                           const void* teacher, forge_dtype teacher_dtype, const void* ids,
+                           int32_t id_bytes, const float* weight, float* loss, void* grad,
+                           forge_dtype grad_dtype, int64_t T, int64_t V, int64_t K,
+                           double temperature, double scale, void* workspace,
+                           int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -87,3 +87,49 @@ def test_layernorm_reaches_the_device_check(lib):
     assert norm(lib, T=1 << 24, d=65536, x=1 << 45, y=1 << 46) == E_DEVICE
     assert back(lib) == back(lib, db=NULL) == back(lib, dX=A, xt=BF16) == E_DEVICE
     assert back(lib, T=0, dY=NULL, x=NULL, gamma=NULL, mean=NULL, rstd=NULL, dX=NULL) == E_DEVICE
+
+
+# --------------------------------------------------------------------------
+# distillation
+# --------------------------------------------------------------------------
+def distill(lib, z=A, zt=BF16, ld=128, u=B, ut=F32, ids=C, ib=8, w=D, loss=E, grad=F, gt=BF16, T=10,
+            V=100, K=5, tau=2.0, scale=1.0, ws=G, ws_bytes=1 << 20):
+    return lib.forge_distill(z, zt, ld, u, ut, ids, ib, w, loss, grad, gt, T, V, K, tau, scale, ws,
+                             ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(zt=2), E_DTYPE), (dict(ut=5), E_DTYPE), (dict(gt=-1), E_DTYPE), (dict(ib=2), E_DTYPE),
+    *[({k: NULL}, E_NULL) for k in ("z", "u", "ids", "loss", "ws")],
+    (dict(T=-1), E_SHAPE), (dict(V=-1), E_SHAPE), (dict(K=-1), E_SHAPE), (dict(K=1025), E_SHAPE),
+    (dict(V=129), E_SHAPE), (dict(ld=(1 << 22) + 8), E_SHAPE), (dict(T=(1 << 30) + 1), E_SHAPE),
+    (dict(T=1 << 30, ld=2048), E_SHAPE), (dict(ws_bytes=10 * 8 + 10 * 5 * 4 - 1), E_SHAPE),
+    (dict(ld=100), E_ALIGN), (dict(ids=C + 4), E_ALIGN), (dict(ids=C + 2, ib=4), E_ALIGN),
+    (dict(w=D + 2), E_ALIGN), (dict(loss=E + 1), E_ALIGN),
+    *[({k: p + 8}, E_ALIGN) for k, p in dict(z=A, grad=F, ws=G).items()],
+    (dict(u=B + 2), E_ALIGN), (dict(u=B + 1, ut=BF16), E_ALIGN),
+    (dict(grad=A, gt=F32), E_ALIAS), (dict(grad=A + 16), E_ALIAS), (dict(grad=B), E_ALIAS),
+    (dict(loss=A + 10 * 128 * 2 - 4), E_ALIAS), (dict(loss=D + 36), E_ALIAS), (dict(ws=C), E_ALIAS),
+    (dict(grad=G), E_ALIAS), (dict(loss=F), E_ALIAS),
+    (dict(tau=0.0), E_HPARAM), (dict(tau=-1.0), E_HPARAM), (dict(tau=NAN), E_HPARAM),
+    (dict(tau=INF), E_HPARAM), (dict(tau=1e-39), E_HPARAM), (dict(tau=1e39), E_HPARAM),
+    (dict(scale=NAN), E_HPARAM), (dict(scale=INF), E_HPARAM), (dict(scale=1e38, tau=100.0), E_HPARAM),
+    (dict(T=0, z=NULL, u=NULL, ids=NULL, w=NULL, loss=NULL, grad=NULL, ws=NULL), OK),
+])
+def test_distill_rejects(lib, kw, status):
+    assert distill(lib, **kw) == status
+
+
+def test_distill_workspace(lib):
+    f = lib.forge_distill_workspace
+    assert f(-1, 8, 1) == f(1, -1, 1) == f(1, 8, 1025) == f(1, (1 << 22) + 1, 1) == 0
+    assert f(0, 0, 0) >= 16 and f(10, 100, 5) >= 10 * 5 * 4
+
+
+def test_distill_reaches_the_device_check(lib):
+    no_gpu()
+    assert distill(lib) == distill(lib, grad=NULL) == distill(lib, grad=A) == E_DEVICE
+    assert distill(lib, w=NULL, K=0, u=NULL, ids=NULL) == distill(lib, V=0, z=NULL) == E_DEVICE
+    assert distill(lib, ib=4, ids=C + 4, loss=E + 4, w=D + 12, u=B + 4) == E_DEVICE
+    assert distill(lib, ut=BF16, u=B + 2) == E_DEVICE
+    assert distill(lib, scale=0.0, tau=1e-37) == distill(lib, scale=-3.0) == E_DEVICE

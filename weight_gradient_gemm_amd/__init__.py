@@ -47,6 +47,7 @@ from ._ops import (  # noqa: F401
     ForgeTensorList,
     forge_adamw_clipped,
     forge_clip_grads,
+    forge_distill,
     forge_embedding,
     forge_embedding_adamw,
     forge_embedding_grad,

@@ -49,6 +49,9 @@ _SIGNATURES = {
     "forge_layernorm_workspace": (_i64, [_i64, _i64]),
     "forge_layernorm_backward": (None, [_vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
                                         _i64, _vp, _i64, _vp]),
+    "forge_distill_workspace": (_i64, [_i64, _i64, _i64]),
+    "forge_distill": (None, [_vp, _i32, _i64, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _i64, _i64,
+                             _i64, _d, _d, _vp, _i64, _vp]),
 }
 
 _DONE = None
@@ -546,3 +549,46 @@ def forge_layernorm_backward(dY, x, gamma, mean, rstd, dX, dgamma, dbeta=None, *
         _float_or_none(torch, cur, dgamma, (d,), "dgamma"),
         _float_or_none(torch, cur, dbeta, (d,), "dbeta"), T, d, ws.data_ptr(), ws.numel(), st),
         "forge_layernorm_backward")
+
+
+# --------------------------------------------------------------------------
+# distillation
+# --------------------------------------------------------------------------
+def forge_distill(logits, teacher, ids, loss, grad=None, *, vocab=None, weight=None, temperature=1.0,
+                  scale=1.0, workspace=None, stream=None) -> None:
+    """loss[t] <- scale * weight[t] * temperature^2 * KL(q_t || p_t), and grad <- its
+    gradient by logits: q_t the softmax of row t's teacher logits over the
+    temperature, p_t that of the student's.
+
+    logits [..., ld] float32 or bfloat16, of which the first ``vocab`` columns (None:
+    all) are the vocabulary; teacher [..., K] float32 or bfloat16 and ids [..., K]
+    int32 or int64, an id outside the vocabulary (-1, say) for an entry that is not
+    there; weight and loss [...] float32. ``grad`` (None: the loss alone) has the
+    logits' shape, float32 or bfloat16, zeros past the vocabulary; it may be the
+    logits themselves. Rows of weight 0 or without entries have loss 0 and a
+    gradient of zeros."""
+    torch, cur, st = _current(stream)
+    zc, uc = _real(torch, logits, "logits"), _real(torch, teacher, "teacher")
+    if logits.dim() < 1:
+        raise ValueError("logits must have at least one dimension")
+    rows, ld = logits.shape[:-1], logits.shape[-1]
+    T, V = rows.numel(), ld if vocab is None else int(vocab)
+    ip, id_bytes, _ = _ids(torch, cur, ids)
+    if teacher.dim() < 1:
+        raise ValueError("teacher must have at least one dimension")
+    K = teacher.shape[-1]
+    _shaped(teacher, (*rows, K), "teacher")
+    _shaped(ids, (*rows, K), "ids")
+    _given(loss, "loss")
+    gc, gp = zc, None
+    if grad is not None:
+        gc = _real(torch, grad, "grad")
+        _shaped(grad, logits.shape, "grad")
+        gp = _in(grad, grad.dtype, "grad", cur)
+    lib = library()
+    ws = _workspace(torch, cur, lib.forge_distill_workspace(T, V, K), workspace, stream)
+    _check(lib.forge_distill(
+        _in(logits, logits.dtype, "logits", cur), zc, ld, _in(teacher, teacher.dtype, "teacher", cur),
+        uc, ip, id_bytes, _float_or_none(torch, cur, weight, rows, "weight"),
+        _float_or_none(torch, cur, loss, rows, "loss"), gp, gc, T, V, K, temperature, scale,
+        ws.data_ptr(), ws.numel(), st), "forge_distill")

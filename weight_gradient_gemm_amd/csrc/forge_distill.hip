@@ -1,0 +1,84 @@
+// Distillation entry points of the forge C ABI.
+#include <algorithm>
+
+#include "distill_kernels.hpp"
+#include "forge_ops.h"
+#include "host.hpp"
+#include "validate_ops.hpp"
+
+namespace forge {
+namespace {
+
+static_assert(kDistillMaxK == FORGE_DISTILL_MAX_K && kDistillChunk == 32 * kDistillThreads,
+              "the kernels' sizes");
+
+// Most workgroups of a launch; what is beyond loops.
+constexpr int64_t kMaxGrid = int64_t(1) << 20;
+dim3 grid_for(int64_t items) { return dim3(uint32_t(std::min(items, kMaxGrid))); }
+
+template <bool ZB, bool GB>
+forge_status launch(DistillArgs a, hipStream_t s) {
+  a.items = a.T * a.chunks;
+  if (a.items > 0 && a.K > 0) {
+    hipLaunchKernelGGL((distill_stats_kernel<ZB>), grid_for(a.items), dim3(kDistillThreads), 0, s, a);
+    if (forge_status st = launch_status()) return st;
+  }
+  a.items = a.T * a.chunks_out;
+  hipLaunchKernelGGL((distill_gradient_kernel<ZB, GB>), grid_for(a.items), dim3(kDistillThreads), 0, s, a);
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace forge
+
+using namespace forge;
+
+extern "C" {
+
+FORGE_API int64_t forge_distill_workspace(int64_t T, int64_t V, int64_t K) {
+  return distill_sizes_ok(T, V, K) ? distill_workspace(T, V, K).bytes : 0;
+}
+
+FORGE_API forge_status forge_distill(const void* logits, forge_dtype z_dtype, int64_t ld,
+                                     const void* teacher, forge_dtype teacher_dtype, const void* ids,
+                                     int32_t id_bytes, const float* weight, float* loss, void* grad,
+                                     forge_dtype grad_dtype, int64_t T, int64_t V, int64_t K,
+                                     double temperature, double scale, void* workspace,
+                                     int64_t workspace_bytes, void* stream) {
+  if (forge_status s = validate_distill(logits, z_dtype, ld, teacher, teacher_dtype, ids, id_bytes,
+                                        weight, loss, grad, grad_dtype, T, V, K, temperature, scale,
+                                        workspace, workspace_bytes))
+    return s;
+  if (T == 0) return FORGE_OK;
+  if (forge_status s = check_device()) return s;
+  (void)hipGetLastError();
+  const DistillWorkspace ws = distill_workspace(T, V, K);
+  char* const base = static_cast<char*>(workspace);
+  DistillArgs a{};
+  a.z = logits;
+  a.teacher = teacher;
+  a.ids = ids;
+  a.weight = weight;
+  a.loss = loss;
+  a.grad = grad;
+  a.stats = reinterpret_cast<float2*>(base + ws.stats);
+  a.logit = reinterpret_cast<float*>(base + ws.logit);
+  a.T = T;
+  a.ld = ld;
+  a.V = int32_t(V);
+  a.K = int32_t(K);
+  a.chunks = int32_t((V + kDistillChunk - 1) / kDistillChunk);
+  a.chunks_out = grad ? std::max(1, int32_t((ld + kDistillChunk - 1) / kDistillChunk)) : 1;
+  a.wide_ids = id_bytes == 8;
+  a.teacher_bf16 = teacher_dtype == FORGE_BF16;
+  a.c = float(1.4426950408889634 / temperature);
+  a.inv_tau = float(1.0 / temperature);
+  a.loss_scale = float(scale * temperature * temperature);
+  a.grad_scale = float(scale * temperature);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (z_dtype == FORGE_BF16)
+    return grad_dtype == FORGE_BF16 ? launch<true, true>(a, st) : launch<true, false>(a, st);
+  return grad_dtype == FORGE_BF16 ? launch<false, true>(a, st) : launch<false, false>(a, st);
+}
+
+}  // extern "C"

@@ -55,7 +55,7 @@ struct Backward {
     if (a.d <= 16384) return launch_backward<XB, YB, 16, 16>(a, parts, s);
     // Sums of so many columns do not fit a workgroup's registers beside the row:
     // the columns first, as dX may overwrite dY.
-    constexpr int E = ln_elems<XB, YB>;
+    constexpr int E = io_elems<XB, YB>;
     parts = int32_t(std::min<int64_t>((a.T + 8 * kLnColumnRows - 1) / (8 * kLnColumnRows), 64));
     hipLaunchKernelGGL((layernorm_columns_kernel<XB, YB>), dim3((a.d + 32 * E - 1) / (32 * E), parts),
                        dim3(256), 0, s, a);

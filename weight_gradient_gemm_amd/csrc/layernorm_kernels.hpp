@@ -18,9 +18,8 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
-#include <type_traits>
 
-#include "wgrad_kernels.hpp"
+#include "row_io.hpp"
 
 namespace forge {
 
@@ -34,61 +33,6 @@ struct LnArgs {
   int32_t d;
   float eps;
 };
-
-// Elements of a vector access: 16 bytes of the wider type.
-template <bool XB, bool YB>
-constexpr int ln_elems = XB && YB ? 8 : 4;
-
-// E consecutive elements of a float32 or bf16 array.
-template <bool BF16, int E>
-__device__ __forceinline__ void ln_load(const void* p, int64_t at, float (&v)[E]) {
-  if constexpr (BF16 && E == 8) {
-    const u32x4_t r = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + at);
-    const f32x4_t lo = unpack_bf16x4(u32x2_t{r[0], r[1]}), hi = unpack_bf16x4(u32x2_t{r[2], r[3]});
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = lo[k];
-      v[4 + k] = hi[k];
-    }
-  } else {
-    const f32x4_t r = BF16 ? unpack_bf16x4(*reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(p) + at))
-                           : *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + at);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = r[k];
-  }
-}
-
-template <bool BF16, int E>
-__device__ __forceinline__ void ln_store(void* p, int64_t at, const float (&v)[E]) {
-  if constexpr (BF16 && E == 8) {
-    const u32x2_t lo = pack_bf16x4(f32x4_t{v[0], v[1], v[2], v[3]});
-    const u32x2_t hi = pack_bf16x4(f32x4_t{v[4], v[5], v[6], v[7]});
-    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + at) = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-  } else {
-    const f32x4_t r = {v[0], v[1], v[2], v[3]};
-    if constexpr (BF16)
-      *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p) + at) = pack_bf16x4(r);
-    else
-      *reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + at) = r;
-  }
-}
-
-// E consecutive elements of a float32 array.
-template <int E>
-__device__ __forceinline__ void ln_load32(const float* p, int64_t at, float (&v)[E]) {
-#pragma unroll
-  for (int j = 0; j < E; j += 4) {
-    const f32x4_t r = *reinterpret_cast<const f32x4_t*>(p + at + j);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[j + k] = r[k];
-  }
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
-}
 
 // Sum of v over the WAVES waves that share a row, in every thread. `part`: WAVES
 // floats, which the next call but one may use again.
@@ -114,7 +58,7 @@ constexpr int ln_rows = WAVES == 1 ? 4 : 1;
 // EL elements of the row to a thread.
 template <bool XB, bool YB, int EL, int WAVES>
 __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_kernel(LnArgs a) {
-  constexpr int E = ln_elems<XB, YB>, NV = EL / E, L = 64 * WAVES;
+  constexpr int E = io_elems<XB, YB>, NV = EL / E, L = 64 * WAVES;
   __shared__ float part[2][WAVES];
   const int me = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
   const int sub = WAVES == 1 ? threadIdx.x >> 6 : 0;
@@ -127,7 +71,7 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_kernel(LnArgs a) 
     for (int i = 0; i < NV; ++i) {
       const int c = (i * L + me) * E;
       if (c < a.d) {
-        ln_load<XB, E>(a.x, base + c, v[i]);
+        load_elems<XB, E>(a.x, base + c, v[i]);
 #pragma unroll
         for (int k = 0; k < E; ++k) s += v[i][k];
       }
@@ -148,11 +92,11 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_kernel(LnArgs a) 
       const int c = (i * L + me) * E;
       if (c < a.d) {
         float g[E], b[E] = {};
-        ln_load32<E>(a.gamma, c, g);
-        if (a.beta) ln_load32<E>(a.beta, c, b);
+        load_f32<E>(a.gamma, c, g);
+        if (a.beta) load_f32<E>(a.beta, c, b);
 #pragma unroll
         for (int k = 0; k < E; ++k) v[i][k] = __builtin_fmaf(v[i][k] * rstd, g[k], b[k]);
-        ln_store<YB, E>(a.out, base + c, v[i]);
+        store_elems<YB, E>(a.out, base + c, v[i]);
       }
     }
     if (me == 0) {
@@ -165,21 +109,21 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_kernel(LnArgs a) 
 // Rows of any length: read three times, the second and third time from the caches.
 template <bool XB, bool YB>
 __global__ __launch_bounds__(1024) void layernorm_wide_kernel(LnArgs a) {
-  constexpr int E = ln_elems<XB, YB>, WAVES = 16;
+  constexpr int E = io_elems<XB, YB>, WAVES = 16;
   __shared__ float part[2][WAVES];
   const float d = float(a.d);
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     const int64_t base = row * a.d;
     float v[E], s = 0.0f;
     for (int c = threadIdx.x * E; c < a.d; c += 1024 * E) {
-      ln_load<XB, E>(a.x, base + c, v);
+      load_elems<XB, E>(a.x, base + c, v);
 #pragma unroll
       for (int k = 0; k < E; ++k) s += v[k];
     }
     const float mean = row_sum<WAVES>(s, part[0]) / d;
     s = 0.0f;
     for (int c = threadIdx.x * E; c < a.d; c += 1024 * E) {
-      ln_load<XB, E>(a.x, base + c, v);
+      load_elems<XB, E>(a.x, base + c, v);
 #pragma unroll
       for (int k = 0; k < E; ++k) {
         const float e = v[k] - mean;
@@ -189,12 +133,12 @@ __global__ __launch_bounds__(1024) void layernorm_wide_kernel(LnArgs a) {
     const float rstd = 1.0f / sqrtf(row_sum<WAVES>(s, part[1]) / d + a.eps);
     for (int c = threadIdx.x * E; c < a.d; c += 1024 * E) {
       float g[E], b[E] = {};
-      ln_load<XB, E>(a.x, base + c, v);
-      ln_load32<E>(a.gamma, c, g);
-      if (a.beta) ln_load32<E>(a.beta, c, b);
+      load_elems<XB, E>(a.x, base + c, v);
+      load_f32<E>(a.gamma, c, g);
+      if (a.beta) load_f32<E>(a.beta, c, b);
 #pragma unroll
       for (int k = 0; k < E; ++k) v[k] = __builtin_fmaf((v[k] - mean) * rstd, g[k], b[k]);
-      ln_store<YB, E>(a.out, base + c, v);
+      store_elems<YB, E>(a.out, base + c, v);
     }
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -206,7 +150,7 @@ __global__ __launch_bounds__(1024) void layernorm_wide_kernel(LnArgs a) {
 // dX of the workgroup's rows, and its sums of dY n and dY.
 template <bool XB, bool YB, int EL, int WAVES>
 __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_backward_kernel(LnArgs a) {
-  constexpr int E = ln_elems<XB, YB>, NV = EL / E, L = 64 * WAVES;
+  constexpr int E = io_elems<XB, YB>, NV = EL / E, L = 64 * WAVES;
   __shared__ float part[2][2][WAVES];
   __shared__ __attribute__((aligned(16))) float join[WAVES == 1 ? 3 * 2 * 64 * EL : 4];
   const int me = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
@@ -218,7 +162,7 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_backward_kernel(L
     const int c = (i * L + me) * E;
 #pragma unroll
     for (int k = 0; k < E; ++k) dg[i][k] = db[i][k] = g[i][k] = 0.0f;
-    if (c < a.d) ln_load32<E>(a.gamma, c, g[i]);
+    if (c < a.d) load_f32<E>(a.gamma, c, g[i]);
   }
   int turn = 0;
   for (int64_t row = int64_t(blockIdx.x) * ln_rows<WAVES> + sub; row < a.T;
@@ -230,8 +174,8 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_backward_kernel(L
     for (int i = 0; i < NV; ++i) {
       const int c = (i * L + me) * E;
       if (c < a.d) {
-        ln_load<XB, E>(a.x, base + c, n[i]);
-        ln_load<YB, E>(a.dy, base + c, y[i]);
+        load_elems<XB, E>(a.x, base + c, n[i]);
+        load_elems<YB, E>(a.dy, base + c, y[i]);
 #pragma unroll
         for (int k = 0; k < E; ++k) {
           n[i][k] = (n[i][k] - mean) * rstd;
@@ -266,7 +210,7 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_backward_kernel(L
       if (c < a.d) {
 #pragma unroll
         for (int k = 0; k < E; ++k) y[i][k] = rstd * (y[i][k] - s1 - n[i][k] * s2);
-        ln_store<XB, E>(a.out, base + c, y[i]);
+        store_elems<XB, E>(a.out, base + c, y[i]);
       }
     }
   }
@@ -310,7 +254,7 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_backward_kernel(L
 // dX alone, of rows of any length: read twice, the second time from the caches.
 template <bool XB, bool YB>
 __global__ __launch_bounds__(1024) void layernorm_dx_wide_kernel(LnArgs a) {
-  constexpr int E = ln_elems<XB, YB>, WAVES = 16;
+  constexpr int E = io_elems<XB, YB>, WAVES = 16;
   __shared__ float part[2][WAVES];
   const float d = float(a.d);
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
@@ -318,9 +262,9 @@ __global__ __launch_bounds__(1024) void layernorm_dx_wide_kernel(LnArgs a) {
     const float mean = a.mean[row], rstd = a.rstd[row];
     float n[E], y[E], g[E], s1 = 0.0f, s2 = 0.0f;
     for (int c = threadIdx.x * E; c < a.d; c += 1024 * E) {
-      ln_load<XB, E>(a.x, base + c, n);
-      ln_load<YB, E>(a.dy, base + c, y);
-      ln_load32<E>(a.gamma, c, g);
+      load_elems<XB, E>(a.x, base + c, n);
+      load_elems<YB, E>(a.dy, base + c, y);
+      load_f32<E>(a.gamma, c, g);
 #pragma unroll
       for (int k = 0; k < E; ++k) {
         const float v = y[k] * g[k];
@@ -331,12 +275,12 @@ __global__ __launch_bounds__(1024) void layernorm_dx_wide_kernel(LnArgs a) {
     s1 = row_sum<WAVES>(s1, part[0]) / d;
     s2 = row_sum<WAVES>(s2, part[1]) / d;
     for (int c = threadIdx.x * E; c < a.d; c += 1024 * E) {
-      ln_load<XB, E>(a.x, base + c, n);
-      ln_load<YB, E>(a.dy, base + c, y);
-      ln_load32<E>(a.gamma, c, g);
+      load_elems<XB, E>(a.x, base + c, n);
+      load_elems<YB, E>(a.dy, base + c, y);
+      load_f32<E>(a.gamma, c, g);
 #pragma unroll
       for (int k = 0; k < E; ++k) y[k] = rstd * (y[k] * g[k] - s1 - (n[k] - mean) * rstd * s2);
-      ln_store<XB, E>(a.out, base + c, y);
+      store_elems<XB, E>(a.out, base + c, y);
     }
   }
 }
@@ -346,7 +290,7 @@ __global__ __launch_bounds__(1024) void layernorm_dx_wide_kernel(LnArgs a) {
 constexpr int kLnColumnRows = 8;
 template <bool XB, bool YB>
 __global__ __launch_bounds__(256) void layernorm_columns_kernel(LnArgs a) {
-  constexpr int E = ln_elems<XB, YB>;
+  constexpr int E = io_elems<XB, YB>;
   __shared__ float join[2][E][256];
   const int me = threadIdx.x & 31, sub = threadIdx.x >> 5;
   const int c = (blockIdx.x * 32 + me) * E;
@@ -356,8 +300,8 @@ __global__ __launch_bounds__(256) void layernorm_columns_kernel(LnArgs a) {
          row += int64_t(gridDim.y) * kLnColumnRows) {
       const float mean = a.mean[row], rstd = a.rstd[row];
       float n[E], y[E];
-      ln_load<XB, E>(a.x, row * a.d + c, n);
-      ln_load<YB, E>(a.dy, row * a.d + c, y);
+      load_elems<XB, E>(a.x, row * a.d + c, n);
+      load_elems<YB, E>(a.dy, row * a.d + c, y);
 #pragma unroll
       for (int k = 0; k < E; ++k) {
         dg[k] = __builtin_fmaf(y[k], (n[k] - mean) * rstd, dg[k]);

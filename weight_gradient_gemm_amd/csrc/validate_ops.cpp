@@ -409,4 +409,51 @@ forge_status validate_layernorm_backward(const void* dY, forge_dtype y_dtype, co
   return any_overlap(spans, 4, 9, xb == yb ? 0 : -1, 4) ? FORGE_ERR_ALIAS : FORGE_OK;
 }
 
+// --------------------------------------------------------------------------
+// distillation
+// --------------------------------------------------------------------------
+bool distill_sizes_ok(int64_t T, int64_t V, int64_t K) {
+  return T >= 0 && T <= kMaxTokens && V >= 0 && V <= kMaxDim && K >= 0 && K <= FORGE_DISTILL_MAX_K &&
+         T * V <= kMaxElems;
+}
+
+DistillWorkspace distill_workspace(int64_t T, int64_t V, int64_t K) {
+  DistillWorkspace w{};
+  w.stats = 0;
+  w.logit = T * ((V + kDistillChunk - 1) / kDistillChunk) * 8;
+  w.bytes = std::max<int64_t>(16, w.logit + T * K * 4);
+  return w;
+}
+
+forge_status validate_distill(const void* logits, forge_dtype z_dtype, int64_t ld,
+                              const void* teacher, forge_dtype teacher_dtype, const void* ids,
+                              int32_t id_bytes, const float* weight, const float* loss,
+                              const void* grad, forge_dtype grad_dtype, int64_t T, int64_t V,
+                              int64_t K, double temperature, double scale, const void* workspace,
+                              int64_t workspace_bytes) {
+  const int zb = dtype_bytes(z_dtype), ub = dtype_bytes(teacher_dtype), gb = dtype_bytes(grad_dtype);
+  if (zb == 0 || ub == 0 || gb == 0 || !ids_ok(id_bytes)) return FORGE_ERR_DTYPE;
+  if (T > 0 && (!loss || !workspace || (V > 0 && !logits) || (K > 0 && (!teacher || !ids))))
+    return FORGE_ERR_NULL;
+  if (!distill_sizes_ok(T, V, K) || ld < V || ld > kMaxDim || T * ld > kMaxElems) return FORGE_ERR_SHAPE;
+  if (T > 0) {
+    if (workspace_bytes < distill_workspace(T, V, K).bytes) return FORGE_ERR_SHAPE;
+    if (ld % 8 != 0 || !aligned16(logits) || !aligned16(grad) || !aligned_ids(teacher, ub) ||
+        !aligned_ids(ids, id_bytes) || !aligned4(weight) || !aligned4(loss) || !aligned16(workspace))
+      return FORGE_ERR_ALIGN;
+    const uint64_t n = uint64_t(T) * uint64_t(ld), k = uint64_t(T) * uint64_t(K), col = uint64_t(T) * 4u;
+    const Span spans[7] = {{grad, grad ? n * uint64_t(gb) : 0}, {loss, col},
+                           {workspace, uint64_t(workspace_bytes)}, {logits, logits ? n * uint64_t(zb) : 0},
+                           {teacher, k * uint64_t(ub)}, {ids, k * uint64_t(id_bytes)},
+                           {weight, weight ? col : 0}};
+    if (any_overlap(spans, 3, 7, zb == gb ? 0 : -1, 3)) return FORGE_ERR_ALIAS;
+  }
+  const auto fine = [](double x) { return std::isfinite(x) && std::isfinite(float(x)); };
+  if (!fine(temperature) || !(float(temperature) > 0.0f) || !fine(1.4426950408889634 / temperature) ||
+      float(1.0 / temperature) == 0.0f || !fine(scale) || !fine(scale * temperature) ||
+      !fine(scale * temperature * temperature))
+    return FORGE_ERR_HPARAM;
+  return FORGE_OK;
+}
+
 }  // namespace forge

@@ -73,4 +73,20 @@ forge_status validate_layernorm_backward(const void* dY, forge_dtype y_dtype, co
                                          int64_t d, const void* workspace,
                                          int64_t workspace_bytes);
 
+// Columns of a chunk of a row of logits, which one workgroup goes through.
+constexpr int64_t kDistillChunk = 8192;
+// Byte offsets of the parts of distillation's workspace: each chunk's maximum
+// and sum of exponentials, and the student's logits of the teacher's ids.
+struct DistillWorkspace {
+  int64_t stats, logit, bytes;
+};
+bool distill_sizes_ok(int64_t T, int64_t V, int64_t K);
+DistillWorkspace distill_workspace(int64_t T, int64_t V, int64_t K);
+forge_status validate_distill(const void* logits, forge_dtype z_dtype, int64_t ld,
+                              const void* teacher, forge_dtype teacher_dtype, const void* ids,
+                              int32_t id_bytes, const float* weight, const float* loss,
+                              const void* grad, forge_dtype grad_dtype, int64_t T, int64_t V,
+                              int64_t K, double temperature, double scale, const void* workspace,
+                              int64_t workspace_bytes);
+
 }  // namespace forge
