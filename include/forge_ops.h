@@ -2,8 +2,9 @@
  * forge_ops.h - C ABI of the operators around the fused weight-gradient step
  * (forge.h) for AMD Instinct MI355X (gfx950): the embedding's lookup and
  * gradient, the global gradient norm with the clipped optimizer steps,
- * microscaled 4-bit products, layer norm with its weight's gradient, and
- * distillation from a teacher's top logits.
+ * microscaled 4-bit products, layer norm with its weight's gradient,
+ * distillation from a teacher's top logits, and 8-bit products with a scale for
+ * each block of 128.
  *
  * The conventions of forge.h hold here too: device pointers owned by the
  * caller, dense row-major arrays, 16-byte aligned pointers, nothing allocated,
@@ -312,6 +313,68 @@ FORGE_API forge_status forge_distill(const void* logits, forge_dtype z_dtype, in
                            forge_dtype grad_dtype, int64_t T, int64_t V, int64_t K,
                            double temperature, double scale, void* workspace,
                            int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit floating point operands with a scale for each block of 128, and their
+ * product.
+ *
+ * Values along the contraction K are cut into blocks of 128. A block has one
+ * scale, a power of two 2^(s - 127) stored as the byte s (E8M0), and 128 fp8
+ * codes (FORGE_FP8_E4M3 or FORGE_FP8_E5M2). s is the least one, at least 0,
+ * with which the block's largest magnitude over the scale is within the
+ * format (448 or 57344), so no value is clipped; values are rounded to the
+ * nearest code, ties to the even one. A block with a NaN or an infinity has
+ * s = 255 (NaN), and every value of it is NaN.
+ *
+ * An operand of R rows and K columns, with Kp = FORGE_FP8_BLOCK_K(K):
+ *   codes  [Kp / 64, R, 64] bytes: entry (g, r) holds row r's columns 64 g .. 64 g + 63;
+ *   scales [Kp / 128, FORGE_FP8_BLOCK_ROWS(R)] bytes: the scale of row r's
+ *          columns 128 g .. 128 g + 127 is byte r / 128 * 128 + r % 32 * 4 +
+ *          r / 32 % 4 of entry g (four rows at a distance of 32 share a word).
+ * Columns K .. Kp - 1 hold zero codes; scales past row R - 1 are written as 0.
+ */
+#define FORGE_FP8_BLOCK_K(K) (((int64_t)(K) + 127) / 128 * 128)
+#define FORGE_FP8_BLOCK_ROWS(R) (((int64_t)(R) + 127) / 128 * 128)
+
+/* Largest padded contraction length; an operand has at most 2^22 rows and a
+ * product at most 2^40 elements (else FORGE_ERR_SHAPE). */
+#define FORGE_FP8_BLOCK_MAX_K 1073741824
+
+/*
+ * Quantises x [R, C] (x_dtype FORGE_F32 or FORGE_BF16) into fmt, into either or
+ * both of
+ *   row_codes, row_scales: the operand of R rows with K = C;
+ *   col_codes, col_scales: the operand of C rows with K = R (transposed).
+ * A pair is left out by two NULLs; one NULL of a pair, or both pairs left out, is
+ * FORGE_ERR_NULL. C % 8 == 0, any R. Both pairs read x once.
+ *   square == 0: a block is 128 values along the contraction;
+ *   square != 0: a block is 128 x 128 values of x, and a value is the same in
+ *     both operands, as a weight's should be in a layer's output and in its
+ *     input gradient.
+ */
+FORGE_API forge_status forge_quantize_fp8_block(const void* x, forge_dtype x_dtype, int64_t R, int64_t C,
+                                      forge_dtype fmt, int32_t square, void* row_codes,
+                                      void* row_scales, void* col_codes, void* col_scales,
+                                      void* stream);
+
+/*
+ * out [M, N] bf16 (rounded to nearest even) = A B^T for operands A of M rows
+ * in a_fmt and B of N rows in b_fmt, both of the padded length Kp (a multiple of
+ * 128, else FORGE_ERR_ALIGN). N % 8 == 0, any M. Kp == 0 writes zeros.
+ *   Weight gradient   g = dY^T X:  A = dY by columns, B = X by columns.
+ *   Input gradient    dX = dY W:   A = dY by rows,    B = W by columns.
+ *   Layer output      Y = X W^T:   A = X by rows,     B = W by rows.
+ * Accumulated in float32 by the fp8 matrix instruction, which truncates the
+ * products of each run of 8 consecutive columns toward zero to 2^-13 of the run's
+ * largest power of two (see forge_wgrad_fp8): at most 2^-10 of it in a run's
+ * sum, which is below half a bf16 step of that product, and so the result is bf16.
+ * tile: the ids of forge.h over [N, M], each of which gives the same bits; the
+ * default may also take other tiles and, for few rows, cut the contraction.
+ */
+FORGE_API forge_status forge_matmul_fp8_block(const void* a_codes, const void* a_scales, forge_dtype a_fmt,
+                                    const void* b_codes, const void* b_scales,
+                                    forge_dtype b_fmt, void* out, int64_t M, int64_t N,
+                                    int64_t Kp, forge_tile tile, void* stream);
 
 #ifdef __cplusplus
 }

@@ -133,3 +133,78 @@ def test_distill_reaches_the_device_check(lib):
     assert distill(lib, ib=4, ids=C + 4, loss=E + 4, w=D + 12, u=B + 4) == E_DEVICE
     assert distill(lib, ut=BF16, u=B + 2) == E_DEVICE
     assert distill(lib, scale=0.0, tau=1e-37) == distill(lib, scale=-3.0) == E_DEVICE
+
+
+# --------------------------------------------------------------------------
+# 8-bit operands with a scale for each block of 128
+# --------------------------------------------------------------------------
+def quantize(lib, x=A, xt=BF16, R=200, C=264, fmt=E4M3, square=0, rc=B, rs=C, cc=D, cs=E):
+    return lib.forge_quantize_fp8_block(x, xt, R, C, fmt, square, rc, rs, cc, cs, None)
+
+
+def matmul(lib, ac=A, as_=B, af=E4M3, bc=C, bs=D, bf=E4M3, out=E, M=100, N=64, Kp=256, tile=0):
+    return lib.forge_matmul_fp8_block(ac, as_, af, bc, bs, bf, out, M, N, Kp, tile, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(xt=2), E_DTYPE), (dict(fmt=0), E_DTYPE), (dict(fmt=1), E_DTYPE), (dict(fmt=4), E_DTYPE),
+    (dict(x=NULL), E_NULL), (dict(rc=NULL), E_NULL), (dict(rs=NULL), E_NULL), (dict(cc=NULL), E_NULL),
+    (dict(cs=NULL), E_NULL), (dict(rc=NULL, rs=NULL, cc=NULL, cs=NULL), E_NULL),
+    (dict(R=-1), E_SHAPE), (dict(C=-8), E_SHAPE), (dict(R=(1 << 22) + 1), E_SHAPE),
+    (dict(R=(1 << 30) + 1, rc=NULL, rs=NULL), E_SHAPE), (dict(C=(1 << 22) + 8, R=8), E_SHAPE),
+    (dict(C=260), E_ALIGN), (dict(x=A + 8), E_ALIGN), (dict(rc=B + 8), E_ALIGN),
+    (dict(rs=C + 4), E_ALIGN), (dict(cc=D + 1), E_ALIGN), (dict(cs=E + 8), E_ALIGN),
+    (dict(rc=A), E_ALIAS), (dict(cs=A + 200 * 264 * 2 - 16), E_ALIAS), (dict(cc=B), E_ALIAS),
+    (dict(rs=B + 200 * 384 - 16), E_ALIAS),                         # 264 columns are padded to 384
+    (dict(cs=C + 3 * 256 - 16), E_ALIAS),                           # scales of 200 rows to 256
+    (dict(R=0, x=NULL), OK), (dict(C=0, x=NULL), OK),
+])
+def test_quantize_fp8_block_rejects(lib, kw, status):
+    assert quantize(lib, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(af=0), E_DTYPE), (dict(bf=1), E_DTYPE), (dict(bf=-1), E_DTYPE),
+    *[({k: NULL}, E_NULL) for k in ("ac", "as_", "bc", "bs", "out")],
+    (dict(M=-1), E_SHAPE), (dict(N=-8), E_SHAPE), (dict(Kp=-128), E_SHAPE),
+    (dict(M=(1 << 22) + 1), E_SHAPE), (dict(N=(1 << 22) + 8), E_SHAPE),
+    (dict(Kp=(1 << 30) + 128), E_SHAPE), (dict(M=1 << 21, N=1 << 20), E_SHAPE),
+    (dict(N=60), E_ALIGN), (dict(Kp=200), E_ALIGN), (dict(Kp=64), E_ALIGN),
+    *[({k: p + 8}, E_ALIGN) for k, p in dict(ac=A, as_=B, bc=C, bs=D, out=E).items()],
+    (dict(out=A), E_ALIAS), (dict(out=A + 100 * 256 - 16), E_ALIAS), (dict(out=D), E_ALIAS),
+    (dict(out=B + 2 * 128 - 16), E_ALIAS), (dict(bs=E + 100 * 64 * 2 - 16), E_ALIAS),
+    (dict(tile=-1), E_TILE), (dict(tile=5), E_TILE),
+    (dict(M=0, ac=NULL, out=NULL), OK), (dict(N=0, bc=NULL, out=NULL), OK),
+])
+def test_matmul_fp8_block_rejects(lib, kw, status):
+    assert matmul(lib, **kw) == status
+
+
+def test_fp8_block_reaches_the_device_check(lib):
+    no_gpu()
+    assert quantize(lib) == quantize(lib, fmt=E5M2, square=1, xt=F32) == E_DEVICE
+    assert quantize(lib, rc=NULL, rs=NULL) == quantize(lib, cc=NULL, cs=NULL) == E_DEVICE
+    assert matmul(lib) == matmul(lib, af=E5M2, bf=E5M2, tile=4) == E_DEVICE
+    assert matmul(lib, Kp=0, ac=NULL, as_=NULL, bc=NULL, bs=NULL) == E_DEVICE
+    assert matmul(lib, bc=A, bs=B) == E_DEVICE                       # one operand twice
+
+
+def test_operand_handles():
+    import torch
+    import weight_gradient_gemm_amd as wg
+    cpu = wg.forge_fp8_block_empty(200, 300, device="cpu")
+    assert cpu.k == 384 and tuple(cpu.codes.shape) == (6, 200, 64) and tuple(cpu.scales.shape) == (3, 256)
+    assert cpu.ptrs == (cpu.codes.data_ptr(), cpu.scales.data_ptr()) and cpu._here()
+    pair = wg.ForgeFp8Block(torch.zeros(6, 200, 64, dtype=torch.uint8),
+                            torch.zeros(3, 256, dtype=torch.uint8), "e5m2")
+    assert (pair.rows, pair.k, pair.code) == (200, 384, E5M2) and pair._here()
+    pair.scales.data = pair.scales.clone()
+    assert not pair._here()
+    for codes, scales, err in (((6, 200, 32), (3, 256), ValueError), ((5, 200, 64), (2, 256), ValueError),
+                               ((6, 200, 64), (3, 200), ValueError)):
+        with pytest.raises(err):
+            wg.ForgeFp8Block(torch.zeros(codes, dtype=torch.uint8), torch.zeros(scales, dtype=torch.uint8))
+    with pytest.raises(TypeError):
+        wg.ForgeFp8Block(torch.zeros(2, 4, 64), torch.zeros(1, 128, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="on the GPU"):
+        _ops._fp8_operand(0, cpu, "A")

@@ -52,6 +52,9 @@ _SIGNATURES = {
     "forge_distill_workspace": (_i64, [_i64, _i64, _i64]),
     "forge_distill": (None, [_vp, _i32, _i64, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _i64, _i64,
                              _i64, _d, _d, _vp, _i64, _vp]),
+    "forge_quantize_fp8_block": (None, [_vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "forge_matmul_fp8_block": (None, [_vp, _vp, _i32, _vp, _vp, _i32, _vp, _i64, _i64, _i64, _i32,
+                                      _vp]),
 }
 
 _DONE = None
@@ -592,3 +595,136 @@ def forge_distill(logits, teacher, ids, loss, grad=None, *, vocab=None, weight=N
         uc, ip, id_bytes, _float_or_none(torch, cur, weight, rows, "weight"),
         _float_or_none(torch, cur, loss, rows, "loss"), gp, gc, T, V, K, temperature, scale,
         ws.data_ptr(), ws.numel(), st), "forge_distill")
+
+
+# --------------------------------------------------------------------------
+# 8-bit operands with a scale for each block of 128
+# --------------------------------------------------------------------------
+_FP8_FORMATS = _lib._FP8
+
+
+def _fp8_format(fmt):
+    try:
+        return _FP8_FORMATS[fmt]
+    except (KeyError, TypeError):
+        raise ValueError(f"fmt must be one of {sorted(_FP8_FORMATS)}, got {fmt!r}") from None
+
+
+class ForgeFp8Block:
+    """An 8-bit operand with a scale for each block of 128: ``rows`` rows, padded
+    contraction length ``k`` (a multiple of 128) and format ``fmt`` ("e4m3" or
+    "e5m2"); uint8 ``codes`` [k / 64, rows, 64] and ``scales`` [k / 128, rows padded
+    to a multiple of 128], laid out as forge_ops.h says. It keeps its tensors and
+    their memory alive; a call raises ValueError where they have moved
+    (``codes.data = ...``, a resized storage)."""
+
+    def __init__(self, codes, scales, fmt="e4m3"):
+        torch = _torch()
+        self.fmt, self.code = fmt, _fp8_format(fmt)
+        for t, name in ((codes, "codes"), (scales, "scales")):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
+                raise TypeError(f"{name} must be a torch.Tensor of uint8")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if codes.dim() != 3 or codes.shape[2] != 64 or codes.shape[0] % 2:
+            raise ValueError("codes must have shape (an even number of groups, rows, 64), "
+                             f"got {tuple(codes.shape)}")
+        groups, rows, _ = codes.shape
+        _shaped(scales, (groups // 2, (rows + 127) // 128 * 128), "scales")
+        if scales.device != codes.device:
+            raise ValueError(f"codes are on {codes.device}, scales on {scales.device}")
+        self.codes, self.scales = codes, scales
+        self.rows, self.k, self.device = rows, groups * 64, codes.get_device()
+        self.ptrs = (codes.data_ptr() or None, scales.data_ptr() or None)
+        self._storages = codes.untyped_storage(), scales.untyped_storage()
+
+    def _here(self):
+        """Whether codes and scales are where the addresses point."""
+        return (self.codes.data_ptr() or None, self.scales.data_ptr() or None) == self.ptrs
+
+
+class _Fp8BlockHeld(ForgeFp8Block):
+    """An operand whose codes and scales are one allocation; their tensors are made
+    when asked for."""
+
+    def __init__(self, rows, k, fmt, device):
+        torch = _torch()
+        self.fmt, self.code = fmt, _fp8_format(fmt)
+        self.rows, self.k = int(rows), (int(k) + 127) // 128 * 128
+        # Scales lie 16 bytes on at least: rows * k is a multiple of 128.
+        n = self.rows * self.k
+        self._hold = t = torch.empty(n + self.k // 128 * ((self.rows + 127) // 128 * 128),
+                                     dtype=torch.uint8, device="cuda" if device is None else device)
+        self._storage = t.untyped_storage()
+        self.device = t.get_device()
+        p = t.data_ptr()
+        self.ptrs = (p, p + n) if n else (None, None)
+
+    def _here(self):
+        return (self._hold.data_ptr() or None) == self.ptrs[0]
+
+    @property
+    def codes(self):
+        return self._hold[:self.rows * self.k].view(self.k // 64, self.rows, 64)
+
+    @property
+    def scales(self):
+        return self._hold[self.rows * self.k:].view(self.k // 128, (self.rows + 127) // 128 * 128)
+
+
+def forge_fp8_block_empty(rows, k, fmt="e4m3", device=None) -> ForgeFp8Block:
+    """An uninitialised operand of `rows` rows and contraction length k (padded to
+    the next multiple of 128), codes and scales in one allocation."""
+    return _Fp8BlockHeld(rows, k, fmt, device)
+
+
+def _fp8_operand(cur, op, name):
+    """An operand that is on device `cur` and has not moved."""
+    if not isinstance(op, ForgeFp8Block):
+        raise TypeError(f"{name} must be a ForgeFp8Block, got {type(op).__name__}")
+    if op.device != cur:
+        raise ValueError(f"{name} must be on the GPU and the current device, cuda:{cur}")
+    if not op._here():
+        raise ValueError(f"{name}'s codes or scales are not where they were when the operand was "
+                         "made (data replaced or storage resized): make the operand again")
+    return op
+
+
+def forge_quantize_fp8_block(x, *, rows=None, cols=None, square=False, stream=None) -> None:
+    """Quantises x [R, C] (float32 or bfloat16) into the operands ``rows`` (R rows,
+    blocks of 128 along a row) and / or ``cols`` (C rows, blocks along a column:
+    transposed), of one format. ``square``: blocks of 128 x 128, so that both hold the
+    same values, as a weight's operands should."""
+    torch, cur, st = _current(stream)
+    code = _real(torch, x, "x")
+    xp = _in(x, x.dtype, "x", cur)
+    R, C = _two(x, "x")
+    ptrs, fmt = [], None
+    for name, op, n, k in (("rows", rows, R, C), ("cols", cols, C, R)):
+        if op is None:
+            ptrs += (None, None)
+            continue
+        op = _fp8_operand(cur, op, name)
+        if op.rows != n or op.k != (k + 127) // 128 * 128:
+            raise ValueError(f"{name} is an operand of {op.rows} rows and padded length {op.k}, not "
+                             f"of {n} rows and length {k}")
+        if fmt not in (None, op.code):
+            raise ValueError(f"rows is in {rows.fmt}, cols in {cols.fmt}: one call has one format")
+        fmt = op.code
+        ptrs += op.ptrs
+    if ptrs != [None] * 4 or (rows is None and cols is None):    # else x is empty
+        _check(library().forge_quantize_fp8_block(xp, code, R, C, _lib.FORGE_FP8_E4M3 if fmt is None
+                                                  else fmt, 1 if square else 0, *ptrs, st),
+               "forge_quantize_fp8_block")
+
+
+def forge_matmul_fp8_block(A, B, out, *, tile=_lib.FORGE_TILE_DEFAULT, stream=None) -> None:
+    """out [M, N] (bfloat16) <- A B^T for operands A of M rows and B of N rows."""
+    torch, cur, st = _current(stream)
+    A, B = _fp8_operand(cur, A, "A"), _fp8_operand(cur, B, "B")
+    if A.k != B.k:
+        raise ValueError(f"A has padded length {A.k}, B has {B.k}")
+    op = _in(out, torch.bfloat16, "out", cur)
+    _shaped(out, (A.rows, B.rows), "out")
+    _check(library().forge_matmul_fp8_block(*A.ptrs, A.code, *B.ptrs, B.code, op, A.rows, B.rows, A.k,
+                                            tile, st), "forge_matmul_fp8_block")

@@ -1,0 +1,443 @@
+// 8-bit floating point operands with a power-of-two scale for each block of 128
+// for gfx950: quantisation along rows and columns, and the product of two
+// operands by v_mfma_scale_f32_32x32x64_f8f6f4, which takes the scales with the
+// codes (its blocks are of 32 values, so four of them have one byte).
+//
+// An operand of R rows and padded length Kp holds codes [Kp / 64][R][64], what one
+// stage of the product takes of neighbouring rows on end, and scales
+// [Kp / 128][R to a multiple of 128], in each 128 of which the four rows at a
+// distance of 32 share a word: a lane's rows of a wave's tile.
+#pragma once
+
+#include <type_traits>
+
+#include "mxfp4_kernels.hpp"
+
+namespace forge {
+
+// --------------------------------------------------------------------------
+// quantisation
+// --------------------------------------------------------------------------
+
+struct Fp8QuantArgs {
+  const void* x;
+  uint8_t *row_codes, *row_scales, *col_codes, *col_scales;
+  int64_t R, C;
+  int64_t row_pitch, col_pitch;      // bytes of a group of scales
+  uint32_t tiles_c;                  // tiles across
+  int32_t square;
+};
+
+constexpr int kFp8Tile = 128;        // rows and columns of a tile: a block each way
+constexpr int kFp8QuantThreads = 256;
+
+// The scale byte of a block from its largest magnitude's bits: the least
+// exponent that brings it to at most 1.75 * 2^REACH (448 or 57344), which is one
+// more where its fraction is beyond 1.75; 255 for a NaN or an infinity.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t fp8_scale_byte(uint32_t top) {
+  constexpr uint32_t reach = E5M2 ? 15 : 8;
+  const uint32_t e = (top + 0x1fffffu) >> 23;
+  return (top >> 23) == 255u ? 255u : e > reach ? e - reach : 0u;
+}
+
+// What values are multiplied by to be encoded: 2^(127 - s), a normal float32 for
+// every s of finite values. Products that are not exact lie below the least code.
+__device__ __forceinline__ float fp8_factor(uint32_t s) {
+  return s == 255u ? 0.0f : __builtin_bit_cast(float, (254u - s) << 23);
+}
+
+// Four values times their factors to four codes, rounded to nearest even.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t fp8_codes4(const float (&v)[4]) {
+  int r = 0;
+  if constexpr (E5M2) {
+    r = __builtin_amdgcn_cvt_pk_bf8_f32(v[0], v[1], r, false);
+    r = __builtin_amdgcn_cvt_pk_bf8_f32(v[2], v[3], r, true);
+  } else {
+    r = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], r, false);
+    r = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], r, true);
+  }
+  return uint32_t(r);
+}
+
+// Largest of v over the 16 lanes of a row of lanes, in each of them.
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+  auto step = [&](auto ctrl) {
+    const uint32_t o = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), decltype(ctrl)::value, 0xf, 0xf, true));
+    v = max(v, o);
+  };
+  step(std::integral_constant<int, 0xB1>{});     // lane ^ 1
+  step(std::integral_constant<int, 0x4E>{});     // lane ^ 2
+  step(std::integral_constant<int, 0x141>{});    // mirrored within 8
+  step(std::integral_constant<int, 0x140>{});    // mirrored within 16
+  return v;
+}
+
+// Byte of row r's scale among its 128.
+__device__ __forceinline__ int fp8_scale_place(int r) { return (r & 31) * 4 + (r >> 5); }
+
+// A tile of 128 x 128 values to a workgroup: thread (j, t) holds rows 8 t .. 8 t + 7
+// of columns 8 j .. 8 j + 7, so that eight codes on end of either operand are its
+// own. They pass through LDS on the way out, 64 bytes of a row (or column) in
+// each half of the tile, and leave as whole lines. Row q of a half is kept at
+// q ^ (q / 8 mod 4) and its 16-byte chunk c at c ^ (q / 32), which spreads one
+// write instruction's rows over all banks.
+template <bool BF16, bool E5M2, bool ROWS, bool COLS>
+__global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp8QuantArgs a) {
+  constexpr int NW = BF16 ? 4 : 8;               // words of 8 values
+  __shared__ __attribute__((aligned(16))) uint8_t out[(ROWS ? 16384 : 0) + (COLS ? 16384 : 0)];
+  __shared__ uint32_t col_top[4][kFp8Tile];
+  __shared__ uint32_t all_top[4];
+  uint8_t* const out_r = out;
+  uint8_t* const out_c = out + (ROWS ? 16384 : 0);
+  const int tid = threadIdx.x, j = tid & 15, t = tid >> 4, wave = tid >> 6;
+  const uint32_t tr = blockIdx.x / a.tiles_c, tc = blockIdx.x - tr * a.tiles_c;
+  const int64_t r0 = int64_t(tr) * kFp8Tile, c0 = int64_t(tc) * kFp8Tile;
+  float v[8][8];
+  uint32_t top[8] = {};                          // of columns
+  uint32_t row_top[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = r0 + 8 * t + i;
+    u32x4_t raw[NW / 4];
+#pragma unroll
+    for (int k = 0; k < NW / 4; ++k) raw[k] = u32x4_t{0u, 0u, 0u, 0u};
+    if (row < a.R && c0 + 8 * j < a.C) {
+      const char* p = static_cast<const char*>(a.x) + (row * a.C + c0 + 8 * j) * (BF16 ? 2 : 4);
+#pragma unroll
+      for (int k = 0; k < NW / 4; ++k)
+        raw[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p) + k);
+    }
+    row_top[i] = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t w = BF16 ? raw[0][k / 2] : raw[(k / 4) % (NW / 4)][k % 4];
+      const uint32_t bits = BF16 ? (k & 1 ? w & 0xffff0000u : w << 16) : w;
+      v[i][k] = __builtin_bit_cast(float, bits);
+      const uint32_t m = abs_bits(bits);
+      top[k] = max(top[k], m);
+      row_top[i] = max(row_top[i], m);
+    }
+  }
+  if (a.square) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, top[k]);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), d)));
+    if ((tid & 63) == 0) all_top[wave] = m;
+    __syncthreads();
+    m = max(max(all_top[0], all_top[1]), max(all_top[2], all_top[3]));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top[k] = row_top[k] = m;
+  } else {
+    if constexpr (ROWS)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) row_top[i] = row16_max(row_top[i]);
+    if constexpr (COLS) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        top[k] = max(top[k], uint32_t(__shfl_xor(int(top[k]), 16)));
+        top[k] = max(top[k], uint32_t(__shfl_xor(int(top[k]), 32)));
+      }
+      if ((tid & 63) < 16)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) col_top[wave][8 * j + k] = top[k];
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        top[k] = max(max(col_top[0][8 * j + k], col_top[1][8 * j + k]),
+                     max(col_top[2][8 * j + k], col_top[3][8 * j + k]));
+    }
+  }
+  auto place = [](int half, int q, int byte) {
+    return half * 8192 + (q ^ ((q >> 3) & 3)) * 64 + (byte ^ (((q >> 5) & 3) << 4));
+  };
+  if constexpr (ROWS) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 8 * t + i;
+      const uint32_t s = fp8_scale_byte<E5M2>(row_top[i]);
+      const float f = fp8_factor(s);
+      const float lo[4] = {v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f};
+      const float hi[4] = {v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f};
+      const uint32_t w0 = s == 255u ? 0u : fp8_codes4<E5M2>(lo), w1 = s == 255u ? 0u : fp8_codes4<E5M2>(hi);
+      *reinterpret_cast<u32x2_t*>(out_r + place(j >> 3, r, (j & 7) * 8)) = u32x2_t{w0, w1};
+      if (j == 0) a.row_scales[tc * a.row_pitch + r0 + fp8_scale_place(r)] = r0 + r < a.R ? uint8_t(s) : 0;
+    }
+  }
+  if constexpr (COLS) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = 8 * j + k;
+      const uint32_t s = fp8_scale_byte<E5M2>(top[k]);
+      const float f = fp8_factor(s);
+      const float lo[4] = {v[0][k] * f, v[1][k] * f, v[2][k] * f, v[3][k] * f};
+      const float hi[4] = {v[4][k] * f, v[5][k] * f, v[6][k] * f, v[7][k] * f};
+      const uint32_t w0 = s == 255u ? 0u : fp8_codes4<E5M2>(lo), w1 = s == 255u ? 0u : fp8_codes4<E5M2>(hi);
+      *reinterpret_cast<u32x2_t*>(out_c + place(t >> 3, c, (t & 7) * 8)) = u32x2_t{w0, w1};
+      if (t == 0) a.col_scales[tr * a.col_pitch + c0 + fp8_scale_place(c)] = c0 + c < a.C ? uint8_t(s) : 0;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = i * 256 + tid, half = n >> 9, q = (n >> 2) & 127, byte = (n & 3) * 16;
+    if constexpr (ROWS)
+      if (r0 + q < a.R)
+        *reinterpret_cast<u32x4_t*>(a.row_codes + ((int64_t(tc) * 2 + half) * a.R + r0 + q) * 64 + byte) =
+            *reinterpret_cast<const u32x4_t*>(out_r + place(half, q, byte));
+    if constexpr (COLS)
+      if (c0 + q < a.C)
+        *reinterpret_cast<u32x4_t*>(a.col_codes + ((int64_t(tr) * 2 + half) * a.C + c0 + q) * 64 + byte) =
+            *reinterpret_cast<const u32x4_t*>(out_c + place(half, q, byte));
+  }
+}
+
+// --------------------------------------------------------------------------
+// product
+// --------------------------------------------------------------------------
+//
+// acc[i, o] = sum_k I[i, k] O[o, k], in the weight gradient's terms (see
+// wgrad_kernels.hpp): I is B of the entry point, O is A.
+//
+// Stages of 64 columns (one MFMA k-step), rows of 64 bytes and then their scale
+// words, straight from memory into a ring of 4 LDS slots. 16-byte chunk c of row r is
+// kept at chunk c ^ (r / 4 mod 4), which puts 16 neighbouring rows' reads on
+// different banks. Per stage s: request stage s + 4 into the slot that the last
+// barrier freed, MFMAs on stage s, whose operands are in registers, while those of
+// stage s + 1 are read from its slot; then wait for these reads and for this
+// wave's loads of stage s + 2, and one barrier. Columns enter each element in
+// ascending steps of 64, whatever the tile.
+struct Fp8BlockArgs {
+  const uint8_t *i_scales, *o_scales;
+  int64_t kp;
+};
+
+// 16-bit elements of a slot: codes, and 256 bytes of scales of each side.
+template <class C>
+__host__ __device__ constexpr int fp8_block_slot() {
+  return C::STAGE + 256;
+}
+
+template <class C, int FI, int FO>
+__device__ __forceinline__ void fp8_block_tile(const WgradArgs& a, const Fp8BlockArgs& x, int tile_m,
+                                               int tile_n, const Slots& sl) {
+  constexpr int BM = C::BM, BN = C::BN, TM = C::TM, TN = C::TN;
+  constexpr int RB = 64;                                // bytes of a row in a stage
+  constexpr int QX = BM * RB / 1024, QY = BN * RB / 1024;
+  constexpr int NQW = (QX + QY) / C::WAVES;             // 1 KB loads per wave and stage
+  constexpr int NL = NQW + 1;                           // and 256 bytes of scales
+  constexpr int kScales = RB * (BM + BN);               // their place in a slot
+  static_assert((QX + QY) % C::WAVES == 0, "stage loads split evenly over the waves");
+  static_assert(RB * (BM + BN) <= C::STAGE * 2 && BM <= 256 && BN <= 256, "stage exceeds a slot");
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % C::WAVES_M, wn = wave / C::WAVES_M;
+  const int d_in = a.d_in, d_out = a.d_out;
+  const int i0 = tile_m * BM, o0 = tile_n * BN;
+  const int nk = int(x.kp / 64);
+
+  // Loads: instruction q covers 16 rows of I (q < QX) or O, 1 KB on end; lane t
+  // fills row t / 4, physical chunk t % 4. Rows past the edge repeat the last one
+  // (their products are not stored). A window reaches from the tile's first row
+  // to the operand's end, so that stages past the last read zeros; a stage is an
+  // offset to it, and it moves on every round of slots.
+  constexpr bool SIDES = QX == QY;                      // waves for each side, else each its share of both
+  constexpr int NF = SIDES ? 1 : 2, QXW = SIDES ? NQW : QX / C::WAVES;
+  static_assert(SIDES ? QX % NQW == 0 : QX % C::WAVES == 0 && QY % C::WAVES == 0, "whole loads");
+  const int left_i = d_in - i0, left_o = d_out > o0 ? d_out - o0 : 1;
+  const int row_o = d_out > o0 ? o0 : d_out - 1;        // a half tile may lie past the edge
+  struct Feed {
+    const uint8_t* p;
+    int64_t left, stage;                                // bytes to the end, and of a stage
+    __amdgpu_buffer_rsrc_t window;
+    __device__ __forceinline__ void open() {
+      window = window32(p, left < 0 ? 0u : uint32_t(left < 0x7fffffff ? left : 0x7fffffff));
+    }
+    __device__ __forceinline__ void advance(int stages) {
+      p += stage * stages;
+      left -= stage * stages;
+      open();
+    }
+  };
+  auto feed = [&](const void* base, int64_t stage, int64_t first, int stages) {
+    Feed f;
+    f.p = static_cast<const uint8_t*>(base) + first;
+    f.stage = stage;
+    f.left = stage * stages - first;
+    f.open();
+    return f;
+  };
+  auto code_feed = [&](bool o_side) {
+    return feed(o_side ? a.dY : a.X, int64_t(o_side ? d_out : d_in) * RB, int64_t(o_side ? row_o : i0) * RB, nk);
+  };
+  const bool scales_o = wave >= C::WAVES / 2;           // two waves load the same words
+  const int rows_s = scales_o ? d_out : d_in, first_s = (scales_o ? row_o : i0) & ~127;
+  Feed codes[NF], scales = feed(scales_o ? x.o_scales : x.i_scales, (rows_s + 127) & ~127, first_s, nk / 2);
+  codes[0] = code_feed(SIDES && wave >= C::WAVES / 2);
+  if constexpr (!SIDES) codes[1] = code_feed(true);
+  uint32_t voff[NQW];
+  auto load_of = [&](int i) { return i < QXW ? wave * QXW + i : QX + wave * (NQW - QXW) + i - QXW; };
+#pragma unroll
+  for (int i = 0; i < NQW; ++i) {
+    const int q = load_of(i);
+    const int row = (q < QX ? q : q - QX) * 16 + (lane >> 2);
+    voff[i] = uint32_t(min(row, (q < QX ? left_i : left_o) - 1) * RB + ((lane & 3) ^ ((lane >> 4) & 3)) * 16);
+  }
+  const uint32_t soff = uint32_t(lane * 4);
+  // Stage j of the round that the windows are at.
+  auto load_stage = [&](uint16_t* slot, int j) {
+    load4_to_lds(scales.window, slot + kScales / 2 + (scales_o ? 128 : 0), soff, int(scales.stage) * (j >> 1));
+#pragma unroll
+    for (int i = 0; i < NQW; ++i) {
+      const Feed& f = codes[i < QXW ? 0 : NF - 1];
+      load16_to_lds(f.window, slot + load_of(i) * 512, voff[i], int(f.stage) * j);
+    }
+  };
+  auto advance = [&]() {
+#pragma unroll
+    for (int k = 0; k < NF; ++k) codes[k].advance(4);
+    scales.advance(2);
+  };
+
+  // Operand addresses in a slot: lane l takes columns 32 (l / 32) .. + 31 of row
+  // l % 32 of a block, two chunks. Its scale is a byte of the word of row l % 32:
+  // block t of the wave's rows has byte t, counted from the wave's first row.
+  const int l32 = lane & 31, h = lane >> 5;
+  uint32_t fa[TM], fb[TN];
+  const uint32_t ch0 = uint32_t(((2 * h) ^ ((l32 >> 2) & 3)) * 16);
+#pragma unroll
+  for (int m = 0; m < TM; ++m) fa[m] = uint32_t((wm * C::WM + m * 32 + l32) * RB) + ch0;
+#pragma unroll
+  for (int n = 0; n < TN; ++n) fb[n] = uint32_t((BM + wn * C::WN + n * 32 + l32) * RB) + ch0;
+  const int ri = (i0 & 127) + wm * C::WM, ro = (row_o & 127) + wn * C::WN;
+  const uint32_t sa = uint32_t(kScales + (ri >> 7) * 128 + l32 * 4);
+  const uint32_t sb = uint32_t(kScales + 256 + (ro >> 7) * 128 + l32 * 4);
+  const int shift_i = ((ri >> 5) & 3) * 8, shift_o = ((ro >> 5) & 3) * 8;
+  i32x8_t frag[2][TM + TN];
+  uint32_t sc[2][2];
+  auto read_frags = [&](int f, const uint16_t* slot) {
+    const char* base = reinterpret_cast<const char*>(slot);
+    sc[f][0] = *reinterpret_cast<const uint32_t*>(base + sa);
+    sc[f][1] = *reinterpret_cast<const uint32_t*>(base + sb);
+    auto operand = [&](uint32_t at) {
+      const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(base + at);
+      const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(base + (at ^ 16u));
+      return i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    };
+#pragma unroll
+    for (int m = 0; m < TM; ++m) frag[f][m] = operand(fa[m]);
+#pragma unroll
+    for (int n = 0; n < TN; ++n) frag[f][TM + n] = operand(fb[n]);
+  };
+  f32x16_t acc[TM][TN];
+#pragma unroll
+  for (int m = 0; m < TM; ++m)
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.0f;
+  auto mfmas = [&](int f) {
+    uint32_t now[TM + TN];
+#pragma unroll
+    for (int m = 0; m < TM; ++m) now[m] = sc[f][0] >> (shift_i + 8 * m);
+#pragma unroll
+    for (int n = 0; n < TN; ++n) now[TM + n] = sc[f][1] >> (shift_o + 8 * n);
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+        acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(frag[f][m], frag[f][TM + n], acc[m][n],
+                                                                    FI, FO, 0, int(now[m]), 0, int(now[TM + n]));
+  };
+  constexpr int NREAD = 2 * (TM + TN) + 2, NM = TM * TN;
+  auto interleave = [&]() {
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                       // MFMA
+      if (i * 3 < NREAD) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);    // DS read
+      if (i < NL) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);           // VMEM read
+    }
+  };
+  constexpr int kWaitStage = waitcnt_imm(2 * NL, 0);
+#define FORGE_FP8_BARRIER(IMM)                \
+  do {                                        \
+    __builtin_amdgcn_sched_barrier(0);        \
+    __builtin_amdgcn_s_waitcnt(IMM);          \
+    asm volatile("" ::: "memory");            \
+    __builtin_amdgcn_s_barrier();             \
+    asm volatile("" ::: "memory");            \
+    __builtin_amdgcn_sched_barrier(0);        \
+  } while (0)
+  // Slot j of a round of four.
+  auto run_slot = [&](uint16_t* cur, const uint16_t* nxt, int j) {
+    if (j == 0) advance();
+    load_stage(cur, j);                          // stage s + 4
+    read_frags((j & 1) ^ 1, nxt);
+    mfmas(j & 1);
+    interleave();
+    FORGE_FP8_BARRIER(kWaitStage);
+  };
+  if (nk > 0) {
+    load_stage(sl.s0, 0);
+    load_stage(sl.s1, 1);
+    load_stage(sl.s2, 2);
+    load_stage(sl.s3, 3);
+    FORGE_FP8_BARRIER(waitcnt_imm(2 * NL, 15));  // stages 0 and 1
+    read_frags(0, sl.s0);
+    // Slot 0 is refilled in the first round's first stage: every wave has read it by then.
+    FORGE_FP8_BARRIER(waitcnt_imm(63, 0));
+    // Whole rounds of 4 slots: the accumulators keep their registers. Stages past
+    // the last add products of zero codes and zero scale bytes: exactly +0.
+    const int rounds = (nk + 3) / 4;
+    for (int r = 0; r < rounds; ++r) {
+      run_slot(sl.s0, sl.s1, 0);
+      run_slot(sl.s1, sl.s2, 1);
+      run_slot(sl.s2, sl.s3, 2);
+      run_slot(sl.s3, sl.s0, 3);
+    }
+  }
+#undef FORGE_FP8_BARRIER
+  uint16_t* ep = wave == 0 ? sl.s0 : wave == 1 ? sl.s1 : wave == 2 ? sl.s2 : sl.s3;
+  epilogue<C, EPI_GRAD | EPI_BF16_OUT>(a, acc, a.W, a.S1, a.S2, i0, o0, wm, wn, lane,
+                                       reinterpret_cast<float*>(ep));
+}
+
+template <class C, int FI, int FO>
+__global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(C::OCC, C::OCC)))
+void fp8_block_kernel(WgradArgs a, Fp8BlockArgs x) {
+  FORGE_DECLARE_SLOTS(fp8_block_slot<C>());
+  int e, tm, tn;
+  map_tile(blockIdx.x, a.num_tiles, a.tiles_m, a.tiles_n, a.group_m, e, tm, tn);
+  fp8_block_tile<C, FI, FO>(a, x, tm, tn, ring);
+}
+
+// The persistent schedule of the bf16 kernel.
+template <class CF, class CH, int FI, int FO>
+__global__ __launch_bounds__(CF::THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void fp8_block_persistent_kernel(WgradArgs a, Fp8BlockArgs x) {
+  static_assert(CF::THREADS == CH::THREADS && CF::BM == CH::BM && CF::BN == 2 * CH::BN,
+                "half tiles must split the full tile's columns");
+  FORGE_DECLARE_SLOTS(fp8_block_slot<CF>());
+  const int b = blockIdx.x, xcd = b & 7, j = b >> 3, nw = gridDim.x >> 3;
+  const int per = a.num_tiles >> 3, rem = a.num_tiles & 7;
+  const int start = xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per;
+  const int R = per + (xcd < rem ? 1 : 0);
+  const int phase = schedule_phase(xcd, R, nw);
+  for (int k = 0;; ++k) {
+    int tile, half;
+    if (!schedule_item(k, j, nw, R, phase, tile, half)) break;
+    int tm, tn;
+    grouped_walk(start + tile, a.tiles_m, a.tiles_n, a.group_m, tm, tn);
+    if (half < 0)
+      fp8_block_tile<CF, FI, FO>(a, x, tm, tn, ring);
+    else
+      fp8_block_tile<CH, FI, FO>(a, x, tm, 2 * tn + half, ring);
+    __syncthreads();
+  }
+}
+
+}  // namespace forge

@@ -456,4 +456,75 @@ forge_status validate_distill(const void* logits, forge_dtype z_dtype, int64_t l
   return FORGE_OK;
 }
 
+// --------------------------------------------------------------------------
+// 8-bit operands with a scale for each block of 128
+// --------------------------------------------------------------------------
+namespace {
+
+bool fp8_format(forge_dtype t) { return t == FORGE_FP8_E4M3 || t == FORGE_FP8_E5M2; }
+Span fp8_codes_span(const void* p, int64_t R, int64_t Kp) { return Span{p, uint64_t(R) * uint64_t(Kp)}; }
+Span fp8_scales_span(const void* p, int64_t R, int64_t Kp) {
+  return Span{p, uint64_t(Kp / 128) * uint64_t(FORGE_FP8_BLOCK_ROWS(R))};
+}
+
+}  // namespace
+
+forge_status validate_quantize_fp8_block(const void* x, forge_dtype x_dtype, int64_t R, int64_t C,
+                                         forge_dtype fmt, const void* row_codes,
+                                         const void* row_scales, const void* col_codes,
+                                         const void* col_scales) {
+  const int xb = dtype_bytes(x_dtype);
+  if (xb == 0 || !fp8_format(fmt)) return FORGE_ERR_DTYPE;
+  if (!row_codes != !row_scales || !col_codes != !col_scales || (!row_codes && !col_codes))
+    return FORGE_ERR_NULL;
+  if (R > 0 && C > 0 && !x) return FORGE_ERR_NULL;
+  if (R < 0 || C < 0 || R > kMaxTokens || C > kMaxTokens) return FORGE_ERR_SHAPE;
+  if ((row_codes && R > kMaxDim) || (col_codes && C > kMaxDim)) return FORGE_ERR_SHAPE;
+  if (R == 0 || C == 0) return FORGE_OK;
+  if (C % 8 != 0 || !aligned16(x)) return FORGE_ERR_ALIGN;
+  Span spans[5] = {};
+  int n = 0;
+  if (row_codes) {
+    if (!aligned16(row_codes) || !aligned16(row_scales)) return FORGE_ERR_ALIGN;
+    spans[n++] = fp8_codes_span(row_codes, R, FORGE_FP8_BLOCK_K(C));
+    spans[n++] = fp8_scales_span(row_scales, R, FORGE_FP8_BLOCK_K(C));
+  }
+  if (col_codes) {
+    if (!aligned16(col_codes) || !aligned16(col_scales)) return FORGE_ERR_ALIGN;
+    spans[n++] = fp8_codes_span(col_codes, C, FORGE_FP8_BLOCK_K(R));
+    spans[n++] = fp8_scales_span(col_scales, C, FORGE_FP8_BLOCK_K(R));
+  }
+  const int written = n;
+  spans[n++] = Span{x, uint64_t(R) * uint64_t(C) * uint64_t(xb)};
+  return any_overlap(spans, written, n) ? FORGE_ERR_ALIAS : FORGE_OK;
+}
+
+forge_status validate_matmul_fp8_block(const void* a_codes, const void* a_scales, forge_dtype a_fmt,
+                                       const void* b_codes, const void* b_scales, forge_dtype b_fmt,
+                                       const void* out, int64_t M, int64_t N, int64_t Kp,
+                                       forge_tile tile) {
+  if (!fp8_format(a_fmt) || !fp8_format(b_fmt)) return FORGE_ERR_DTYPE;
+  if (M < 0 || N < 0 || Kp < 0) return FORGE_ERR_SHAPE;
+  const bool work = M > 0 && N > 0;
+  const void* const in[4] = {a_codes, a_scales, b_codes, b_scales};
+  if (work) {
+    if (!out) return FORGE_ERR_NULL;
+    for (const void* p : in)
+      if (Kp > 0 && !p) return FORGE_ERR_NULL;
+  }
+  if (M > kMaxDim || N > kMaxDim || Kp > FORGE_FP8_BLOCK_MAX_K || M * N > kMaxElems)
+    return FORGE_ERR_SHAPE;
+  if (work) {
+    if (N % 8 != 0 || Kp % 128 != 0 || !aligned16(out)) return FORGE_ERR_ALIGN;
+    if (Kp > 0)
+      for (const void* p : in)
+        if (!aligned16(p)) return FORGE_ERR_ALIGN;
+    const Span spans[5] = {{out, uint64_t(M) * uint64_t(N) * 2u}, fp8_codes_span(a_codes, M, Kp),
+                           fp8_scales_span(a_scales, M, Kp), fp8_codes_span(b_codes, N, Kp),
+                           fp8_scales_span(b_scales, N, Kp)};
+    if (any_overlap(spans, 1, 5)) return FORGE_ERR_ALIAS;
+  }
+  return check_tile(tile);
+}
+
 }  // namespace forge

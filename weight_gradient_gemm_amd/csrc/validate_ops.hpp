@@ -89,4 +89,13 @@ forge_status validate_distill(const void* logits, forge_dtype z_dtype, int64_t l
                               int64_t K, double temperature, double scale, const void* workspace,
                               int64_t workspace_bytes);
 
+forge_status validate_quantize_fp8_block(const void* x, forge_dtype x_dtype, int64_t R, int64_t C,
+                                         forge_dtype fmt, const void* row_codes,
+                                         const void* row_scales, const void* col_codes,
+                                         const void* col_scales);
+forge_status validate_matmul_fp8_block(const void* a_codes, const void* a_scales, forge_dtype a_fmt,
+                                       const void* b_codes, const void* b_scales, forge_dtype b_fmt,
+                                       const void* out, int64_t M, int64_t N, int64_t Kp,
+                                       forge_tile tile);
+
 }  // namespace forge
