@@ -20,6 +20,8 @@
 
 namespace forge {
 
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
 constexpr int kDistillThreads = 256;
 constexpr int kDistillMaxK = 1024;
 
@@ -233,6 +235,271 @@ __global__ __launch_bounds__(kDistillThreads) void distill_gradient_kernel(Disti
         static_cast<__bf16*>(a.grad)[row * a.ld + id] = __bf16(g[0]);
       else
         static_cast<float*>(a.grad)[row * a.ld + id] = g[0];
+    }
+  }
+}
+
+
+// --------------------------------------------------------------------------
+// rows in registers
+// --------------------------------------------------------------------------
+
+// A vector of 16 bytes of a row and its elements.
+template <bool ZB>
+constexpr int kVec = ZB ? 8 : 4;
+template <bool ZB>
+__device__ __forceinline__ void unpack(const u32x4_t& r, float (&v)[kVec<ZB>]) {
+#pragma unroll
+  for (int k = 0; k < kVec<ZB>; ++k)
+    v[k] = __builtin_bit_cast(float, ZB ? (k & 1 ? r[k / 2] & 0xffff0000u : r[k / 2] << 16) : r[k]);
+}
+
+// The compiler may not keep what it made of r before.
+__device__ __forceinline__ void forget(u32x4_t& r) { asm volatile("" : "+v"(r)); }
+
+template <bool ZB, bool GB, bool GRAD, int THREADS, int NV>
+__global__ __launch_bounds__(THREADS) void distill_rows_kernel(DistillArgs a) {
+  constexpr int E = kVec<ZB>, W = THREADS / 64, EPT = (kDistillMaxK + THREADS - 1) / THREADS;
+  constexpr int kBlock = THREADS * E;                  // columns of one load instruction of all waves
+  constexpr int ZS = ZB ? 2 : 4, GS = GB ? 2 : 4;
+  constexpr uint32_t kLow = ZB ? 0xff80ff80u : 0xff800000u;    // -infinity
+  __shared__ __attribute__((aligned(16))) Entries entry;
+  __shared__ float part[6][W];
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const uint32_t vz = uint32_t(tid * E * ZS), vg = uint32_t(tid * E * GS);
+  u32x4_t raw[NV];
+  int id[EPT];
+  float u[EPT], zt[EPT];
+
+  // A row that is not looked at has an empty window: its loads cost no memory access.
+  auto row_window = [&](int64_t row, bool wanted) {
+    return window(static_cast<const char*>(a.z) + (wanted ? row * a.ld * ZS : 0),
+                  wanted ? int64_t(a.V + 7) / 8 * 8 * ZS : 0);
+  };
+  // Block i of a row: zeros past its end.
+  auto load = [&](__amdgpu_buffer_rsrc_t r, int i) {
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, int(vz), i * kBlock * ZS, kStatePolicy));
+  };
+  // Blocks before `full` are whole, block `full` has `rest` columns or none.
+  const int full = a.V / kBlock, rest = a.V - full * kBlock, blocks = full + (rest > 0);
+  // Its elements past V as -infinity.
+  auto cut = [&](u32x4_t& r) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (ZB) {
+        const bool lo = tid * E + 2 * k >= rest, hi = tid * E + 2 * k + 1 >= rest;
+        r[k] = lo ? kLow : hi ? (r[k] & 0xffffu) | (kLow & 0xffff0000u) : r[k];
+      } else {
+        r[k] = tid * E + k >= rest ? kLow : r[k];
+      }
+    }
+  };
+  auto load_entries_of = [&](int64_t row, int (&id)[EPT], float (&u)[EPT], float (&zt)[EPT]) {
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      const int j = e * THREADS + tid;
+      id[e] = -1;
+      u[e] = zt[e] = 0.0f;
+      if (j < a.K) {
+        const int64_t n = entry_id(a, row * a.K + j);
+        if (n >= 0 && n < a.V) {
+          u[e] = entry_logit(a, row * a.K + j);
+          zt[e] = student_logit<ZB>(a, row * a.ld + n);
+          if (u[e] != -INFINITY) id[e] = int(n);
+        }
+      }
+    }
+  };
+  auto combine = [&](const float* p, auto op) {
+    float v = p[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v = op(v, p[w]);
+    return v;
+  };
+  auto add = [](float x, float y) { return x + y; };
+  auto larger = [](float x, float y) { return fmaxf(x, y); };
+
+  const int64_t step = gridDim.x;
+  int64_t row = blockIdx.x;
+  float w = row >= a.T ? 0.0f : a.weight ? a.weight[row] : 1.0f;
+  {
+    const __amdgpu_buffer_rsrc_t r = row_window(row, w != 0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) raw[i] = load(r, i);
+    if (w != 0.0f) load_entries_of(row, id, u, zt);
+  }
+  for (; row < a.T; row += step) {
+    const int64_t next = row + step;
+    const float wn = next >= a.T ? 0.0f : a.weight ? a.weight[next] : 1.0f;
+    const bool ahead = wn != 0.0f;                     // the next row is loaded meanwhile
+    const __amdgpu_buffer_rsrc_t here = row_window(row, w != 0.0f), there = row_window(next, ahead);
+    // Block i of a row that is longer than what is held.
+    auto streamed = [&](int i) {
+      u32x4_t r = load(here, i);
+      if (i == full) cut(r);
+      return r;
+    };
+    float m = -INFINITY, top = -INFINITY;
+    bool some = false;
+    auto most = [&](const u32x4_t& r) {
+      float v[E];
+      unpack<ZB>(r, v);
+#pragma unroll
+      for (int k = 0; k < E; ++k) m = fmaxf(m, v[k]);
+    };
+    int shown = w != 0.0f ? blocks : 0;                // blocks of the row that count
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (i == full) cut(raw[i]);
+      if (i < shown) most(raw[i]);
+      forget(raw[i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    for (int i = NV; i < shown; ++i) most(streamed(i));
+    if (w != 0.0f)
+#pragma unroll
+      for (int e = 0; e < EPT; ++e)
+        if (id[e] >= 0) {
+          top = fmaxf(top, u[e]);
+          some = true;
+        }
+    m = wave_max(m);
+    top = wave_max(top);
+    const bool any = __ballot(some) != 0;
+    if ((tid & 63) == 0) {
+      part[0][wave] = m;
+      part[1][wave] = top;
+      part[2][wave] = any ? 1.0f : 0.0f;
+    }
+    __syncthreads();
+    m = finite_max(combine(part[0], larger));
+    top = finite_max(combine(part[1], larger));
+    const bool live = combine(part[2], larger) != 0.0f;
+    shown = live ? blocks : 0;
+
+    float s = 0.0f, total = 0.0f;
+    auto sum = [&](const u32x4_t& r) {
+      float v[E];
+      unpack<ZB>(r, v);
+#pragma unroll
+      for (int k = 0; k < E; ++k) s += exp2_fast((v[k] - m) * a.c);
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (i < shown) sum(raw[i]);
+      forget(raw[i]);
+      if (!GRAD) raw[i] = load(there, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    for (int i = NV; i < shown; ++i) sum(streamed(i));
+    if (live)
+#pragma unroll
+      for (int e = 0; e < EPT; ++e) {
+        const int j = e * THREADS + tid;
+        const float q = id[e] >= 0 ? exp2_fast((u[e] - top) * a.c) : 0.0f;
+        total += q;
+        if (GRAD && j < (a.K + 3 & ~3)) {              // up to a multiple of 4
+          entry.id[j] = id[e];
+          entry.q[j] = q;
+        }
+      }
+    s = wave_sum(s);
+    total = wave_sum(total);
+    if ((tid & 63) == 0) {
+      part[3][wave] = s;
+      part[4][wave] = total;
+    }
+    __syncthreads();
+    s = combine(part[3], add);
+    total = combine(part[4], add);
+    if (live) {
+      float l = 0.0f;
+#pragma unroll
+      for (int e = 0; e < EPT; ++e)
+        if (id[e] >= 0) {
+          const float du = u[e] - top, q = exp2_fast(du * a.c) / total;
+          if (q != 0.0f) l += q * (du * a.inv_tau - (zt[e] - m) * a.inv_tau);
+        }
+      l = wave_sum(l);
+      if ((tid & 63) == 0) part[5][wave] = l;
+    }
+    int nid[EPT];
+    float nu[EPT], nz[EPT];
+    if (ahead) load_entries_of(next, nid, nu, nz);
+    if constexpr (GRAD) {
+      const float coef = a.grad_scale * w, inv = 1.0f / s;
+      const __amdgpu_buffer_rsrc_t out =
+          window(static_cast<char*>(a.grad) + row * a.ld * GS, a.ld * GS);
+      auto emit = [&](const u32x4_t& r, int i) {
+        float v[E] = {};
+        if (i < shown) {
+          unpack<ZB>(r, v);
+#pragma unroll
+          for (int k = 0; k < E; ++k) v[k] = coef * (exp2_fast((v[k] - m) * a.c) * inv);
+          if (i == full)                               // zeros past V, whatever the sums are
+#pragma unroll
+            for (int k = 0; k < E; ++k) v[k] = tid * E + k >= rest ? 0.0f : v[k];
+        }
+        const int at = i * kBlock * GS;
+#pragma unroll
+        for (int k = 0; k < E; k += 4) {
+          const f32x4_t g = {v[k], v[k + 1], v[k + 2], v[k + 3]};
+          if constexpr (GB && E == 8) {
+            if (k == 0) {
+              const u32x2_t lo = pack_bf16x4(g), hi = pack_bf16x4(f32x4_t{v[4], v[5], v[6], v[7]});
+              __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, out, int(vg), at, kStatePolicy);
+            }
+          } else {
+            store4<GS>(out, vg + k * GS, at, g);
+          }
+        }
+      };
+      const int out_blocks = int((a.ld + kBlock - 1) / kBlock);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (i < out_blocks) emit(raw[i], i);
+        raw[i] = load(there, i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      for (int i = NV; i < out_blocks; ++i) emit(streamed(i), i);
+    }
+    __syncthreads();
+    if (tid == 0)
+      a.loss[row] = live ? a.loss_scale * w * (combine(part[5], add) + (logf(s) - logf(total))) : 0.0f;
+    if constexpr (GRAD) {
+      // The teacher's columns: the first entry of an id writes it.
+      if (live)
+#pragma unroll
+        for (int e = 0; e < EPT; ++e)
+          if (id[e] >= 0) {
+            const int j = e * THREADS + tid;
+            float q = 0.0f;
+            bool again = false;
+            for (int k = 0; k < a.K; k += 4) {
+              const i32x4_t ids = *reinterpret_cast<const i32x4_t*>(&entry.id[k]);
+              const f32x4_t qs = *reinterpret_cast<const f32x4_t*>(&entry.q[k]);
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+                if (ids[n] == id[e]) {
+                  again = again || k + n < j;
+                  q += qs[n];
+                }
+            }
+            if (!again) {
+              const float g = a.grad_scale * w * (exp2_fast((zt[e] - m) * a.c) / s - q / total);
+              if constexpr (GB)
+                static_cast<__bf16*>(a.grad)[row * a.ld + id[e]] = __bf16(g);
+              else
+                static_cast<float*>(a.grad)[row * a.ld + id[e]] = g;
+            }
+          }
+    }
+    w = wn;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      id[e] = nid[e];
+      u[e] = nu[e];
+      zt[e] = nz[e];
     }
   }
 }

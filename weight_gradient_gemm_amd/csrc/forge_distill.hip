@@ -16,8 +16,26 @@ static_assert(kDistillMaxK == FORGE_DISTILL_MAX_K && kDistillChunk == 32 * kDist
 constexpr int64_t kMaxGrid = int64_t(1) << 20;
 dim3 grid_for(int64_t items) { return dim3(uint32_t(std::min(items, kMaxGrid))); }
 
+template <bool ZB, bool GB, bool GRAD, int THREADS, int NV>
+forge_status launch_rows_t(const DistillArgs& a, int per_cu, hipStream_t s) {
+  const int64_t grid = int64_t(std::max(16, persistent_grid())) * per_cu;
+  hipLaunchKernelGGL((distill_rows_kernel<ZB, GB, GRAD, THREADS, NV>), dim3(uint32_t(std::min(grid, a.T))),
+                     dim3(THREADS), 0, s, a);
+  return launch_status();
+}
+
+template <bool ZB, bool GB, bool GRAD>
+forge_status launch_rows(const DistillArgs& a, hipStream_t s) {
+  constexpr int E = kVec<ZB>;
+  if (a.V <= 256 * 4 * E) return launch_rows_t<ZB, GB, GRAD, 256, 4>(a, 8, s);
+  if (a.V <= 256 * 16 * E) return launch_rows_t<ZB, GB, GRAD, 256, 16>(a, 4, s);
+  if (a.V <= 512 * 16 * E) return launch_rows_t<ZB, GB, GRAD, 512, 16>(a, 2, s);
+  return launch_rows_t<ZB, GB, GRAD, 1024, 16>(a, 1, s);
+}
+
 template <bool ZB, bool GB>
 forge_status launch(DistillArgs a, hipStream_t s) {
+  if (a.T >= 256) return a.grad ? launch_rows<ZB, GB, true>(a, s) : launch_rows<ZB, false, false>(a, s);
   a.items = a.T * a.chunks;
   if (a.items > 0 && a.K > 0) {
     hipLaunchKernelGGL((distill_stats_kernel<ZB>), grid_for(a.items), dim3(kDistillThreads), 0, s, a);
