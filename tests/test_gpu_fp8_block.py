@@ -350,6 +350,30 @@ def test_matmul_of_an_operand_beyond_31_bits(env, M):
         check_product(torch, out[:, r:r + part.rows], A, part)
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 100008, 25600), (40, 131072, 18432), (20, 16, 1 << 20)])
+def test_matmul_of_few_rows_and_a_long_operand(env, M, N, K):
+    # Groups of more than 2^31 bytes of codes apart, and a contraction of 8192 groups.
+    torch, wg = env
+    g = torch.Generator(device="cuda").manual_seed(4)
+    A, B = random_operand(torch, wg, g, M, K), random_operand(torch, wg, g, N, K)
+    out, ok = into(torch, M, N)
+    wg.forge_matmul_fp8_block(A, B, out)
+    assert ok()
+    for r in {0, (N // 2) // 128 * 128, (N - 8) // 128 * 128}:
+        part = some_rows(wg, B, r, min(16, N - r))
+        check_product(torch, out[:, r:r + part.rows], A, part)
+
+
+@pytest.mark.parametrize("M", list(range(1, 66, 3)) + [16, 32, 48, 64])
+def test_matmul_of_every_few_rows(env, M):
+    torch, wg = env
+    A, B = operands(torch, wg, M, 264, 900, M, "e5m2")
+    out, ok = into(torch, M, 264)
+    wg.forge_matmul_fp8_block(A, B, out)
+    check_product(torch, out, A, B)
+    assert ok()
+
+
 @pytest.mark.parametrize("M,N", [(4400, 4400), (4096, 4360), (2560, 8200)])
 def test_many_tiles_through_the_persistent_schedule(env, M, N):
     torch, wg = env

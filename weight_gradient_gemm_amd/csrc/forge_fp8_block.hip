@@ -12,13 +12,14 @@ namespace forge {
 namespace {
 
 // Tiles of the library's own choice, beside the public ids.
-enum : forge_tile { FP8_TILE_128x64 = FORGE_TILE_COUNT, FP8_TILE_64x64 };
+enum : forge_tile { FP8_TILE_128x64 = FORGE_TILE_COUNT, FP8_TILE_64x64, FP8_TILE_ROWS };
 
 using Fp8128x64 = SmallTileCfg<128, 64, 2, 2, 2, 1>;
 using Fp864x64 = SmallTileCfg<64, 64, 2, 2, 4, 1>;
 
 // The library's choice of tile: the largest that gives every compute unit some.
 forge_tile choose_tile(int64_t N, int64_t M) {
+  if (M <= 64 && N <= 131072) return FP8_TILE_ROWS;
   const int64_t tiles = count_tiles(N, M, TileShape{256, 256});
   if (persistent_grid() > 0 && tiles >= persistent_grid()) return FORGE_TILE_PERSISTENT;
   if (count_tiles(N, M, TileShape{256, 128}) >= 256) return FORGE_TILE_256x128;
@@ -34,9 +35,23 @@ forge_status launch_tile(WgradArgs a, const Fp8BlockArgs& x, hipStream_t s) {
   return launch_status();
 }
 
+template <int MB, int W, int U, int FI, int FO>
+forge_status launch_rows_t(const WgradArgs& a, const Fp8BlockArgs& x, hipStream_t s) {
+  hipLaunchKernelGGL((fp8_block_rows_kernel<MB, W, U, FI, FO>), dim3((a.d_in + 15) / 16), dim3(64 * W), 0, s, a, x);
+  return launch_status();
+}
+
+template <int FI, int FO>
+forge_status launch_rows(const WgradArgs& a, const Fp8BlockArgs& x, hipStream_t s) {
+  if (a.d_out <= 16) return launch_rows_t<1, 16, 4, FI, FO>(a, x, s);
+  if (a.d_out <= 32) return launch_rows_t<2, 16, 2, FI, FO>(a, x, s);
+  return launch_rows_t<4, 8, 2, FI, FO>(a, x, s);
+}
+
 template <int FI, int FO>
 forge_status launch_product(WgradArgs a, const Fp8BlockArgs& x, forge_tile tile, hipStream_t s) {
   switch (tile) {
+    case FP8_TILE_ROWS: return launch_rows<FI, FO>(a, x, s);
     case FP8_TILE_64x64: return launch_tile<Fp864x64, FI, FO>(a, x, s);
     case FP8_TILE_128x64: return launch_tile<Fp8128x64, FI, FO>(a, x, s);
     case FORGE_TILE_128x128: return launch_tile<Cfg128x128, FI, FO>(a, x, s);

@@ -440,4 +440,87 @@ void fp8_block_persistent_kernel(WgradArgs a, Fp8BlockArgs x) {
   }
 }
 
+// --------------------------------------------------------------------------
+// product of few rows
+// --------------------------------------------------------------------------
+//
+// Up to 16 MB rows of O (A of the entry point): 16 rows of I to a workgroup, whose W
+// waves cut the contraction by its groups of 128 columns, one MFMA of 16 x 16 x 128
+// for each 16 rows of O, and join their sums through LDS in the order of the
+// waves. Bound by the bytes of I, which go straight into registers, U groups at a
+// time: a lane holds 16 bytes of either half of a group, so that each load is
+// 1 KB on end (a run of 8 columns stays one, and the order of runs does not
+// matter to a sum that is joined in any case). Groups past the end read zeros.
+template <int MB, int W, int U, int FI, int FO>
+__global__ __launch_bounds__(64 * W) void fp8_block_rows_kernel(WgradArgs a, Fp8BlockArgs x) {
+  __shared__ float join[W][MB * 4][64];
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int N = a.d_in, M = a.d_out, n0 = blockIdx.x * 16;
+  const int64_t groups = x.kp / 128, pitch_i = (N + 127) & ~127, pitch_o = (M + 127) & ~127;
+  const int ni = min(n0 + r16, N - 1);
+  const uint32_t vi = uint32_t((ni - n0) * 64 + q * 16), si = uint32_t((ni & ~127) + fp8_scale_place(ni & 127));
+  uint32_t vo[MB], so[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    const int m = min(16 * b + r16, M - 1);              // M <= 16 MB <= 128
+    vo[b] = uint32_t(m * 64 + q * 16);
+    so[b] = uint32_t(fp8_scale_place(m));
+  }
+  f32x4_t acc[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) acc[b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const uint8_t* const ic = reinterpret_cast<const uint8_t*>(a.X);
+  const uint8_t* const oc = reinterpret_cast<const uint8_t*>(a.dY);
+  for (int64_t g = wave; g < groups; g += U * W) {
+    const int64_t left = groups - g;
+    const __amdgpu_buffer_rsrc_t wi = window(ic + (2 * g * N + n0) * 64, 2 * left * N * 64 - int64_t(n0) * 64);
+    const __amdgpu_buffer_rsrc_t wo = window(oc + 2 * g * M * 64, 2 * left * M * 64);
+    const __amdgpu_buffer_rsrc_t wsi = window(x.i_scales + g * pitch_i, left * pitch_i);
+    const __amdgpu_buffer_rsrc_t wso = window(x.o_scales + g * pitch_o, left * pitch_o);
+    u32x4_t fi[U][2], fo[U][MB][2];
+    uint32_t ci[U], co[U][MB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        fi[u][h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wi, int(vi), (2 * u * W + h) * N * 64, 0));
+      ci[u] = __builtin_amdgcn_raw_buffer_load_b8(wsi, int(si), u * W * int(pitch_i), 0);
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          fo[u][b][h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wo, int(vo[b]), (2 * u * W + h) * M * 64, 0));
+        co[u][b] = __builtin_amdgcn_raw_buffer_load_b8(wso, int(so[b]), u * W * int(pitch_o), 0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);                   // all loads in flight
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      auto wide = [](const u32x4_t (&v)[2]) {
+        return i32x8_t{int(v[0][0]), int(v[0][1]), int(v[0][2]), int(v[0][3]),
+                       int(v[1][0]), int(v[1][1]), int(v[1][2]), int(v[1][3])};
+      };
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+        acc[b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(fo[u][b]), wide(fi[u]), acc[b], FO, FI,
+                                                                  0, int(co[u][b]), 0, int(ci[u]));
+    }
+  }
+  // Lane (q, r16) holds rows 4 q .. 4 q + 3 of O and row r16 of I.
+#pragma unroll
+  for (int b = 0; b < MB; ++b)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) join[wave][b * 4 + k][lane] = acc[b][k];
+  __syncthreads();
+  __bf16* const out = reinterpret_cast<__bf16*>(a.W);
+  for (int e = threadIdx.x; e < MB * 256; e += 64 * W) {
+    float s = join[0][e >> 6][e & 63];
+#pragma unroll
+    for (int w = 1; w < W; ++w) s += join[w][e >> 6][e & 63];
+    const int m = (e >> 8) * 16 + ((e & 63) >> 4) * 4 + ((e >> 6) & 3), n = n0 + (e & 15);
+    if (m < M && n < N) out[int64_t(m) * N + n] = __bf16(s);
+  }
+}
+
 }  // namespace forge
