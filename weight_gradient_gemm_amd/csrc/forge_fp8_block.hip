@@ -14,18 +14,69 @@ namespace {
 // Tiles of the library's own choice, beside the public ids.
 enum : forge_tile { FP8_TILE_128x64 = FORGE_TILE_COUNT, FP8_TILE_64x64, FP8_TILE_ROWS };
 
-using Fp8128x64 = SmallTileCfg<128, 64, 2, 2, 2, 1>;
-using Fp864x64 = SmallTileCfg<64, 64, 2, 2, 4, 1>;
+// Most rows of the long operand for the kernel of few rows: offsets of a batch of
+// groups (24 N kB apart) stay below 2^31.
+constexpr int64_t kRowsMaxN = 1 << 17;
 
-// The library's choice of tile: the largest that gives every compute unit some.
-forge_tile choose_tile(int64_t N, int64_t M) {
-  if (M <= 64 && N <= 131072) return FP8_TILE_ROWS;
+using Fp8128x64 = SmallTileCfg<128, 64, 2, 2, 1, 2>;
+using Fp864x64 = SmallTileCfg<64, 64, 2, 2, 2, 2>;
+
+// The library's choice of tile: the least estimated time in microseconds, from
+// times measured on this kernel. A stage (64 columns) of a tile takes `alone`
+// where its CU has nothing else to do, and a CU with `slots` of them finishes one
+// every `full`; `ends` is what a round of tiles adds at its two ends. The
+// persistent schedule runs 256x256 tiles, its rounds counted in full tiles. Of
+// 35 sizes from 64 x 64 x 128 to 16384 x 6144 x 4096 one is 15% behind the fastest
+// tile and the others within 10% (333 x 520 x 1024: 4.7 us at 64x64, 5.8 to 14 at the others;
+// 1024 x 4096 x 4096: 17.8 at 128x128, 22 to 36; 8192 x 4096 x 14336: 312 at 256x256,
+// 318 by the persistent schedule; 4096 x 6144 x 16384: 276 by that, 297 at 256x256).
+//
+// Up to 16 rows take the kernel that cuts the contraction, whose time is that of
+// the long operand's bytes (1 x 4096 x 14336: 11.5 us, 24 at 64x64; 1 x 128256 x 4096: 90,
+// 91 at 128x128); up to 64 where its reads of the short operand by every
+// workgroup, 11.5 TB/s with the long one's, take less than the tiles (32 x 4096 x
+// 14336: 17.5 us, 24 at 64x64; 32 x 6144 x 4096: 9.3, 14.5 at 128x128; 64 x 14336 x 4096:
+// 29, 20 at 128x128).
+forge_tile choose_tile(int64_t N, int64_t M, int64_t Kp) {
+  struct Kind {
+    forge_tile id;
+    int bm, bn, slots, ring;       // ring: stages of a round of its LDS slots
+    double alone, full, ends;
+  };
+  static const Kind kinds[] = {{FORGE_TILE_256x256, 256, 256, 1, 4, 0.447, 0.667, 7.2},
+                               {FORGE_TILE_256x128, 256, 128, 1, 4, 0.30, 0.375, 4.9},
+                               {FORGE_TILE_128x128, 128, 128, 2, 4, 0.19, 0.215, 3.1},
+                               {FP8_TILE_128x64, 128, 64, 1, 8, 0.136, 0.17, 3.2},
+                               {FP8_TILE_64x64, 64, 64, 2, 8, 0.096, 0.10, 2.4}};
+  const bool rows = M <= 64 && N <= kRowsMaxN;
+  if (rows && M <= 16) return FP8_TILE_ROWS;
+  auto stages = [&](int ring) { return double((Kp / 64 + ring - 1) / ring * ring); };
+  auto round = [&](const Kind& k, int64_t tiles) {
+    if (tiles == 0) return 0.0;
+    const double load = double(tiles) / 256.0;
+    return stages(k.ring) * std::max(k.alone, (load <= 1.0 ? load : std::ceil(load)) * k.full) + k.ends;
+  };
+  forge_tile best = FORGE_TILE_256x256;
+  double least = 0.0;
+  for (const Kind& k : kinds) {
+    const int64_t tiles = count_tiles(N, M, TileShape{k.bm, k.bn}), slots = 256 * k.slots;
+    const double t = double(tiles / slots) * round(k, slots) + round(k, tiles % slots);
+    if (least == 0.0 || t < least) {
+      least = t;
+      best = k.id;
+    }
+  }
+  const int grid = persistent_grid();
   const int64_t tiles = count_tiles(N, M, TileShape{256, 256});
-  if (persistent_grid() > 0 && tiles >= persistent_grid()) return FORGE_TILE_PERSISTENT;
-  if (count_tiles(N, M, TileShape{256, 128}) >= 256) return FORGE_TILE_256x128;
-  if (count_tiles(N, M, TileShape{128, 128}) >= 256) return FORGE_TILE_128x128;
-  if (count_tiles(N, M, TileShape{128, 64}) >= 256) return FP8_TILE_128x64;
-  return FP8_TILE_64x64;
+  if (grid > 0 && tiles >= grid) {
+    const double t = persistent_makespan(tiles, grid) * (stages(4) * 0.645 + 7.0);
+    if (t < least) {
+      least = t;
+      best = FORGE_TILE_PERSISTENT;
+    }
+  }
+  if (rows && 2.5 + double(N) * double(Kp) * (M <= 32 ? 3 : 5) / 11.5e6 < least) return FP8_TILE_ROWS;
+  return best;
 }
 
 template <class C, int FI, int FO>
@@ -43,8 +94,8 @@ forge_status launch_rows_t(const WgradArgs& a, const Fp8BlockArgs& x, hipStream_
 
 template <int FI, int FO>
 forge_status launch_rows(const WgradArgs& a, const Fp8BlockArgs& x, hipStream_t s) {
-  if (a.d_out <= 16) return launch_rows_t<1, 16, 4, FI, FO>(a, x, s);
-  if (a.d_out <= 32) return launch_rows_t<2, 16, 2, FI, FO>(a, x, s);
+  if (a.d_out <= 16) return launch_rows_t<1, 8, 2, FI, FO>(a, x, s);
+  if (a.d_out <= 32) return launch_rows_t<2, 8, 2, FI, FO>(a, x, s);
   return launch_rows_t<4, 8, 2, FI, FO>(a, x, s);
 }
 
@@ -125,7 +176,7 @@ FORGE_API forge_status forge_matmul_fp8_block(const void* a_codes, const void* a
   if (M == 0 || N == 0) return FORGE_OK;
   if (forge_status s = check_device()) return s;
   if (!grid_fits(N, M, FORGE_TILE_128x128, 1)) return FORGE_ERR_SHAPE;
-  if (tile == FORGE_TILE_DEFAULT) tile = choose_tile(N, M);
+  if (tile == FORGE_TILE_DEFAULT) tile = choose_tile(N, M, Kp);
   (void)hipGetLastError();
   const WgradArgs w = base_args(b_codes, a_codes, static_cast<float*>(out), nullptr, nullptr, Kp, N, M);
   const Fp8BlockArgs x{static_cast<const uint8_t*>(b_scales), static_cast<const uint8_t*>(a_scales), Kp};

@@ -205,20 +205,22 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
 // Stages of 64 columns (one MFMA k-step), rows of 64 bytes and then their scale
 // words, straight from memory into a ring of 4 LDS slots. 16-byte chunk c of row r is
 // kept at chunk c ^ (r / 4 mod 4), which puts 16 neighbouring rows' reads on
-// different banks. Per stage s: request stage s + 4 into the slot that the last
+// different banks. A slot of one stage: request stage s + 4 into the slot that the last
 // barrier freed, MFMAs on stage s, whose operands are in registers, while those of
 // stage s + 1 are read from its slot; then wait for these reads and for this
-// wave's loads of stage s + 2, and one barrier. Columns enter each element in
-// ascending steps of 64, whatever the tile.
+// wave's loads of stage s + 2, and one barrier. Small tiles, whose waves have few
+// MFMAs to a stage, have slots of two: the barrier comes between their stages.
+// Columns enter each element in ascending steps of 64, whatever the tile.
 struct Fp8BlockArgs {
   const uint8_t *i_scales, *o_scales;
   int64_t kp;
 };
 
-// 16-bit elements of a slot: codes, and 256 bytes of scales of each side.
+// 16-bit elements of a slot: the codes of its stages, and 256 bytes of scales of
+// each side.
 template <class C>
 __host__ __device__ constexpr int fp8_block_slot() {
-  return C::STAGE + 256;
+  return mx_stages<C> * C::STAGE + 256;
 }
 
 template <class C, int FI, int FO>
@@ -228,8 +230,10 @@ __device__ __forceinline__ void fp8_block_tile(const WgradArgs& a, const Fp8Bloc
   constexpr int RB = 64;                                // bytes of a row in a stage
   constexpr int QX = BM * RB / 1024, QY = BN * RB / 1024;
   constexpr int NQW = (QX + QY) / C::WAVES;             // 1 KB loads per wave and stage
-  constexpr int NL = NQW + 1;                           // and 256 bytes of scales
-  constexpr int kScales = RB * (BM + BN);               // their place in a slot
+  constexpr int KS = mx_stages<C>;                      // stages of a slot
+  static_assert(KS <= 2, "a slot is within a group of scales");
+  constexpr int NL = KS * NQW + 1;                      // with 256 bytes of scales
+  constexpr int kStage = RB * (BM + BN), kScales = KS * kStage;   // places in a slot
   static_assert((QX + QY) % C::WAVES == 0, "stage loads split evenly over the waves");
   static_assert(RB * (BM + BN) <= C::STAGE * 2 && BM <= 256 && BN <= 256, "stage exceeds a slot");
 
@@ -288,19 +292,22 @@ __device__ __forceinline__ void fp8_block_tile(const WgradArgs& a, const Fp8Bloc
     voff[i] = uint32_t(min(row, (q < QX ? left_i : left_o) - 1) * RB + ((lane & 3) ^ ((lane >> 4) & 3)) * 16);
   }
   const uint32_t soff = uint32_t(lane * 4);
-  // Stage j of the round that the windows are at.
-  auto load_stage = [&](uint16_t* slot, int j) {
-    load4_to_lds(scales.window, slot + kScales / 2 + (scales_o ? 128 : 0), soff, int(scales.stage) * (j >> 1));
+  // Slot j of the round that the windows are at.
+  auto load_slot = [&](uint16_t* slot, int j) {
+    load4_to_lds(scales.window, slot + kScales / 2 + (scales_o ? 128 : 0), soff,
+                 int(scales.stage) * (KS == 1 ? j >> 1 : j));
 #pragma unroll
-    for (int i = 0; i < NQW; ++i) {
-      const Feed& f = codes[i < QXW ? 0 : NF - 1];
-      load16_to_lds(f.window, slot + load_of(i) * 512, voff[i], int(f.stage) * j);
-    }
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int i = 0; i < NQW; ++i) {
+        const Feed& f = codes[i < QXW ? 0 : NF - 1];
+        load16_to_lds(f.window, slot + k * kStage / 2 + load_of(i) * 512, voff[i], int(f.stage) * (KS * j + k));
+      }
   };
   auto advance = [&]() {
 #pragma unroll
-    for (int k = 0; k < NF; ++k) codes[k].advance(4);
-    scales.advance(2);
+    for (int k = 0; k < NF; ++k) codes[k].advance(4 * KS);
+    scales.advance(2 * KS);
   };
 
   // Operand addresses in a slot: lane l takes columns 32 (l / 32) .. + 31 of row
@@ -319,10 +326,11 @@ __device__ __forceinline__ void fp8_block_tile(const WgradArgs& a, const Fp8Bloc
   const int shift_i = ((ri >> 5) & 3) * 8, shift_o = ((ro >> 5) & 3) * 8;
   i32x8_t frag[2][TM + TN];
   uint32_t sc[2][2];
-  auto read_frags = [&](int f, const uint16_t* slot) {
+  auto read_frags = [&](int f, const uint16_t* slot, int k) {
     const char* base = reinterpret_cast<const char*>(slot);
     sc[f][0] = *reinterpret_cast<const uint32_t*>(base + sa);
     sc[f][1] = *reinterpret_cast<const uint32_t*>(base + sb);
+    base += k * kStage;
     auto operand = [&](uint32_t at) {
       const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(base + at);
       const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(base + (at ^ 16u));
@@ -362,7 +370,7 @@ __device__ __forceinline__ void fp8_block_tile(const WgradArgs& a, const Fp8Bloc
       if (i < NL) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);           // VMEM read
     }
   };
-  constexpr int kWaitStage = waitcnt_imm(2 * NL, 0);
+  constexpr int kWaitSlot = waitcnt_imm(2 * NL, 0);
 #define FORGE_FP8_BARRIER(IMM)                \
   do {                                        \
     __builtin_amdgcn_sched_barrier(0);        \
@@ -374,25 +382,38 @@ __device__ __forceinline__ void fp8_block_tile(const WgradArgs& a, const Fp8Bloc
   } while (0)
   // Slot j of a round of four.
   auto run_slot = [&](uint16_t* cur, const uint16_t* nxt, int j) {
-    if (j == 0) advance();
-    load_stage(cur, j);                          // stage s + 4
-    read_frags((j & 1) ^ 1, nxt);
-    mfmas(j & 1);
-    interleave();
-    FORGE_FP8_BARRIER(kWaitStage);
+    if constexpr (KS == 1) {
+      if (j == 0) advance();
+      load_slot(cur, j);                         // stage s + 4
+      read_frags((j & 1) ^ 1, nxt, 0);
+      mfmas(j & 1);
+      interleave();
+      FORGE_FP8_BARRIER(kWaitSlot);
+    } else {
+      read_frags(1, cur, 1);
+      mfmas(0);
+      FORGE_FP8_BARRIER(kWaitSlot);
+      if (j == 0) advance();
+      load_slot(cur, j);                         // of the next round
+      read_frags(0, nxt, 0);
+      mfmas(1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   if (nk > 0) {
-    load_stage(sl.s0, 0);
-    load_stage(sl.s1, 1);
-    load_stage(sl.s2, 2);
-    load_stage(sl.s3, 3);
-    FORGE_FP8_BARRIER(waitcnt_imm(2 * NL, 15));  // stages 0 and 1
-    read_frags(0, sl.s0);
-    // Slot 0 is refilled in the first round's first stage: every wave has read it by then.
-    FORGE_FP8_BARRIER(waitcnt_imm(63, 0));
+    load_slot(sl.s0, 0);
+    load_slot(sl.s1, 1);
+    load_slot(sl.s2, 2);
+    load_slot(sl.s3, 3);
+    FORGE_FP8_BARRIER(waitcnt_imm(KS == 1 ? 2 * NL : 3 * NL, 15));
+    read_frags(0, sl.s0, 0);
+    if constexpr (KS == 1) {
+      // Slot 0 is refilled at once: every wave has read it by then.
+      FORGE_FP8_BARRIER(waitcnt_imm(63, 0));
+    }
     // Whole rounds of 4 slots: the accumulators keep their registers. Stages past
     // the last add products of zero codes and zero scale bytes: exactly +0.
-    const int rounds = (nk + 3) / 4;
+    const int rounds = (nk + 4 * KS - 1) / (4 * KS);
     for (int r = 0; r < rounds; ++r) {
       run_slot(sl.s0, sl.s1, 0);
       run_slot(sl.s1, sl.s2, 1);
