@@ -9,6 +9,8 @@
 namespace forge {
 namespace {
 
+static_assert(kLayernormParts <= 8 * kLnReduceGroups, "parts that the last sum reads");
+
 // Most workgroups of a launch; what is beyond loops.
 constexpr int64_t kMaxGrid = int64_t(1) << 20;
 
@@ -17,7 +19,8 @@ dim3 grid_for(int64_t blocks) { return dim3(uint32_t(std::min(blocks, kMaxGrid))
 template <bool XB, bool YB, int EL, int WAVES>
 forge_status launch_forward(const LnArgs& a, hipStream_t s) {
   const int64_t blocks = (a.T + ln_rows<WAVES> - 1) / ln_rows<WAVES>;
-  hipLaunchKernelGGL((layernorm_kernel<XB, YB, EL, WAVES>), grid_for(blocks),
+  const int64_t most = int64_t(std::max(16, persistent_grid())) * (WAVES == 8 ? 2 : 6);
+  hipLaunchKernelGGL((layernorm_kernel<XB, YB, EL, WAVES>), dim3(uint32_t(std::min(blocks, most))),
                      dim3(ln_threads<WAVES>), 0, s, a);
   return launch_status();
 }
@@ -30,7 +33,7 @@ struct Forward {
     if (a.d <= 2048) return launch_forward<XB, YB, 8, 4>(a, s);
     if (a.d <= 4096) return launch_forward<XB, YB, 16, 4>(a, s);
     if (a.d <= 8192) return launch_forward<XB, YB, 32, 4>(a, s);
-    if (a.d <= 16384) return launch_forward<XB, YB, 16, 16>(a, s);
+    if (a.d <= 16384) return launch_forward<XB, YB, 32, 8>(a, s);
     hipLaunchKernelGGL((layernorm_wide_kernel<XB, YB>), grid_for(a.T), dim3(1024), 0, s, a);
     return launch_status();
   }
@@ -52,7 +55,7 @@ struct Backward {
     if (a.d <= 2048) return launch_backward<XB, YB, 8, 4>(a, parts, s);
     if (a.d <= 4096) return launch_backward<XB, YB, 16, 4>(a, parts, s);
     if (a.d <= 8192) return launch_backward<XB, YB, 32, 4>(a, parts, s);
-    if (a.d <= 16384) return launch_backward<XB, YB, 16, 16>(a, parts, s);
+    if (a.d <= 16384) return launch_backward<XB, YB, 32, 8>(a, parts, s);
     // Sums of so many columns do not fit a workgroup's registers beside the row:
     // the columns first, as dX may overwrite dY.
     constexpr int E = io_elems<XB, YB>;
@@ -132,7 +135,8 @@ FORGE_API forge_status forge_layernorm_backward(const void* dY, forge_dtype y_dt
   }
   const LnReduce r{static_cast<const float*>(workspace), dgamma, dbeta, int32_t(d), parts,
                    int32_t(dbeta ? 2 * d : d)};
-  hipLaunchKernelGGL(layernorm_reduce_kernel, dim3((r.columns + 63) / 64), dim3(256), 0, st, r);
+  hipLaunchKernelGGL(layernorm_reduce_kernel, dim3((r.columns + kLnReduceColumns - 1) / kLnReduceColumns),
+                     dim3(8 * kLnReduceGroups), 0, st, r);
   return launch_status();
 }
 

@@ -18,6 +18,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "row_io.hpp"
 
@@ -34,17 +35,18 @@ struct LnArgs {
   float eps;
 };
 
-// Sum of v over the WAVES waves that share a row, in every thread. `part`: WAVES
-// floats, which the next call but one may use again.
-template <int WAVES>
-__device__ __forceinline__ float row_sum(float v, float* part) {
-  v = wave_sum(v);
+// Sum of v over the WAVES waves that share a row, in every thread. `part`: a
+// number for each wave, which the next call but one may use again.
+template <int WAVES, class F>
+__device__ __forceinline__ F row_sum(F v, F* part) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
   if constexpr (WAVES > 1) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = 0.0f;
+    v = part[0];
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) v += part[w];
+    for (int w = 1; w < WAVES; ++w) v += part[w];
   }
   return v;
 }
@@ -55,49 +57,101 @@ constexpr int ln_threads = WAVES == 1 ? 256 : 64 * WAVES;
 template <int WAVES>
 constexpr int ln_rows = WAVES == 1 ? 4 : 1;
 
-// EL elements of the row to a thread.
+// A row's vectors as they lie in memory: thread `me` of the row's L has the
+// elements (i L + me) E .. + E - 1 for each i. Those past the row's end, and all of a
+// row that is not wanted, read as zeros without a memory access.
+template <bool BF16, int E>
+using LnRaw = typename std::conditional<BF16 && E == 4, u32x2_t, u32x4_t>::type;
+
+template <bool BF16, int E, int NV, int L>
+__device__ __forceinline__ void ln_fetch(const void* p, int64_t row, int d, bool wanted, int me,
+                                         LnRaw<BF16, E> (&raw)[NV]) {
+  constexpr int S = BF16 ? 2 : 4;
+  const __amdgpu_buffer_rsrc_t r =
+      window(static_cast<const char*>(p) + (wanted ? row * d * S : 0), wanted ? int64_t(d) * S : 0);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if constexpr (E * S == 8)
+      raw[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, me * 8, i * L * 8, kStatePolicy));
+    else
+      raw[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, me * 16, i * L * 16, kStatePolicy));
+  }
+}
+
+template <bool BF16, int E>
+__device__ __forceinline__ void ln_values(const LnRaw<BF16, E>& r, float (&v)[E]) {
+#pragma unroll
+  for (int k = 0; k < E; ++k)
+    v[k] = __builtin_bit_cast(float, BF16 ? (k & 1 ? r[k / 2] & 0xffff0000u : r[k / 2] << 16) : r[k]);
+}
+
+// Vector i of row `row`; past the row's end nothing is written. The offset is a
+// vector register's as a whole: with a part of it in a scalar register the compiler
+// takes a 16-byte store's data to be read when the next instruction issues, and
+// where two waves share a SIMD it was not (lanes 12 to 15 of each 16 had the first
+// word of what the next instruction wrote there).
+template <bool BF16, int E, int L>
+__device__ __forceinline__ void ln_put(void* p, int64_t row, int d, int me, int i, const float (&v)[E]) {
+  constexpr int S = BF16 ? 2 : 4;
+  const __amdgpu_buffer_rsrc_t r = window(static_cast<char*>(p) + row * d * S, int64_t(d) * S);
+  const f32x4_t lo = {v[0], v[1], v[2], v[3]};
+  if constexpr (E == 8) {
+    const u32x2_t a = pack_bf16x4(lo), b = pack_bf16x4(f32x4_t{v[4], v[5], v[6], v[7]});
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{a[0], a[1], b[0], b[1]}, r, (i * L + me) * 16, 0, kStatePolicy);
+  } else {
+    store4<S>(r, uint32_t((i * L + me) * 4 * S), 0u, lo);
+  }
+}
+
+// EL elements of the row to a thread. A workgroup goes from row to row with gamma
+// and beta in registers, the next row's loads in flight.
 template <bool XB, bool YB, int EL, int WAVES>
 __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_kernel(LnArgs a) {
   constexpr int E = io_elems<XB, YB>, NV = EL / E, L = 64 * WAVES;
-  __shared__ float part[2][WAVES];
+  __shared__ double part_s[WAVES];
+  __shared__ float part_v[WAVES];
   const int me = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int sub = WAVES == 1 ? threadIdx.x >> 6 : 0;
-  const float d = float(a.d);
-  for (int64_t row = int64_t(blockIdx.x) * ln_rows<WAVES> + sub; row < a.T;
-       row += int64_t(gridDim.x) * ln_rows<WAVES>) {
-    const int64_t base = row * a.d;
-    float v[NV][E], s = 0.0f;
+  const int sub = WAVES == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  const int64_t step = int64_t(gridDim.x) * ln_rows<WAVES>;
+  int64_t row = int64_t(blockIdx.x) * ln_rows<WAVES> + sub;
+  LnRaw<XB, E> raw[NV];
+  ln_fetch<XB, E, NV, L>(a.x, row, a.d, row < a.T, me, raw);
+  float g[NV][E] = {}, b[NV][E] = {};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * L + me) * E;
+    if (c < a.d) {
+      load_f32<E>(a.gamma, c, g[i]);
+      if (a.beta) load_f32<E>(a.beta, c, b[i]);
+    }
+  }
+  for (; row < a.T; row += step) {
+    float v[NV][E];
+    double s = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * L + me) * E;
-      if (c < a.d) {
-        load_elems<XB, E>(a.x, base + c, v[i]);
+      ln_values<XB, E>(raw[i], v[i]);
 #pragma unroll
-        for (int k = 0; k < E; ++k) s += v[i][k];
+      for (int k = 0; k < E; ++k) s += double(v[i][k]);
+    }
+    ln_fetch<XB, E, NV, L>(a.x, row + step, a.d, row + step < a.T, me, raw);
+    const float mean = float(row_sum<WAVES>(s, part_s) / double(a.d));
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = (i * L + me) * E < a.d;
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        v[i][k] = in ? v[i][k] - mean : 0.0f;
+        q = __builtin_fmaf(v[i][k], v[i][k], q);
       }
     }
-    const float mean = row_sum<WAVES>(s, part[0]) / d;
-    s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if ((i * L + me) * E < a.d)
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-          v[i][k] -= mean;
-          s = __builtin_fmaf(v[i][k], v[i][k], s);
-        }
-    const float rstd = 1.0f / sqrtf(row_sum<WAVES>(s, part[1]) / d + a.eps);
+    const float rstd = 1.0f / sqrtf(row_sum<WAVES>(q, part_v) / float(a.d) + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * L + me) * E;
-      if (c < a.d) {
-        float g[E], b[E] = {};
-        load_f32<E>(a.gamma, c, g);
-        if (a.beta) load_f32<E>(a.beta, c, b);
 #pragma unroll
-        for (int k = 0; k < E; ++k) v[i][k] = __builtin_fmaf(v[i][k] * rstd, g[k], b[k]);
-        store_elems<YB, E>(a.out, base + c, v[i]);
-      }
+      for (int k = 0; k < E; ++k) v[i][k] = __builtin_fmaf(v[i][k] * rstd, g[i][k], b[i][k]);
+      ln_put<YB, E, L>(a.out, row, a.d, me, i, v[i]);
     }
     if (me == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -110,18 +164,19 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_kernel(LnArgs a) 
 template <bool XB, bool YB>
 __global__ __launch_bounds__(1024) void layernorm_wide_kernel(LnArgs a) {
   constexpr int E = io_elems<XB, YB>, WAVES = 16;
-  __shared__ float part[2][WAVES];
+  __shared__ double part_s[WAVES];
+  __shared__ float part_v[WAVES];
   const float d = float(a.d);
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     const int64_t base = row * a.d;
     float v[E], s = 0.0f;
+    double sum = 0.0;
     for (int c = threadIdx.x * E; c < a.d; c += 1024 * E) {
       load_elems<XB, E>(a.x, base + c, v);
 #pragma unroll
-      for (int k = 0; k < E; ++k) s += v[k];
+      for (int k = 0; k < E; ++k) sum += double(v[k]);
     }
-    const float mean = row_sum<WAVES>(s, part[0]) / d;
-    s = 0.0f;
+    const float mean = float(row_sum<WAVES>(sum, part_s) / double(a.d));
     for (int c = threadIdx.x * E; c < a.d; c += 1024 * E) {
       load_elems<XB, E>(a.x, base + c, v);
 #pragma unroll
@@ -130,7 +185,7 @@ __global__ __launch_bounds__(1024) void layernorm_wide_kernel(LnArgs a) {
         s = __builtin_fmaf(e, e, s);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<WAVES>(s, part[1]) / d + a.eps);
+    const float rstd = 1.0f / sqrtf(row_sum<WAVES>(s, part_v) / d + a.eps);
     for (int c = threadIdx.x * E; c < a.d; c += 1024 * E) {
       float g[E], b[E] = {};
       load_elems<XB, E>(a.x, base + c, v);
@@ -147,46 +202,73 @@ __global__ __launch_bounds__(1024) void layernorm_wide_kernel(LnArgs a) {
   }
 }
 
-// dX of the workgroup's rows, and its sums of dY n and dY.
+// dX of the workgroup's rows, and its sums of dY n and dY. The next row's loads are
+// in flight; dX may be dY, whose rows no other workgroup reads.
 template <bool XB, bool YB, int EL, int WAVES>
 __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_backward_kernel(LnArgs a) {
   constexpr int E = io_elems<XB, YB>, NV = EL / E, L = 64 * WAVES;
   __shared__ float part[2][2][WAVES];
   __shared__ __attribute__((aligned(16))) float join[WAVES == 1 ? 3 * 2 * 64 * EL : 4];
   const int me = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int sub = WAVES == 1 ? threadIdx.x >> 6 : 0;
+  const int sub = WAVES == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
   const float d = float(a.d);
-  float dg[NV][E], db[NV][E], g[NV][E];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * L + me) * E;
-#pragma unroll
-    for (int k = 0; k < E; ++k) dg[i][k] = db[i][k] = g[i][k] = 0.0f;
-    if (c < a.d) load_f32<E>(a.gamma, c, g[i]);
-  }
-  int turn = 0;
-  for (int64_t row = int64_t(blockIdx.x) * ln_rows<WAVES> + sub; row < a.T;
-       row += int64_t(gridDim.x) * ln_rows<WAVES>, turn ^= 1) {
-    const int64_t base = row * a.d;
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    float n[NV][E], y[NV][E], s1 = 0.0f, s2 = 0.0f;
+  const int64_t step = int64_t(gridDim.x) * ln_rows<WAVES>;
+  int64_t row = int64_t(blockIdx.x) * ln_rows<WAVES> + sub;
+  LnRaw<XB, E> rx[NV];
+  LnRaw<YB, E> ry[NV];
+  float mean = 0.0f, rstd = 0.0f;
+  auto fetch = [&](int64_t r) {
+    const bool wanted = r < a.T;
+    ln_fetch<XB, E, NV, L>(a.x, r, a.d, wanted, me, rx);
+    ln_fetch<YB, E, NV, L>(a.dy, r, a.d, wanted, me, ry);
+    mean = wanted ? a.mean[r] : 0.0f;
+    rstd = wanted ? a.rstd[r] : 0.0f;
+  };
+  fetch(row);
+  // gamma stays in registers where there is room; else it comes from the caches.
+  constexpr bool HELD = EL <= 16;
+  float dg[NV][E] = {}, db[NV][E] = {}, held[HELD ? NV : 1][E] = {};
+  if constexpr (HELD)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * L + me) * E;
-      if (c < a.d) {
-        load_elems<XB, E>(a.x, base + c, n[i]);
-        load_elems<YB, E>(a.dy, base + c, y[i]);
+      if (c < a.d) load_f32<E>(a.gamma, c, held[i]);
+    }
+  const __amdgpu_buffer_rsrc_t gammas = window(a.gamma, int64_t(a.d) * 4);
+  int turn = 0;
+  for (; row < a.T; row += step, turn ^= 1) {
+    // Past the row's end dY is 0, and so is all that it is multiplied with.
+    float n[NV][E], y[NV][E], s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          n[i][k] = (n[i][k] - mean) * rstd;
-          dg[i][k] = __builtin_fmaf(y[i][k], n[i][k], dg[i][k]);
-          db[i][k] += y[i][k];
-          y[i][k] *= g[i][k];
-          s1 += y[i][k];
-          s2 = __builtin_fmaf(y[i][k], n[i][k], s2);
+    for (int i = 0; i < NV; ++i) {
+      ln_values<XB, E>(rx[i], n[i]);
+      ln_values<YB, E>(ry[i], y[i]);
+      const bool in = (i * L + me) * E < a.d;
+      float g[E];
+      if constexpr (HELD) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) g[k] = held[i][k];
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; j += 4) {
+          const f32x4_t r = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+              gammas, me * E * 4 + j * 4, i * L * E * 4, 0));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) g[j + k] = r[k];
         }
       }
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        n[i][k] = in ? (n[i][k] - mean) * rstd : 0.0f;
+        dg[i][k] = __builtin_fmaf(y[i][k], n[i][k], dg[i][k]);
+        db[i][k] += y[i][k];
+        y[i][k] *= g[k];
+        s1 += y[i][k];
+        s2 = __builtin_fmaf(y[i][k], n[i][k], s2);
+      }
     }
+    const float r = rstd;
+    fetch(row + step);
     s1 = wave_sum(s1);
     s2 = wave_sum(s2);
     if constexpr (WAVES > 1) {
@@ -206,12 +288,9 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_backward_kernel(L
     s2 /= d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * L + me) * E;
-      if (c < a.d) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) y[i][k] = rstd * (y[i][k] - s1 - n[i][k] * s2);
-        store_elems<XB, E>(a.out, base + c, y[i]);
-      }
+      for (int k = 0; k < E; ++k) y[i][k] = r * (y[i][k] - s1 - n[i][k] * s2);
+      ln_put<XB, E, L>(a.out, row, a.d, me, i, y[i]);
     }
   }
   if constexpr (WAVES == 1) {                // four waves' sums to one
@@ -327,26 +406,40 @@ __global__ __launch_bounds__(256) void layernorm_columns_kernel(LnArgs a) {
   }
 }
 
-// dgamma and dbeta: column c of `columns` summed over the parts, 16 lanes of 4
-// columns by 16 groups that take every 16th part.
+// dgamma and dbeta: column c of `columns` summed over the parts, 8 lanes of 4
+// columns (a line) by 64 groups that take every 64th part.
 struct LnReduce {
   const float* part;
   float *dgamma, *dbeta;
   int32_t d, parts, columns;         // columns: 2 d, or d without dbeta
 };
-__global__ __launch_bounds__(256) void layernorm_reduce_kernel(LnReduce a) {
-  __shared__ f32x4_t join[16][16];
-  const int me = threadIdx.x & 15, grp = threadIdx.x >> 4;
-  const int c = (blockIdx.x * 16 + me) * 4;
+constexpr int kLnReduceColumns = 32, kLnReduceGroups = 64;
+__global__ __launch_bounds__(512) void layernorm_reduce_kernel(LnReduce a) {
+  __shared__ f32x4_t join[kLnReduceGroups][8];
+  const int me = threadIdx.x & 7, grp = threadIdx.x >> 3;
+  const int c = blockIdx.x * kLnReduceColumns + me * 4;
   f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (c < a.columns)
-    for (int p = grp; p < a.parts; p += 16)
-      s = s + *reinterpret_cast<const f32x4_t*>(a.part + int64_t(p) * 2 * a.d + c);
+  if (c < a.columns) {
+    const float* p = a.part + c;
+    const int64_t step = int64_t(kLnReduceGroups) * 2 * a.d;
+    f32x4_t v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {              // at most kLayernormParts = 512 parts
+      const bool in = grp + k * kLnReduceGroups < a.parts;
+      v[k] = in ? *reinterpret_cast<const f32x4_t*>(p + int64_t(grp) * 2 * a.d + k * step) : s;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s = s + v[k];
+  }
   join[grp][me] = s;
   __syncthreads();
-  if (grp > 0 || c >= a.columns) return;
-  for (int k = 1; k < 16; ++k) s = s + join[k][me];
-  *reinterpret_cast<f32x4_t*>(c < a.d ? a.dgamma + c : a.dbeta + (c - a.d)) = s;
+  if (threadIdx.x >= kLnReduceColumns) return;
+  const int col = blockIdx.x * kLnReduceColumns + threadIdx.x;
+  if (col >= a.columns) return;
+  float r = 0.0f;
+#pragma unroll 8
+  for (int k = 0; k < kLnReduceGroups; ++k) r += join[k][threadIdx.x >> 2][threadIdx.x & 3];
+  (col < a.d ? a.dgamma + col : a.dbeta + (col - a.d))[0] = r;
 }
 
 }  // namespace forge
