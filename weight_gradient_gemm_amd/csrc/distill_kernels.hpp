@@ -440,18 +440,17 @@ __global__ __launch_bounds__(THREADS) void distill_rows_kernel(DistillArgs a) {
 #pragma unroll
             for (int k = 0; k < E; ++k) v[k] = tid * E + k >= rest ? 0.0f : v[k];
         }
-        // The whole offset in a vector register, as in ln_put (layernorm_kernels.hpp).
-        const uint32_t at = vg + uint32_t(i * kBlock * GS);
+        const uint32_t at = uint32_t(i * kBlock * GS);
 #pragma unroll
         for (int k = 0; k < E; k += 4) {
           const f32x4_t g = {v[k], v[k + 1], v[k + 2], v[k + 3]};
           if constexpr (GB && E == 8) {
             if (k == 0) {
               const u32x2_t lo = pack_bf16x4(g), hi = pack_bf16x4(f32x4_t{v[4], v[5], v[6], v[7]});
-              __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{lo[0], lo[1], hi[0], hi[1]}, out, int(at), 0, kStatePolicy);
+              store16(out, vg, at, u32x4_t{lo[0], lo[1], hi[0], hi[1]});
             }
           } else {
-            store4<GS>(out, at + k * GS, 0u, g);
+            store4<GS>(out, vg + k * GS, at, g);
           }
         }
       };

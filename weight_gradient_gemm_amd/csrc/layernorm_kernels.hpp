@@ -85,11 +85,7 @@ __device__ __forceinline__ void ln_values(const LnRaw<BF16, E>& r, float (&v)[E]
     v[k] = __builtin_bit_cast(float, BF16 ? (k & 1 ? r[k / 2] & 0xffff0000u : r[k / 2] << 16) : r[k]);
 }
 
-// Vector i of row `row`; past the row's end nothing is written. The offset is a
-// vector register's as a whole: with a part of it in a scalar register the compiler
-// takes a 16-byte store's data to be read when the next instruction issues, and
-// where two waves share a SIMD it was not (lanes 12 to 15 of each 16 had the first
-// word of what the next instruction wrote there).
+// Vector i of row `row`; past the row's end nothing is written.
 template <bool BF16, int E, int L>
 __device__ __forceinline__ void ln_put(void* p, int64_t row, int d, int me, int i, const float (&v)[E]) {
   constexpr int S = BF16 ? 2 : 4;
@@ -97,9 +93,9 @@ __device__ __forceinline__ void ln_put(void* p, int64_t row, int d, int me, int 
   const f32x4_t lo = {v[0], v[1], v[2], v[3]};
   if constexpr (E == 8) {
     const u32x2_t a = pack_bf16x4(lo), b = pack_bf16x4(f32x4_t{v[4], v[5], v[6], v[7]});
-    __builtin_amdgcn_raw_buffer_store_b128(u32x4_t{a[0], a[1], b[0], b[1]}, r, (i * L + me) * 16, 0, kStatePolicy);
+    store16(r, uint32_t(me * 16), uint32_t(i * L * 16), u32x4_t{a[0], a[1], b[0], b[1]});
   } else {
-    store4<S>(r, uint32_t((i * L + me) * 4 * S), 0u, lo);
+    store4<S>(r, uint32_t(me * 4 * S), uint32_t(i * L * 4 * S), lo);
   }
 }
 
