@@ -244,6 +244,21 @@ def test_a_row_that_is_not_finite_stays_alone(env, T):
         assert torch.equal(l2[rest], loss[rest]) and torch.equal(g2[rest], grad[rest])
 
 
+@pytest.mark.parametrize("T", [3, 300])
+def test_logits_far_below_zero(env, T):
+    """Threads, waves and chunks whose columns are all masked beside logits of -900."""
+    torch, wg = env
+    for V in (700, 9000, 50000):
+        z, u, ids, weight, V = inputs(torch, T, V, 6, masked=False)
+        z[:, :V] -= 900
+        keep = z.gather(1, ids)
+        z[0, : V // 2] = -INF
+        z[1, V // 3:V] = -INF
+        z[2, 64:] = -INF
+        z.scatter_(1, ids, keep)
+        check(torch, wg, (z, u, ids, weight, V))
+
+
 def test_far_logits(env):
     """A student that is sure, and temperatures far from 1."""
     torch, wg = env

@@ -5,10 +5,14 @@
 //   loss = scale w tau^2 sum_j q_j (log q_j - log p[id_j])
 //   dz_i = scale w tau (p_i - sum of the q_j with id_j == i)
 //
-// Bound by HBM: the logits are read and the gradient is written. A row is cut into
-// chunks, a workgroup each: the first launch forms each chunk's maximum and sum
-// of exponentials, the second joins a row's chunks and forms the gradient. The
-// teacher's columns are written with the others and once more, with their q,
+// Bound by HBM: the logits are read and the gradient is written. Of many rows a
+// workgroup takes one after the other and holds it in registers, 16 vectors of 16
+// bytes to a thread (a row of 128256 bf16 logits is 250 KB, a CU's registers hold
+// 512), so that it is read once. Few rows are cut into chunks, a workgroup each:
+// one launch forms each chunk's maximum and sum of exponentials, a second joins
+// them and forms the gradient.
+//
+// The teacher's columns are written with the others and once more, with their q,
 // behind a barrier: the workgroup that has the column does both.
 #pragma once
 
@@ -22,7 +26,6 @@ namespace forge {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kDistillThreads = 256;
 constexpr int kDistillMaxK = 1024;
 
 struct DistillArgs {
@@ -38,37 +41,14 @@ struct DistillArgs {
   float c, inv_tau, loss_scale, grad_scale;    // log2(e) / tau, 1 / tau, scale tau^2, scale tau
 };
 
-// The row's entries in LDS: ids (-1: not there) and q, as they are formed.
+// A row's entries: id (-1: not there), 2^((u - largest) c), the student's logit.
 struct Entries {
   int32_t id[kDistillMaxK];
   float q[kDistillMaxK];
+  float z[kDistillMaxK];
 };
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// Maximum and sum over the workgroup, in every thread. `part`: a float for each wave.
-template <int THREADS>
-__device__ __forceinline__ float block_max(float v, float* part) {
-  v = wave_max(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = part[0];
-#pragma unroll
-  for (int w = 1; w < THREADS / 64; ++w) v = fmaxf(v, part[w]);
-  return v;
-}
-template <int THREADS>
-__device__ __forceinline__ float block_total(float v, float* part) {
-  v = wave_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = part[0];
-#pragma unroll
-  for (int w = 1; w < THREADS / 64; ++w) v += part[w];
-  return v;
-}
 
 __device__ __forceinline__ int64_t entry_id(const DistillArgs& a, int64_t at) {
   return a.wide_ids ? static_cast<const int64_t*>(a.ids)[at] : int64_t(static_cast<const int32_t*>(a.ids)[at]);
@@ -84,165 +64,9 @@ __device__ __forceinline__ float student_logit(const DistillArgs& a, int64_t at)
 }
 
 // The value that stands for a maximum in differences: 0 where everything is
-// -infinity, so that a difference is -infinity and no NaN.
+// -infinity, so that a difference is -infinity and no NaN. What is scaled from one
+// maximum to a larger one keeps its own as it is: a sum of nothing times 2^-infinity.
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
-
-// Columns [first, first + 32 * THREADS) of a row to a thread's 32 registers: thread t
-// has vectors t, t + THREADS and so on. Columns past V are -infinity.
-template <bool ZB, int THREADS, int E>
-__device__ __forceinline__ void load_chunk(const DistillArgs& a, int64_t row, int first,
-                                           float (&v)[32 / E][E]) {
-#pragma unroll
-  for (int i = 0; i < 32 / E; ++i) {
-    const int c = first + (i * THREADS + int(threadIdx.x)) * E;
-    if (c < a.V) load_elems<ZB, E>(a.z, row * a.ld + c, v[i]);
-#pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (c + k >= a.V) v[i][k] = -INFINITY;
-  }
-}
-
-template <bool ZB>
-__global__ __launch_bounds__(kDistillThreads) void distill_stats_kernel(DistillArgs a) {
-  constexpr int N = kDistillThreads, E = ZB ? 8 : 4;
-  __shared__ float part[N / 64];
-  for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
-    const int64_t row = item / a.chunks;
-    const int chunk = int(item - row * a.chunks);
-    if (a.weight && a.weight[row] == 0.0f) continue;
-    const int first = chunk * 32 * N;
-    float v[32 / E][E];
-    load_chunk<ZB, N, E>(a, row, first, v);
-    for (int j = threadIdx.x; j < a.K; j += N) {
-      const int64_t id = entry_id(a, row * a.K + j);
-      if (id >= first && id < first + 32 * N && id < a.V)
-        a.logit[row * a.K + j] = student_logit<ZB>(a, row * a.ld + id);
-    }
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 32 / E; ++i)
-#pragma unroll
-      for (int k = 0; k < E; ++k) m = fmaxf(m, v[i][k]);
-    m = block_max<N>(m, part);
-    const float ms = finite_max(m);
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32 / E; ++i)
-#pragma unroll
-      for (int k = 0; k < E; ++k) s += exp2_fast((v[i][k] - ms) * a.c);
-    s = block_total<N>(s, part);
-    if (threadIdx.x == 0) a.stats[item] = make_float2(m, s);
-  }
-}
-
-// The row's entries to LDS. False if there are none.
-template <int THREADS>
-__device__ __forceinline__ bool load_entries(const DistillArgs& a, int64_t row, Entries& e, float* part,
-                                             float& top, float& sum) {
-  float m = -INFINITY;
-  bool some = false;
-  __syncthreads();
-  for (int j = threadIdx.x; j < a.K; j += THREADS) {
-    const int64_t id = entry_id(a, row * a.K + j);
-    bool kept = id >= 0 && id < a.V;
-    const float u = kept ? entry_logit(a, row * a.K + j) : 0.0f;
-    kept = kept && u != -INFINITY;
-    e.id[j] = kept ? int32_t(id) : -1;
-    e.q[j] = u;
-    if (kept) m = fmaxf(m, u);
-    some = some || kept;
-  }
-  if (!__syncthreads_or(some)) return false;
-  m = finite_max(block_max<THREADS>(m, part));
-  float s = 0.0f;
-  for (int j = threadIdx.x; j < a.K; j += THREADS)
-    if (e.id[j] >= 0) s += exp2_fast((e.q[j] - m) * a.c);
-  top = m;
-  sum = block_total<THREADS>(s, part);
-  return true;
-}
-
-template <bool ZB, bool GB>
-__global__ __launch_bounds__(kDistillThreads) void distill_gradient_kernel(DistillArgs a) {
-  constexpr int N = kDistillThreads, E = io_elems<ZB, GB>;
-  __shared__ float part[N / 64];
-  __shared__ Entries entry;
-  for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
-    const int64_t row = item / a.chunks_out;
-    const int chunk = int(item - row * a.chunks_out);
-    const int first = chunk * 32 * N;
-    const float w = a.weight ? a.weight[row] : 1.0f;
-    float top, total;
-    if (w == 0.0f || !load_entries<N>(a, row, entry, part, top, total)) {
-      if (chunk == 0 && threadIdx.x == 0) a.loss[row] = 0.0f;
-      if (a.grad) {
-        const float zero[E] = {};
-#pragma unroll
-        for (int i = 0; i < 32 / E; ++i) {
-          const int c = first + (i * N + int(threadIdx.x)) * E;
-          if (c < a.ld) store_elems<GB, E>(a.grad, row * a.ld + c, zero);
-        }
-      }
-      continue;
-    }
-    // The row's maximum and sum from its chunks'.
-    float m = -INFINITY, s = 0.0f;
-    for (int k = threadIdx.x; k < a.chunks; k += N) m = fmaxf(m, a.stats[row * a.chunks + k].x);
-    m = finite_max(block_max<N>(m, part));
-    for (int k = threadIdx.x; k < a.chunks; k += N) {
-      const float2 st = a.stats[row * a.chunks + k];
-      s += st.y * exp2_fast((finite_max(st.x) - m) * a.c);
-    }
-    s = block_total<N>(s, part);
-    if (chunk == 0) {
-      float l = 0.0f;
-      for (int j = threadIdx.x; j < a.K; j += N)
-        if (entry.id[j] >= 0) {
-          const float du = entry.q[j] - top, q = exp2_fast(du * a.c) / total;
-          if (q != 0.0f) l += q * (du * a.inv_tau - (a.logit[row * a.K + j] - m) * a.inv_tau);
-        }
-      l = block_total<N>(l, part);
-      if (threadIdx.x == 0) a.loss[row] = a.loss_scale * w * (l + (logf(s) - logf(total)));
-    }
-    if (!a.grad) continue;
-    const float inv = 1.0f / s, coef = a.grad_scale * w;
-    float v[32 / E][E];
-    load_chunk<ZB, N, E>(a, row, first, v);
-#pragma unroll
-    for (int i = 0; i < 32 / E; ++i) {
-      const int c = first + (i * N + int(threadIdx.x)) * E;
-#pragma unroll
-      for (int k = 0; k < E; ++k)
-        v[i][k] = c + k < a.V ? coef * (exp2_fast((v[i][k] - m) * a.c) * inv) : 0.0f;
-      if (c < a.ld) store_elems<GB, E>(a.grad, row * a.ld + c, v[i]);
-    }
-    __syncthreads();
-    // The teacher's columns: the first entry of an id writes it.
-    for (int j = threadIdx.x; j < a.K; j += N) {
-      const int id = entry.id[j];
-      if (id < first || id >= first + 32 * N) continue;
-      float q = 0.0f;
-      bool again = false;
-      for (int k = 0; k < a.K; ++k)
-        if (entry.id[k] == id) {
-          again = again || k < j;
-          q += exp2_fast((entry.q[k] - top) * a.c);
-        }
-      if (again) continue;
-      const float p = exp2_fast((a.logit[row * a.K + j] - m) * a.c) * inv;
-      const float g[1] = {coef * (p - q / total)};
-      if constexpr (GB)
-        static_cast<__bf16*>(a.grad)[row * a.ld + id] = __bf16(g[0]);
-      else
-        static_cast<float*>(a.grad)[row * a.ld + id] = g[0];
-    }
-  }
-}
-
-
-// --------------------------------------------------------------------------
-// rows in registers
-// --------------------------------------------------------------------------
 
 // A vector of 16 bytes of a row and its elements.
 template <bool ZB>
@@ -254,19 +78,309 @@ __device__ __forceinline__ void unpack(const u32x4_t& r, float (&v)[kVec<ZB>]) {
     v[k] = __builtin_bit_cast(float, ZB ? (k & 1 ? r[k / 2] & 0xffff0000u : r[k / 2] << 16) : r[k]);
 }
 
-// The compiler may not keep what it made of r before.
-__device__ __forceinline__ void forget(u32x4_t& r) { asm volatile("" : "+v"(r)); }
+// Elements of a vector from its thread's element number `rest` on as -infinity.
+template <bool ZB>
+__device__ __forceinline__ void cut_vector(u32x4_t& r, int rest) {
+  constexpr uint32_t kLow = ZB ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (ZB)
+      r[k] = 2 * k >= rest ? kLow : 2 * k + 1 >= rest ? (r[k] & 0xffffu) | (kLow & 0xffff0000u) : r[k];
+    else
+      r[k] = k >= rest ? kLow : r[k];
+  }
+}
 
-template <bool ZB, bool GB, bool GRAD, int THREADS, int NV>
-__global__ __launch_bounds__(THREADS) void distill_rows_kernel(DistillArgs a) {
+// A vector's elements into a maximum m and a sum s of 2^((v - m) c).
+template <bool ZB>
+__device__ __forceinline__ void running(const u32x4_t& r, float c, float& m, float& s) {
+  float v[kVec<ZB>], most = m;
+  unpack<ZB>(r, v);
+#pragma unroll
+  for (int k = 0; k < kVec<ZB>; ++k) most = fmaxf(most, v[k]);
+  const float mf = finite_max(most);
+  s *= exp2_fast((m - mf) * c);
+#pragma unroll
+  for (int k = 0; k < kVec<ZB>; ++k) s += exp2_fast((v[k] - mf) * c);
+  m = most;
+}
+
+// A vector's gradients at byte offsets voff + soff of a row's window.
+template <bool GB, int E>
+__device__ __forceinline__ void store_gradient(__amdgpu_buffer_rsrc_t out, uint32_t voff, uint32_t soff,
+                                               const float (&v)[E]) {
+  const f32x4_t lo = {v[0], v[1], v[2], v[3]};
+  if constexpr (E == 8) {
+    const f32x4_t hi = {v[4], v[5], v[6], v[7]};
+    if constexpr (GB) {
+      const u32x2_t a = pack_bf16x4(lo), b = pack_bf16x4(hi);
+      store16(out, voff, soff, u32x4_t{a[0], a[1], b[0], b[1]});
+    } else {
+      store16(out, voff, soff, lo);
+      store16(out, voff + 16u, soff, hi);
+    }
+  } else {
+    store4<GB ? 2 : 4>(out, voff, soff, lo);
+  }
+}
+
+// The gradients of the row's entries with ids in [lo, hi), behind a barrier after
+// the columns: the first entry of an id writes it, with the q of all of them.
+// Up to 16 threads share an entry, each looking through its part of the others.
+template <int THREADS, bool GB>
+__device__ __forceinline__ void entry_gradients(const DistillArgs& a, int64_t row, const Entries& e, int lo,
+                                                int hi, float coef, float m, float s, float total) {
+  int share = 0;                                       // log2 of the threads of an entry
+  while (share < 4 && (a.K << (share + 1)) <= THREADS) ++share;
+  const int sub = threadIdx.x & ((1 << share) - 1);
+  for (int j0 = 0; j0 < a.K; j0 += THREADS >> share) {
+    const int j = j0 + (int(threadIdx.x) >> share);
+    const int id = j < a.K ? e.id[j] : -1;
+    const bool mine = id >= lo && id < hi;
+    float q = 0.0f;
+    int again = 0;
+    if (mine)
+      for (int k = 4 * sub; k < a.K; k += 4 << share) {
+        const i32x4_t ids = *reinterpret_cast<const i32x4_t*>(&e.id[k]);
+        const f32x4_t qs = *reinterpret_cast<const f32x4_t*>(&e.q[k]);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if (ids[n] == id) {
+            again |= int(k + n < j);
+            q += qs[n];
+          }
+      }
+    for (int d = 1; d < 1 << share; d <<= 1) {
+      q += __shfl_xor(q, d);
+      again |= __shfl_xor(again, d);
+    }
+    if (mine && sub == 0 && !again) {
+      const float g = coef * (exp2_fast((e.z[j] - m) * a.c) / s - q / total);
+      if constexpr (GB)
+        static_cast<__bf16*>(a.grad)[row * a.ld + id] = __bf16(g);
+      else
+        static_cast<float*>(a.grad)[row * a.ld + id] = g;
+    }
+  }
+}
+
+// An entry's share of the loss, without the logarithms of the two sums.
+__device__ __forceinline__ float entry_loss(const DistillArgs& a, float u, float top, float total, float z,
+                                            float m) {
+  const float du = u - top, q = exp2_fast(du * a.c) / total;
+  return q != 0.0f ? q * (du * a.inv_tau - (z - m) * a.inv_tau) : 0.0f;
+}
+
+// --------------------------------------------------------------------------
+// few rows: chunks
+// --------------------------------------------------------------------------
+constexpr int kChunkThreads = 256;
+constexpr int kChunkColumns = 16 * kChunkThreads;
+
+// The chunk's vectors of a thread, columns past V as -infinity.
+template <bool ZB>
+__device__ __forceinline__ void load_chunk(const DistillArgs& a, int64_t row, int first,
+                                           u32x4_t (&raw)[16 / kVec<ZB>]) {
+  constexpr int E = kVec<ZB>, S = ZB ? 2 : 4;
+  const int columns = min((a.V + 7) / 8 * 8 - first, kChunkColumns);
+  const __amdgpu_buffer_rsrc_t r =
+      window(static_cast<const char*>(a.z) + (row * a.ld + first) * S, int64_t(columns) * S);
+#pragma unroll
+  for (int i = 0; i < 16 / E; ++i)
+    raw[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+        r, int(threadIdx.x) * 16, i * kChunkThreads * 16, 0));
+  if (first + kChunkColumns > a.V)
+#pragma unroll
+    for (int i = 0; i < 16 / E; ++i)
+      cut_vector<ZB>(raw[i], a.V - first - (i * kChunkThreads + int(threadIdx.x)) * E);
+}
+
+template <bool ZB>
+__global__ __launch_bounds__(kChunkThreads) void distill_stats_kernel(DistillArgs a) {
+  constexpr int E = kVec<ZB>, W = kChunkThreads / 64;
+  __shared__ float2 part[W];
+  for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
+    const int64_t row = item / a.chunks;
+    const int first = int(item - row * a.chunks) * kChunkColumns;
+    if (a.weight && a.weight[row] == 0.0f) continue;
+    u32x4_t raw[16 / E];
+    load_chunk<ZB>(a, row, first, raw);
+    for (int j = threadIdx.x; j < a.K; j += kChunkThreads) {
+      const int64_t id = entry_id(a, row * a.K + j);
+      if (id >= first && id < first + kChunkColumns && id < a.V)
+        a.logit[row * a.K + j] = student_logit<ZB>(a, row * a.ld + id);
+    }
+    float m = -INFINITY, s = 0.0f, v[E];
+#pragma unroll
+    for (int i = 0; i < 16 / E; ++i) {
+      unpack<ZB>(raw[i], v);
+#pragma unroll
+      for (int k = 0; k < E; ++k) m = fmaxf(m, v[k]);
+    }
+    m = wave_max(m);
+    const float mf = finite_max(m);
+#pragma unroll
+    for (int i = 0; i < 16 / E; ++i) {
+      unpack<ZB>(raw[i], v);
+#pragma unroll
+      for (int k = 0; k < E; ++k) s += exp2_fast((v[k] - mf) * a.c);
+    }
+    s = wave_sum(s);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = make_float2(m, s);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float most = part[0].x, sum = 0.0f;
+#pragma unroll
+      for (int w = 1; w < W; ++w) most = fmaxf(most, part[w].x);
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        sum += part[w].y * exp2_fast((part[w].x - finite_max(most)) * a.c);
+      a.stats[item] = make_float2(most, sum);
+    }
+    __syncthreads();                                   // `part` is written again
+  }
+}
+
+template <bool ZB, bool GB>
+__global__ __launch_bounds__(kChunkThreads) void distill_gradient_kernel(DistillArgs a) {
+  constexpr int E = kVec<ZB>, N = kChunkThreads, W = N / 64, EPT = kDistillMaxK / N, GS = GB ? 2 : 4;
+  __shared__ __attribute__((aligned(16))) Entries entry;
+  __shared__ float part[4][W];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
+    const int64_t row = item / a.chunks_out;
+    const int chunk = int(item - row * a.chunks_out), first = chunk * kChunkColumns;
+    const float w = a.weight ? a.weight[row] : 1.0f;
+    u32x4_t raw[16 / E];
+    if (w != 0.0f && a.grad) load_chunk<ZB>(a, row, first, raw);
+    // Entries: each wave's largest and sum, joined behind the barrier.
+    int id[EPT];
+    float u[EPT], zt[EPT], top = -INFINITY, total = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      const int j = e * N + tid;
+      id[e] = -1;
+      u[e] = zt[e] = 0.0f;
+      if (j < a.K && w != 0.0f) {
+        const int64_t n = entry_id(a, row * a.K + j);
+        if (n >= 0 && n < a.V) {
+          u[e] = entry_logit(a, row * a.K + j);
+          zt[e] = a.logit[row * a.K + j];
+          if (u[e] != -INFINITY) {
+            id[e] = int(n);
+            top = fmaxf(top, u[e]);
+          }
+        }
+      }
+    }
+    // The row's maximum and sum from its chunks', by each wave for itself.
+    float m = -INFINITY, s = 0.0f;
+    if (w != 0.0f) {
+      for (int k = lane; k < a.chunks; k += 64) m = fmaxf(m, a.stats[row * a.chunks + k].x);
+      m = finite_max(wave_max(m));
+      for (int k = lane; k < a.chunks; k += 64) {
+        const float2 st = a.stats[row * a.chunks + k];
+        s += st.y * exp2_fast((st.x - m) * a.c);
+      }
+      s = wave_sum(s);
+    }
+    bool some = false;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) some = some || id[e] >= 0;
+    top = wave_max(top);
+    const bool any = __ballot(some) != 0;
+    if (lane == 0) {
+      part[0][wave] = top;
+      part[1][wave] = any ? 1.0f : 0.0f;
+    }
+    __syncthreads();
+    top = -INFINITY;
+    float live = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      top = fmaxf(top, part[0][k]);
+      live = fmaxf(live, part[1][k]);
+    }
+    top = finite_max(top);
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      const int j = e * N + tid;
+      const float q = id[e] >= 0 ? exp2_fast((u[e] - top) * a.c) : 0.0f;
+      total += q;
+      if (j < (a.K + 3 & ~3)) {                        // up to a multiple of 4
+        entry.id[j] = id[e];
+        entry.q[j] = q;
+        entry.z[j] = zt[e];
+      }
+    }
+    total = wave_sum(total);
+    if (lane == 0) part[2][wave] = total;
+    __syncthreads();
+    total = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) total += part[2][k];
+    const float coef = a.grad_scale * w, inv = 1.0f / s;
+    if (a.grad) {
+      const int shown = live != 0.0f ? a.V - first : 0;            // columns of the chunk that count
+      const int columns = int(min(a.ld - first, int64_t(kChunkColumns)));
+      const __amdgpu_buffer_rsrc_t out =
+          window(static_cast<char*>(a.grad) + (row * a.ld + first) * GS, int64_t(columns) * GS);
+#pragma unroll
+      for (int i = 0; i < 16 / E; ++i) {
+        const int c = (i * N + tid) * E;
+        float v[E] = {};
+        if (c < shown) {
+          unpack<ZB>(raw[i], v);
+#pragma unroll
+          for (int k = 0; k < E; ++k)
+            v[k] = c + k < shown ? coef * (exp2_fast((v[k] - m) * a.c) * inv) : 0.0f;
+        }
+        store_gradient<GB, E>(out, uint32_t(tid * E * GS), uint32_t(i * N * E * GS), v);
+      }
+    }
+    if (chunk == 0) {
+      float l = 0.0f;
+#pragma unroll
+      for (int e = 0; e < EPT; ++e)
+        if (id[e] >= 0) l += entry_loss(a, u[e], top, total, zt[e], m);
+      l = wave_sum(l);
+      if (lane == 0) part[3][wave] = l;
+    }
+    __syncthreads();
+    if (chunk == 0 && tid == 0) {
+      float l = 0.0f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) l += part[3][k];
+      a.loss[row] = live != 0.0f ? a.loss_scale * w * (l + (logf(s) - logf(total))) : 0.0f;
+    }
+    if (a.grad && live != 0.0f)
+      entry_gradients<N, GB>(a, row, entry, first, first + kChunkColumns, coef, m, s, total);
+    if (a.items > gridDim.x) __syncthreads();          // the LDS is written again
+  }
+}
+
+// --------------------------------------------------------------------------
+// rows in registers
+// --------------------------------------------------------------------------
+
+// The compiler may not keep what it made of r before, and compares n anew where it
+// is used (16 comparisons kept as masks fill the scalar registers).
+__device__ __forceinline__ void forget(u32x4_t& r) { asm volatile("" : "+v"(r)); }
+__device__ __forceinline__ int anew(int n) {
+  asm volatile("" : "+s"(n));
+  return n;
+}
+
+template <bool ZB, bool GB, int THREADS, int NV>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(4)))
+void distill_rows_kernel(DistillArgs a) {
   constexpr int E = kVec<ZB>, W = THREADS / 64, EPT = (kDistillMaxK + THREADS - 1) / THREADS;
   constexpr int kBlock = THREADS * E;                  // columns of one load instruction of all waves
   constexpr int ZS = ZB ? 2 : 4, GS = GB ? 2 : 4;
-  constexpr uint32_t kLow = ZB ? 0xff80ff80u : 0xff800000u;    // -infinity
   __shared__ __attribute__((aligned(16))) Entries entry;
   __shared__ float part[6][W];
   const int tid = threadIdx.x, wave = tid >> 6;
-  const uint32_t vz = uint32_t(tid * E * ZS), vg = uint32_t(tid * E * GS);
+  const uint32_t vz = uint32_t(tid * E * ZS);
   u32x4_t raw[NV];
   int id[EPT];
   float u[EPT], zt[EPT];
@@ -282,31 +396,26 @@ __global__ __launch_bounds__(THREADS) void distill_rows_kernel(DistillArgs a) {
   };
   // Blocks before `full` are whole, block `full` has `rest` columns or none.
   const int full = a.V / kBlock, rest = a.V - full * kBlock, blocks = full + (rest > 0);
-  // Its elements past V as -infinity.
-  auto cut = [&](u32x4_t& r) {
+  auto cut = [&](u32x4_t& r) { cut_vector<ZB>(r, rest - tid * E); };
+  // The entries' numbers, then what belongs to those within the vocabulary.
+  auto load_ids = [&](int64_t row, bool wanted, int64_t (&n)[EPT]) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if constexpr (ZB) {
-        const bool lo = tid * E + 2 * k >= rest, hi = tid * E + 2 * k + 1 >= rest;
-        r[k] = lo ? kLow : hi ? (r[k] & 0xffffu) | (kLow & 0xffff0000u) : r[k];
-      } else {
-        r[k] = tid * E + k >= rest ? kLow : r[k];
-      }
+    for (int e = 0; e < EPT; ++e) {
+      const int j = e * THREADS + tid;
+      n[e] = -1;
+      if (wanted && j < a.K) n[e] = entry_id(a, row * a.K + j);
     }
   };
-  auto load_entries_of = [&](int64_t row, int (&id)[EPT], float (&u)[EPT], float (&zt)[EPT]) {
+  auto load_logits = [&](int64_t row, const int64_t (&n)[EPT]) {
 #pragma unroll
     for (int e = 0; e < EPT; ++e) {
       const int j = e * THREADS + tid;
       id[e] = -1;
       u[e] = zt[e] = 0.0f;
-      if (j < a.K) {
-        const int64_t n = entry_id(a, row * a.K + j);
-        if (n >= 0 && n < a.V) {
-          u[e] = entry_logit(a, row * a.K + j);
-          zt[e] = student_logit<ZB>(a, row * a.ld + n);
-          if (u[e] != -INFINITY) id[e] = int(n);
-        }
+      if (n[e] >= 0 && n[e] < a.V) {
+        id[e] = int(n[e]);
+        u[e] = entry_logit(a, row * a.K + j);
+        zt[e] = student_logit<ZB>(a, row * a.ld + n[e]);
       }
     }
   };
@@ -326,13 +435,17 @@ __global__ __launch_bounds__(THREADS) void distill_rows_kernel(DistillArgs a) {
     const __amdgpu_buffer_rsrc_t r = row_window(row, w != 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) raw[i] = load(r, i);
-    if (w != 0.0f) load_entries_of(row, id, u, zt);
+    int64_t n[EPT];
+    load_ids(row, w != 0.0f, n);
+    load_logits(row, n);
   }
   for (; row < a.T; row += step) {
     const int64_t next = row + step;
     const float wn = next >= a.T ? 0.0f : a.weight ? a.weight[next] : 1.0f;
     const bool ahead = wn != 0.0f;                     // the next row is loaded meanwhile
     const __amdgpu_buffer_rsrc_t here = row_window(row, w != 0.0f), there = row_window(next, ahead);
+    int64_t ids[EPT];
+    load_ids(next, ahead, ids);
     // Block i of a row that is longer than what is held.
     auto streamed = [&](int i) {
       u32x4_t r = load(here, i);
@@ -350,19 +463,23 @@ __global__ __launch_bounds__(THREADS) void distill_rows_kernel(DistillArgs a) {
     int shown = w != 0.0f ? blocks : 0;                // blocks of the row that count
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (i == full) cut(raw[i]);
-      if (i < shown) most(raw[i]);
+      if (i == anew(full)) cut(raw[i]);
+      if (i < anew(shown)) most(raw[i]);
       forget(raw[i]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    for (int i = NV; i < shown; ++i) most(streamed(i));
-    if (w != 0.0f)
+    // Blocks that are not held: maximum and sum in one pass, as distill_loss_kernel.
+    float far_m = -INFINITY, far_s = 0.0f;
+    for (int i = NV; i < shown; ++i) running<ZB>(streamed(i), a.c, far_m, far_s);
+    m = fmaxf(m, far_m);
 #pragma unroll
-      for (int e = 0; e < EPT; ++e)
-        if (id[e] >= 0) {
-          top = fmaxf(top, u[e]);
-          some = true;
-        }
+    for (int e = 0; e < EPT; ++e) {
+      if (u[e] == -INFINITY) id[e] = -1;
+      if (id[e] >= 0) {
+        top = fmaxf(top, u[e]);
+        some = true;
+      }
+    }
     m = wave_max(m);
     top = wave_max(top);
     const bool any = __ballot(some) != 0;
@@ -386,21 +503,21 @@ __global__ __launch_bounds__(THREADS) void distill_rows_kernel(DistillArgs a) {
     };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (i < shown) sum(raw[i]);
+      if (i < anew(shown)) sum(raw[i]);
       forget(raw[i]);
-      if (!GRAD) raw[i] = load(there, i);
       __builtin_amdgcn_sched_barrier(0);
     }
-    for (int i = NV; i < shown; ++i) sum(streamed(i));
+    if (shown > NV) s += far_s * exp2_fast((far_m - m) * a.c);
     if (live)
 #pragma unroll
       for (int e = 0; e < EPT; ++e) {
         const int j = e * THREADS + tid;
         const float q = id[e] >= 0 ? exp2_fast((u[e] - top) * a.c) : 0.0f;
         total += q;
-        if (GRAD && j < (a.K + 3 & ~3)) {              // up to a multiple of 4
+        if (j < (a.K + 3 & ~3)) {              // up to a multiple of 4
           entry.id[j] = id[e];
           entry.q[j] = q;
+          entry.z[j] = zt[e];
         }
       }
     s = wave_sum(s);
@@ -416,90 +533,163 @@ __global__ __launch_bounds__(THREADS) void distill_rows_kernel(DistillArgs a) {
       float l = 0.0f;
 #pragma unroll
       for (int e = 0; e < EPT; ++e)
-        if (id[e] >= 0) {
-          const float du = u[e] - top, q = exp2_fast(du * a.c) / total;
-          if (q != 0.0f) l += q * (du * a.inv_tau - (zt[e] - m) * a.inv_tau);
-        }
+        if (id[e] >= 0) l += entry_loss(a, u[e], top, total, zt[e], m);
       l = wave_sum(l);
       if ((tid & 63) == 0) part[5][wave] = l;
     }
-    int nid[EPT];
-    float nu[EPT], nz[EPT];
-    if (ahead) load_entries_of(next, nid, nu, nz);
-    if constexpr (GRAD) {
-      const float coef = a.grad_scale * w, inv = 1.0f / s;
-      const __amdgpu_buffer_rsrc_t out =
-          window(static_cast<char*>(a.grad) + row * a.ld * GS, a.ld * GS);
-      auto emit = [&](const u32x4_t& r, int i) {
-        float v[E] = {};
-        if (i < shown) {
-          unpack<ZB>(r, v);
+    load_logits(next, ids);                            // this row's are in LDS
+    const float coef = a.grad_scale * w;
+    const float inv = 1.0f / s;
+    const __amdgpu_buffer_rsrc_t out =
+        window(static_cast<char*>(a.grad) + row * a.ld * GS, a.ld * GS);
+    auto emit = [&](const u32x4_t& r, int i) {
+      float v[E] = {};
+      if (i < anew(shown)) {
+        unpack<ZB>(r, v);
 #pragma unroll
-          for (int k = 0; k < E; ++k) v[k] = coef * (exp2_fast((v[k] - m) * a.c) * inv);
-          if (i == full)                               // zeros past V, whatever the sums are
-#pragma unroll
-            for (int k = 0; k < E; ++k) v[k] = tid * E + k >= rest ? 0.0f : v[k];
-        }
-        const uint32_t at = uint32_t(i * kBlock * GS);
-#pragma unroll
-        for (int k = 0; k < E; k += 4) {
-          const f32x4_t g = {v[k], v[k + 1], v[k + 2], v[k + 3]};
-          if constexpr (GB && E == 8) {
-            if (k == 0) {
-              const u32x2_t lo = pack_bf16x4(g), hi = pack_bf16x4(f32x4_t{v[4], v[5], v[6], v[7]});
-              store16(out, vg, at, u32x4_t{lo[0], lo[1], hi[0], hi[1]});
-            }
-          } else {
-            store4<GS>(out, vg + k * GS, at, g);
-          }
-        }
-      };
-      const int out_blocks = int((a.ld + kBlock - 1) / kBlock);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (i < out_blocks) emit(raw[i], i);
-        raw[i] = load(there, i);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int k = 0; k < E; ++k) v[k] = coef * (exp2_fast((v[k] - m) * a.c) * inv);
       }
-      for (int i = NV; i < out_blocks; ++i) emit(streamed(i), i);
+      store_gradient<GB, E>(out, uint32_t(tid * E * GS), uint32_t(i * kBlock * GS), v);
+    };
+    const int out_blocks = int((a.ld + kBlock - 1) / kBlock);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (i < anew(out_blocks)) emit(raw[i], i);
+      raw[i] = load(there, i);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    for (int i = NV; i < out_blocks; ++i) emit(streamed(i), i);
     __syncthreads();
     if (tid == 0)
       a.loss[row] = live ? a.loss_scale * w * (combine(part[5], add) + (logf(s) - logf(total))) : 0.0f;
-    if constexpr (GRAD) {
-      // The teacher's columns: the first entry of an id writes it.
-      if (live)
-#pragma unroll
-        for (int e = 0; e < EPT; ++e)
-          if (id[e] >= 0) {
-            const int j = e * THREADS + tid;
-            float q = 0.0f;
-            bool again = false;
-            for (int k = 0; k < a.K; k += 4) {
-              const i32x4_t ids = *reinterpret_cast<const i32x4_t*>(&entry.id[k]);
-              const f32x4_t qs = *reinterpret_cast<const f32x4_t*>(&entry.q[k]);
-#pragma unroll
-              for (int n = 0; n < 4; ++n)
-                if (ids[n] == id[e]) {
-                  again = again || k + n < j;
-                  q += qs[n];
-                }
-            }
-            if (!again) {
-              const float g = a.grad_scale * w * (exp2_fast((zt[e] - m) * a.c) / s - q / total);
-              if constexpr (GB)
-                static_cast<__bf16*>(a.grad)[row * a.ld + id[e]] = __bf16(g);
-              else
-                static_cast<float*>(a.grad)[row * a.ld + id[e]] = g;
-            }
-          }
+    if (live) {
+      entry_gradients<THREADS, GB>(a, row, entry, 0, a.V, coef, m, s, total);
+      // Columns past V of the last block that counts: 0 times a sum that is not finite is not 0.
+      const int64_t end = min(a.ld, int64_t(blocks) * kBlock);
+      for (int64_t c = a.V + tid; c < end; c += THREADS) {
+        if constexpr (GB)
+          static_cast<uint16_t*>(a.grad)[row * a.ld + c] = 0;
+        else
+          static_cast<float*>(a.grad)[row * a.ld + c] = 0.0f;
+      }
     }
     w = wn;
+  }
+}
+
+// --------------------------------------------------------------------------
+// the loss alone
+// --------------------------------------------------------------------------
+//
+// One pass over a row, each thread with a running maximum and a sum that is scaled
+// when the maximum moves, kVec elements at a time: nothing is held, so several
+// workgroups share a CU. Four loads are ahead of the four being added.
+constexpr int kLossThreads = 512;
+template <bool ZB>
+__global__ __launch_bounds__(kLossThreads) void distill_loss_kernel(DistillArgs a) {
+  constexpr int E = kVec<ZB>, W = kLossThreads / 64, EPT = kDistillMaxK / kLossThreads, U = 4;
+  constexpr int kBlock = kLossThreads * E, ZS = ZB ? 2 : 4;
+  __shared__ float part[6][W];
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const int full = a.V / kBlock, rest = a.V - full * kBlock, blocks = full + (rest > 0);
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    const float w = a.weight ? a.weight[row] : 1.0f;
+    if (w == 0.0f) {
+      if (tid == 0) a.loss[row] = 0.0f;
+      continue;
+    }
+    const __amdgpu_buffer_rsrc_t r =
+        window(static_cast<const char*>(a.z) + row * a.ld * ZS, int64_t(a.V + 7) / 8 * 8 * ZS);
+    u32x4_t raw[2][U];
+    auto load = [&](u32x4_t (&to)[U], int i) {         // past the row's end: zeros, not looked at
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        to[k] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+            r, tid * 16, (i + k) * kLossThreads * 16, kStatePolicy));
+    };
+    load(raw[0], 0);
+    int id[EPT];
+    float u[EPT], zt[EPT], top = -INFINITY;
+    bool some = false;
 #pragma unroll
     for (int e = 0; e < EPT; ++e) {
-      id[e] = nid[e];
-      u[e] = nu[e];
-      zt[e] = nz[e];
+      const int j = e * kLossThreads + tid;
+      id[e] = -1;
+      u[e] = zt[e] = 0.0f;
+      if (j < a.K) {
+        const int64_t n = entry_id(a, row * a.K + j);
+        if (n >= 0 && n < a.V) {
+          u[e] = entry_logit(a, row * a.K + j);
+          zt[e] = student_logit<ZB>(a, row * a.ld + n);
+          if (u[e] != -INFINITY) {
+            id[e] = int(n);
+            top = fmaxf(top, u[e]);
+            some = true;
+          }
+        }
+      }
+    }
+    float m = -INFINITY, s = 0.0f;
+    auto add = [&](u32x4_t v4, int i) {
+      if (i >= blocks) return;
+      if (i == full) cut_vector<ZB>(v4, rest - tid * E);
+      running<ZB>(v4, a.c, m, s);
+    };
+    for (int i = 0; i < blocks; i += 2 * U) {
+      load(raw[1], i + U);
+#pragma unroll
+      for (int k = 0; k < U; ++k) add(raw[0][k], i + k);
+      load(raw[0], i + 2 * U);
+#pragma unroll
+      for (int k = 0; k < U; ++k) add(raw[1][k], i + U + k);
+    }
+    // The waves' maxima and sums, then all of them.
+    const float mine = m;
+    m = wave_max(m);
+    s = wave_sum(s * exp2_fast((mine - finite_max(m)) * a.c));
+    top = wave_max(top);
+    const bool any = __ballot(some) != 0;
+    if ((tid & 63) == 0) {
+      part[0][wave] = m;
+      part[1][wave] = s;
+      part[2][wave] = top;
+      part[3][wave] = any ? 1.0f : 0.0f;
+    }
+    __syncthreads();
+    float live = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      m = fmaxf(m, part[0][k]);
+      top = fmaxf(top, part[2][k]);
+      live = fmaxf(live, part[3][k]);
+    }
+    m = finite_max(m);
+    top = finite_max(top);
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) s += part[1][k] * exp2_fast((part[0][k] - m) * a.c);
+    float total = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e)
+      if (id[e] >= 0) total += exp2_fast((u[e] - top) * a.c);
+    total = wave_sum(total);
+    if ((tid & 63) == 0) part[4][wave] = total;
+    __syncthreads();
+    total = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) total += part[4][k];
+    float l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e)
+      if (id[e] >= 0) l += entry_loss(a, u[e], top, total, zt[e], m);
+    l = wave_sum(l);
+    if ((tid & 63) == 0) part[5][wave] = l;
+    __syncthreads();
+    if (tid == 0) {
+      l = 0.0f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) l += part[5][k];
+      a.loss[row] = live != 0.0f ? a.loss_scale * w * (l + (logf(s) - logf(total))) : 0.0f;
     }
   }
 }

@@ -9,40 +9,61 @@
 namespace forge {
 namespace {
 
-static_assert(kDistillMaxK == FORGE_DISTILL_MAX_K && kDistillChunk == 32 * kDistillThreads,
+static_assert(kDistillMaxK == FORGE_DISTILL_MAX_K && kDistillChunk == kChunkColumns,
               "the kernels' sizes");
 
 // Most workgroups of a launch; what is beyond loops.
 constexpr int64_t kMaxGrid = int64_t(1) << 20;
 dim3 grid_for(int64_t items) { return dim3(uint32_t(std::min(items, kMaxGrid))); }
 
-template <bool ZB, bool GB, bool GRAD, int THREADS, int NV>
+template <bool ZB, bool GB, int THREADS, int NV>
 forge_status launch_rows_t(const DistillArgs& a, int per_cu, hipStream_t s) {
   const int64_t grid = int64_t(std::max(16, persistent_grid())) * per_cu;
-  hipLaunchKernelGGL((distill_rows_kernel<ZB, GB, GRAD, THREADS, NV>), dim3(uint32_t(std::min(grid, a.T))),
+  hipLaunchKernelGGL((distill_rows_kernel<ZB, GB, THREADS, NV>), dim3(uint32_t(std::min(grid, a.T))),
                      dim3(THREADS), 0, s, a);
   return launch_status();
 }
 
-template <bool ZB, bool GB, bool GRAD>
+template <bool ZB, bool GB>
 forge_status launch_rows(const DistillArgs& a, hipStream_t s) {
   constexpr int E = kVec<ZB>;
-  if (a.V <= 256 * 4 * E) return launch_rows_t<ZB, GB, GRAD, 256, 4>(a, 8, s);
-  if (a.V <= 256 * 16 * E) return launch_rows_t<ZB, GB, GRAD, 256, 16>(a, 4, s);
-  if (a.V <= 512 * 16 * E) return launch_rows_t<ZB, GB, GRAD, 512, 16>(a, 2, s);
-  return launch_rows_t<ZB, GB, GRAD, 1024, 16>(a, 1, s);
+  if (a.V <= 256 * 4 * E) return launch_rows_t<ZB, GB, 256, 4>(a, 5, s);
+  if (a.V <= 512 * 8 * E) return launch_rows_t<ZB, GB, 512, 8>(a, 2, s);
+  if (a.V <= 512 * 16 * E) return launch_rows_t<ZB, GB, 512, 16>(a, 2, s);
+  return launch_rows_t<ZB, GB, 1024, 16>(a, 1, s);
 }
 
 template <bool ZB, bool GB>
-forge_status launch(DistillArgs a, hipStream_t s) {
-  if (a.T >= 256) return a.grad ? launch_rows<ZB, GB, true>(a, s) : launch_rows<ZB, false, false>(a, s);
+forge_status launch_chunks(DistillArgs a, hipStream_t s) {
   a.items = a.T * a.chunks;
   if (a.items > 0 && a.K > 0) {
-    hipLaunchKernelGGL((distill_stats_kernel<ZB>), grid_for(a.items), dim3(kDistillThreads), 0, s, a);
+    hipLaunchKernelGGL((distill_stats_kernel<ZB>), grid_for(a.items), dim3(kChunkThreads), 0, s, a);
     if (forge_status st = launch_status()) return st;
   }
   a.items = a.T * a.chunks_out;
-  hipLaunchKernelGGL((distill_gradient_kernel<ZB, GB>), grid_for(a.items), dim3(kDistillThreads), 0, s, a);
+  hipLaunchKernelGGL((distill_gradient_kernel<ZB, GB>), grid_for(a.items), dim3(kChunkThreads), 0, s, a);
+  return launch_status();
+}
+
+// A row to a workgroup, or chunks of it. Chunks take a launch more (3 us) and read
+// the logits twice, but a workgroup takes 5 us and one more for each 7000 columns
+// with a row (for each 3500 where it does not hold it), however few there are: bf16 8 x
+// 128256 8.8 us in chunks and 22 by rows, 64 x 128256 18 and 23, 128 x 128256 30 and 24,
+// 64 x 32000 9.8 and 10.0, 8 x 8192 8.4 and 6.1; float32 128 x 128256 (not held) 39 and 50,
+// 256 x 128256 70 and 54. The loss alone: 8 x 128256 7.3 us in chunks and 10.7 by rows, 64
+// x 128256 11.0 and 11.4, 8 x 60000 7.3 and 7.0.
+template <bool ZB>
+bool few_rows(const DistillArgs& a) {
+  if (!a.grad) return a.V > 65536 && a.T <= 64;
+  return a.V > 16384 && a.T <= (a.V <= 1024 * 16 * kVec<ZB> ? 64 : 192);
+}
+
+template <bool ZB, bool GB>
+forge_status launch(const DistillArgs& a, hipStream_t s) {
+  if (few_rows<ZB>(a)) return launch_chunks<ZB, GB>(a, s);
+  if (a.grad) return launch_rows<ZB, GB>(a, s);
+  const int64_t grid = int64_t(std::max(16, persistent_grid())) * 3;
+  hipLaunchKernelGGL((distill_loss_kernel<ZB>), dim3(uint32_t(std::min(grid, a.T))), dim3(kLossThreads), 0, s, a);
   return launch_status();
 }
 

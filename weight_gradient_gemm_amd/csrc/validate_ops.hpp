@@ -74,7 +74,7 @@ forge_status validate_layernorm_backward(const void* dY, forge_dtype y_dtype, co
                                          int64_t workspace_bytes);
 
 // Columns of a chunk of a row of logits, which one workgroup goes through.
-constexpr int64_t kDistillChunk = 8192;
+constexpr int64_t kDistillChunk = 4096;
 // Byte offsets of the parts of distillation's workspace: each chunk's maximum
 // and sum of exponentials, and the student's logits of the teacher's ids.
 struct DistillWorkspace {
