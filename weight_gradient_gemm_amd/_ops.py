@@ -648,14 +648,12 @@ class _Fp8BlockHeld(ForgeFp8Block):
     when asked for."""
 
     def __init__(self, rows, k, fmt, device):
-        torch = _torch()
+        torch = _TORCH or _torch()
         self.fmt, self.code = fmt, _fp8_format(fmt)
-        self.rows, self.k = int(rows), (int(k) + 127) // 128 * 128
-        # Scales lie 16 bytes on at least: rows * k is a multiple of 128.
-        n = self.rows * self.k
-        self._hold = t = torch.empty(n + self.k // 128 * ((self.rows + 127) // 128 * 128),
-                                     dtype=torch.uint8, device="cuda" if device is None else device)
-        self._storage = t.untyped_storage()
+        self.rows, self.k = rows, k = int(rows), (int(k) + 127) // 128 * 128
+        n = rows * k                             # a multiple of 128: scales are aligned as codes are
+        self._hold = t = torch.empty(n + k // 128 * ((rows + 127) // 128 * 128), dtype=torch.uint8,
+                                     device=torch.cuda.current_device() if device is None else device)
         self.device = t.get_device()
         p = t.data_ptr()
         self.ptrs = (p, p + n) if n else (None, None)

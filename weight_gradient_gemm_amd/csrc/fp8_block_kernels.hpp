@@ -78,8 +78,9 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
 __device__ __forceinline__ int fp8_scale_place(int r) { return (r & 31) * 4 + (r >> 5); }
 
 // A tile of 128 x 128 values to a workgroup: thread (j, t) holds rows 8 t .. 8 t + 7
-// of columns 8 j .. 8 j + 7, so that eight codes on end of either operand are its
-// own. They pass through LDS on the way out, 64 bytes of a row (or column) in
+// of eight columns, bf16 8 j .. 8 j + 7, float32 4 j .. 4 j + 3 of each half (so that a
+// load instruction's 16 lanes are on end), and so eight codes on end of the
+// operand along columns, eight or twice four of that along rows. They pass through LDS on the way out, 64 bytes of a row (or column) in
 // each half of the tile, and leave as whole lines. Row q of a half is kept at
 // q ^ (q / 8 mod 4) and its 16-byte chunk c at c ^ (q / 32), which spreads one
 // write instruction's rows over all banks.
@@ -94,6 +95,7 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
   const int tid = threadIdx.x, j = tid & 15, t = tid >> 4, wave = tid >> 6;
   const uint32_t tr = blockIdx.x / a.tiles_c, tc = blockIdx.x - tr * a.tiles_c;
   const int64_t r0 = int64_t(tr) * kFp8Tile, c0 = int64_t(tc) * kFp8Tile;
+  auto column = [&](int k) { return BF16 ? 8 * j + k : (k >> 2) * 64 + 4 * j + (k & 3); };
   float v[8][8];
   uint32_t top[8] = {};                          // of columns
   uint32_t row_top[8];
@@ -103,11 +105,12 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
     u32x4_t raw[NW / 4];
 #pragma unroll
     for (int k = 0; k < NW / 4; ++k) raw[k] = u32x4_t{0u, 0u, 0u, 0u};
-    if (row < a.R && c0 + 8 * j < a.C) {
-      const char* p = static_cast<const char*>(a.x) + (row * a.C + c0 + 8 * j) * (BF16 ? 2 : 4);
 #pragma unroll
-      for (int k = 0; k < NW / 4; ++k)
-        raw[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p) + k);
+    for (int k = 0; k < NW / 4; ++k) {
+      const int64_t c = c0 + column(4 * k);
+      if (row < a.R && c < a.C)
+        raw[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(
+            static_cast<const char*>(a.x) + (row * a.C + c) * (BF16 ? 2 : 4)));
     }
     row_top[i] = 0;
 #pragma unroll
@@ -143,12 +146,12 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
       }
       if ((tid & 63) < 16)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) col_top[wave][8 * j + k] = top[k];
+        for (int k = 0; k < 8; ++k) col_top[wave][column(k)] = top[k];
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        top[k] = max(max(col_top[0][8 * j + k], col_top[1][8 * j + k]),
-                     max(col_top[2][8 * j + k], col_top[3][8 * j + k]));
+        top[k] = max(max(col_top[0][column(k)], col_top[1][column(k)]),
+                     max(col_top[2][column(k)], col_top[3][column(k)]));
     }
   }
   auto place = [](int half, int q, int byte) {
@@ -163,14 +166,19 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
       const float lo[4] = {v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f};
       const float hi[4] = {v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f};
       const uint32_t w0 = s == 255u ? 0u : fp8_codes4<E5M2>(lo), w1 = s == 255u ? 0u : fp8_codes4<E5M2>(hi);
-      *reinterpret_cast<u32x2_t*>(out_r + place(j >> 3, r, (j & 7) * 8)) = u32x2_t{w0, w1};
+      if constexpr (BF16) {
+        *reinterpret_cast<u32x2_t*>(out_r + place(j >> 3, r, (j & 7) * 8)) = u32x2_t{w0, w1};
+      } else {
+        *reinterpret_cast<uint32_t*>(out_r + place(0, r, 4 * j)) = w0;
+        *reinterpret_cast<uint32_t*>(out_r + place(1, r, 4 * j)) = w1;
+      }
       if (j == 0) a.row_scales[tc * a.row_pitch + r0 + fp8_scale_place(r)] = r0 + r < a.R ? uint8_t(s) : 0;
     }
   }
   if constexpr (COLS) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int c = 8 * j + k;
+      const int c = column(k);
       const uint32_t s = fp8_scale_byte<E5M2>(top[k]);
       const float f = fp8_factor(s);
       const float lo[4] = {v[0][k] * f, v[1][k] * f, v[2][k] * f, v[3][k] * f};
