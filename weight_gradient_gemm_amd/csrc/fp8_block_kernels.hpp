@@ -90,6 +90,7 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
   __shared__ __attribute__((aligned(16))) uint8_t out[(ROWS ? 16384 : 0) + (COLS ? 16384 : 0)];
   __shared__ uint32_t col_top[4][kFp8Tile];
   __shared__ uint32_t all_top[4];
+  __shared__ __attribute__((aligned(4))) uint8_t scales[2][kFp8Tile];
   uint8_t* const out_r = out;
   uint8_t* const out_c = out + (ROWS ? 16384 : 0);
   const int tid = threadIdx.x, j = tid & 15, t = tid >> 4, wave = tid >> 6;
@@ -172,7 +173,7 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
         *reinterpret_cast<uint32_t*>(out_r + place(0, r, 4 * j)) = w0;
         *reinterpret_cast<uint32_t*>(out_r + place(1, r, 4 * j)) = w1;
       }
-      if (j == 0) a.row_scales[tc * a.row_pitch + r0 + fp8_scale_place(r)] = r0 + r < a.R ? uint8_t(s) : 0;
+      if (j == 0) scales[0][fp8_scale_place(r)] = r0 + r < a.R ? uint8_t(s) : 0;
     }
   }
   if constexpr (COLS) {
@@ -185,10 +186,18 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
       const float hi[4] = {v[4][k] * f, v[5][k] * f, v[6][k] * f, v[7][k] * f};
       const uint32_t w0 = s == 255u ? 0u : fp8_codes4<E5M2>(lo), w1 = s == 255u ? 0u : fp8_codes4<E5M2>(hi);
       *reinterpret_cast<u32x2_t*>(out_c + place(t >> 3, c, (t & 7) * 8)) = u32x2_t{w0, w1};
-      if (t == 0) a.col_scales[tr * a.col_pitch + c0 + fp8_scale_place(c)] = c0 + c < a.C ? uint8_t(s) : 0;
+      if (t == 0) scales[1][fp8_scale_place(c)] = c0 + c < a.C ? uint8_t(s) : 0;
     }
   }
   __syncthreads();
+  if (tid < kFp8Tile / 4) {
+    if constexpr (ROWS)
+      *reinterpret_cast<uint32_t*>(a.row_scales + tc * a.row_pitch + r0 + 4 * tid) =
+          *reinterpret_cast<const uint32_t*>(&scales[0][4 * tid]);
+    if constexpr (COLS)
+      *reinterpret_cast<uint32_t*>(a.col_scales + tr * a.col_pitch + c0 + 4 * tid) =
+          *reinterpret_cast<const uint32_t*>(&scales[1][4 * tid]);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int n = i * 256 + tid, half = n >> 9, q = (n >> 2) & 127, byte = (n & 3) * 16;
