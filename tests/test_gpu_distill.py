@@ -62,8 +62,10 @@ def reference(torch, z, u, ids, weight, V, tau, scale, gt):
         grad[:, :V] = torch.where(live[:, None], c * (p - target), 0)
         # An exponential is off by 2 U (the instruction) and by its argument's error: the
         # difference to the maximum, its product with a rounded constant, 4 U of it.
-        # A sum adds at most 32 terms of a thread, 10 steps of a workgroup and the
-        # chunks one after the other (all rounded: 60 U); the teacher's as well.
+        # A thread adds up to V / 512 terms of one sign one after the other (the loss
+        # alone, 256 here), each addition off by up to U of what it has so far: on average
+        # half of the sum and of random sign, 0.6 sqrt(256) = 10 U of the sum as a root mean
+        # square, and threads' errors differ. 60 U are asked for; the teacher's as well.
         gap = (zz.amax(1, keepdim=True) - zz).clamp(max=1e30)
         gapu = torch.where(kept, (torch.where(kept, u64, -INF).amax(1, keepdim=True) - u64) / tau, 0)
         e_sum = (60 + 4 * (p * gap).sum(1, keepdim=True)) * U
@@ -135,6 +137,15 @@ def test_types(env, T, V, K, tau, zt, gt, ut, it):
     check(torch, wg, inputs(torch, T, V, K, zt, ut, it, seed=V), gt, tau, scale=1.0 / T)
 
 
+# Every thread of either path with all the entries it can have.
+@pytest.mark.parametrize("zt", list(HALF))
+@pytest.mark.parametrize("T,V,K", [(2, 40000, 1024), (3, 200001, 1000), (1, 17000, 1023), (70, 40000, 1024),
+                                   (70, 5000, 769), (200, 140000, 1022)])
+def test_the_most_entries(env, T, V, K, zt):
+    torch, wg = env
+    check(torch, wg, inputs(torch, T, V, K, zt, "bfloat16", "int32", seed=14), "bfloat16", 1.5, 0.5)
+
+
 @pytest.mark.parametrize("zt", list(HALF))
 @pytest.mark.parametrize("T,V,K", [(5, 1003, 17), (3, 20000, 40), (290, 9001, 5), (270, 131072, 9),
                                    (300, 70001, 3), (2, 140000, 20)])
@@ -168,6 +179,46 @@ def test_padded_columns(env):
         for T in (3, 400):
             _, grad = check(torch, wg, inputs(torch, T, V, 9, "bfloat16", ld=ld), "bfloat16")
             assert (grad[:, V:] == 0).all()
+
+
+@pytest.mark.parametrize("zt,gt", [("bfloat16", "bfloat16"), ("float32", "bfloat16"), ("float32", "float32")])
+@pytest.mark.parametrize("V,ld", [(17000, 40000), (20480, 24576), (20481, 20488), (33000, 33016), (70001, 100000)])
+def test_padded_columns_of_few_rows(env, V, ld, zt, gt):
+    """Chunks that lie past the vocabulary, in part or as a whole; into the logits too."""
+    torch, wg = env
+    args = inputs(torch, 3, V, 9, zt, ld=ld, seed=4)
+    _, grad = check(torch, wg, args, gt)
+    assert (grad[:, V:] == 0).all()
+    if zt == gt:
+        check(torch, wg, args, gt, in_place=True)
+
+
+@pytest.mark.parametrize("T", [8, 70])
+def test_rows_of_a_large_vocabulary_left_out_or_masked(env, T):
+    """The loss alone too is cut into chunks, or not, at this vocabulary."""
+    torch, wg = env
+    z, u, ids, weight, V = inputs(torch, T, 70000, 10, masked=False)
+    weight[0] = 0
+    ids[1] = -1
+    u[2] = -INF
+    z[0, 5] = NAN
+    z[1] = INF
+    z[2] = -INF
+    keep = z.gather(1, ids.clamp(min=0))
+    z[3, : V // 2] = -INF
+    z[4, 100:] = -INF
+    z[5] = torch.finfo(torch.float32).min
+    z.scatter_(1, ids.clamp(min=0), keep)
+    ids[6, 1:] = ids[6, 0]
+    u[6, 2:] = -INF
+    loss, grad = check(torch, wg, (z, u, ids, weight, V))
+    assert (loss[:3] == 0).all() and (grad[:3] == 0).all() and torch.isfinite(loss).all()
+    loss, grad = torch.full((T,), 5.0, device="cuda"), torch.full((T, V), 5.0, device="cuda")
+    none = u[:, :0].contiguous(), ids[:, :0].contiguous()
+    wg.forge_distill(z, *none, loss, grad, weight=weight)
+    assert (loss == 0).all() and (grad == 0).all()
+    wg.forge_distill(z, *none, loss.fill_(5.0), weight=weight)
+    assert (loss == 0).all()
 
 
 @pytest.mark.parametrize("T", [4, 300])
