@@ -8,9 +8,18 @@
 // Bound by HBM: the logits are read and the gradient is written. Of many rows a
 // workgroup takes one after the other and holds it in registers, 16 vectors of 16
 // bytes to a thread (a row of 128256 bf16 logits is 250 KB, a CU's registers hold
-// 512), so that it is read once. Few rows are cut into chunks, a workgroup each:
-// one launch forms each chunk's maximum and sum of exponentials, a second joins
-// them and forms the gradient.
+// 512), so that it is read once, and the next row's vectors are requested as this
+// one's leave. What is beyond the registers (65536 float32 columns) is read again for
+// the gradient. Few rows are cut into chunks, a workgroup each: one launch forms
+// each chunk's maximum and sum of exponentials, a second joins them and forms the
+// gradient. The loss alone goes once through a row and holds nothing.
+//
+// Measured: 4096 x 128256 bf16, a row in 8 left out, 433 us for 1.97 GB, 4.5 TB/s (a
+// copy reaches 4.8); 1021 x 32003 float32 with a bf16 gradient 44 us, 4.1 TB/s;
+// 1024 x 128256 float32, not held whole, 214 us for the 1.05 GB that it cannot do without
+// and 0.26 again; the loss of 511 x 50021 float32 17 us, 5.3 TB/s; 8 x 128256 bf16 9.0 us, two
+// launches that wait for memory two and one time. A row read twice by the same grid, the
+// maximum first, took 1642 us for the first of these.
 //
 // The teacher's columns are written with the others and once more, with their q,
 // behind a barrier: the workgroup that has the column does both.
@@ -19,6 +28,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "row_io.hpp"
 
@@ -138,7 +148,7 @@ __device__ __forceinline__ void entry_gradients(const DistillArgs& a, int64_t ro
     const int id = j < a.K ? e.id[j] : -1;
     const bool mine = id >= lo && id < hi;
     float q = 0.0f;
-    int again = 0;
+    uint32_t again = 0;
     if (mine)
       for (int k = 4 * sub; k < a.K; k += 4 << share) {
         const i32x4_t ids = *reinterpret_cast<const i32x4_t*>(&e.id[k]);
@@ -146,14 +156,19 @@ __device__ __forceinline__ void entry_gradients(const DistillArgs& a, int64_t ro
 #pragma unroll
         for (int n = 0; n < 4; ++n)
           if (ids[n] == id) {
-            again |= int(k + n < j);
+            again |= uint32_t(k + n < j);
             q += qs[n];
           }
       }
-    for (int d = 1; d < 1 << share; d <<= 1) {
-      q += __shfl_xor(q, d);
-      again |= __shfl_xor(again, d);
-    }
+    // As row16_all, over the entry's threads.
+    auto join = [&](auto ctrl) {
+      q += lanes_dpp<decltype(ctrl)::value>(q);
+      again |= lanes_dpp<decltype(ctrl)::value>(again);
+    };
+    if (share > 0) join(std::integral_constant<int, 0xB1>{});
+    if (share > 1) join(std::integral_constant<int, 0x4E>{});
+    if (share > 2) join(std::integral_constant<int, 0x141>{});
+    if (share > 3) join(std::integral_constant<int, 0x140>{});
     if (mine && sub == 0 && !again) {
       const float g = coef * (exp2_fast((e.z[j] - m) * a.c) / s - q / total);
       if constexpr (GB)
@@ -177,7 +192,12 @@ __device__ __forceinline__ float entry_loss(const DistillArgs& a, float u, float
 constexpr int kChunkThreads = 256;
 constexpr int kChunkColumns = 16 * kChunkThreads;
 
-// The chunk's vectors of a thread, columns past V as -infinity.
+// Whether loads go out before it is known that the row counts (its weight is not 0): at
+// most a workgroup to a CU, so that latency is all there is. More of them wait for the
+// weight and read no row of weight 0.
+__device__ __forceinline__ bool eager(const DistillArgs& a) { return a.items <= 256; }
+
+// The chunk's vectors of a thread, zeros past the row's end.
 template <bool ZB>
 __device__ __forceinline__ void load_chunk(const DistillArgs& a, int64_t row, int first,
                                            u32x4_t (&raw)[16 / kVec<ZB>]) {
@@ -189,11 +209,68 @@ __device__ __forceinline__ void load_chunk(const DistillArgs& a, int64_t row, in
   for (int i = 0; i < 16 / E; ++i)
     raw[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
         r, int(threadIdx.x) * 16, i * kChunkThreads * 16, 0));
+}
+
+// Columns past V as -infinity.
+template <bool ZB>
+__device__ __forceinline__ void cut_chunk(const DistillArgs& a, int first, u32x4_t (&raw)[16 / kVec<ZB>]) {
+  constexpr int E = kVec<ZB>;
   if (first + kChunkColumns > a.V)
 #pragma unroll
     for (int i = 0; i < 16 / E; ++i)
       cut_vector<ZB>(raw[i], a.V - first - (i * kChunkThreads + int(threadIdx.x)) * E);
 }
+
+// What a thread loads of its entries, as it lies in memory: halves of the ids and of the
+// teacher's logits, by the same instructions for either type. No load waits for another
+// one, nor for the side of a branch that was not taken.
+constexpr int kChunkEntries = kDistillMaxK / kChunkThreads;
+struct EntryWords {
+  uint32_t lo[kChunkEntries], hi[kChunkEntries], u0[kChunkEntries], u1[kChunkEntries];
+
+  __device__ __forceinline__ void load_ids(const DistillArgs& a, int64_t row, bool look) {
+    const int K = look ? a.K : 0, wide = a.wide_ids;
+    const uint32_t* const p = static_cast<const uint32_t*>(a.ids) + (row * a.K << wide);
+#pragma unroll
+    for (int e = 0; e < kChunkEntries; ++e) {
+      const int j = e * kChunkThreads + int(threadIdx.x);
+      lo[e] = hi[e] = ~0u;
+      if (j < K) {
+        lo[e] = p[j << wide];
+        hi[e] = p[(j << wide) + wide];               // the same word again where there is one
+      }
+    }
+  }
+  __device__ __forceinline__ void load_logits(const DistillArgs& a, int64_t row, bool look) {
+    const int K = look ? a.K : 0, wide = !a.teacher_bf16;
+    const uint16_t* const p = static_cast<const uint16_t*>(a.teacher) + (row * a.K << wide);
+#pragma unroll
+    for (int e = 0; e < kChunkEntries; ++e) {
+      const int j = e * kChunkThreads + int(threadIdx.x);
+      u0[e] = u1[e] = 0;
+      if (j < K) {
+        u0[e] = p[j << wide];
+        u1[e] = p[(j << wide) + wide];
+      }
+    }
+  }
+  // The compiler may not look into the words before this point.
+  __device__ __forceinline__ void arrived_ids() {
+#pragma unroll
+    for (int e = 0; e < kChunkEntries; ++e) asm volatile("" : "+v"(lo[e]), "+v"(hi[e]));
+  }
+  __device__ __forceinline__ void arrived_logits() {
+#pragma unroll
+    for (int e = 0; e < kChunkEntries; ++e) asm volatile("" : "+v"(u0[e]), "+v"(u1[e]));
+  }
+  // The column, -1 where there is none. V is below 2^31.
+  __device__ __forceinline__ int id(const DistillArgs& a, int e) const {
+    return (!a.wide_ids || hi[e] == 0) && lo[e] < uint32_t(a.V) ? int(lo[e]) : -1;
+  }
+  __device__ __forceinline__ float logit(const DistillArgs& a, int e) const {
+    return __builtin_bit_cast(float, u1[e] << 16 | (a.teacher_bf16 ? 0u : u0[e]));
+  }
+};
 
 template <bool ZB>
 __global__ __launch_bounds__(kChunkThreads) void distill_stats_kernel(DistillArgs a) {
@@ -202,14 +279,25 @@ __global__ __launch_bounds__(kChunkThreads) void distill_stats_kernel(DistillArg
   for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
     const int64_t row = item / a.chunks;
     const int first = int(item - row * a.chunks) * kChunkColumns;
-    if (a.weight && a.weight[row] == 0.0f) continue;
+    if (!eager(a) && a.weight && a.weight[row] == 0.0f) continue;
+    EntryWords words;
+    words.load_ids(a, row, true);
     u32x4_t raw[16 / E];
     load_chunk<ZB>(a, row, first, raw);
-    for (int j = threadIdx.x; j < a.K; j += kChunkThreads) {
-      const int64_t id = entry_id(a, row * a.K + j);
-      if (id >= first && id < first + kChunkColumns && id < a.V)
-        a.logit[row * a.K + j] = student_logit<ZB>(a, row * a.ld + id);
+    words.arrived_ids();
+    int id[kChunkEntries];                             // of entries in this chunk
+    uint32_t zt[kChunkEntries];
+#pragma unroll
+    for (int e = 0; e < kChunkEntries; ++e) {
+      id[e] = words.id(a, e);
+      if (id[e] < first || id[e] >= first + kChunkColumns) id[e] = -1;
+      zt[e] = 0;
+      if (id[e] >= 0) {
+        const int64_t at = row * a.ld + id[e];
+        zt[e] = ZB ? static_cast<const uint16_t*>(a.z)[at] : static_cast<const uint32_t*>(a.z)[at];
+      }
     }
+    cut_chunk<ZB>(a, first, raw);
     float m = -INFINITY, s = 0.0f, v[E];
 #pragma unroll
     for (int i = 0; i < 16 / E; ++i) {
@@ -224,6 +312,13 @@ __global__ __launch_bounds__(kChunkThreads) void distill_stats_kernel(DistillArg
       unpack<ZB>(raw[i], v);
 #pragma unroll
       for (int k = 0; k < E; ++k) s += exp2_fast((v[k] - mf) * a.c);
+    }
+#pragma unroll
+    for (int e = 0; e < kChunkEntries; ++e) {
+      asm volatile("" : "+v"(zt[e]));                  // not looked into before
+      if (id[e] >= 0)
+        a.logit[row * a.K + e * kChunkThreads + int(threadIdx.x)] =
+            __builtin_bit_cast(float, ZB ? zt[e] << 16 : zt[e]);
     }
     s = wave_sum(s);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = make_float2(m, s);
@@ -243,50 +338,56 @@ __global__ __launch_bounds__(kChunkThreads) void distill_stats_kernel(DistillArg
 
 template <bool ZB, bool GB>
 __global__ __launch_bounds__(kChunkThreads) void distill_gradient_kernel(DistillArgs a) {
-  constexpr int E = kVec<ZB>, N = kChunkThreads, W = N / 64, EPT = kDistillMaxK / N, GS = GB ? 2 : 4;
+  constexpr int E = kVec<ZB>, N = kChunkThreads, W = N / 64, EPT = kChunkEntries, GS = GB ? 2 : 4;
   __shared__ __attribute__((aligned(16))) Entries entry;
   __shared__ float part[4][W];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
     const int64_t row = item / a.chunks_out;
     const int chunk = int(item - row * a.chunks_out), first = chunk * kChunkColumns;
-    const float w = a.weight ? a.weight[row] : 1.0f;
+    float w = 1.0f;
+    if (!eager(a) && a.weight) w = a.weight[row];
+    const bool look = eager(a) || w != 0.0f;
     u32x4_t raw[16 / E];
-    if (w != 0.0f && a.grad) load_chunk<ZB>(a, row, first, raw);
-    // Entries: each wave's largest and sum, joined behind the barrier.
+    if (look && a.grad) load_chunk<ZB>(a, row, first, raw);
+    EntryWords words;
+    words.load_ids(a, row, look);
+    words.load_logits(a, row, look);
     int id[EPT];
     float u[EPT], zt[EPT], top = -INFINITY, total = 0.0f;
 #pragma unroll
     for (int e = 0; e < EPT; ++e) {
       const int j = e * N + tid;
-      id[e] = -1;
-      u[e] = zt[e] = 0.0f;
-      if (j < a.K && w != 0.0f) {
-        const int64_t n = entry_id(a, row * a.K + j);
-        if (n >= 0 && n < a.V) {
-          u[e] = entry_logit(a, row * a.K + j);
-          zt[e] = a.logit[row * a.K + j];
-          if (u[e] != -INFINITY) {
-            id[e] = int(n);
-            top = fmaxf(top, u[e]);
-          }
-        }
-      }
+      zt[e] = j < a.K && look ? a.logit[row * a.K + j] : 0.0f;     // means nothing where there is no id
     }
+    if (eager(a) && a.weight) w = a.weight[row];
     // The row's maximum and sum from its chunks', by each wave for itself.
     float m = -INFINITY, s = 0.0f;
-    if (w != 0.0f) {
-      for (int k = lane; k < a.chunks; k += 64) m = fmaxf(m, a.stats[row * a.chunks + k].x);
-      m = finite_max(wave_max(m));
+    if (look) {
       for (int k = lane; k < a.chunks; k += 64) {
         const float2 st = a.stats[row * a.chunks + k];
-        s += st.y * exp2_fast((st.x - m) * a.c);
+        const float most = fmaxf(m, st.x), mf = finite_max(most);
+        s = s * exp2_fast((m - mf) * a.c) + st.y * exp2_fast((st.x - mf) * a.c);
+        m = most;
       }
-      s = wave_sum(s);
+      const float mine = m;
+      m = finite_max(wave_max(m));
+      s = wave_sum(s * exp2_fast((mine - m) * a.c));
+    }
+    // Entries: each wave's largest and sum, joined behind the barrier.
+    words.arrived_ids();
+    words.arrived_logits();
+#pragma unroll
+    for (int e = 0; e < EPT; ++e) {
+      id[e] = w != 0.0f ? words.id(a, e) : -1;
+      u[e] = words.logit(a, e);
+      if (u[e] == -INFINITY) id[e] = -1;
+      if (id[e] >= 0) top = fmaxf(top, u[e]);
     }
     bool some = false;
 #pragma unroll
     for (int e = 0; e < EPT; ++e) some = some || id[e] >= 0;
+    if (look && a.grad) cut_chunk<ZB>(a, first, raw);
     top = wave_max(top);
     const bool any = __ballot(some) != 0;
     if (lane == 0) {

@@ -9,9 +9,8 @@
 // distance of 32 share a word: a lane's rows of a wave's tile.
 #pragma once
 
-#include <type_traits>
-
 #include "mxfp4_kernels.hpp"
+#include "row_io.hpp"
 
 namespace forge {
 
@@ -61,29 +60,24 @@ __device__ __forceinline__ uint32_t fp8_codes4(const float (&v)[4]) {
   return uint32_t(r);
 }
 
-// Largest of v over the 16 lanes of a row of lanes, in each of them.
-__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
-  auto step = [&](auto ctrl) {
-    const uint32_t o = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), decltype(ctrl)::value, 0xf, 0xf, true));
-    v = max(v, o);
-  };
-  step(std::integral_constant<int, 0xB1>{});     // lane ^ 1
-  step(std::integral_constant<int, 0x4E>{});     // lane ^ 2
-  step(std::integral_constant<int, 0x141>{});    // mirrored within 8
-  step(std::integral_constant<int, 0x140>{});    // mirrored within 16
-  return v;
-}
+struct Larger {
+  __device__ __forceinline__ uint32_t operator()(uint32_t x, uint32_t y) const { return max(x, y); }
+};
 
 // Byte of row r's scale among its 128.
 __device__ __forceinline__ int fp8_scale_place(int r) { return (r & 31) * 4 + (r >> 5); }
 
 // A tile of 128 x 128 values to a workgroup: thread (j, t) holds rows 8 t .. 8 t + 7
 // of eight columns, bf16 8 j .. 8 j + 7, float32 4 j .. 4 j + 3 of each half (so that a
-// load instruction's 16 lanes are on end), and so eight codes on end of the
-// operand along columns, eight or twice four of that along rows. They pass through LDS on the way out, 64 bytes of a row (or column) in
-// each half of the tile, and leave as whole lines. Row q of a half is kept at
-// q ^ (q / 8 mod 4) and its 16-byte chunk c at c ^ (q / 32), which spreads one
-// write instruction's rows over all banks.
+// load instruction's 16 lanes are on end: 8192 x 14336 by columns 97 us, 112 with
+// 8 columns on end). So it has eight codes on end of the operand along columns, and
+// eight or twice four of that along rows. They pass through LDS on the way out, 64
+// bytes of a row (or column) in each half of the tile, and leave as whole lines. Row q
+// of a half is kept at q ^ (q / 8 mod 4) and its 16-byte chunk c at c ^ (q / 32),
+// which spreads one write instruction's rows over all banks.
+//
+// Bound by HBM: 8192 x 14336 takes, from bf16, 71 us by rows, 61 by columns (5.8 TB/s)
+// and 97 for both, which is 4.8 TB/s, a copy's rate; from float32 102, 97 and 138.
 template <bool BF16, bool E5M2, bool ROWS, bool COLS>
 __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp8QuantArgs a) {
   constexpr int NW = BF16 ? 4 : 8;               // words of 8 values
@@ -128,8 +122,7 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
     uint32_t m = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) m = max(m, top[k]);
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), d)));
+    m = rows_all(row16_all(m, Larger()), Larger());
     if ((tid & 63) == 0) all_top[wave] = m;
     __syncthreads();
     m = max(max(all_top[0], all_top[1]), max(all_top[2], all_top[3]));
@@ -138,13 +131,10 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
   } else {
     if constexpr (ROWS)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) row_top[i] = row16_max(row_top[i]);
+      for (int i = 0; i < 8; ++i) row_top[i] = row16_all(row_top[i], Larger());
     if constexpr (COLS) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        top[k] = max(top[k], uint32_t(__shfl_xor(int(top[k]), 16)));
-        top[k] = max(top[k], uint32_t(__shfl_xor(int(top[k]), 32)));
-      }
+      for (int k = 0; k < 8; ++k) top[k] = rows_all(top[k], Larger());
       if ((tid & 63) < 16)
 #pragma unroll
         for (int k = 0; k < 8; ++k) col_top[wave][column(k)] = top[k];
@@ -228,6 +218,15 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
 // wave's loads of stage s + 2, and one barrier. Small tiles, whose waves have few
 // MFMAs to a stage, have slots of two: the barrier comes between their stages.
 // Columns enter each element in ascending steps of 64, whatever the tile.
+//
+// Bound by the board's power: MLP-down's output (8192 x 4096 x 14336) takes 308 to 318 us,
+// 3.0-3.1 PFLOP/s, at 1.57 GHz with the matrix cores busy 81% of the cycles; the
+// instruction alone, without operand traffic, reaches 4.06 PFLOP/s there on codes of
+// normal values. The 16 x 16 x 128 form alone reaches 4.42, but its stages of 128
+// columns leave room for two slots of 256x256 tiles where a load needs three. Fewer
+// LDS reads or loads between two MFMAs, or the loads last, take the same time; without
+// the interleaving, or with s_setprio around the MFMAs, it is 13% slower. Slots of two
+// stages pay off at 128x64 and 64x64 only (128x128: 0.21 us a stage and 0.18).
 struct Fp8BlockArgs {
   const uint8_t *i_scales, *o_scales;
   int64_t kp;
@@ -489,6 +488,8 @@ void fp8_block_persistent_kernel(WgradArgs a, Fp8BlockArgs x) {
 // time: a lane holds 16 bytes of either half of a group, so that each load is
 // 1 KB on end (a run of 8 columns stays one, and the order of runs does not
 // matter to a sum that is joined in any case). Groups past the end read zeros.
+// 1 x 4096 x 14336 takes 11.5 us, 5.1 TB/s of its 59 MB, of which the chip's caches
+// may hold all; 1 x 128256 x 4096 90 us, 5.8 TB/s; with 16 waves and U = 4 152.
 template <int MB, int W, int U, int FI, int FO>
 __global__ __launch_bounds__(64 * W) void fp8_block_rows_kernel(WgradArgs a, Fp8BlockArgs x) {
   __shared__ float join[W][MB * 4][64];
