@@ -39,23 +39,32 @@ struct Forward {
   }
 };
 
-template <bool XB, bool YB, int EL, int WAVES>
+// Workgroups: what is added up behind them grows with their number. One to a CU of
+// more than four waves (4096 x 16384 bf16 92 us, with two 104); two of four waves where there is
+// work for many rounds (16384 x 4096 bf16 75 us, with one 92), else one (1000 x 4096 15.9
+// and 20.0; 4000 rows 33 and 31), and half as many for few rows (256 x 4096 8.9 and 10.8).
+template <bool XB, bool YB, int EL, int WAVES, int ROWS>
 forge_status launch_backward(const LnArgs& a, int32_t& parts, hipStream_t s) {
-  parts = int32_t(std::min((a.T + ln_rows<WAVES> - 1) / ln_rows<WAVES>, kLayernormParts));
-  hipLaunchKernelGGL((layernorm_backward_kernel<XB, YB, EL, WAVES>), dim3(parts),
-                     dim3(ln_threads<WAVES>), 0, s, a);
+  const int64_t rounds = (a.T + ROWS - 1) / ROWS;
+  const int64_t most = WAVES * ROWS > 4   ? kLayernormParts / 2
+                       : rounds >= 4096 ? kLayernormParts
+                       : rounds >= 512  ? kLayernormParts / 2
+                                        : kLayernormParts / 4;
+  parts = int32_t(std::min(rounds, most));
+  hipLaunchKernelGGL((layernorm_backward_kernel<XB, YB, EL, WAVES, ROWS>), dim3(parts),
+                     dim3(64 * WAVES * ROWS), 0, s, a);
   return launch_status();
 }
 
 template <bool XB, bool YB>
 struct Backward {
   static forge_status run(const LnArgs& a, int32_t& parts, hipStream_t s) {
-    if (a.d <= 512) return launch_backward<XB, YB, 8, 1>(a, parts, s);
-    if (a.d <= 1024) return launch_backward<XB, YB, 16, 1>(a, parts, s);
-    if (a.d <= 2048) return launch_backward<XB, YB, 8, 4>(a, parts, s);
-    if (a.d <= 4096) return launch_backward<XB, YB, 16, 4>(a, parts, s);
-    if (a.d <= 8192) return launch_backward<XB, YB, 32, 4>(a, parts, s);
-    if (a.d <= 16384) return launch_backward<XB, YB, 32, 8>(a, parts, s);
+    if (a.d <= 512) return launch_backward<XB, YB, 8, 1, 4>(a, parts, s);
+    if (a.d <= 1024) return launch_backward<XB, YB, 16, 1, 4>(a, parts, s);
+    if (a.d <= 2048) return launch_backward<XB, YB, 8, 4, 4>(a, parts, s);
+    if (a.d <= 4096) return launch_backward<XB, YB, 16, 4, 1>(a, parts, s);
+    if (a.d <= 8192) return launch_backward<XB, YB, 32, 4, 1>(a, parts, s);
+    if (a.d <= 16384) return launch_backward<XB, YB, 32, 8, 1>(a, parts, s);
     // Sums of so many columns do not fit a workgroup's registers beside the row:
     // the columns first, as dX may overwrite dY.
     constexpr int E = io_elems<XB, YB>;

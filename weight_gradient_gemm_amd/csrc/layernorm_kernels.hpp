@@ -207,18 +207,22 @@ __global__ __launch_bounds__(1024) void layernorm_wide_kernel(LnArgs a) {
   }
 }
 
-// dX of the workgroup's rows, and its sums of dY n and dY. The next row's loads are
-// in flight; dX may be dY, whose rows no other workgroup reads.
-template <bool XB, bool YB, int EL, int WAVES>
-__global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_backward_kernel(LnArgs a) {
+// dX of the workgroup's rows, and its sums of dY n and dY. ROWS rows at a time, WAVES
+// waves to each, whose sums are joined at the end: rows of up to 1024 columns, and those of up to
+// 2048, of which a CU takes more waves than the others' registers leave room for
+// (32768 x 2048 bf16 82 us, 102 with a row and 512 workgroups; 16384 x 4096 with two
+// rows 87, with one 79). The next rows' loads are in flight; dX may be dY, whose rows no
+// other workgroup reads.
+template <bool XB, bool YB, int EL, int WAVES, int ROWS>
+__global__ __launch_bounds__(64 * WAVES * ROWS) void layernorm_backward_kernel(LnArgs a) {
   constexpr int E = io_elems<XB, YB>, NV = EL / E, L = 64 * WAVES;
-  __shared__ float part[2][2][WAVES];
-  __shared__ __attribute__((aligned(16))) float join[WAVES == 1 ? 3 * 2 * 64 * EL : 4];
-  const int me = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int sub = WAVES == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  __shared__ float part[2][2][WAVES * ROWS];
+  __shared__ float join[ROWS > 1 ? (ROWS - 1) * 2 * L * EL : 1];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int sub = wave / WAVES, me = int(threadIdx.x) - sub * L;
   const float d = float(a.d);
-  const int64_t step = int64_t(gridDim.x) * ln_rows<WAVES>;
-  int64_t row = int64_t(blockIdx.x) * ln_rows<WAVES> + sub;
+  const int64_t step = int64_t(gridDim.x) * ROWS;
+  int64_t first = int64_t(blockIdx.x) * ROWS;
   LnRaw<XB, E> rx[NV];
   LnRaw<YB, E> ry[NV];
   float mean = 0.0f, rstd = 0.0f;
@@ -229,7 +233,7 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_backward_kernel(L
     mean = wanted ? a.mean[r] : 0.0f;
     rstd = wanted ? a.rstd[r] : 0.0f;
   };
-  fetch(row);
+  fetch(first + sub);
   // gamma stays in registers where there is room; else it comes from the caches.
   constexpr bool HELD = EL <= 16;
   float dg[NV][E] = {}, db[NV][E] = {}, held[HELD ? NV : 1][E] = {};
@@ -241,8 +245,11 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_backward_kernel(L
     }
   const __amdgpu_buffer_rsrc_t gammas = window(a.gamma, int64_t(a.d) * 4);
   int turn = 0;
-  for (; row < a.T; row += step, turn ^= 1) {
-    // Past the row's end dY is 0, and so is all that it is multiplied with.
+  // Waves that wait for each other have the same number of rounds.
+  for (; WAVES == 1 ? first + sub < a.T : first < a.T; first += step, turn ^= 1) {
+    const int64_t row = first + sub;
+    // Past the row's end, and in a row past the last, dY is 0, and so is all that it is
+    // multiplied with.
     float n[NV][E], y[NV][E], s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -278,15 +285,15 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_backward_kernel(L
     s2 = wave_sum(s2);
     if constexpr (WAVES > 1) {
       if ((threadIdx.x & 63) == 0) {
-        part[turn][0][threadIdx.x >> 6] = s1;
-        part[turn][1][threadIdx.x >> 6] = s2;
+        part[turn][0][wave] = s1;
+        part[turn][1][wave] = s2;
       }
       __syncthreads();
       s1 = s2 = 0.0f;
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) {
-        s1 += part[turn][0][w];
-        s2 += part[turn][1][w];
+        s1 += part[turn][0][sub * WAVES + w];
+        s2 += part[turn][1][sub * WAVES + w];
       }
     }
     s1 /= d;
@@ -295,30 +302,30 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_backward_kernel(L
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int k = 0; k < E; ++k) y[i][k] = r * (y[i][k] - s1 - n[i][k] * s2);
-      ln_put<XB, E, L>(a.out, row, a.d, me, i, y[i]);
+      if (WAVES == 1 || ROWS == 1 || row < a.T) ln_put<XB, E, L>(a.out, row, a.d, me, i, y[i]);
     }
   }
-  if constexpr (WAVES == 1) {                // four waves' sums to one
+  if constexpr (ROWS > 1) {                  // the rows' sums to one
     if (sub > 0) {
-      float* const at = join + (sub - 1) * 2 * 64 * EL;
+      float* const at = join + (sub - 1) * 2 * L * EL;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int k = 0; k < E; ++k) {
-          at[(i * E + k) * 64 + me] = dg[i][k];
-          at[(EL + i * E + k) * 64 + me] = db[i][k];
+          at[(i * E + k) * L + me] = dg[i][k];
+          at[(EL + i * E + k) * L + me] = db[i][k];
         }
     }
     __syncthreads();
     if (sub > 0) return;
 #pragma unroll
-    for (int w = 0; w < 3; ++w)
+    for (int w = 0; w < ROWS - 1; ++w)
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int k = 0; k < E; ++k) {
-          dg[i][k] += join[w * 2 * 64 * EL + (i * E + k) * 64 + me];
-          db[i][k] += join[w * 2 * 64 * EL + (EL + i * E + k) * 64 + me];
+          dg[i][k] += join[w * 2 * L * EL + (i * E + k) * L + me];
+          db[i][k] += join[w * 2 * L * EL + (EL + i * E + k) * L + me];
         }
   }
   float* const out = a.part + int64_t(blockIdx.x) * 2 * a.d;
