@@ -139,7 +139,8 @@ def test_types(env, T, d, xt, yt):
 
 
 @pytest.mark.parametrize("T,d", [(70001, 8), (9000, 1024), (40000, 256), (5000, 4096), (3000, 8192),
-                                 (1100, 16384), (600, 24576)])
+                                 (1100, 16384), (600, 24576), (4099, 1560), (1023, 2048), (511, 4096),
+                                 (513, 4104), (4097, 2056), (16387, 520)])
 def test_many_rows(env, T, d):
     # Workgroups that go round their loops, parts with unequal numbers of rows.
     torch, wg = env

@@ -123,8 +123,8 @@ forge_status launch_product(WgradArgs a, const Fp8BlockArgs& x, forge_tile tile,
 template <bool BF16, bool E5M2>
 void (*quantize_kernel(const Fp8QuantArgs& a))(Fp8QuantArgs) {
   if (!a.row_codes) return quantize_fp8_block_kernel<BF16, E5M2, false, true>;
-  return a.col_codes ? quantize_fp8_block_kernel<BF16, E5M2, true, true>
-                     : quantize_fp8_block_kernel<BF16, E5M2, true, false>;
+  if (a.col_codes) return quantize_fp8_block_kernel<BF16, E5M2, true, true>;
+  return a.square ? quantize_fp8_block_kernel<BF16, E5M2, true, false> : quantize_fp8_block_rows_kernel<BF16, E5M2>;
 }
 
 }  // namespace
@@ -155,7 +155,8 @@ FORGE_API forge_status forge_quantize_fp8_block(const void* x, forge_dtype x_dty
   a.row_pitch = FORGE_FP8_BLOCK_ROWS(R);
   a.col_pitch = FORGE_FP8_BLOCK_ROWS(C);
   a.square = square != 0;
-  const int64_t across = (C + kFp8Tile - 1) / kFp8Tile, tiles = (R + kFp8Tile - 1) / kFp8Tile * across;
+  const int64_t rows = row_codes && !col_codes && !square ? kFp8RowsOf : kFp8Tile;    // of a workgroup
+  const int64_t across = (C + kFp8Tile - 1) / kFp8Tile, tiles = (R + rows - 1) / rows * across;
   if (tiles >= int64_t(1) << 31) return FORGE_ERR_SHAPE;
   a.tiles_c = uint32_t(across);
   const bool bf16 = x_dtype == FORGE_BF16;

@@ -76,8 +76,8 @@ __device__ __forceinline__ int fp8_scale_place(int r) { return (r & 31) * 4 + (r
 // of a half is kept at q ^ (q / 8 mod 4) and its 16-byte chunk c at c ^ (q / 32),
 // which spreads one write instruction's rows over all banks.
 //
-// Bound by HBM: 8192 x 14336 takes, from bf16, 71 us by rows, 61 by columns (5.8 TB/s)
-// and 97 for both, which is 4.8 TB/s, a copy's rate; from float32 102, 97 and 138.
+// Rows alone come here in squares only. Bound by HBM: 8192 x 14336 takes, from bf16, 61 us
+// by columns (5.8 TB/s) and 97 for both, 4.8 TB/s, what a copy reaches; from float32 97 and 138.
 template <bool BF16, bool E5M2, bool ROWS, bool COLS>
 __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp8QuantArgs a) {
   constexpr int NW = BF16 ? 4 : 8;               // words of 8 values
@@ -118,7 +118,7 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
       row_top[i] = max(row_top[i], m);
     }
   }
-  if (a.square) {
+  if (!COLS || a.square) {
     uint32_t m = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) m = max(m, top[k]);
@@ -132,18 +132,16 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
     if constexpr (ROWS)
 #pragma unroll
       for (int i = 0; i < 8; ++i) row_top[i] = row16_all(row_top[i], Larger());
-    if constexpr (COLS) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) top[k] = rows_all(top[k], Larger());
-      if ((tid & 63) < 16)
+    for (int k = 0; k < 8; ++k) top[k] = rows_all(top[k], Larger());
+    if ((tid & 63) < 16)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) col_top[wave][column(k)] = top[k];
-      __syncthreads();
+      for (int k = 0; k < 8; ++k) col_top[wave][column(k)] = top[k];
+    __syncthreads();
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        top[k] = max(max(col_top[0][column(k)], col_top[1][column(k)]),
-                     max(col_top[2][column(k)], col_top[3][column(k)]));
-    }
+    for (int k = 0; k < 8; ++k)
+      top[k] = max(max(col_top[0][column(k)], col_top[1][column(k)]),
+                   max(col_top[2][column(k)], col_top[3][column(k)]));
   }
   auto place = [](int half, int q, int byte) {
     return half * 8192 + (q ^ ((q >> 3) & 3)) * 64 + (byte ^ (((q >> 5) & 3) << 4));
@@ -199,6 +197,50 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_kernel(Fp
       if (c0 + q < a.C)
         *reinterpret_cast<u32x4_t*>(a.col_codes + ((int64_t(tr) * 2 + half) * a.C + c0 + q) * 64 + byte) =
             *reinterpret_cast<const u32x4_t*>(out_c + place(half, q, byte));
+  }
+}
+
+// Along rows alone, 128 at a time: 16 lanes to a block, 16 rows of one block to a
+// workgroup, so that a store instruction's codes are two runs of 1 KB at most, and nothing goes
+// through LDS. The last rows' workgroup clears the scales behind them. 1 x 14336 bf16 takes
+// 2.5 us (4.0 by the kernel of tiles), 333 x 1024 2.6 (4.2), 4096 x 4096 10.5 (12.6), 8192 x
+// 14336 65 (69), from float32 107 (110). Loads past the caches: 4096 x 4096 11.4 us,
+// from float32 17 instead of 13.5.
+constexpr int kFp8RowsOf = 16;
+template <bool BF16, bool E5M2>
+__global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_rows_kernel(Fp8QuantArgs a) {
+  const int tid = threadIdx.x, j = tid & 15;
+  const uint32_t tr = blockIdx.x / a.tiles_c, tc = blockIdx.x - tr * a.tiles_c;
+  const int64_t row = int64_t(tr) * kFp8RowsOf + (tid >> 4), c = int64_t(tc) * 128 + 8 * j;
+  u32x4_t raw[BF16 ? 1 : 2] = {};
+  if (row < a.R && c < a.C) {
+    const u32x4_t* const p =
+        reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.x) + (row * a.C + c) * (BF16 ? 2 : 4));
+    raw[0] = p[0];
+    if constexpr (!BF16) raw[1] = p[1];
+  }
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t w = BF16 ? raw[0][k / 2] : raw[BF16 ? 0 : k / 4][k % 4];
+    v[k] = __builtin_bit_cast(float, BF16 ? (k & 1 ? w & 0xffff0000u : w << 16) : w);
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) top = max(top, abs_bits(__builtin_bit_cast(uint32_t, v[k])));
+  const uint32_t s = fp8_scale_byte<E5M2>(row16_all(top, Larger()));
+  const float f = fp8_factor(s);
+  const float lo[4] = {v[0] * f, v[1] * f, v[2] * f, v[3] * f}, hi[4] = {v[4] * f, v[5] * f, v[6] * f, v[7] * f};
+  const uint32_t w0 = s == 255u ? 0u : fp8_codes4<E5M2>(lo), w1 = s == 255u ? 0u : fp8_codes4<E5M2>(hi);
+  uint8_t* const scales = a.row_scales + tc * a.row_pitch;
+  if (row < a.R) {
+    *reinterpret_cast<u32x2_t*>(a.row_codes + ((int64_t(tc) * 2 + (j >> 3)) * a.R + row) * 64 + (j & 7) * 8) =
+        u32x2_t{w0, w1};
+    if (j == 0) scales[(row & ~127) + fp8_scale_place(int(row & 127))] = uint8_t(s);
+  }
+  if ((int64_t(tr) + 1) * kFp8RowsOf >= a.R && tid < 128) {
+    const int64_t pad = (a.R & ~127) + tid;
+    if (pad >= a.R && pad < a.row_pitch) scales[(pad & ~127) + fp8_scale_place(int(pad & 127))] = 0;
   }
 }
 
