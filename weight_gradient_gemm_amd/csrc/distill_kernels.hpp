@@ -477,7 +477,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(4)))
 void distill_rows_kernel(DistillArgs a) {
   constexpr int E = kVec<ZB>, W = THREADS / 64, EPT = (kDistillMaxK + THREADS - 1) / THREADS;
   constexpr int kBlock = THREADS * E;                  // columns of one load instruction of all waves
-  constexpr int ZS = ZB ? 2 : 4, GS = GB ? 2 : 4;
+  constexpr int ZS = ZB ? 2 : 4, GS = GB ? 2 : 4, kAhead = NV < 8 ? 2 : 6;
   __shared__ __attribute__((aligned(16))) Entries entry;
   __shared__ float part[6][W];
   const int tid = threadIdx.x, wave = tid >> 6;
@@ -520,14 +520,22 @@ void distill_rows_kernel(DistillArgs a) {
       }
     }
   };
-  auto combine = [&](const float* p, auto op) {
-    float v = p[0];
-#pragma unroll
-    for (int w = 1; w < W; ++w) v = op(v, p[w]);
-    return v;
-  };
+  // op over the waves' numbers: 16 lanes have one each, so that few registers do.
+  const int part_lane = tid & 15;
+  auto of_wave = [&](const float* p, float none) { return part_lane < W ? p[part_lane] : none; };
+  auto combine = [&](float v, auto op) { return row16_all(v, op); };
   auto add = [](float x, float y) { return x + y; };
   auto larger = [](float x, float y) { return fmaxf(x, y); };
+
+  // Vector i, which is held, into the thread's maximum and sum, if its row has `shown`
+  // blocks that count.
+  float mine_m = -INFINITY, mine_s = 0.0f;
+  auto take = [&](int i, int shown) {
+    if (i == anew(full)) cut(raw[i]);
+    if (i < anew(shown)) running<ZB>(raw[i], a.c, mine_m, mine_s);
+    forget(raw[i]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
 
   const int64_t step = gridDim.x;
   int64_t row = blockIdx.x;
@@ -539,6 +547,8 @@ void distill_rows_kernel(DistillArgs a) {
     int64_t n[EPT];
     load_ids(row, w != 0.0f, n);
     load_logits(row, n);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) take(i, w != 0.0f ? blocks : 0);
   }
   for (; row < a.T; row += step) {
     const int64_t next = row + step;
@@ -553,26 +563,10 @@ void distill_rows_kernel(DistillArgs a) {
       if (i == full) cut(r);
       return r;
     };
-    float m = -INFINITY, top = -INFINITY;
+    // The blocks that are not held.
+    for (int i = NV; i < (w != 0.0f ? blocks : 0); ++i) running<ZB>(streamed(i), a.c, mine_m, mine_s);
+    float top = -INFINITY;
     bool some = false;
-    auto most = [&](const u32x4_t& r) {
-      float v[E];
-      unpack<ZB>(r, v);
-#pragma unroll
-      for (int k = 0; k < E; ++k) m = fmaxf(m, v[k]);
-    };
-    int shown = w != 0.0f ? blocks : 0;                // blocks of the row that count
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (i == anew(full)) cut(raw[i]);
-      if (i < anew(shown)) most(raw[i]);
-      forget(raw[i]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    // Blocks that are not held: maximum and sum in one pass, as distill_loss_kernel.
-    float far_m = -INFINITY, far_s = 0.0f;
-    for (int i = NV; i < shown; ++i) running<ZB>(streamed(i), a.c, far_m, far_s);
-    m = fmaxf(m, far_m);
 #pragma unroll
     for (int e = 0; e < EPT; ++e) {
       if (u[e] == -INFINITY) id[e] = -1;
@@ -581,34 +575,25 @@ void distill_rows_kernel(DistillArgs a) {
         some = true;
       }
     }
-    m = wave_max(m);
+    float m = wave_max(mine_m);
+    float s = wave_sum(mine_s * exp2_fast((mine_m - finite_max(m)) * a.c));
     top = wave_max(top);
     const bool any = __ballot(some) != 0;
     if ((tid & 63) == 0) {
       part[0][wave] = m;
       part[1][wave] = top;
       part[2][wave] = any ? 1.0f : 0.0f;
+      part[3][wave] = s;
     }
     __syncthreads();
-    m = finite_max(combine(part[0], larger));
-    top = finite_max(combine(part[1], larger));
-    const bool live = combine(part[2], larger) != 0.0f;
-    shown = live ? blocks : 0;
+    const float wave_m = of_wave(part[0], -INFINITY);
+    m = finite_max(combine(wave_m, larger));
+    s = combine(of_wave(part[3], 0.0f) * exp2_fast((wave_m - m) * a.c), add);
+    top = finite_max(combine(of_wave(part[1], -INFINITY), larger));
+    const bool live = __builtin_amdgcn_readfirstlane(int(combine(of_wave(part[2], 0.0f), larger))) != 0;
+    const int shown = live ? blocks : 0;
 
-    float s = 0.0f, total = 0.0f;
-    auto sum = [&](const u32x4_t& r) {
-      float v[E];
-      unpack<ZB>(r, v);
-#pragma unroll
-      for (int k = 0; k < E; ++k) s += exp2_fast((v[k] - m) * a.c);
-    };
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (i < anew(shown)) sum(raw[i]);
-      forget(raw[i]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if (shown > NV) s += far_s * exp2_fast((far_m - m) * a.c);
+    float total = 0.0f;
     if (live)
 #pragma unroll
       for (int e = 0; e < EPT; ++e) {
@@ -621,15 +606,10 @@ void distill_rows_kernel(DistillArgs a) {
           entry.z[j] = zt[e];
         }
       }
-    s = wave_sum(s);
     total = wave_sum(total);
-    if ((tid & 63) == 0) {
-      part[3][wave] = s;
-      part[4][wave] = total;
-    }
+    if ((tid & 63) == 0) part[4][wave] = total;
     __syncthreads();
-    s = combine(part[3], add);
-    total = combine(part[4], add);
+    total = combine(of_wave(part[4], 0.0f), add);
     if (live) {
       float l = 0.0f;
 #pragma unroll
@@ -653,16 +633,22 @@ void distill_rows_kernel(DistillArgs a) {
       store_gradient<GB, E>(out, uint32_t(tid * E * GS), uint32_t(i * kBlock * GS), v);
     };
     const int out_blocks = int((a.ld + kBlock - 1) / kBlock);
+    // As vectors leave, the next row's come, and are added up kAhead of them later.
+    mine_m = -INFINITY;
+    mine_s = 0.0f;
+    const int coming = ahead ? blocks : 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (i < anew(out_blocks)) emit(raw[i], i);
       raw[i] = load(there, i);
       __builtin_amdgcn_sched_barrier(0);
+      if (i >= kAhead) take(i - kAhead, coming);
     }
     for (int i = NV; i < out_blocks; ++i) emit(streamed(i), i);
     __syncthreads();
+    const float l = combine(of_wave(part[5], 0.0f), add);
     if (tid == 0)
-      a.loss[row] = live ? a.loss_scale * w * (combine(part[5], add) + (logf(s) - logf(total))) : 0.0f;
+      a.loss[row] = live ? a.loss_scale * w * (l + (logf(s) - logf(total))) : 0.0f;
     if (live) {
       entry_gradients<THREADS, GB>(a, row, entry, 0, a.V, coef, m, s, total);
       // Columns past V of the last block that counts: 0 times a sum that is not finite is not 0.
@@ -674,6 +660,8 @@ void distill_rows_kernel(DistillArgs a) {
           static_cast<float*>(a.grad)[row * a.ld + c] = 0.0f;
       }
     }
+#pragma unroll
+    for (int i = NV - kAhead; i < NV; ++i) take(i, coming);
     w = wn;
   }
 }
