@@ -14,12 +14,13 @@
 // each chunk's maximum and sum of exponentials, a second joins them and forms the
 // gradient. The loss alone goes once through a row and holds nothing.
 //
-// Measured: 4096 x 128256 bf16, a row in 8 left out, 433 us for 1.97 GB, 4.5 TB/s (a
-// copy reaches 4.8); 1021 x 32003 float32 with a bf16 gradient 44 us, 4.1 TB/s;
-// 1024 x 128256 float32, not held whole, 214 us for the 1.05 GB that it cannot do without
-// and 0.26 again; the loss of 511 x 50021 float32 17 us, 5.3 TB/s; 8 x 128256 bf16 9.0 us, two
-// launches that wait for memory two and one time. A row read twice by the same grid, the
-// maximum first, took 1642 us for the first of these.
+// Measured: 4096 x 128256 bf16, a row in 8 left out, 411 us for 1.97 GB, 4.8 TB/s, what
+// a copy reaches; 1021 x 32003 float32 with a bf16 gradient 42 us, 4.3 TB/s of the needed
+// bytes (entries' columns are written twice); 1024 x 128256 float32, not held whole, 206
+// us for the 1.05 GB that it cannot do without and 0.26 again; the loss of 511 x 50021
+// float32 17 us, 5.3 TB/s; 8 x 128256 bf16 9.0 us, two launches that wait for memory two
+// and one time. A row read twice by the same grid, the maximum first, took 1642 us for
+// the first of these.
 //
 // The teacher's columns are written with the others and once more, with their q,
 // behind a barrier: the workgroup that has the column does both.
@@ -477,7 +478,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(4)))
 void distill_rows_kernel(DistillArgs a) {
   constexpr int E = kVec<ZB>, W = THREADS / 64, EPT = (kDistillMaxK + THREADS - 1) / THREADS;
   constexpr int kBlock = THREADS * E;                  // columns of one load instruction of all waves
-  constexpr int ZS = ZB ? 2 : 4, GS = GB ? 2 : 4, kAhead = NV < 8 ? 2 : 6;
+  constexpr int ZS = ZB ? 2 : 4, GS = GB ? 2 : 4, kAhead = NV < 8 ? 2 : 3;
   __shared__ __attribute__((aligned(16))) Entries entry;
   __shared__ float part[6][W];
   const int tid = threadIdx.x, wave = tid >> 6;
@@ -633,7 +634,9 @@ void distill_rows_kernel(DistillArgs a) {
       store_gradient<GB, E>(out, uint32_t(tid * E * GS), uint32_t(i * kBlock * GS), v);
     };
     const int out_blocks = int((a.ld + kBlock - 1) / kBlock);
-    // As vectors leave, the next row's come, and are added up kAhead of them later.
+    // As vectors leave, the next row's come, and are added up kAhead of them later: with
+    // the sums behind the last store the memory waits for them (4096 x 128256 431 us, so
+    // 411). 3, 6 or 10 vectors: 1021 x 32003 42.4, 43.4, 44.6 us, the others within 1%.
     mine_m = -INFINITY;
     mine_s = 0.0f;
     const int coming = ahead ? blocks : 0;

@@ -48,9 +48,9 @@ forge_status launch_chunks(DistillArgs a, hipStream_t s) {
 // A row to a workgroup, or chunks of it. Chunks take a launch more (3 us) and read
 // the logits twice, but a workgroup takes 5 us and one more for each 7000 columns
 // with a row (for each 3500 where it does not hold it), however few there are: bf16 8 x
-// 128256 8.8 us in chunks and 22 by rows, 64 x 128256 18 and 23, 128 x 128256 30 and 24,
-// 64 x 32000 9.8 and 10.0, 8 x 8192 8.4 and 6.1; float32 128 x 128256 (not held) 39 and 50,
-// 256 x 128256 70 and 54. The loss alone: 8 x 128256 7.3 us in chunks and 10.7 by rows, 64
+// 128256 7.9 us in chunks and 22 by rows, 64 x 128256 18 and 23, 128 x 128256 30 and 23,
+// 64 x 32000 9.8 and 10.0, 8 x 8192 8.4 and 6.1; float32 128 x 128256 (not held) 33 and 50,
+// 256 x 128256 70 and 53. The loss alone: 8 x 128256 6.7 us in chunks and 10.7 by rows, 64
 // x 128256 11.0 and 11.4, 8 x 60000 7.3 and 7.0.
 template <bool ZB>
 bool few_rows(const DistillArgs& a) {
