@@ -110,6 +110,29 @@ def test_quantize(env, R, C, dtype, fmt, square):
         assert torch.equal(decode(torch, rows)[0][:, :C], decode(torch, cols)[0][:, :R].t())
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_quantize_more_rows_than_workgroups(env, dtype):
+    # Beyond 2^20 workgroups of 16 rows and 128 columns they loop; x has more than 2^32 bytes.
+    torch, wg = env
+    R, C = 131085, 16520
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.zeros(R, C, dtype=getattr(torch, dtype), device="cuda")
+    x[-200:] = torch.randn(200, C, generator=g, device="cuda").to(x.dtype)
+    x[:16] = x[-16:]
+    op = wg.forge_fp8_block_empty(R, C)
+    op.codes.fill_(0xA5)
+    op.scales.fill_(0xA5)
+    wg.forge_quantize_fp8_block(x, rows=op)
+    first = (R - 200 + 127) // 128 * 128
+    last = wg.forge_fp8_block_empty(R - first, C)
+    wg.forge_quantize_fp8_block(x[first:].contiguous(), rows=last)
+    same(torch, last, x[first:])
+    assert torch.equal(op.codes[:, first:], last.codes) and torch.equal(op.scales[:, first:], last.scales)
+    assert torch.equal(op.codes[:, :16], op.codes[:, R - 16:])
+    assert not op.codes[:, 16:R - 200].any()
+    assert not op.scales[:, 128:(R - 200) // 128 * 128].any()
+
+
 @pytest.mark.parametrize("fmt", list(FORMAT))
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_quantize_borders_at_every_exponent(env, dtype, fmt):

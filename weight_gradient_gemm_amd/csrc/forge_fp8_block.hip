@@ -18,6 +18,9 @@ enum : forge_tile { FP8_TILE_128x64 = FORGE_TILE_COUNT, FP8_TILE_64x64, FP8_TILE
 // groups (24 N kB apart) stay below 2^31.
 constexpr int64_t kRowsMaxN = 1 << 17;
 
+// Most workgroups that quantise along rows alone; what is beyond loops.
+constexpr int64_t kMaxRowGroups = int64_t(1) << 20;
+
 using Fp8128x64 = SmallTileCfg<128, 64, 2, 2, 1, 2>;
 using Fp864x64 = SmallTileCfg<64, 64, 2, 2, 2, 2>;
 
@@ -158,11 +161,13 @@ FORGE_API forge_status forge_quantize_fp8_block(const void* x, forge_dtype x_dty
   const int64_t rows = row_codes && !col_codes && !square ? kFp8RowsOf : kFp8Tile;    // of a workgroup
   const int64_t across = (C + kFp8Tile - 1) / kFp8Tile, tiles = (R + rows - 1) / rows * across;
   if (tiles >= int64_t(1) << 31) return FORGE_ERR_SHAPE;
+  a.tiles = uint32_t(tiles);
   a.tiles_c = uint32_t(across);
   const bool bf16 = x_dtype == FORGE_BF16;
   const auto kernel = fmt == FORGE_FP8_E5M2 ? (bf16 ? quantize_kernel<true, true>(a) : quantize_kernel<false, true>(a))
                                             : (bf16 ? quantize_kernel<true, false>(a) : quantize_kernel<false, false>(a));
-  hipLaunchKernelGGL(kernel, dim3(uint32_t(tiles)), dim3(kFp8QuantThreads), 0,
+  hipLaunchKernelGGL(kernel, dim3(uint32_t(rows == kFp8Tile ? tiles : std::min(tiles, kMaxRowGroups))),
+                     dim3(kFp8QuantThreads), 0,
                      static_cast<hipStream_t>(stream), a);
   return launch_status();
 }

@@ -23,7 +23,7 @@ struct Fp8QuantArgs {
   uint8_t *row_codes, *row_scales, *col_codes, *col_scales;
   int64_t R, C;
   int64_t row_pitch, col_pitch;      // bytes of a group of scales
-  uint32_t tiles_c;                  // tiles across
+  uint32_t tiles, tiles_c;           // tiles, and tiles across
   int32_t square;
 };
 
@@ -210,37 +210,39 @@ constexpr int kFp8RowsOf = 16;
 template <bool BF16, bool E5M2>
 __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_rows_kernel(Fp8QuantArgs a) {
   const int tid = threadIdx.x, j = tid & 15;
-  const uint32_t tr = blockIdx.x / a.tiles_c, tc = blockIdx.x - tr * a.tiles_c;
-  const int64_t row = int64_t(tr) * kFp8RowsOf + (tid >> 4), c = int64_t(tc) * 128 + 8 * j;
-  u32x4_t raw[BF16 ? 1 : 2] = {};
-  if (row < a.R && c < a.C) {
-    const u32x4_t* const p =
-        reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.x) + (row * a.C + c) * (BF16 ? 2 : 4));
-    raw[0] = p[0];
-    if constexpr (!BF16) raw[1] = p[1];
-  }
-  float v[8];
+  for (uint32_t item = blockIdx.x; item < a.tiles; item += gridDim.x) {
+    const uint32_t tr = item / a.tiles_c, tc = item - tr * a.tiles_c;
+    const int64_t row = int64_t(tr) * kFp8RowsOf + (tid >> 4), c = int64_t(tc) * 128 + 8 * j;
+    u32x4_t raw[BF16 ? 1 : 2] = {};
+    if (row < a.R && c < a.C) {
+      const u32x4_t* const p =
+          reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.x) + (row * a.C + c) * (BF16 ? 2 : 4));
+      raw[0] = p[0];
+      if constexpr (!BF16) raw[1] = p[1];
+    }
+    float v[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t w = BF16 ? raw[0][k / 2] : raw[BF16 ? 0 : k / 4][k % 4];
-    v[k] = __builtin_bit_cast(float, BF16 ? (k & 1 ? w & 0xffff0000u : w << 16) : w);
-  }
-  uint32_t top = 0;
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t w = BF16 ? raw[0][k / 2] : raw[BF16 ? 0 : k / 4][k % 4];
+      v[k] = __builtin_bit_cast(float, BF16 ? (k & 1 ? w & 0xffff0000u : w << 16) : w);
+    }
+    uint32_t top = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) top = max(top, abs_bits(__builtin_bit_cast(uint32_t, v[k])));
-  const uint32_t s = fp8_scale_byte<E5M2>(row16_all(top, Larger()));
-  const float f = fp8_factor(s);
-  const float lo[4] = {v[0] * f, v[1] * f, v[2] * f, v[3] * f}, hi[4] = {v[4] * f, v[5] * f, v[6] * f, v[7] * f};
-  const uint32_t w0 = s == 255u ? 0u : fp8_codes4<E5M2>(lo), w1 = s == 255u ? 0u : fp8_codes4<E5M2>(hi);
-  uint8_t* const scales = a.row_scales + tc * a.row_pitch;
-  if (row < a.R) {
-    *reinterpret_cast<u32x2_t*>(a.row_codes + ((int64_t(tc) * 2 + (j >> 3)) * a.R + row) * 64 + (j & 7) * 8) =
-        u32x2_t{w0, w1};
-    if (j == 0) scales[(row & ~127) + fp8_scale_place(int(row & 127))] = uint8_t(s);
-  }
-  if ((int64_t(tr) + 1) * kFp8RowsOf >= a.R && tid < 128) {
-    const int64_t pad = (a.R & ~127) + tid;
-    if (pad >= a.R && pad < a.row_pitch) scales[(pad & ~127) + fp8_scale_place(int(pad & 127))] = 0;
+    for (int k = 0; k < 8; ++k) top = max(top, abs_bits(__builtin_bit_cast(uint32_t, v[k])));
+    const uint32_t s = fp8_scale_byte<E5M2>(row16_all(top, Larger()));
+    const float f = fp8_factor(s);
+    const float lo[4] = {v[0] * f, v[1] * f, v[2] * f, v[3] * f}, hi[4] = {v[4] * f, v[5] * f, v[6] * f, v[7] * f};
+    const uint32_t w0 = s == 255u ? 0u : fp8_codes4<E5M2>(lo), w1 = s == 255u ? 0u : fp8_codes4<E5M2>(hi);
+    uint8_t* const scales = a.row_scales + tc * a.row_pitch;
+    if (row < a.R) {
+      *reinterpret_cast<u32x2_t*>(a.row_codes + ((int64_t(tc) * 2 + (j >> 3)) * a.R + row) * 64 + (j & 7) * 8) =
+          u32x2_t{w0, w1};
+      if (j == 0) scales[(row & ~127) + fp8_scale_place(int(row & 127))] = uint8_t(s);
+    }
+    if ((int64_t(tr) + 1) * kFp8RowsOf >= a.R && tid < 128) {
+      const int64_t pad = (a.R & ~127) + tid;
+      if (pad >= a.R && pad < a.row_pitch) scales[(pad & ~127) + fp8_scale_place(int(pad & 127))] = 0;
+    }
   }
 }
 
@@ -262,7 +264,7 @@ __global__ __launch_bounds__(kFp8QuantThreads) void quantize_fp8_block_rows_kern
 // Columns enter each element in ascending steps of 64, whatever the tile.
 //
 // Bound by the board's power: MLP-down's output (8192 x 4096 x 14336) takes 308 to 318 us,
-// 3.0-3.1 PFLOP/s, at 1.57 GHz with the matrix cores busy 81% of the cycles; the
+// 3.0-3.1 PFLOP/s, at 1400 W and 1.72 GHz with the matrix cores busy 84% of the cycles; the
 // instruction alone, without operand traffic, reaches 4.06 PFLOP/s there on codes of
 // normal values. The 16 x 16 x 128 form alone reaches 4.42, but its stages of 128
 // columns leave room for two slots of 256x256 tiles where a load needs three. Fewer
