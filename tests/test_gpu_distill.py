@@ -480,3 +480,19 @@ def test_refused_tensors(env):
                 call(**kw)
     with pytest.raises(wg.ForgeError, match="SHAPE"):
         call(z, u, ids, loss, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("byte", [0, 0x7F, 0xFF])
+@pytest.mark.parametrize("T,V", [(4, 40000), (40, 70000), (300, 9000)])
+def test_what_the_workspace_holds_means_nothing(env, T, V, byte):
+    """Zeros, large numbers or NaN there, with rows of weight 0 and entries that are not there."""
+    torch, wg = env
+    z, u, ids, weight, V = inputs(torch, T, V, 30, seed=5)
+    weight[1], weight[2] = 0, 1
+    ids[2, 1:] = -1
+    ws = torch.full((1 << 20,), byte, dtype=torch.uint8, device="cuda")
+    loss, grad = check(torch, wg, (z, u, ids, weight, V), "bfloat16", workspace=ws)
+    assert float(loss[1]) == 0 and not grad[1].any()
+    l2, g2 = torch.empty_like(loss), torch.empty_like(grad)
+    wg.forge_distill(z, u, ids, l2, g2, vocab=V, weight=weight)
+    assert torch.equal(loss, l2) and torch.equal(grad, g2)
