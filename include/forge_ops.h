@@ -241,10 +241,10 @@ FORGE_API forge_status forge_wgrad_adamw_mxfp4(const void* x_codes, const void* 
  *
  * x and dX are of x_dtype, y and dY of y_dtype, each FORGE_F32 or FORGE_BF16;
  * gamma, beta, dgamma, dbeta [d] and mean, rstd [T] are float32. mean and rstd
- * need the alignment of a float only. Arithmetic is float32, the mean's sum
- * float64, each result is rounded once; a row whose squared deviations pass
- * float32's range (deviations beyond 1e19) has rstd 0. 0 <= T <= 2^30, d a multiple of 8 up to FORGE_LAYERNORM_MAX_D,
- * T d <= 2^40. d == 0 does nothing.
+ * need the alignment of a float only. Arithmetic is float32; the mean's sum is
+ * float64, and so is the variance's where squared deviations leave float32's
+ * range; each result is rounded once. 0 <= T <= 2^30, d a multiple of 8 up to
+ * FORGE_LAYERNORM_MAX_D, T d <= 2^40. d == 0 does nothing.
  */
 #define FORGE_LAYERNORM_MAX_D 65536
 

@@ -11,8 +11,7 @@
 // row lies in the registers of one wave (up to 1024 columns), of four (up to 8192) or
 // of eight (up to 16384), so it is read once; longer ones are read again from the
 // caches. The mean is summed in 64 bits, the variance from the deviations, which no mean
-// makes cancel; both are float32, as all the rest, so squares of deviations beyond
-// 1e19 overflow. The backward pass's workgroups go from row to row with their columns'
+// makes cancel, in float32, and in 64 bits where their squares leave its range. The backward pass's workgroups go from row to row with their columns'
 // sums of dY n and dY in registers, store them at the end, and a second launch
 // adds up the workgroups' sums in a fixed order.
 //
@@ -58,6 +57,19 @@ __device__ __forceinline__ F row_sum(F v, F* part) {
     for (int w = 1; w < WAVES; ++w) v += part[w];
   }
   return v;
+}
+
+// Whether a variance (with eps) was summed in float32 as it should be. Below 2^-100 squares
+// count that float32 holds as denormals or not at all (each of them is off by at most 2^-150),
+// and one that is no number or infinite may be a sum that passed the range. The value is
+// the same in all waves of the row.
+__device__ __forceinline__ bool ln_in_range(float var) {
+  return __builtin_amdgcn_readfirstlane(int(var >= 0x1p-100f && var <= 0x1.fffffep127f)) != 0;
+}
+
+// 1 / sqrt(sum of squares / d + eps) in 64 bits.
+__device__ __forceinline__ float ln_rstd(double squares, int d, float eps) {
+  return float(1.0 / sqrt(squares / double(d) + double(eps)));
 }
 
 // Workgroups: WAVES waves to a row, or four rows of a wave each.
@@ -113,7 +125,7 @@ __device__ __forceinline__ void ln_put(void* p, int64_t row, int d, int me, int 
 template <bool XB, bool YB, int EL, int WAVES>
 __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_kernel(LnArgs a) {
   constexpr int E = io_elems<XB, YB>, NV = EL / E, L = 64 * WAVES;
-  __shared__ double part_s[WAVES];
+  __shared__ double part_s[WAVES], part_w[WAVES];
   __shared__ float part_v[WAVES];
   const int me = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
   const int sub = WAVES == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
@@ -151,7 +163,16 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_kernel(LnArgs a) 
         q = __builtin_fmaf(v[i][k], v[i][k], q);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<WAVES>(q, part_v) / float(a.d) + a.eps);
+    const float var = row_sum<WAVES>(q, part_v) / float(a.d) + a.eps;
+    float rstd = 1.0f / sqrtf(var);
+    if (!ln_in_range(var)) {
+      double w = 0.0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < E; ++k) w += double(v[i][k]) * double(v[i][k]);
+      rstd = ln_rstd(row_sum<WAVES>(w, part_w), a.d, a.eps);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
@@ -169,7 +190,7 @@ __global__ __launch_bounds__(ln_threads<WAVES>) void layernorm_kernel(LnArgs a) 
 template <bool XB, bool YB>
 __global__ __launch_bounds__(1024) void layernorm_wide_kernel(LnArgs a) {
   constexpr int E = io_elems<XB, YB>, WAVES = 16;
-  __shared__ double part_s[WAVES];
+  __shared__ double part_s[WAVES], part_w[WAVES];
   __shared__ float part_v[WAVES];
   const float d = float(a.d);
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
@@ -190,7 +211,20 @@ __global__ __launch_bounds__(1024) void layernorm_wide_kernel(LnArgs a) {
         s = __builtin_fmaf(e, e, s);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<WAVES>(s, part_v) / d + a.eps);
+    const float var = row_sum<WAVES>(s, part_v) / d + a.eps;
+    float rstd = 1.0f / sqrtf(var);
+    if (!ln_in_range(var)) {
+      sum = 0.0;
+      for (int c = threadIdx.x * E; c < a.d; c += 1024 * E) {
+        load_elems<XB, E>(a.x, base + c, v);
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+          const double e = double(v[k] - mean);
+          sum += e * e;
+        }
+      }
+      rstd = ln_rstd(row_sum<WAVES>(sum, part_w), a.d, a.eps);
+    }
     for (int c = threadIdx.x * E; c < a.d; c += 1024 * E) {
       float g[E], b[E] = {};
       load_elems<XB, E>(a.x, base + c, v);
