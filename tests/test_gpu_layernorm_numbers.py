@@ -1,7 +1,8 @@
 """Layer norm where its numbers are hard."""
 import pytest
 
-from test_gpu_layernorm import HALF, check_backward, check_forward, inputs
+from test_gpu_layernorm import (HALF, TINY, U, backward64, check_backward, check_forward, inputs,
+                                within)
 
 
 @pytest.fixture(scope="module")
@@ -44,3 +45,34 @@ def test_equal_values_without_eps(env, d):
     wg.forge_layernorm(x, gamma, beta, y, None, rstd, eps=0.0)
     assert torch.isnan(y[[2, 4]]).all() and torch.isfinite(y[[0, 1, 3, 5, 6]]).all()
     assert torch.isinf(rstd[[2, 4]]).all()
+
+
+# --------------------------------------------------------------------------
+# sums over the rows
+# --------------------------------------------------------------------------
+def few_rows_tolerance(dY, x, mean, rstd):
+    """Rows that each are a workgroup's only one: its dY n is off by the roundings of the
+    deviation, of n and of the product, its dY not at all; what adds the rows up rounds once."""
+    y = dY.double()
+    n = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    size = (y * n).abs().sum(0)
+    T = x.shape[0]
+    tiny = T * TINY["float32"]
+    return (3.01 * U * size + U * (y * n).sum(0).abs() + T * 2.0 ** -52 * size + tiny,
+            U * y.sum(0).abs() + T * 2.0 ** -52 * y.abs().sum(0) + TINY["float32"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("xt,yt", [("float32", "float32"), ("bfloat16", "bfloat16"), ("float32", "bfloat16")])
+@pytest.mark.parametrize("T", [1, 2, 9, 63, 64, 65, 100, 128])
+@pytest.mark.parametrize("d", [2056, 4096, 8200, 16384])
+def test_rows_are_added_up_without_loss(env, T, d, xt, yt):
+    """Up to 128 rows of more than 2048 columns: dbeta is the sum rounded once."""
+    torch, wg = env
+    x, gamma, beta, dY = inputs(torch, T, d, xt, yt, seed=T)
+    _, mean, rstd = check_forward(torch, wg, x, gamma, beta, "float32")
+    _, dg, db = check_backward(torch, wg, dY, x, gamma, mean, rstd)
+    want = backward64(torch, dY, x, gamma, mean, rstd, xt)
+    e_g, e_b = few_rows_tolerance(dY, x, mean, rstd)
+    within(torch, db, want[2], e_b, "dbeta")
+    within(torch, dg, want[1], e_g, "dgamma")

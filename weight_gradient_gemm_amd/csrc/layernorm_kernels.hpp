@@ -453,7 +453,8 @@ __global__ __launch_bounds__(256) void layernorm_columns_kernel(LnArgs a) {
 }
 
 // dgamma and dbeta: column c of `columns` summed over the parts, 8 lanes of 4
-// columns (a line) by 64 groups that take every 64th part.
+// columns (a line) by 64 groups that take every 64th part. In 64 bits, so that up to 512
+// sums are joined with one rounding.
 struct LnReduce {
   const float* part;
   float *dgamma, *dbeta;
@@ -461,10 +462,10 @@ struct LnReduce {
 };
 constexpr int kLnReduceColumns = 32, kLnReduceGroups = 64;
 __global__ __launch_bounds__(512) void layernorm_reduce_kernel(LnReduce a) {
-  __shared__ f32x4_t join[kLnReduceGroups][8];
+  __shared__ double join[kLnReduceGroups][kLnReduceColumns + 1];
   const int me = threadIdx.x & 7, grp = threadIdx.x >> 3;
   const int c = blockIdx.x * kLnReduceColumns + me * 4;
-  f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
   if (c < a.columns) {
     const float* p = a.part + c;
     const int64_t step = int64_t(kLnReduceGroups) * 2 * a.d;
@@ -472,20 +473,27 @@ __global__ __launch_bounds__(512) void layernorm_reduce_kernel(LnReduce a) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {              // at most kLayernormParts = 512 parts
       const bool in = grp + k * kLnReduceGroups < a.parts;
-      v[k] = in ? *reinterpret_cast<const f32x4_t*>(p + int64_t(grp) * 2 * a.d + k * step) : s;
+      v[k] = in ? *reinterpret_cast<const f32x4_t*>(p + int64_t(grp) * 2 * a.d + k * step)
+                : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s = s + v[k];
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] += double(v[k][j]);
   }
-  join[grp][me] = s;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) join[grp][me * 4 + j] = s[j];
   __syncthreads();
-  if (threadIdx.x >= kLnReduceColumns) return;
-  const int col = blockIdx.x * kLnReduceColumns + threadIdx.x;
-  if (col >= a.columns) return;
-  float r = 0.0f;
-#pragma unroll 8
-  for (int k = 0; k < kLnReduceGroups; ++k) r += join[k][threadIdx.x >> 2][threadIdx.x & 3];
-  (col < a.d ? a.dgamma + col : a.dbeta + (col - a.d))[0] = r;
+  // Eight lanes to a column, each with eight groups.
+  if (threadIdx.x >= 8 * kLnReduceColumns) return;
+  const int at = threadIdx.x >> 3, col = blockIdx.x * kLnReduceColumns + at;
+  double r = 0.0;
+#pragma unroll
+  for (int k = 0; k < kLnReduceGroups / 8; ++k) r += join[me * (kLnReduceGroups / 8) + k][at];
+  r += lanes_dpp<0xB1>(r);
+  r += lanes_dpp<0x4E>(r);
+  r += lanes_dpp<0x141>(r);
+  if (me == 0 && col < a.columns) (col < a.d ? a.dgamma + col : a.dbeta + (col - a.d))[0] = float(r);
 }
 
 }  // namespace forge
