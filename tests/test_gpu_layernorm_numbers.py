@@ -1,8 +1,8 @@
 """Layer norm where its numbers are hard."""
 import pytest
 
-from test_gpu_layernorm import (HALF, TINY, U, backward64, check_backward, check_forward, inputs,
-                                within)
+from test_gpu_layernorm import (HALF, ROW, TINY, U, backward64, check_backward, check_forward,
+                                forward64, inputs, within)
 
 
 @pytest.fixture(scope="module")
@@ -45,6 +45,72 @@ def test_equal_values_without_eps(env, d):
     wg.forge_layernorm(x, gamma, beta, y, None, rstd, eps=0.0)
     assert torch.isnan(y[[2, 4]]).all() and torch.isfinite(y[[0, 1, 3, 5, 6]]).all()
     assert torch.isinf(rstd[[2, 4]]).all()
+
+
+# --------------------------------------------------------------------------
+# the mean's sum in 64 bits
+# --------------------------------------------------------------------------
+def mean_tolerance(x):
+    """Rows' means as they are promised: float64 sums of d values, off by up to d steps of
+    2^-53 of the magnitudes, and one rounding."""
+    x = x.double()
+    return U * x.mean(1).abs() + (x.shape[1] + 2) * 2.0 ** -53 * x.abs().mean(1) + TINY["float32"]
+
+
+def cancelling_rows(torch, d, dtype, device):
+    """Small values with large ones of either sign between them that cancel: neighbours,
+    the halves of a row, and a few of them far apart; and a mean far from zero."""
+    g = torch.Generator().manual_seed(d)
+    x = torch.randn(5, d, generator=g)
+    big = 2.0 ** 21 * (1 + torch.rand(5, d // 2, generator=g))
+    x[0, 0::2] += big[0]
+    x[0, 1::2] -= big[0]
+    x[1, : d // 2] += big[1]
+    x[1, d // 2:] -= big[1]
+    x[2, 0], x[2, d // 2 - 1], x[2, d // 2], x[2, d - 1] = 3e7, 1e7, -1e7, -3e7
+    x[3] += 1e4
+    x[4, 0::4] += big[4, : (d + 3) // 4]
+    x[4, 2::4] -= big[4, : (d + 1) // 4]
+    return x.to(getattr(torch, dtype)).to(device)
+
+
+NUMBERS = [8, 264, 1000, 1024, 2048, 4096, 5000, 8200, 16384, 16392, 40000]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("xt", list(HALF))
+@pytest.mark.parametrize("d", NUMBERS)
+def test_mean_is_summed_in_64_bits(env, d, xt):
+    torch, wg = env
+    x = cancelling_rows(torch, d, xt, "cuda")
+    gamma, beta = torch.ones(d, device="cuda"), torch.zeros(d, device="cuda")
+    y, mean, rstd = torch.empty(5, d, device="cuda"), torch.empty(5, device="cuda"), torch.empty(5, device="cuda")
+    wg.forge_layernorm(x, gamma, beta, y, mean, rstd)
+    tol = mean_tolerance(x)
+    within(torch, mean, x.double().mean(1), tol, "mean")
+    # And y, which a mean that is off shifts as a whole (see forward64 for the other terms).
+    want = forward64(torch, x, gamma, beta, 1e-5, "float32")
+    r = want[2][:, None]
+    n = want[0]
+    e_rstd = (ROW / 2 + 6) * U + tol[:, None] ** 2 * r * r / 2
+    within(torch, y, n, n.abs() * (e_rstd + 4 * U) + 1.01 * r * tol[:, None] + TINY["float32"], "y")
+
+
+@pytest.mark.parametrize("d", NUMBERS)
+def test_a_float32_sum_is_seen(d):
+    """The bound above against sums in float32, and in float64 without its low word, of the
+    same rows: both are far outside."""
+    import torch
+    x = cancelling_rows(torch, d, "float32", "cpu")
+    want, tol = x.double().mean(1), mean_tolerance(x)
+    lanes = x[:, : d // 8 * 8].view(5, -1, 8)                    # 8 values on end to a thread
+    thread = torch.zeros(5, lanes.shape[1])
+    for k in range(8):
+        thread = thread + lanes[:, :, k]
+    float32 = thread.sum(1) / d
+    assert int(((float32.double() - want).abs() > tol).sum()) >= 3
+    half = (lanes.double().sum(2).view(torch.int64) & ~0xFFFFFFFF).view(torch.float64).sum(1) / d
+    assert d == 8 or int(((half - want).abs() > tol).sum()) >= 2
 
 
 # --------------------------------------------------------------------------
