@@ -142,3 +142,47 @@ def test_rows_are_added_up_without_loss(env, T, d, xt, yt):
     e_g, e_b = few_rows_tolerance(dY, x, mean, rstd)
     within(torch, db, want[2], e_b, "dbeta")
     within(torch, dg, want[1], e_g, "dgamma")
+
+
+# --------------------------------------------------------------------------
+# large tensors
+# --------------------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d", [(4500001, 512), (2300003, 1000), (1100001, 2048), (560003, 4096), (280001, 8192),
+                                 (140003, 16384), ((1 << 20) + 37, 16392)])
+def test_offsets_beyond_32_bits(env, T, d):
+    """More than 2^31 elements and 2^32 bytes of each tensor; the last of these has more
+    rows than the launches of long rows have workgroups. All rows are zeros but a few, of the
+    first, of those around 2^31 elements and 2^32 bytes, and of the last."""
+    torch, wg = env
+    assert T * d > 1 << 31
+    at = [r for c in (0, (1 << 31) // d, (1 << 32) // d, T) for r in range(c - 8, c + 8) if 0 <= r < T]
+    at = torch.tensor(sorted(set(at)), device="cuda")
+    some, gamma, beta, dY = inputs(torch, len(at), d, "bfloat16", "bfloat16", seed=d)
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    x[at] = some
+    y = torch.full_like(x, 7.0)
+    mean, rstd = torch.full((T,), 7.0, device="cuda"), torch.full((T,), 7.0, device="cuda")
+    wg.forge_layernorm(x, gamma, beta, y, mean, rstd)
+    want = forward64(torch, some, gamma, beta, 1e-5, "bfloat16")
+    within(torch, y[at], want[0], want[3], "y")
+    within(torch, mean[at], want[1], want[4], "mean")
+    within(torch, rstd[at], want[2], want[5], "rstd")
+    others = torch.ones(T, dtype=torch.bool, device="cuda")
+    others[at] = False
+    assert not mean[others].any() and bool((rstd[others] == rstd[others][0]).all())
+    zero_row = y[int(torch.nonzero(others)[0])].clone()          # beta, rounded
+    assert torch.equal(zero_row, beta.bfloat16())
+    y[at] = zero_row
+    step = (1 << 28) // d
+    assert all(bool((y[r:r + step] == zero_row).all()) for r in range(0, T, step))
+    # Backward in place: dY is zero elsewhere, and so are dX and what is added up.
+    y.zero_()
+    y[at] = dY
+    dg, db = torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    wg.forge_layernorm_backward(y, x, gamma, mean, rstd, y, dg, db)
+    want = backward64(torch, dY, some, gamma, mean[at], rstd[at], "bfloat16")
+    for got, k, what in ((y[at], 0, "dX"), (dg, 1, "dgamma"), (db, 2, "dbeta")):
+        within(torch, got, want[k], want[3 + k], what)
+    y[at] = 0
+    assert not any(bool(y[r:r + step].any()) for r in range(0, T, step))

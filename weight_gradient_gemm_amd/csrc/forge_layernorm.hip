@@ -11,7 +11,9 @@ namespace {
 
 static_assert(kLayernormParts <= 8 * kLnReduceGroups, "parts that the last sum reads");
 
-// Most workgroups of a launch; what is beyond loops.
+// Most workgroups of a launch over rows that registers do not hold; what is beyond loops.
+// A few to a CU that loop take longer: 20000 x 16392 bf16 forward 345 us, with 1, 2 and 4 to
+// a CU 440, 391 and 382, 8192 x 24576 197 and 255, 226, 222; backward 3 to 5% longer.
 constexpr int64_t kMaxGrid = int64_t(1) << 20;
 
 dim3 grid_for(int64_t blocks) { return dim3(uint32_t(std::min(blocks, kMaxGrid))); }
