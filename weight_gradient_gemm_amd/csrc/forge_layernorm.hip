@@ -1,5 +1,6 @@
 // Layer norm entry points of the forge C ABI.
 #include <algorithm>
+#include <cstdint>
 
 #include "forge_ops.h"
 #include "host.hpp"
@@ -42,14 +43,18 @@ struct Forward {
 };
 
 // Workgroups: what is added up behind them grows with their number. One to a CU of
-// more than four waves (4096 x 16384 bf16 92 us, with two 104); two of four waves where there is
-// work for many rounds (16384 x 4096 bf16 75 us, with one 92), else one (1000 x 4096 15.9
-// and 20.0; 4000 rows 33 and 31), and half as many for few rows (256 x 4096 8.9 and 10.8).
+// more than four waves (4096 x 16384 bf16 92 us, with two 104). Of four waves two to a CU
+// where there is work for many rounds: 4000 x 4096 bf16 31 us, with one 33, float32 44.7 and 45.6;
+// 2800 rows 27.1 and 26.7, 36.4 and 35.4; 3500 x 5000 bf16 37 and 41. Rows of more than 4096
+// columns gain later or not at all where they are float32: x alone, 4096 x 8192 69 and
+// 65, 8192 x 5000 88 and 90; both, 8192 x 5000 100 and 94, 8192 x 8192 144 and 138. Half as
+// many as CUs for few rows (256 x 4096 8.9 and 10.8).
 template <bool XB, bool YB, int EL, int WAVES, int ROWS>
 forge_status launch_backward(const LnArgs& a, int32_t& parts, hipStream_t s) {
   const int64_t rounds = (a.T + ROWS - 1) / ROWS;
-  const int64_t most = WAVES * ROWS > 4   ? kLayernormParts / 2
-                       : rounds >= 4096 ? kLayernormParts
+  const int64_t many = EL <= 16 || (XB && YB) ? 3500 : XB || YB ? 4096 : INT64_MAX;
+  const int64_t most = WAVES * ROWS > 4 ? kLayernormParts / 2
+                       : rounds >= many ? kLayernormParts
                        : rounds >= 512  ? kLayernormParts / 2
                                         : kLayernormParts / 4;
   parts = int32_t(std::min(rounds, most));
