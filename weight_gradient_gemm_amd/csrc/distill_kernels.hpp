@@ -49,7 +49,7 @@ struct DistillArgs {
   int64_t T, ld, items;              // items: rows times chunks of the launch
   int32_t V, K, chunks, chunks_out;  // chunks of V and of ld columns
   int32_t wide_ids, teacher_bf16;
-  float c, inv_tau, loss_scale, grad_scale;    // log2(e) / tau, 1 / tau, scale tau^2, scale tau
+  float c, loss_scale, grad_scale;   // log2(e) / tau, scale tau^2, scale tau
 };
 
 // A row's entries: id (-1: not there), 2^((u - largest) c), the student's logit.
@@ -180,11 +180,17 @@ __device__ __forceinline__ void entry_gradients(const DistillArgs& a, int64_t ro
   }
 }
 
-// An entry's share of the loss, without the logarithms of the two sums.
+// An entry's share of tau times the loss, without the logarithms of the two sums.
 __device__ __forceinline__ float entry_loss(const DistillArgs& a, float u, float top, float total, float z,
                                             float m) {
   const float du = u - top, q = exp2_fast(du * a.c) / total;
-  return q != 0.0f ? q * (du * a.inv_tau - (z - m) * a.inv_tau) : 0.0f;
+  return q != 0.0f ? q * (du - (z - m)) : 0.0f;
+}
+
+// A row's loss from its entries' shares l. Those count tau, the logarithms tau^2, which
+// float32 may not hold where it holds tau (below 1e-19): then they do not count either.
+__device__ __forceinline__ float row_loss(const DistillArgs& a, float w, float l, float s, float total) {
+  return w * __builtin_fmaf(a.grad_scale, l, a.loss_scale * (logf(s) - logf(total)));
 }
 
 // --------------------------------------------------------------------------
@@ -453,7 +459,7 @@ __global__ __launch_bounds__(kChunkThreads) void distill_gradient_kernel(Distill
       float l = 0.0f;
 #pragma unroll
       for (int k = 0; k < W; ++k) l += part[3][k];
-      a.loss[row] = live != 0.0f ? a.loss_scale * w * (l + (logf(s) - logf(total))) : 0.0f;
+      a.loss[row] = live != 0.0f ? row_loss(a, w, l, s, total) : 0.0f;
     }
     if (a.grad && live != 0.0f)
       entry_gradients<N, GB>(a, row, entry, first, first + kChunkColumns, coef, m, s, total);
@@ -651,7 +657,7 @@ void distill_rows_kernel(DistillArgs a) {
     __syncthreads();
     const float l = combine(of_wave(part[5], 0.0f), add);
     if (tid == 0)
-      a.loss[row] = live ? a.loss_scale * w * (l + (logf(s) - logf(total))) : 0.0f;
+      a.loss[row] = live ? row_loss(a, w, l, s, total) : 0.0f;
     if (live) {
       entry_gradients<THREADS, GB>(a, row, entry, 0, a.V, coef, m, s, total);
       // Columns past V of the last block that counts: 0 times a sum that is not finite is not 0.
@@ -781,7 +787,7 @@ __global__ __launch_bounds__(kLossThreads) void distill_loss_kernel(DistillArgs 
       l = 0.0f;
 #pragma unroll
       for (int k = 0; k < W; ++k) l += part[5][k];
-      a.loss[row] = live != 0.0f ? a.loss_scale * w * (l + (logf(s) - logf(total))) : 0.0f;
+      a.loss[row] = live != 0.0f ? row_loss(a, w, l, s, total) : 0.0f;
     }
   }
 }

@@ -111,7 +111,6 @@ FORGE_API forge_status forge_distill(const void* logits, forge_dtype z_dtype, in
   a.wide_ids = id_bytes == 8;
   a.teacher_bf16 = teacher_dtype == FORGE_BF16;
   a.c = float(1.4426950408889634 / temperature);
-  a.inv_tau = float(1.0 / temperature);
   a.loss_scale = float(scale * temperature * temperature);
   a.grad_scale = float(scale * temperature);
   const hipStream_t st = static_cast<hipStream_t>(stream);
