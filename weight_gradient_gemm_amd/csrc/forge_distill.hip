@@ -9,7 +9,8 @@
 namespace forge {
 namespace {
 
-static_assert(kDistillMaxK == FORGE_DISTILL_MAX_K && kDistillChunk == kChunkColumns,
+static_assert(kDistillMaxK == FORGE_DISTILL_MAX_K && kDistillChunk == kChunkColumns &&
+                  kDistillHeld == 1024 * 16 * kVec<true> && kDistillHeld == 2 * 1024 * 16 * kVec<false>,
               "the kernels' sizes");
 
 // Most workgroups of a launch; what is beyond loops.
@@ -45,22 +46,16 @@ forge_status launch_chunks(DistillArgs a, hipStream_t s) {
   return launch_status();
 }
 
-// A row to a workgroup, or chunks of it. Chunks take a launch more (3 us) and read
-// the logits twice, but a workgroup takes 5 us and one more for each 7000 columns
+// A row to a workgroup, or chunks of it (distill_in_chunks). Chunks take a launch
+// more (3 us) and read the logits twice, but a workgroup takes 5 us and one more for each 7000 columns
 // with a row (for each 3500 where it does not hold it), however few there are: bf16 8 x
 // 128256 7.9 us in chunks and 22 by rows, 64 x 128256 18 and 23, 128 x 128256 30 and 23,
 // 64 x 32000 9.8 and 10.0, 8 x 8192 8.4 and 6.1; float32 128 x 128256 (not held) 33 and 50,
 // 256 x 128256 70 and 53. The loss alone: 8 x 128256 6.7 us in chunks and 10.7 by rows, 64
 // x 128256 11.0 and 11.4, 8 x 60000 7.3 and 7.0.
-template <bool ZB>
-bool few_rows(const DistillArgs& a) {
-  if (!a.grad) return a.V > 65536 && a.T <= 64;
-  return a.V > 16384 && a.T <= (a.V <= 1024 * 16 * kVec<ZB> ? 64 : 192);
-}
-
 template <bool ZB, bool GB>
 forge_status launch(const DistillArgs& a, hipStream_t s) {
-  if (few_rows<ZB>(a)) return launch_chunks<ZB, GB>(a, s);
+  if (distill_in_chunks(a.T, a.V, ZB, a.grad != nullptr)) return launch_chunks<ZB, GB>(a, s);
   if (a.grad) return launch_rows<ZB, GB>(a, s);
   const int64_t grid = int64_t(std::max(16, persistent_grid())) * 3;
   hipLaunchKernelGGL((distill_loss_kernel<ZB>), dim3(uint32_t(std::min(grid, a.T))), dim3(kLossThreads), 0, s, a);

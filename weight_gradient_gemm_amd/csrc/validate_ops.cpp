@@ -417,8 +417,15 @@ bool distill_sizes_ok(int64_t T, int64_t V, int64_t K) {
          T * V <= kMaxElems;
 }
 
+bool distill_in_chunks(int64_t T, int64_t V, bool bf16, bool grad) {
+  if (!grad) return V > 65536 && T <= 64;
+  return V > 16384 && T <= (V <= (bf16 ? kDistillHeld : kDistillHeld / 2) ? 64 : kDistillChunkRows);
+}
+
 DistillWorkspace distill_workspace(int64_t T, int64_t V, int64_t K) {
   DistillWorkspace w{};
+  w.bytes = 16;
+  if (T > kDistillChunkRows) return w;
   w.stats = 0;
   w.logit = T * ((V + kDistillChunk - 1) / kDistillChunk) * 8;
   w.bytes = std::max<int64_t>(16, w.logit + T * K * 4);

@@ -75,8 +75,14 @@ forge_status validate_layernorm_backward(const void* dY, forge_dtype y_dtype, co
 
 // Columns of a chunk of a row of logits, which one workgroup goes through.
 constexpr int64_t kDistillChunk = 4096;
+// Most columns of a row of bf16 logits that a workgroup's registers hold; float32 half.
+constexpr int64_t kDistillHeld = 131072;
+// Most rows that are cut into chunks, of any type of logits, and whether a call's are.
+constexpr int64_t kDistillChunkRows = 192;
+bool distill_in_chunks(int64_t T, int64_t V, bool bf16, bool grad);
 // Byte offsets of the parts of distillation's workspace: each chunk's maximum
-// and sum of exponentials, and the student's logits of the teacher's ids.
+// and sum of exponentials, and the student's logits of the teacher's ids. Only
+// rows that are cut into chunks have them.
 struct DistillWorkspace {
   int64_t stats, logit, bytes;
 };
