@@ -305,8 +305,9 @@ FORGE_API forge_status forge_layernorm_backward(const void* dY, forge_dtype y_dt
  */
 #define FORGE_DISTILL_MAX_K 1024
 
-/* Bytes of forge_distill's workspace, at least 16, which is what many rows take; 0 if
- * a size is out of range. */
+/* Bytes of forge_distill's workspace, at least 16; 0 if a size is out of range. It
+ * grows with T only up to some hundred rows, and never falls with T, V or K: a
+ * workspace does for all smaller sizes. */
 FORGE_API int64_t forge_distill_workspace(int64_t T, int64_t V, int64_t K);
 
 FORGE_API forge_status forge_distill(const void* logits, forge_dtype z_dtype, int64_t ld,

@@ -424,8 +424,7 @@ bool distill_in_chunks(int64_t T, int64_t V, bool bf16, bool grad) {
 
 DistillWorkspace distill_workspace(int64_t T, int64_t V, int64_t K) {
   DistillWorkspace w{};
-  w.bytes = 16;
-  if (T > kDistillChunkRows) return w;
+  T = std::min(T, kDistillChunkRows);
   w.stats = 0;
   w.logit = T * ((V + kDistillChunk - 1) / kDistillChunk) * 8;
   w.bytes = std::max<int64_t>(16, w.logit + T * K * 4);

@@ -82,7 +82,8 @@ constexpr int64_t kDistillChunkRows = 192;
 bool distill_in_chunks(int64_t T, int64_t V, bool bf16, bool grad);
 // Byte offsets of the parts of distillation's workspace: each chunk's maximum
 // and sum of exponentials, and the student's logits of the teacher's ids. Only
-// rows that are cut into chunks have them.
+// rows that are cut into chunks have them, but its size never falls with T, V or K: what was
+// made for the largest batch does for a smaller one.
 struct DistillWorkspace {
   int64_t stats, logit, bytes;
 };
