@@ -46,7 +46,7 @@ struct DistillArgs {
   void* grad;                        // NULL: the loss alone
   float2* stats;                     // [T][chunks]: maximum, sum of 2^((z - maximum) c)
   float* logit;                      // [T][K]: the student's logit of each entry
-  int64_t T, ld, items;              // items: rows times chunks of the launch
+  int64_t T, ld, items;              // items: rows times chunks of the launch, one to a workgroup
   int32_t V, K, chunks, chunks_out;  // chunks of V and of ld columns
   int32_t wide_ids, teacher_bf16;
   float c, loss_scale, grad_scale;   // log2(e) / tau, scale tau^2, scale tau
@@ -283,63 +283,61 @@ template <bool ZB>
 __global__ __launch_bounds__(kChunkThreads) void distill_stats_kernel(DistillArgs a) {
   constexpr int E = kVec<ZB>, W = kChunkThreads / 64;
   __shared__ float2 part[W];
-  for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
-    const int64_t row = item / a.chunks;
-    const int first = int(item - row * a.chunks) * kChunkColumns;
-    if (!eager(a) && a.weight && a.weight[row] == 0.0f) continue;
-    EntryWords words;
-    words.load_ids(a, row, true);
-    u32x4_t raw[16 / E];
-    load_chunk<ZB>(a, row, first, raw);
-    words.arrived_ids();
-    int id[kChunkEntries];                             // of entries in this chunk
-    uint32_t zt[kChunkEntries];
+  const int64_t item = blockIdx.x;
+  const int64_t row = item / a.chunks;
+  const int first = int(item - row * a.chunks) * kChunkColumns;
+  if (!eager(a) && a.weight && a.weight[row] == 0.0f) return;
+  EntryWords words;
+  words.load_ids(a, row, true);
+  u32x4_t raw[16 / E];
+  load_chunk<ZB>(a, row, first, raw);
+  words.arrived_ids();
+  int id[kChunkEntries];                             // of entries in this chunk
+  uint32_t zt[kChunkEntries];
 #pragma unroll
-    for (int e = 0; e < kChunkEntries; ++e) {
-      id[e] = words.id(a, e);
-      if (id[e] < first || id[e] >= first + kChunkColumns) id[e] = -1;
-      zt[e] = 0;
-      if (id[e] >= 0) {
-        const int64_t at = row * a.ld + id[e];
-        zt[e] = ZB ? static_cast<const uint16_t*>(a.z)[at] : static_cast<const uint32_t*>(a.z)[at];
-      }
+  for (int e = 0; e < kChunkEntries; ++e) {
+    id[e] = words.id(a, e);
+    if (id[e] < first || id[e] >= first + kChunkColumns) id[e] = -1;
+    zt[e] = 0;
+    if (id[e] >= 0) {
+      const int64_t at = row * a.ld + id[e];
+      zt[e] = ZB ? static_cast<const uint16_t*>(a.z)[at] : static_cast<const uint32_t*>(a.z)[at];
     }
-    cut_chunk<ZB>(a, first, raw);
-    float m = -INFINITY, s = 0.0f, v[E];
+  }
+  cut_chunk<ZB>(a, first, raw);
+  float m = -INFINITY, s = 0.0f, v[E];
 #pragma unroll
-    for (int i = 0; i < 16 / E; ++i) {
-      unpack<ZB>(raw[i], v);
+  for (int i = 0; i < 16 / E; ++i) {
+    unpack<ZB>(raw[i], v);
 #pragma unroll
-      for (int k = 0; k < E; ++k) m = fmaxf(m, v[k]);
-    }
-    m = wave_max(m);
-    const float mf = finite_max(m);
+    for (int k = 0; k < E; ++k) m = fmaxf(m, v[k]);
+  }
+  m = wave_max(m);
+  const float mf = finite_max(m);
 #pragma unroll
-    for (int i = 0; i < 16 / E; ++i) {
-      unpack<ZB>(raw[i], v);
+  for (int i = 0; i < 16 / E; ++i) {
+    unpack<ZB>(raw[i], v);
 #pragma unroll
-      for (int k = 0; k < E; ++k) s += exp2_fast((v[k] - mf) * a.c);
-    }
+    for (int k = 0; k < E; ++k) s += exp2_fast((v[k] - mf) * a.c);
+  }
 #pragma unroll
-    for (int e = 0; e < kChunkEntries; ++e) {
-      asm volatile("" : "+v"(zt[e]));                  // not looked into before
-      if (id[e] >= 0)
-        a.logit[row * a.K + e * kChunkThreads + int(threadIdx.x)] =
-            __builtin_bit_cast(float, ZB ? zt[e] << 16 : zt[e]);
-    }
-    s = wave_sum(s);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = make_float2(m, s);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float most = part[0].x, sum = 0.0f;
+  for (int e = 0; e < kChunkEntries; ++e) {
+    asm volatile("" : "+v"(zt[e]));                  // not looked into before
+    if (id[e] >= 0)
+      a.logit[row * a.K + e * kChunkThreads + int(threadIdx.x)] =
+          __builtin_bit_cast(float, ZB ? zt[e] << 16 : zt[e]);
+  }
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float most = part[0].x, sum = 0.0f;
 #pragma unroll
-      for (int w = 1; w < W; ++w) most = fmaxf(most, part[w].x);
+    for (int w = 1; w < W; ++w) most = fmaxf(most, part[w].x);
 #pragma unroll
-      for (int w = 0; w < W; ++w)
-        sum += part[w].y * exp2_fast((part[w].x - finite_max(most)) * a.c);
-      a.stats[item] = make_float2(most, sum);
-    }
-    __syncthreads();                                   // `part` is written again
+    for (int w = 0; w < W; ++w)
+      sum += part[w].y * exp2_fast((part[w].x - finite_max(most)) * a.c);
+    a.stats[item] = make_float2(most, sum);
   }
 }
 
@@ -349,122 +347,120 @@ __global__ __launch_bounds__(kChunkThreads) void distill_gradient_kernel(Distill
   __shared__ __attribute__((aligned(16))) Entries entry;
   __shared__ float part[4][W];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
-    const int64_t row = item / a.chunks_out;
-    const int chunk = int(item - row * a.chunks_out), first = chunk * kChunkColumns;
-    float w = 1.0f;
-    if (!eager(a) && a.weight) w = a.weight[row];
-    const bool look = eager(a) || w != 0.0f;
-    u32x4_t raw[16 / E];
-    if (look && a.grad) load_chunk<ZB>(a, row, first, raw);
-    EntryWords words;
-    words.load_ids(a, row, look);
-    words.load_logits(a, row, look);
-    int id[EPT];
-    float u[EPT], zt[EPT], top = -INFINITY, total = 0.0f;
+  const int64_t item = blockIdx.x;
+  const int64_t row = item / a.chunks_out;
+  const int chunk = int(item - row * a.chunks_out), first = chunk * kChunkColumns;
+  float w = 1.0f;
+  if (!eager(a) && a.weight) w = a.weight[row];
+  const bool look = eager(a) || w != 0.0f;
+  u32x4_t raw[16 / E];
+  if (look && a.grad) load_chunk<ZB>(a, row, first, raw);
+  EntryWords words;
+  words.load_ids(a, row, look);
+  words.load_logits(a, row, look);
+  int id[EPT];
+  float u[EPT], zt[EPT], top = -INFINITY, total = 0.0f;
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-      const int j = e * N + tid;
-      zt[e] = j < a.K && look ? a.logit[row * a.K + j] : 0.0f;     // means nothing where there is no id
-    }
-    if (eager(a) && a.weight) w = a.weight[row];
-    // The row's maximum and sum from its chunks', by each wave for itself.
-    float m = -INFINITY, s = 0.0f;
-    if (look) {
-      for (int k = lane; k < a.chunks; k += 64) {
-        const float2 st = a.stats[row * a.chunks + k];
-        const float most = fmaxf(m, st.x), mf = finite_max(most);
-        s = s * exp2_fast((m - mf) * a.c) + st.y * exp2_fast((st.x - mf) * a.c);
-        m = most;
-      }
-      const float mine = m;
-      m = finite_max(wave_max(m));
-      s = wave_sum(s * exp2_fast((mine - m) * a.c));
-    }
-    // Entries: each wave's largest and sum, joined behind the barrier.
-    words.arrived_ids();
-    words.arrived_logits();
-#pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-      id[e] = w != 0.0f ? words.id(a, e) : -1;
-      u[e] = words.logit(a, e);
-      if (u[e] == -INFINITY) id[e] = -1;
-      if (id[e] >= 0) top = fmaxf(top, u[e]);
-    }
-    bool some = false;
-#pragma unroll
-    for (int e = 0; e < EPT; ++e) some = some || id[e] >= 0;
-    if (look && a.grad) cut_chunk<ZB>(a, first, raw);
-    top = wave_max(top);
-    const bool any = __ballot(some) != 0;
-    if (lane == 0) {
-      part[0][wave] = top;
-      part[1][wave] = any ? 1.0f : 0.0f;
-    }
-    __syncthreads();
-    top = -INFINITY;
-    float live = 0.0f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      top = fmaxf(top, part[0][k]);
-      live = fmaxf(live, part[1][k]);
-    }
-    top = finite_max(top);
-#pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-      const int j = e * N + tid;
-      const float q = id[e] >= 0 ? exp2_fast((u[e] - top) * a.c) : 0.0f;
-      total += q;
-      if (j < (a.K + 3 & ~3)) {                        // up to a multiple of 4
-        entry.id[j] = id[e];
-        entry.q[j] = q;
-        entry.z[j] = zt[e];
-      }
-    }
-    total = wave_sum(total);
-    if (lane == 0) part[2][wave] = total;
-    __syncthreads();
-    total = 0.0f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) total += part[2][k];
-    const float coef = a.grad_scale * w, inv = 1.0f / s;
-    if (a.grad) {
-      const int shown = live != 0.0f ? a.V - first : 0;            // columns of the chunk that count
-      const int columns = int(min(a.ld - first, int64_t(kChunkColumns)));
-      const __amdgpu_buffer_rsrc_t out =
-          window(static_cast<char*>(a.grad) + (row * a.ld + first) * GS, int64_t(columns) * GS);
-#pragma unroll
-      for (int i = 0; i < 16 / E; ++i) {
-        const int c = (i * N + tid) * E;
-        float v[E] = {};
-        if (c < shown) {
-          unpack<ZB>(raw[i], v);
-#pragma unroll
-          for (int k = 0; k < E; ++k)
-            v[k] = c + k < shown ? coef * (exp2_fast((v[k] - m) * a.c) * inv) : 0.0f;
-        }
-        store_gradient<GB, E>(out, uint32_t(tid * E * GS), uint32_t(i * N * E * GS), v);
-      }
-    }
-    if (chunk == 0) {
-      float l = 0.0f;
-#pragma unroll
-      for (int e = 0; e < EPT; ++e)
-        if (id[e] >= 0) l += entry_loss(a, u[e], top, total, zt[e], m);
-      l = wave_sum(l);
-      if (lane == 0) part[3][wave] = l;
-    }
-    __syncthreads();
-    if (chunk == 0 && tid == 0) {
-      float l = 0.0f;
-#pragma unroll
-      for (int k = 0; k < W; ++k) l += part[3][k];
-      a.loss[row] = live != 0.0f ? row_loss(a, w, l, s, total) : 0.0f;
-    }
-    if (a.grad && live != 0.0f)
-      entry_gradients<N, GB>(a, row, entry, first, first + kChunkColumns, coef, m, s, total);
-    if (a.items > gridDim.x) __syncthreads();          // the LDS is written again
+  for (int e = 0; e < EPT; ++e) {
+    const int j = e * N + tid;
+    zt[e] = j < a.K && look ? a.logit[row * a.K + j] : 0.0f;     // means nothing where there is no id
   }
+  if (eager(a) && a.weight) w = a.weight[row];
+  // The row's maximum and sum from its chunks', by each wave for itself.
+  float m = -INFINITY, s = 0.0f;
+  if (look) {
+    for (int k = lane; k < a.chunks; k += 64) {
+      const float2 st = a.stats[row * a.chunks + k];
+      const float most = fmaxf(m, st.x), mf = finite_max(most);
+      s = s * exp2_fast((m - mf) * a.c) + st.y * exp2_fast((st.x - mf) * a.c);
+      m = most;
+    }
+    const float mine = m;
+    m = finite_max(wave_max(m));
+    s = wave_sum(s * exp2_fast((mine - m) * a.c));
+  }
+  // Entries: each wave's largest and sum, joined behind the barrier.
+  words.arrived_ids();
+  words.arrived_logits();
+#pragma unroll
+  for (int e = 0; e < EPT; ++e) {
+    id[e] = w != 0.0f ? words.id(a, e) : -1;
+    u[e] = words.logit(a, e);
+    if (u[e] == -INFINITY) id[e] = -1;
+    if (id[e] >= 0) top = fmaxf(top, u[e]);
+  }
+  bool some = false;
+#pragma unroll
+  for (int e = 0; e < EPT; ++e) some = some || id[e] >= 0;
+  if (look && a.grad) cut_chunk<ZB>(a, first, raw);
+  top = wave_max(top);
+  const bool any = __ballot(some) != 0;
+  if (lane == 0) {
+    part[0][wave] = top;
+    part[1][wave] = any ? 1.0f : 0.0f;
+  }
+  __syncthreads();
+  top = -INFINITY;
+  float live = 0.0f;
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    top = fmaxf(top, part[0][k]);
+    live = fmaxf(live, part[1][k]);
+  }
+  top = finite_max(top);
+#pragma unroll
+  for (int e = 0; e < EPT; ++e) {
+    const int j = e * N + tid;
+    const float q = id[e] >= 0 ? exp2_fast((u[e] - top) * a.c) : 0.0f;
+    total += q;
+    if (j < (a.K + 3 & ~3)) {                        // up to a multiple of 4
+      entry.id[j] = id[e];
+      entry.q[j] = q;
+      entry.z[j] = zt[e];
+    }
+  }
+  total = wave_sum(total);
+  if (lane == 0) part[2][wave] = total;
+  __syncthreads();
+  total = 0.0f;
+#pragma unroll
+  for (int k = 0; k < W; ++k) total += part[2][k];
+  const float coef = a.grad_scale * w, inv = 1.0f / s;
+  if (a.grad) {
+    const int shown = live != 0.0f ? a.V - first : 0;            // columns of the chunk that count
+    const int columns = int(min(a.ld - first, int64_t(kChunkColumns)));
+    const __amdgpu_buffer_rsrc_t out =
+        window(static_cast<char*>(a.grad) + (row * a.ld + first) * GS, int64_t(columns) * GS);
+#pragma unroll
+    for (int i = 0; i < 16 / E; ++i) {
+      const int c = (i * N + tid) * E;
+      float v[E] = {};
+      if (c < shown) {
+        unpack<ZB>(raw[i], v);
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          v[k] = c + k < shown ? coef * (exp2_fast((v[k] - m) * a.c) * inv) : 0.0f;
+      }
+      store_gradient<GB, E>(out, uint32_t(tid * E * GS), uint32_t(i * N * E * GS), v);
+    }
+  }
+  if (chunk == 0) {
+    float l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPT; ++e)
+      if (id[e] >= 0) l += entry_loss(a, u[e], top, total, zt[e], m);
+    l = wave_sum(l);
+    if (lane == 0) part[3][wave] = l;
+  }
+  __syncthreads();
+  if (chunk == 0 && tid == 0) {
+    float l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) l += part[3][k];
+    a.loss[row] = live != 0.0f ? row_loss(a, w, l, s, total) : 0.0f;
+  }
+  if (a.grad && live != 0.0f)
+    entry_gradients<N, GB>(a, row, entry, first, first + kChunkColumns, coef, m, s, total);
 }
 
 // --------------------------------------------------------------------------

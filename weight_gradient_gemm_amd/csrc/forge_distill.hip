@@ -13,9 +13,8 @@ static_assert(kDistillMaxK == FORGE_DISTILL_MAX_K && kDistillChunk == kChunkColu
                   kDistillHeld == 1024 * 16 * kVec<true> && kDistillHeld == 2 * 1024 * 16 * kVec<false>,
               "the kernels' sizes");
 
-// Most workgroups of a launch; what is beyond loops.
-constexpr int64_t kMaxGrid = int64_t(1) << 20;
-dim3 grid_for(int64_t items) { return dim3(uint32_t(std::min(items, kMaxGrid))); }
+// A chunk to a workgroup: 2^20 at most, of rows of up to 2^22 columns.
+static_assert(kDistillChunkRows * ((int64_t(1) << 22) / kDistillChunk) <= int64_t(1) << 20, "workgroups of a launch");
 
 template <bool ZB, bool GB, int THREADS, int NV>
 forge_status launch_rows_t(const DistillArgs& a, int per_cu, hipStream_t s) {
@@ -38,11 +37,11 @@ template <bool ZB, bool GB>
 forge_status launch_chunks(DistillArgs a, hipStream_t s) {
   a.items = a.T * a.chunks;
   if (a.items > 0 && a.K > 0) {
-    hipLaunchKernelGGL((distill_stats_kernel<ZB>), grid_for(a.items), dim3(kChunkThreads), 0, s, a);
+    hipLaunchKernelGGL((distill_stats_kernel<ZB>), dim3(uint32_t(a.items)), dim3(kChunkThreads), 0, s, a);
     if (forge_status st = launch_status()) return st;
   }
   a.items = a.T * a.chunks_out;
-  hipLaunchKernelGGL((distill_gradient_kernel<ZB, GB>), grid_for(a.items), dim3(kChunkThreads), 0, s, a);
+  hipLaunchKernelGGL((distill_gradient_kernel<ZB, GB>), dim3(uint32_t(a.items)), dim3(kChunkThreads), 0, s, a);
   return launch_status();
 }
 
