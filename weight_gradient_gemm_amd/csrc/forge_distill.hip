@@ -48,18 +48,18 @@ forge_status launch_chunks(DistillArgs a, hipStream_t s) {
 // A row to a workgroup, or chunks of it (distill_in_chunks). Chunks take a launch
 // more (3 us) and read the logits twice, but a workgroup takes 5 us and one more for each 7000
 // columns with a row (for each 3500 where it does not hold it), however few there are: bf16
-// 8 x 128256 7.9 us in chunks and 21 by rows, 64 x 128256 18 and 23, 128 x 128256 30 and 24,
-// 64 x 32000 9.8 and 10.0, 8 x 8192 8.4 and 6.1. The loss alone: 8 x 128256 6.7 us in
-// chunks and 10.7 by rows, 64 x 128256 11.0 and 11.4, 8 x 60000 7.3 and 7.0.
+// 8 x 128256 7.6 us in chunks and 21 by rows, 64 x 128256 16 and 22, 96 x 128256 22 and 23, 128 x
+// 128256 26 and 23, 96 x 32000 10.5 and 10.6, 8 x 8192 7.8 and 6.6. The loss alone: 8 x 128256
+// 6.3 us in chunks and 10.0 by rows, 96 x 128256 11.0 and 10.9, 8 x 60000 6.5 and 6.5.
 //
 // Rows that are not held run one to a CU, and a last round of 256 of them takes half of a round
 // however few they are, where chunks take time by the row. So the rows of the last round
-// count: float32 with a bf16 gradient, 128256 columns, 128 rows 35 us in chunks and 45 by
-// rows, 192 47 and 52, 224 53 and 51; 257 59 and 82, 400 92 and 96, 448 101 and 103, 512 115 and 110;
-// 513 116 and 134, 600 137 and 147, 640 148 and 150, 700 162 and 155. Where most of the row is
-// held (70000 columns: 128 rows 24 and 23, 192 31 and 26, 257 38 and 40, 352 48 and 46) and
-// for bf16 (200000: 128 43 and 44, 192 56 and 48, 257 72 and 83, 320 86 and 86, 384 105 and 90, 513
-// 138 and 131) rows catch up earlier.
+// count: float32 with a bf16 gradient, 128256 columns, 128 rows 33 us in chunks and 45 by
+// rows, 256 55 and 55; 257 56 and 82, 448 95 and 104, 512 108 and 110; 513 108 and 134, 640 144 and
+// 150, 700 158 and 156 (100000 columns: 224 rows 40 and 39, 512 86 and 82, 700 118 and 116).
+// Where most of the row is held (70000 columns: 128 rows 22 and 23, 192 29 and 26, 352 45 and 46,
+// 384 48 and 47, 560 67 and 69, 600 72 and 71) and for bf16 (200000: 128 37 and 44, 192 49 and 48,
+// 384 89 and 90, 400 93 and 91, 513 120 and 131, 600 136 and 136) rows catch up earlier.
 template <bool ZB, bool GB>
 forge_status launch(const DistillArgs& a, hipStream_t s) {
   if (distill_in_chunks(a.T, a.V, ZB, a.grad != nullptr)) return launch_chunks<ZB, GB>(a, s);

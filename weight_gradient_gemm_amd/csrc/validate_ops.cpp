@@ -418,12 +418,12 @@ bool distill_sizes_ok(int64_t T, int64_t V, int64_t K) {
 }
 
 bool distill_in_chunks(int64_t T, int64_t V, bool bf16, bool grad) {
-  if (!grad) return V > 65536 && T <= 64;
+  if (!grad) return V > 65536 && T <= 96;
   const int64_t held = bf16 ? kDistillHeld : kDistillHeld / 2;
-  if (V <= held) return V > 16384 && T <= 64;
+  if (V <= held) return V > 16384 && T <= 96;
   if (T > kDistillChunkRows) return false;
   const int64_t rounds = (T - 1) / 256, last = T - 256 * rounds;      // one workgroup to a CU
-  return last <= (!bf16 && 2 * V >= 3 * held ? 192 - 40 * rounds : 128 - 64 * rounds);
+  return last <= (!bf16 && 2 * V >= 3 * held ? 208 - 32 * rounds : 160 - 48 * rounds);
 }
 
 DistillWorkspace distill_workspace(int64_t T, int64_t V, int64_t K) {

@@ -78,7 +78,7 @@ constexpr int64_t kDistillChunk = 4096;
 // Most columns of a row of bf16 logits that a workgroup's registers hold; float32 half.
 constexpr int64_t kDistillHeld = 131072;
 // Most rows that are cut into chunks, of any type of logits, and whether a call's are.
-constexpr int64_t kDistillChunkRows = 624;
+constexpr int64_t kDistillChunkRows = 656;
 bool distill_in_chunks(int64_t T, int64_t V, bool bf16, bool grad);
 // Byte offsets of the parts of distillation's workspace: each chunk's maximum
 // and sum of exponentials, and the student's logits of the teacher's ids. Only
