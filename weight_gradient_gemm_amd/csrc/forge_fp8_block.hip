@@ -14,10 +14,6 @@ namespace {
 // Tiles of the library's own choice, beside the public ids.
 enum : forge_tile { FP8_TILE_128x64 = FORGE_TILE_COUNT, FP8_TILE_64x64, FP8_TILE_ROWS };
 
-// Most rows of the long operand for the kernel of few rows: offsets of a batch of
-// groups (24 N kB apart) stay below 2^31.
-constexpr int64_t kRowsMaxN = 1 << 17;
-
 // Most workgroups that quantise along rows alone; what is beyond loops.
 constexpr int64_t kMaxRowGroups = int64_t(1) << 20;
 
@@ -34,12 +30,14 @@ using Fp864x64 = SmallTileCfg<64, 64, 2, 2, 2, 2>;
 // 1024 x 4096 x 4096: 17.8 at 128x128, 22 to 36; 8192 x 4096 x 14336: 312 at 256x256,
 // 318 by the persistent schedule; 4096 x 6144 x 16384: 276 by that, 297 at 256x256).
 //
-// Up to 16 rows take the kernel that cuts the contraction, whose time is that of
-// the long operand's bytes (1 x 4096 x 14336: 11.5 us, 24 at 64x64; 1 x 128256 x 4096: 90,
-// 91 at 128x128); up to 64 where its reads of the short operand by every
-// workgroup, 11.5 TB/s with the long one's, take less than the tiles (32 x 4096 x
-// 14336: 17.5 us, 24 at 64x64; 32 x 6144 x 4096: 9.3, 14.5 at 128x128; 64 x 14336 x 4096:
-// 29, 20 at 128x128).
+// Up to 64 rows take the kernel that cuts the contraction where 64x64 tiles are few:
+// up to so many workgroups of it (16 rows of the long operand each) to a CU as its reads of the
+// short operand leave room for, three for up to 4 rows, two for up to 16, one for more. Beyond
+// that tiles fill the chip as well and read the short operand less often (rows and tiles, us:
+// 1 x 4096 x 14336 11.8 and 24.3; 4 x 12288 x 14336 31.4 and 35.2, x 1024 5.5 and 5.3; 4 x 14336 x 14336
+// 40.2 and 36.7; 16 x 8192 x 4096 9.1 and 9.6, 16 x 9216 x 4096 10.2 and 9.7, x 14336 35.3 and 32.0; 32 x
+// 4096 x 4096 6.9 and 9.8, 32 x 5120 x 4096 9.8 and 9.6; 64 x 4096 x 14336 23.2 and 24.4, x 1024 5.5 and
+// 5.2, 64 x 5120 x 4096 14.4 and 9.7; 16 x 128256 x 4096 117 and 89, one row of it 92 and 92).
 forge_tile choose_tile(int64_t N, int64_t M, int64_t Kp) {
   struct Kind {
     forge_tile id;
@@ -51,8 +49,8 @@ forge_tile choose_tile(int64_t N, int64_t M, int64_t Kp) {
                                {FORGE_TILE_128x128, 128, 128, 2, 4, 0.19, 0.215, 3.1},
                                {FP8_TILE_128x64, 128, 64, 1, 8, 0.136, 0.17, 3.2},
                                {FP8_TILE_64x64, 64, 64, 2, 8, 0.096, 0.10, 2.4}};
-  const bool rows = M <= 64 && N <= kRowsMaxN;
-  if (rows && M <= 16) return FP8_TILE_ROWS;
+  const int64_t per_cu = M <= 4 ? 3 : M <= 16 ? 2 : M <= 64 ? 1 : 0;
+  if (N <= per_cu * 256 * 16) return FP8_TILE_ROWS;
   auto stages = [&](int ring) { return double((Kp / 64 + ring - 1) / ring * ring); };
   auto round = [&](const Kind& k, int64_t tiles) {
     if (tiles == 0) return 0.0;
@@ -78,7 +76,6 @@ forge_tile choose_tile(int64_t N, int64_t M, int64_t Kp) {
       best = FORGE_TILE_PERSISTENT;
     }
   }
-  if (rows && 2.5 + double(N) * double(Kp) * (M <= 32 ? 3 : 5) / 11.5e6 < least) return FP8_TILE_ROWS;
   return best;
 }
 

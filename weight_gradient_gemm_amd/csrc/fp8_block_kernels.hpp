@@ -532,8 +532,9 @@ void fp8_block_persistent_kernel(WgradArgs a, Fp8BlockArgs x) {
 // time: a lane holds 16 bytes of either half of a group, so that each load is
 // 1 KB on end (a run of 8 columns stays one, and the order of runs does not
 // matter to a sum that is joined in any case). Groups past the end read zeros.
-// 1 x 4096 x 14336 takes 11.5 us, 5.1 TB/s of its 59 MB, of which the chip's caches
-// may hold all; 1 x 128256 x 4096 90 us, 5.8 TB/s; with 16 waves and U = 4 152.
+// Launched for N of up to 12288, so that offsets within a batch (16 groups of 128 N bytes) are
+// small. 1 x 4096 x 14336 takes 11.8 us, 5.0 TB/s of its 59 MB, of which the chip's caches may
+// hold all; 4 x 12288 x 14336 31 us, 5.6 TB/s; 16 waves and U = 4 take 1.7 times as long where N is large.
 template <int MB, int W, int U, int FI, int FO>
 __global__ __launch_bounds__(64 * W) void fp8_block_rows_kernel(WgradArgs a, Fp8BlockArgs x) {
   __shared__ float join[W][MB * 4][64];
