@@ -370,7 +370,7 @@ FORGE_API forge_status forge_quantize_fp8_block(const void* x, forge_dtype x_dty
  * Accumulated in float32 by the fp8 matrix instruction, which truncates the
  * products of each run of 8 consecutive columns toward zero to 2^-13 of the run's
  * largest power of two (see forge_wgrad_fp8): at most 2^-10 of it in a run's
- * sum, which is below half a bf16 step of that product, and so the result is bf16.
+ * sum, which is below half a bf16 step of that product. The result comes in bf16 only.
  * tile: the ids of forge.h over [N, M], each of which gives the same bits; the
  * default may also take other tiles and, for few rows, cut the contraction.
  */

@@ -15,12 +15,12 @@
 // gradient. The loss alone goes once through a row and holds nothing.
 //
 // Measured: 4096 x 128256 bf16, a row in 8 left out, 411 us for 1.97 GB, 4.8 TB/s, what
-// a copy reaches; 1021 x 32003 float32 with a bf16 gradient 42 us, 4.3 TB/s of the needed
+// a copy reaches; 1021 x 32003 float32 with a bf16 gradient 43 us, 4.2 TB/s of the needed
 // bytes (entries' columns are written twice); 1024 x 128256 float32, not held whole, 206
 // us for the 1.05 GB that it cannot do without and 0.26 again; the loss of 511 x 50021
-// float32 17 us, 5.3 TB/s; 8 x 128256 bf16 9.0 us, two launches that wait for memory two
-// and one time. A row read twice by the same grid, the maximum first, took 1642 us for
-// the first of these.
+// float32 17 us, 5.3 TB/s; 8 x 128256 bf16 7.6 us in a graph (traced alone 3.3 and 5.1), two
+// launches that wait for memory two and one time. A row read twice by the same grid, the
+// maximum first, took 1642 us for the first of these.
 //
 // The teacher's columns are written with the others and once more, with their q,
 // behind a barrier: the workgroup that has the column does both.

@@ -21,7 +21,7 @@
 // registers, against a workgroup to a row: backward 77 and 103 us (with 8 instead of 64
 // groups in the second launch). Accesses past the caches (kStatePolicy): loads and
 // stores 56.4 us, one of the two 57.5 and 57.8, none 59.0, when the sums over a wave
-// still took 7 of them. One row of 4096 takes 2.3 us, 333 x 1000 float32 backward 4.2 + 3.2.
+// still took 7 of them. One row of 4096 takes 2.3 us, 333 x 1000 float32 backward 4.2 + 2.7.
 #pragma once
 
 #include <hip/hip_runtime.h>
